@@ -56,6 +56,10 @@ typedef enum {
                                  outside the exact window of mla_decode_fwd_mxfp4 (or NaN)  */
 #define MLA_DERR_DEBUG_BOUNDS 32 /* debug builds only: an index failed its bounds check and the
                                     access was skipped (never set by release builds)        */
+#define MLA_DERR_SEQ_LEN 64    /* mla_page_map: a negative length, or a row longer than its pages */
+#define MLA_DERR_FREE_PAGES 128 /* mla_page_map: the step needs more pages than free_pages holds  */
+#define MLA_DERR_CAPACITY 256  /* mla_page_map: an output array is shorter than the step's tokens */
+#define MLA_DERR_POSITION 512  /* mla_kv_append: a token's position lies outside the rope table   */
 
 /*
  * Launch plan for a batch shape.  The split-KV schedule (flash-decoding split,
@@ -417,6 +421,212 @@ mla_status_t mla_fp8_quantize_per_tensor(const void* src_bf16, int64_t n, void* 
  */
 mla_status_t mla_mxfp4_quantize(const void* src_bf16, int64_t rows, void* dst_fp4, void* dst_scales,
                                 cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the decode step: the page tables it reads, the cache rows it reads,
+ * and the attention of the prompts that fill them.  Their order in a serving
+ * step: mla_page_map (lengths -> tables and maps), mla_kv_append (new tokens ->
+ * cache), then mla_decode_fwd over kv_indptr / kv_indices, or mla_prefill_fwd
+ * over the prompt's expanded keys and values (in pieces joined by
+ * mla_attn_merge when the keys are attended a part at a time).
+ *
+ * As on the forward path nothing is allocated and nothing synchronises, work is
+ * ordered on `stream`, the device of the pointers must be current, and every
+ * call can be captured into a CUDA graph after one call outside capture.
+ * mla_page_map and mla_kv_append take a small workspace (at least
+ * MLA_STEP_WORKSPACE_BYTES, 256-byte aligned, zeroed once by
+ * mla_decode_workspace_init) that holds only the sticky error word read by
+ * mla_decode_read_error; any number of calls, overlapping ones too, may share it.
+ */
+#define MLA_STEP_WORKSPACE_BYTES 256
+#define MLA_MAX_MAP_ROWS 16384
+
+/*
+ * mla_page_map — block table, index and slot maps of one step, from the rows'
+ * lengths, in one kernel.  Row b holds L_b = kv_lens[b] cached tokens and gets
+ * n_b = new_lens[b] more; with P = page_size it owns ceil(L_b / P) pages and
+ * needs ceil((L_b + n_b) / P).  The missing pages are taken from free_pages
+ * front to back, rows in order:
+ *   block_table[b][ceil(L_b/P) + i] = free_pages[k_b + i],  k_b pages taken by rows before b
+ *   kv_indptr   prefix sums of L_b + n_b;   qo_indptr  prefix sums of n_b
+ *   kv_indices[kv_indptr[b] + j] = block_table[b][j / P] * P + j % P  for j < L_b + n_b:
+ *               the page-size-1 table of mla_decode_fwd
+ *   positions[qo_indptr[b] + i]  = L_b + i                            for i < n_b
+ *   slots[qo_indptr[b] + i]      = the cache row of that token, as in kv_indices
+ *   pages_used[0] = pages taken from free_pages
+ * slots past the last new token are set to -1 and positions there to 0 up to
+ * slots_len, so that an append launched for slots_len tokens skips them;
+ * kv_indices past the last token keeps its values.  Table entries other than the
+ * new pages' are not written.
+ *   kv_lens, new_lens  device int32 [batch], batch 1 .. MLA_MAX_MAP_ROWS; 0 allowed.
+ *   block_table   device int32, row b at block_table + b * table_stride, max_pages
+ *                 entries each (table_stride >= max_pages >= 1).
+ *   page_size, num_pages  >= 1, page_size * num_pages <= INT32_MAX: rows of the pool.
+ *   free_pages    device int32 [num_free] (NULL when num_free is 0).  Its entries
+ *                 must be distinct pages that no row owns.
+ *   qo_indptr, kv_indptr  device int32 [batch + 1].
+ *   kv_indices    device int32 [kv_indices_len], 16-byte aligned.
+ *   slots, positions  device int32 [slots_len] (NULL when slots_len is 0).
+ *   pages_used    device int32 [1].
+ * Both lengths are at most INT32_MAX - 1.  No output may overlap another array
+ * of the call; the inputs are not written, so repeating the call repeats its
+ * outputs.  A step that cannot be mapped (MLA_DERR_SEQ_LEN, MLA_DERR_FREE_PAGES,
+ * MLA_DERR_CAPACITY in the error word) is emptied: both indptrs and pages_used
+ * are 0, slots -1, and neither kv_indices nor the table is written.  A page id
+ * outside [0, num_pages) sets MLA_DERR_KV_INDEX; tokens on that page get -1.
+ */
+mla_status_t mla_page_map(const int32_t* kv_lens, const int32_t* new_lens, int32_t batch,
+                          int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                          int32_t page_size, int32_t num_pages, const int32_t* free_pages,
+                          int32_t num_free, int32_t* qo_indptr, int32_t* kv_indptr,
+                          int32_t* kv_indices, int64_t kv_indices_len, int32_t* slots,
+                          int32_t* positions, int64_t slots_len, int32_t* pages_used,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * mla_kv_append — new tokens into the cache: norm of the latent, rotation of the
+ * key's and the queries' position parts, quantisation and scatter, in one kernel.
+ * For token t with slot = slots[t] >= 0, pos = positions[t]:
+ *   c = kv[t][0:512], k = kv[t][512:576], (cos, sin) = rope_table[pos][0:32], [32:64]
+ *   c'[i] = c[i] * rsqrt(mean(c^2) + eps) * norm_weight[i]
+ *   rotation of pair i: (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i), the pair
+ *     being elements (2i, 2i + 1) if interleaved, else (i, i + 32)
+ *   cache[slot] = e4m3(clamp((c' | k') / *kv_scale, -448, 448)), float32 division and
+ *     rounding to nearest even as mla_fp8_quantize_per_tensor does it
+ *   latent_out[t] = bf16(c' | k')            (unless latent_out is NULL)
+ *   q_out[t][h] = bf16(rotated q_pe[t][h])   (64 dims of each head; num_heads may be 0)
+ * All in float32, rounded once.  A negative slot marks a padding token: nothing
+ * is written for it, neither its queries nor its latent_out row.  A slot outside
+ * the pool (MLA_DERR_KV_INDEX) or a position outside the table
+ * (MLA_DERR_POSITION) skips its token the same way.  Inputs must be finite.
+ * Slots must be distinct: of two tokens with one slot, each 8- or 16-byte piece
+ * of the cache row comes from either.
+ *   kv_bf16     device bf16, token t at kv_bf16 + t * kv_stride (>= 576).
+ *   norm_weight device bf16 [512];  rope_table device float [max_positions][64].
+ *   positions, slots  device int32 [num_tokens] (num_tokens 0 launches nothing).
+ *   cache_fp8   device e4m3fn [kv_rows][576]; kv_scale device float[1], > 0.
+ *   latent_out  device bf16 [num_tokens][576]; may be kv_bf16 itself (stride 576).
+ *   q_pe, q_out device bf16, head h of token t at t * token stride + h * head
+ *               stride; q_out may be q_pe itself with the same strides.
+ * Pointers are 16-byte aligned (positions, slots, kv_scale: 4), strides in
+ * elements, multiples of 8, >= 0 (of q_pe) or at least the row's dims (of the
+ * others); the stride of a single token or head is not used.  Other overlaps of inputs and outputs are
+ * not allowed.  mla_kv_append_bf16kv stores bf16 rows instead: cache_bf16 device
+ * bf16 [kv_rows][576], no scale.  There is no MXFP4 form: that cache's rows are
+ * written by mla_mxfp4_quantize.
+ */
+mla_status_t mla_kv_append(const void* kv_bf16, int64_t kv_stride, const void* norm_weight,
+                           float eps, const float* rope_table, int32_t max_positions,
+                           int32_t interleaved, const int32_t* positions, const int32_t* slots,
+                           int32_t num_tokens, void* cache_fp8, const float* kv_scale,
+                           int64_t kv_rows, void* latent_out, const void* q_pe,
+                           int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                           int64_t qo_token_stride, int64_t qo_head_stride, int32_t num_heads,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const void* norm_weight,
+                                  float eps, const float* rope_table, int32_t max_positions,
+                                  int32_t interleaved, const int32_t* positions,
+                                  const int32_t* slots, int32_t num_tokens, void* cache_bf16,
+                                  int64_t kv_rows, void* latent_out, const void* q_pe,
+                                  int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                                  int64_t qo_token_stride, int64_t qo_head_stride,
+                                  int32_t num_heads, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * mla_prefill_fwd — attention of prompts in the expanded form of latent
+ * attention: keys and values expanded from the latents for each head, the
+ * rotated 64-dim part of the key shared by the heads.  For query i (of n_b) of
+ * row b, head h, over the row's L_b keys j that it sees:
+ *   s_j = scale * (q[i][h][0:128] . k_nope[j][h] + q[i][h][128:192] . k_rope[j])
+ *   out[i][h] = softmax_j(s) . v[j][h],   lse[i][h] = log sum_j exp(s_j)
+ * causal != 0: query i sees the first L_b - n_b + 1 + i keys (the row's last
+ * n_b keys are the queries' own, as for rows of several tokens of the decode
+ * step), none if that is not positive; causal == 0: all L_b keys.  A query that
+ * sees no key gets zeros and lse -inf.  Products run on bf16 tensor-core operands
+ * with float32 accumulation, the probabilities rounded to bf16 before the second
+ * product; softmax statistics are float32; out is rounded once.
+ *   q       device bf16, token t head h at t * q_token_stride + h * q_head_stride, 192 dims.
+ *   k_nope  device bf16, 128 dims;  v device bf16, 128 dims: strided the same way
+ *           (both are usually halves of one [tokens][heads][256] product).
+ *   k_rope  device bf16, token t at t * kr_token_stride, 64 dims (for instance the
+ *           last 64 dims of mla_kv_append's latent_out).
+ *   total_kv  rows of k_nope, k_rope and v (0 .. INT32_MAX).
+ *   qo_indptr, kv_indptr  device int32 [batch + 1], non-decreasing; row b owns
+ *           query tokens [qo_indptr[b], qo_indptr[b+1]) and keys [kv_indptr[b],
+ *           kv_indptr[b+1]).  Empty rows are allowed on either side.
+ *   scale   positive and finite (1 / sqrt(192) for the plain step).
+ *   out     device bf16 [total_q][num_heads][128], 16-byte aligned; lse device
+ *           float [total_q][num_heads], or NULL.  Tokens of no row are left alone.
+ *   plan, workspace  from mla_prefill_plan; workspace 256-byte aligned, zeroed
+ *           once.  Calls sharing a workspace must not overlap on the GPU.
+ * Base pointers are 16-byte aligned; strides are in elements, multiples of 8, at
+ * least the row's dims, below 2^36 (tokens or heads outermost; the stride of a
+ * single token or head is not used).  Values of the rows' own tokens must be finite; what lies outside
+ * the rows (padding, other rows' tokens) may hold anything.  No output may
+ * overlap an input.  Rows outside total_q or total_kv set MLA_DERR_QO_INDPTR /
+ * MLA_DERR_KV_INDPTR and are not written.  Deterministic for a given plan.
+ */
+#define MLA_PREFILL_QK_DIM 192
+#define MLA_PREFILL_NOPE_DIM 128
+#define MLA_PREFILL_V_DIM 128
+typedef struct {
+  int32_t batch;       /* rows                                                        */
+  int32_t total_q;     /* query tokens that q and out have room for (0 allowed)        */
+  int32_t max_kv_len;  /* upper bound on a row's keys (sizes the split only)           */
+  int32_t num_heads;   /* 1 .. 1024                                                    */
+  int32_t num_sms;     /* SMs the split is sized for                                   */
+  int32_t splits;      /* parts a row's keys are cut into when the queries alone leave
+                        * SMs idle; the parts are joined by a second kernel            */
+  int32_t tiles;       /* blocks of up to 256 queries, at most: total_q / 256 + min(batch, total_q) */
+  int32_t abi_version; /* MLA_ABI_VERSION                                              */
+  uint64_t ws_bytes;   /* workspace bytes mla_prefill_fwd needs                        */
+  uint64_t ws_lse_offset;     /* float[splits][total_q][num_heads] when splits > 1     */
+  uint64_t ws_partial_offset; /* float[splits][total_q][num_heads][128] when splits > 1 */
+} mla_prefill_plan_t;
+
+/* Pure host.  batch 1 .. 2^20, total_q and max_kv_len >= 0; num_sms <= 0 asks the device. */
+mla_status_t mla_prefill_plan(int32_t batch, int32_t total_q, int32_t max_kv_len,
+                              int32_t num_heads, int32_t num_sms, mla_prefill_plan_t* plan);
+
+mla_status_t mla_prefill_fwd(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             const void* k_nope, int64_t kn_token_stride, int64_t kn_head_stride,
+                             const void* k_rope, int64_t kr_token_stride, const void* v,
+                             int64_t v_token_stride, int64_t v_head_stride, int64_t total_kv,
+                             const int32_t* qo_indptr, const int32_t* kv_indptr, float scale,
+                             int32_t causal, void* out, float* lse, cudaStream_t stream,
+                             const mla_prefill_plan_t* plan, void* workspace,
+                             size_t workspace_bytes);
+
+/* Test hook for the bounded waits, as mla_decode_fwd_stall_stream: no copy is
+ * issued, every wait runs out, the call reports MLA_DERR_TIMEOUT and returns. */
+mla_status_t mla_prefill_fwd_stall_stream(const void* q, int64_t q_token_stride,
+                                          int64_t q_head_stride, const void* k_nope,
+                                          int64_t kn_token_stride, int64_t kn_head_stride,
+                                          const void* k_rope, int64_t kr_token_stride,
+                                          const void* v, int64_t v_token_stride,
+                                          int64_t v_head_stride, int64_t total_kv,
+                                          const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                          float scale, int32_t causal, void* out, float* lse,
+                                          cudaStream_t stream, const mla_prefill_plan_t* plan,
+                                          void* workspace, size_t workspace_bytes);
+
+/*
+ * mla_attn_merge — joins attention over disjoint sets of keys.  Piece s holds for
+ * each of `rows` (token, head) rows its output parts[s][row][dim] and the natural
+ * log-sum-exp lses[s][row] of its scores:
+ *   lse[row] = log sum_s exp(lses[s][row]);  out[row] = sum_s exp(lses[s][row] - lse[row]) parts[s][row]
+ * in float32, out rounded once to bf16.  A piece whose lse is -inf saw no key: its
+ * output is not read.  A row that no piece saw gets zeros and lse -inf.
+ *   parts_bf16 device bf16 [num_parts][rows][dim];  lses device float [num_parts][rows]
+ *   out_bf16   device bf16 [rows][dim] (may be one of the parts)
+ *   lse_out    device float [rows], or NULL; must not overlap lses
+ *   num_parts 1 .. 64;  rows 0 .. INT32_MAX;  dim a multiple of 8, 8 .. 1024.
+ * bf16 arrays 16-byte aligned.  Deterministic.
+ */
+mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t num_parts,
+                            int64_t rows, int32_t dim, void* out_bf16, float* lse_out,
+                            cudaStream_t stream);
 
 /* Zero a workspace (cudaMemsetAsync of ws_bytes on `stream`). */
 mla_status_t mla_decode_workspace_init(void* workspace, size_t workspace_bytes, cudaStream_t stream);

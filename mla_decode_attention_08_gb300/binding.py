@@ -18,7 +18,11 @@ NUM_HEADS, QK_HEAD_DIM, V_HEAD_DIM, TILE_TOKENS = 16, 576, 512, 128
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported device", 3: "workspace too small",
           4: "CUDA call failed"}
-DERR = {1: "qo_indptr", 2: "kv_indptr", 4: "kv_index", 8: "timeout", 16: "mx_scale"}
+DERR = {1: "qo_indptr", 2: "kv_indptr", 4: "kv_index", 8: "timeout", 16: "mx_scale",
+        64: "seq_len", 128: "free_pages", 256: "capacity", 512: "position"}
+STEP_WORKSPACE_BYTES = 256
+PREFILL_QK_DIM, PREFILL_NOPE_DIM, PREFILL_V_DIM = 192, 128, 128
+ROPE_DIM = QK_HEAD_DIM - V_HEAD_DIM
 
 
 class MlaError(RuntimeError):
@@ -37,13 +41,39 @@ class mla_plan_t(ctypes.Structure):
                 ("ws_partial_offset", ctypes.c_uint64)]
 
 
+class mla_prefill_plan_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("max_kv_len", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("num_sms", ctypes.c_int32), ("splits", ctypes.c_int32),
+                ("tiles", ctypes.c_int32), ("abi_version", ctypes.c_int32),
+                ("ws_bytes", ctypes.c_uint64), ("ws_lse_offset", ctypes.c_uint64),
+                ("ws_partial_offset", ctypes.c_uint64)]
+
+
 _VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _PLANP = ctypes.POINTER(mla_plan_t)
 _FWD_ARGS = [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _PLANP, _VP, _I64, _I64, _VP, _SZ]
 _FWD_BF16KV_ARGS = _FWD_ARGS[:2] + _FWD_ARGS[3:]  # no kv_scale
 # q, kv_fp4, kv_scales, scale_bias, qo_indptr, kv_indptr, out, stream, plan, kv_rows, ws, ws_bytes
 _FWD_MXFP4_ARGS = [_VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _PLANP, _I64, _VP, _SZ]
+_F32 = ctypes.c_float
+_PREFILL_PLANP = ctypes.POINTER(mla_prefill_plan_t)
+# kv, kv_stride, weight, eps, rope_table, max_positions, interleaved, positions, slots, num_tokens,
+# cache, kv_scale, kv_rows, latent_out, q_pe + strides, q_out + strides, heads, ws, ws_bytes, stream
+_APPEND_ARGS = [_VP, _I64, _VP, _F32, _VP, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I64, _VP,
+                _VP, _I64, _I64, _VP, _I64, _I64, _I32, _VP, _SZ, _VP]
+# q, k_nope, k_rope, v with their strides, total_kv, indptrs, scale, causal, out, lse, stream, plan, ws
+_PREFILL_ARGS = [_VP, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _VP, _I64, _I64, _I64, _VP, _VP, _F32,
+                 _I32, _VP, _VP, _VP, _PREFILL_PLANP, _VP, _SZ]
 SIGNATURES = {
+    "mla_page_map": (ctypes.c_int, [_VP, _VP, _I32, _VP, _I64, _I32, _I32, _I32, _VP, _I32, _VP, _VP,
+                                    _VP, _I64, _VP, _VP, _I64, _VP, _VP, _SZ, _VP]),
+    "mla_kv_append": (ctypes.c_int, _APPEND_ARGS),
+    "mla_kv_append_bf16kv": (ctypes.c_int, _APPEND_ARGS[:11] + _APPEND_ARGS[12:]),  # no kv_scale
+    "mla_prefill_plan": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _PREFILL_PLANP]),
+    "mla_prefill_fwd": (ctypes.c_int, _PREFILL_ARGS),
+    "mla_prefill_fwd_stall_stream": (ctypes.c_int, _PREFILL_ARGS),
+    "mla_attn_merge": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _VP, _VP, _VP]),
     "mla_decode_plan": (ctypes.c_int, [_I32, _I32, _I32, _PLANP]),
     "mla_decode_plan_mtp": (ctypes.c_int, [_I32, _I32, _I32, _I32, _PLANP]),
     "mla_decode_fwd": (ctypes.c_int, _FWD_ARGS),
@@ -291,6 +321,243 @@ def mla_fp8_quantize_per_tensor(src_bf16, dst_fp8, scale_out, tmp, stream=None) 
         _dev_ptr(src_bf16, "src", torch.bfloat16), src_bf16.numel(), _dev_ptr(dst_fp8, "dst"),
         _dev_ptr(scale_out, "scale_out", torch.float32), _dev_ptr(tmp, "tmp"),
         tmp.numel() * tmp.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the decode step
+def _operands(fn: str, *named) -> torch.device:
+    """The one CUDA device of (name, tensor, dtype) operands of ``fn`` (None tensors are skipped)."""
+    dev = None
+    for name, t, dtype in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, the other tensors on {dev}")
+    return dev
+
+
+def _dense(*named) -> None:
+    for name, t in named:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _shape(name: str, t: torch.Tensor, *dims) -> None:
+    """``t`` must have these sizes (None: any)."""
+    if t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape)):
+        want = ", ".join("*" if d is None else str(d) for d in dims)
+        raise ValueError(f"{name} must be [{want}], got {list(t.shape)}")
+
+
+def _strides(name: str, t: torch.Tensor):
+    """Element strides of the leading dims of a tensor whose last dim is dense."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # a dimension of size one has no stride of its own (torch may report any value)
+    return [s if n > 1 else t.shape[-1] for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+def _launch(fn: str, device: torch.device, stream, make_args) -> None:
+    """Call ``fn`` with ``device`` current, on ``stream`` or that device's current stream."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _check(fn, getattr(load_library(), fn)(*make_args(_stream(stream))))
+    else:
+        _check(fn, getattr(load_library(), fn)(*make_args(_stream(stream))))
+
+
+def mla_page_map(kv_lens, new_lens, block_table, free_pages, qo_indptr, kv_indptr, kv_indices, slots,
+                 positions, pages_used, stream=None, *, page_size: int, num_pages: int,
+                 workspace) -> None:
+    """Tables and maps of one step from the rows' lengths (see the C header).
+
+    ``kv_lens``/``new_lens`` int32 [B] (cached tokens, and tokens this step adds),
+    ``block_table`` int32 [B, max_pages] (rows may be strided; new pages are filled
+    in from ``free_pages`` int32 [F] or None), then the outputs: ``qo_indptr``,
+    ``kv_indptr`` int32 [B + 1], ``kv_indices`` int32, ``slots`` and ``positions``
+    int32 of one length (or both None), ``pages_used`` int32 [1].  ``workspace``:
+    STEP_WORKSPACE_BYTES, zeroed once; errors are read by mla_decode_read_error."""
+    i32 = torch.int32
+    dev = _operands("mla_page_map", ("kv_lens", kv_lens, i32), ("new_lens", new_lens, i32),
+                    ("block_table", block_table, i32), ("free_pages", free_pages, i32),
+                    ("qo_indptr", qo_indptr, i32), ("kv_indptr", kv_indptr, i32),
+                    ("kv_indices", kv_indices, i32), ("slots", slots, i32),
+                    ("positions", positions, i32), ("pages_used", pages_used, i32),
+                    ("workspace", workspace, None))
+    _dense(("kv_lens", kv_lens), ("new_lens", new_lens), ("free_pages", free_pages),
+           ("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("kv_indices", kv_indices),
+           ("slots", slots), ("positions", positions), ("pages_used", pages_used),
+           ("workspace", workspace))
+    b = kv_lens.numel()
+    _shape("block_table", block_table, b, None)
+    if (new_lens.numel() != b or qo_indptr.numel() != b + 1 or kv_indptr.numel() != b + 1
+            or pages_used.numel() != 1):
+        raise ValueError("new_lens must hold B entries, the indptrs B + 1, pages_used one")
+    n_slots = 0 if slots is None else slots.numel()
+    if n_slots != (0 if positions is None else positions.numel()):
+        raise ValueError("slots and positions must have one length")
+    width = block_table.shape[1]
+    if width > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table's rows must be contiguous")
+    if b > 1 and block_table.stride(0) < width:
+        raise ValueError("block_table's rows must not overlap")
+    _launch("mla_page_map", dev, stream, lambda s: (
+        kv_lens.data_ptr(), new_lens.data_ptr(), b, block_table.data_ptr(),
+        block_table.stride(0) if b > 1 else width, width, int(page_size), int(num_pages),
+        None if free_pages is None else free_pages.data_ptr(),
+        0 if free_pages is None else free_pages.numel(), qo_indptr.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_indices.numel(), None if slots is None else slots.data_ptr(),
+        None if positions is None else positions.data_ptr(), n_slots, pages_used.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+
+
+def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, stream, workspace,
+            eps, interleaved, q_pe, q_out, latent_out):
+    bf16, i32 = torch.bfloat16, torch.int32
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out come together")
+    dev = _operands(fn, ("kv", kv, bf16), ("norm_weight", norm_weight, bf16),
+                    ("rope_table", rope_table, torch.float32), ("positions", positions, i32),
+                    ("slots", slots, i32), ("cache", cache, None), ("kv_scale", kv_scale, torch.float32),
+                    ("q_pe", q_pe, bf16), ("q_out", q_out, bf16), ("latent_out", latent_out, bf16),
+                    ("workspace", workspace, None))
+    _dense(("norm_weight", norm_weight), ("rope_table", rope_table), ("positions", positions),
+           ("slots", slots), ("cache", cache), ("latent_out", latent_out), ("workspace", workspace))
+    t = kv.shape[0]
+    _shape("kv", kv, None, QK_HEAD_DIM)
+    _shape("rope_table", rope_table, None, ROPE_DIM)
+    if norm_weight.numel() != V_HEAD_DIM or positions.numel() != t or slots.numel() != t:
+        raise ValueError("norm_weight must hold 512 values, positions and slots one entry a token")
+    if latent_out is not None:
+        _shape("latent_out", latent_out, t, QK_HEAD_DIM)
+    heads, qs, os_ = 0, (0, 0), (0, 0)
+    if q_pe is not None:
+        heads = q_pe.shape[1] if q_pe.dim() == 3 else -1
+        _shape("q_pe", q_pe, t, heads, ROPE_DIM)
+        _shape("q_out", q_out, t, heads, ROPE_DIM)
+        qs, os_ = _strides("q_pe", q_pe), _strides("q_out", q_out)
+    ks = _strides("kv", kv)[0]
+    scale = () if kv_scale is None else (kv_scale.data_ptr(),)
+    _launch(fn, dev, stream, lambda s: (
+        kv.data_ptr(), ks, norm_weight.data_ptr(), float(eps), rope_table.data_ptr(),
+        rope_table.shape[0], int(interleaved), positions.data_ptr(), slots.data_ptr(), t,
+        cache.data_ptr(), *scale, cache.shape[0], None if latent_out is None else latent_out.data_ptr(),
+        None if q_pe is None else q_pe.data_ptr(), *qs, None if q_out is None else q_out.data_ptr(),
+        *os_, heads, workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+
+
+def mla_kv_append(kv, norm_weight, rope_table, positions, slots, kv_fp8, kv_scale, stream=None, *,
+                  workspace, eps: float = 1e-6, interleaved: bool = True, q_pe=None, q_out=None,
+                  latent_out=None) -> None:
+    """New tokens into an e4m3 cache: norm of the latent, rotation of the key (and of
+    the queries), quantisation, scatter (see the C header).
+
+    ``kv`` bf16 [T, 576] (rows may be strided), ``norm_weight`` bf16 [512], ``rope_table``
+    float32 [positions, 64] (cos | sin of 32 pairs), ``positions``/``slots`` int32 [T]
+    (a negative slot skips the token), ``kv_fp8`` [rows, 576], ``kv_scale`` float32 [1];
+    ``q_pe`` -> ``q_out`` bf16 [T, H, 64] (strided; may be one tensor), ``latent_out``
+    bf16 [T, 576].  ``workspace``: STEP_WORKSPACE_BYTES, zeroed once."""
+    if kv_scale is None or kv_scale.numel() != 1:
+        raise ValueError("kv_scale must be one float32")
+    _append("mla_kv_append", kv, norm_weight, rope_table, positions, slots, _e4m3_cache(kv_fp8),
+            kv_scale, stream, workspace, eps, interleaved, q_pe, q_out, latent_out)
+
+
+def mla_kv_append_bf16kv(kv, norm_weight, rope_table, positions, slots, kv_bf16, stream=None, *,
+                         workspace, eps: float = 1e-6, interleaved: bool = True, q_pe=None,
+                         q_out=None, latent_out=None) -> None:
+    """mla_kv_append into a bf16 cache ``[rows, 576]`` (no scale)."""
+    if not isinstance(kv_bf16, torch.Tensor) or kv_bf16.dtype != torch.bfloat16:
+        raise TypeError("kv_bf16 must be a bfloat16 CUDA tensor")
+    if kv_bf16.dim() not in (2, 3) or kv_bf16.numel() != kv_bf16.shape[0] * QK_HEAD_DIM:
+        raise ValueError(f"kv_bf16 must be [rows, 576] or [rows, 1, 576], got {tuple(kv_bf16.shape)}")
+    _append("mla_kv_append_bf16kv", kv, norm_weight, rope_table, positions, slots, kv_bf16, None,
+            stream, workspace, eps, interleaved, q_pe, q_out, latent_out)
+
+
+def mla_prefill_plan(batch: int, total_q: int, max_kv_len: int, num_heads: int = NUM_HEADS,
+                     num_sms: int = 0) -> mla_prefill_plan_t:
+    """Plan of mla_prefill_fwd for ``batch`` rows with ``total_q`` query tokens in all."""
+    plan = mla_prefill_plan_t()
+    _check("mla_prefill_plan", load_library().mla_prefill_plan(batch, total_q, max_kv_len, num_heads,
+                                                              num_sms, ctypes.byref(plan)))
+    return plan
+
+
+def _prefill(fn, q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream, plan, workspace, scale,
+             causal, lse):
+    bf16, i32 = torch.bfloat16, torch.int32
+    dev = _operands(fn, ("q", q, bf16), ("k_nope", k_nope, bf16), ("k_rope", k_rope, bf16),
+                    ("v", v, bf16), ("qo_indptr", qo_indptr, i32), ("kv_indptr", kv_indptr, i32),
+                    ("out", out, bf16), ("lse", lse, torch.float32), ("workspace", workspace, None))
+    _dense(("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("out", out), ("lse", lse),
+           ("workspace", workspace))
+    t, h, b = int(plan.total_q), int(plan.num_heads), int(plan.batch)
+    n = k_nope.shape[0]
+    _shape("q", q, t, h, PREFILL_QK_DIM)
+    _shape("k_nope", k_nope, n, h, PREFILL_NOPE_DIM)
+    _shape("k_rope", k_rope, n, PREFILL_QK_DIM - PREFILL_NOPE_DIM)
+    _shape("v", v, n, h, PREFILL_V_DIM)
+    _shape("out", out, t, h, PREFILL_V_DIM)
+    if lse is not None:
+        _shape("lse", lse, t, h)
+    if qo_indptr.numel() != b + 1 or kv_indptr.numel() != b + 1:
+        raise ValueError("qo_indptr and kv_indptr must hold plan.batch + 1 entries")
+    qs, ns, rs, vs = (_strides("q", q), _strides("k_nope", k_nope), _strides("k_rope", k_rope),
+                      _strides("v", v))
+    if scale is None:
+        scale = PREFILL_QK_DIM ** -0.5
+    _launch(fn, dev, stream, lambda s: (
+        q.data_ptr(), *qs, k_nope.data_ptr(), *ns, k_rope.data_ptr(), *rs, v.data_ptr(), *vs, n,
+        qo_indptr.data_ptr(), kv_indptr.data_ptr(), float(scale), int(causal), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), s, ctypes.byref(plan), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size()))
+
+
+def mla_prefill_fwd(q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream=None, *, plan, workspace,
+                    scale: Optional[float] = None, causal: bool = True, lse=None) -> torch.Tensor:
+    """Attention of prompts in the expanded form (see the C header); writes and returns ``out``.
+
+    ``q`` bf16 [total_q, H, 192], ``k_nope`` and ``v`` bf16 [tokens, H, 128], ``k_rope`` bf16
+    [tokens, 64] (all may be strided views with a dense last dimension), ``out`` bf16
+    [total_q, H, 128], ``lse`` float32 [total_q, H] or None; ``scale`` defaults to 192 ** -0.5."""
+    _prefill("mla_prefill_fwd", q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream, plan,
+             workspace, scale, causal, lse)
+    return out
+
+
+def mla_prefill_fwd_stall_stream(q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream=None, *,
+                                 plan, workspace, scale: Optional[float] = None,
+                                 causal: bool = True, lse=None) -> None:
+    """Test hook: the launch of mla_prefill_fwd with copies that never arrive, so that the
+    bounded waits run out and the call reports MLA_DERR_TIMEOUT."""
+    _prefill("mla_prefill_fwd_stall_stream", q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream,
+             plan, workspace, scale, causal, lse)
+
+
+def mla_attn_merge(parts, lses, out, stream=None, *, lse_out=None) -> torch.Tensor:
+    """Join attention over disjoint keys: ``parts`` bf16 [S, ..., dim] with natural
+    log-sum-exps ``lses`` float32 [S, ...] into ``out`` bf16 [..., dim] (and ``lse_out``
+    float32 [...]); returns ``out`` (see the C header)."""
+    dev = _operands("mla_attn_merge", ("parts", parts, torch.bfloat16), ("lses", lses, torch.float32),
+                    ("out", out, torch.bfloat16), ("lse_out", lse_out, torch.float32))
+    _dense(("parts", parts), ("lses", lses), ("out", out), ("lse_out", lse_out))
+    rows = parts.shape[1:-1]
+    if parts.dim() < 2 or lses.shape != parts.shape[:-1] or out.shape != parts.shape[1:]:
+        raise ValueError("parts must be [S, ..., dim], lses [S, ...], out [..., dim]")
+    if lse_out is not None and lse_out.shape != rows:
+        raise ValueError("lse_out must have one entry a row")
+    _launch("mla_attn_merge", dev, stream, lambda s: (
+        parts.data_ptr(), lses.data_ptr(), parts.shape[0], rows.numel(), parts.shape[-1],
+        out.data_ptr(), None if lse_out is None else lse_out.data_ptr(), s))
+    return out
 
 
 def mla_debug_q_operand(q, kv_scale, tokens_per_cta: int = 1, stream=None):

@@ -24,7 +24,8 @@ BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmla_decode_debug.so")
 BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(PKG, "libmla_decode_trace.so")
-SOURCES = ["stage1.cu", "stage2.cu", "fp8_quant.cu", "mxfp4_quant.cu", "api.cu", "static_scratch.cu"]
+SOURCES = ["stage1.cu", "stage2.cu", "fp8_quant.cu", "mxfp4_quant.cu", "api.cu", "static_scratch.cu",
+           "page_map.cu", "kv_append.cu", "attn_merge.cu", "prefill.cu", "api_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -7,6 +7,7 @@
 
 #include "../../include/mla_decode.h"
 #include "kernels.h"
+#include "ops.h"
 #include "schedule.h"
 
 namespace {
@@ -180,7 +181,10 @@ mla_status_t prepare_device(int* device_out) {
     return MLA_ERR_CUDA;
   if (major != 10 || minor != 3) return MLA_ERR_UNSUPPORTED;
   if (static_cast<size_t>(smem) < mla::stage1_smem_bytes()) return MLA_ERR_UNSUPPORTED;
-  if (mla::stage1_prepare(device) != cudaSuccess) return MLA_ERR_CUDA;
+  if (static_cast<size_t>(smem) < mla::prefill_smem_bytes()) return MLA_ERR_UNSUPPORTED;
+  if (mla::stage1_prepare(device) != cudaSuccess || mla::page_map_prepare() != cudaSuccess ||
+      mla::prefill_prepare() != cudaSuccess)
+    return MLA_ERR_CUDA;
   ready[device].store(1, std::memory_order_release);
   return MLA_OK;
 }
@@ -332,6 +336,8 @@ mla_status_t run_decode(const void* q, const void* kv, const float* kv_scale,
 }
 
 }  // namespace
+
+mla_status_t mla::device_ready(int* device) { return prepare_device(device); }
 
 extern "C" {
 

@@ -1,0 +1,533 @@
+// mla_prefill_fwd: attention of prompts with keys and values expanded for each
+// head (192-dim queries, keys = 128 dims of the head | 64 rotated dims shared by
+// the heads, 128-dim values).
+//
+// A block owns 256 queries of one row and head as two tiles of 128 (t = 0, 1)
+// and walks the row's keys in tiles of 128 (j):
+//   * warp 8 streams K(j) (three 64-dim panels of 128 keys) and V(j) (two panels
+//     of 64 keys x 128 dims) by TMA into a ring of eight 16 KB slots,
+//   * warp 9 issues S_t = Q_t . K(j)^T and O_t += P_t . V(j) (tcgen05, float32
+//     accumulators in TMEM, P_t read from TMEM),
+//   * warps 0-3 and 4-7 run the online softmax of tile t, a thread a row: S out
+//     of TMEM, running maximum and sum in registers, P back over S as bf16.
+// TMEM is full: S_0 | S_1 | O_0 | O_1, 128 columns each, P_t in S_t's first 64.
+// The two tiles alternate: while the tensor cores work on one tile's products
+// the other tile's softmax runs.  K and V are read from shared memory for both
+// tiles, so a block moves 80 KB for 2 x 128 x 128 x 320 multiply-adds.
+#include <cstddef>
+
+#include "ops.h"
+#include "ptx.cuh"
+#include "kernels.h"
+
+namespace mla {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kPanelBytes = 16384;
+constexpr int kQPanels = kPrefillQk / 64;              // per query tile
+constexpr int kKPanels = kPrefillQk / 64;              // per key tile: 2 of the head, 1 shared
+constexpr int kVPanels = 2;                            // 64 keys x 128 dims each
+constexpr int kFillsPerTile = kKPanels + kVPanels;
+constexpr int kSlots = 8;
+constexpr int kOffQ = 0;
+constexpr int kOffRing = kOffQ + 2 * kQPanels * kPanelBytes;
+constexpr int kOffMisc = kOffRing + kSlots * kPanelBytes;
+// Three warpgroups: two of softmax, one with the producer, the MMA issuer and
+// two idle warps, whose registers go to the softmax (a row of 128 scores stays
+// in registers).
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
+              "register split exceeds the launch allocation");
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kLayoutSw128 = 2;
+constexpr uint32_t kColS = 0, kColO = 256;             // + 128 t
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdescQK = idesc_bf16(kTile, kTile, false, false);
+constexpr uint32_t kIdescPV = idesc_bf16(kTile, kPrefillV, false, true);
+// The running reference of the exponent follows the maximum only when it is
+// passed by more than this many powers of two: P then stays below 2^8, which
+// costs bf16 nothing, and most tiles rescale nothing.
+constexpr float kRescaleThreshold = 8.0f;
+
+struct Misc {
+  uint64_t q_full[2];
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t s_full[2];   // S_t(j) complete, and with it every product before it
+  uint64_t p_full[2];   // P_t(j) written (and O_t rescaled)
+  uint64_t o_full[2];   // the last product of tile t complete
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  volatile int32_t abort_flag;
+  // This block's work.
+  int32_t q0;           // first query token (of the batch)
+  int32_t nq;           // queries of this block, 0: nothing to do
+  int32_t k0, len;      // the row's first key and number of keys
+  int32_t see;          // keys that the block's first query sees, when causal
+};
+constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of one block");
+static_assert(kPrefillV == 128 && kPrefillNope == 128 && kPrefillRope == 64, "tile layout");
+
+// Bounded wait on an mbarrier phase; false when the call is being abandoned.
+// (Inlined: code whose register count setmaxnreg raised admits no calls.)
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Misc* ms, int32_t* err) {
+  const long long start = clock64();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 15) == 0) {
+      if (ms->abort_flag) return false;
+      if (clock64() - start > kWaitLimitCycles) {
+        ms->abort_flag = 1;
+        atomicOr(err, MLA_DERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_on(const uint64_t* bar, uint32_t parity, Misc* ms, int32_t* err) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return true;
+  return wait_slow(b, parity, ms, err);
+}
+// The same by a whole warp, which goes on or gives up together.
+__device__ __forceinline__ bool warp_wait_on(const uint64_t* bar, uint32_t parity, Misc* ms, int32_t* err) {
+  return __all_sync(0xffffffffu, wait_on(bar, parity, ms, err));
+}
+// Bounded wait while draining at the end of a call.
+__device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
+  const long long start = clock64();
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(smem_u32(bar), parity)) return;
+    if ((n & 15) == 15 && clock64() - start > kWaitLimitCycles) return;
+  }
+}
+
+__device__ __forceinline__ int32_t tiles_256(int32_t n) { return n / kPrefillRows + (n % kPrefillRows != 0); }
+
+// Finds block `rank`'s row and queries (one warp).  The rows' blocks of 256
+// queries, in order, are handed out from the last one: with causal rows a
+// row's later queries see more keys, so its long blocks start first.
+__device__ __forceinline__ void find_work(const PrefillParams& p, int32_t rank, bool report, Misc* ms) {
+  const int lane = threadIdx.x & 31;
+  const int32_t run = (p.batch + 31) / 32;
+  const int32_t b0 = min(p.batch, lane * run), b1 = min(p.batch, b0 + run);
+  auto row_tiles = [&](int32_t b, bool tell) {
+    const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
+    const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
+    const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || ke < ks || ke > p.total_kv;
+    if (tell && (bad_q || bad_k))
+      atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
+    return bad_q || bad_k ? 0 : tiles_256(qe - qs);
+  };
+  int32_t mine = 0;
+  for (int32_t b = b0; b < b1; ++b) mine += row_tiles(b, report);
+  int32_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  const int32_t total = __shfl_sync(0xffffffffu, incl, 31);
+  int32_t target = total - 1 - rank;
+  if (target < 0) {
+    if (lane == 0) ms->nq = 0;
+    return;
+  }
+  if (target < incl - mine || target >= incl) return;
+  target -= incl - mine;
+  for (int32_t b = b0; b < b1; ++b) {
+    const int32_t nt = row_tiles(b, false);
+    if (target < nt) {
+      const int32_t qs = __ldg(p.qo_indptr + b), n = __ldg(p.qo_indptr + b + 1) - qs;
+      const int32_t ks = __ldg(p.kv_indptr + b), len = __ldg(p.kv_indptr + b + 1) - ks;
+      const int32_t i0 = target * kPrefillRows;
+      ms->q0 = qs + i0;
+      ms->nq = min(kPrefillRows, n - i0);
+      ms->k0 = ks;
+      ms->len = len;
+      ms->see = len - n + i0 + 1;
+      return;
+    }
+    target -= nt;
+  }
+}
+
+// A block's key tiles: [j0, j1) of the row for its split, and how many of them
+// query tile t needs.
+struct Range {
+  int32_t j0, nt[2];
+};
+__device__ __forceinline__ Range key_range(const PrefillParams& p, const Misc* ms, int32_t split) {
+  Range r;
+  auto tiles = [&](int32_t last) {  // key tiles up to the block's query `last`
+    const int32_t keys = p.causal ? max(0, min(ms->len, ms->see + last)) : ms->len;
+    return keys / kTile + (keys % kTile != 0);
+  };
+  const int32_t all = ms->nq > 0 ? tiles(ms->nq - 1) : 0;
+  const int32_t share = (all + p.splits - 1) / p.splits;
+  r.j0 = min(all, split * share);
+  const int32_t j1 = min(all, r.j0 + share);
+  r.nt[0] = all > 0 ? max(0, min(j1, tiles(min(ms->nq, kTile) - 1)) - r.j0) : 0;
+  r.nt[1] = ms->nq > kTile ? j1 - r.j0 : 0;
+  return r;
+}
+
+// ------------------------------------------------------------ producer (one thread)
+__device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms,
+                                             uint32_t sbase, const Range& r, int32_t head) {
+  const int32_t n = max(r.nt[0], r.nt[1]);
+  if (n == 0 || p.stall_stream) return;
+  const uint64_t keep = l2_policy_evict_normal();
+  for (int t = 0; t < 2; ++t) {
+    if (r.nt[t] == 0) continue;
+    const uint32_t bar = smem_u32(&ms->q_full[t]);
+    mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
+    for (int c = 0; c < kQPanels; ++c)
+      tma_load_3d(sbase + kOffQ + (t * kQPanels + c) * kPanelBytes, &m.q, 64 * c, head, ms->q0 + t * kTile, bar, keep);
+  }
+  const int32_t fills = n * kFillsPerTile;
+  int32_t f = 0;
+  bool ok = true;
+  for (int32_t j = 0; j < n && ok; ++j) {
+    const int32_t key = ms->k0 + (r.j0 + j) * kTile;
+#pragma unroll
+    for (int c = 0; c < kFillsPerTile; ++c, ++f) {
+      const int slot = f % kSlots;
+      if (f >= kSlots) {
+        ok = wait_on(&ms->empty[slot], (f / kSlots - 1) & 1, ms, p.err);
+        if (!ok) break;
+      }
+      const uint32_t bar = smem_u32(&ms->full[slot]), dst = sbase + kOffRing + slot * kPanelBytes;
+      mbar_arrive_expect_tx(bar, kPanelBytes);
+      if (c < 2) {
+        tma_load_3d(dst, &m.k_nope, 64 * c, head, key, bar, keep);
+      } else if (c == 2) {
+        tma_load_2d(dst, &m.k_rope, 0, key, bar, keep);
+      } else {
+        tma_load_3d(dst, &m.v, 0, head, key + 64 * (c - 3), bar, keep);
+        tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, head, key + 64 * (c - 3), bar, keep);
+      }
+    }
+  }
+  if (!ms->abort_flag && f == fills) return;  // the MMA issuer waits for every panel
+  // Abandoned: the copies in flight land before the block's memory is given up.
+  for (int t = 0; t < 2; ++t)
+    if (r.nt[t] > 0) drain(&ms->q_full[t], 0);
+  for (int32_t g = max(0, f - kSlots); g < f; ++g) drain(&ms->full[g % kSlots], (g / kSlots) & 1);
+}
+
+// ------------------------------------------------------------ MMA issuer (one warp, lane 0 issues)
+__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_t* smem, uint32_t sbase,
+                                        uint32_t tmem, const Range& r) {
+  const int lane = threadIdx.x & 31;
+  const int32_t n = max(r.nt[0], r.nt[1]);
+  auto panel = [&](int32_t f) { return warp_wait_on(&ms->full[f % kSlots], (f / kSlots) & 1, ms, p.err); };
+  // S_t = Q_t . K(j)^T; releases K(j)'s slots after the last tile that reads it.
+  auto qk = [&](int t, int32_t j, bool last) {
+    const int32_t f0 = j * kFillsPerTile;
+    for (int c = 0; c < kKPanels; ++c) {
+      if (!panel(f0 + c)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t q = sbase + kOffQ + (t * kQPanels + c) * kPanelBytes;
+        const uint32_t k = sbase + kOffRing + ((f0 + c) % kSlots) * kPanelBytes;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16(tmem + kColS + 128 * t, smem_desc(q + 32 * kk, 1024, 1024, kLayoutSw128),
+                   smem_desc(k + 32 * kk, 1024, 1024, kLayoutSw128), kIdescQK, c != 0 || kk != 0);
+        if (last) umma_commit(smem_u32(&ms->empty[(f0 + c) % kSlots]));
+      }
+    }
+    if (lane == 0) umma_commit(smem_u32(&ms->s_full[t]));
+    return true;
+  };
+  bool ok = true;
+  for (int t = 0; t < 2 && ok; ++t) {
+    if (r.nt[t] == 0) continue;
+    ok = warp_wait_on(&ms->q_full[t], 0, ms, p.err) && qk(t, 0, t == 1 || r.nt[1] == 0);
+  }
+  for (int32_t j = 0; j < n && ok; ++j) {
+    const int32_t f0 = j * kFillsPerTile + kKPanels;
+    bool cleared = false;
+    for (int t = 0; t < 2 && ok; ++t) {
+      if (j >= r.nt[t]) continue;
+      const bool last_v = t == 1 || j >= r.nt[1];
+      ok = panel(f0) && panel(f0 + 1);
+      if (!ok) break;
+      // The row's last tile: rows of V behind the row's end are another row's, or
+      // never written; P is zero there, but zero times NaN is NaN.
+      const int32_t valid = ms->len - (r.j0 + j) * kTile;
+      if (valid < kTile && !cleared) {
+        cleared = true;
+        for (int32_t i = lane; i < (kTile - valid) * 16; i += 32) {
+          const int32_t key = valid + i / 16, piece = i % 16;
+          *reinterpret_cast<uint4*>(smem + kOffRing + ((f0 + (key >> 6)) % kSlots) * kPanelBytes +
+                                    (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      ok = warp_wait_on(&ms->p_full[t], j & 1, ms, p.err);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t v = sbase + kOffRing + ((f0 + (kk >> 2)) % kSlots) * kPanelBytes + (kk & 3) * 2048;
+          umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk,
+                      smem_desc(v, kPanelBytes / 2, 1024, kLayoutSw128), kIdescPV, j != 0 || kk != 0);
+        }
+        if (last_v) {
+          umma_commit(smem_u32(&ms->empty[f0 % kSlots]));
+          umma_commit(smem_u32(&ms->empty[(f0 + 1) % kSlots]));
+        }
+        if (j + 1 == r.nt[t]) umma_commit(smem_u32(&ms->o_full[t]));
+      }
+      if (j + 1 < r.nt[t]) ok = qk(t, j + 1, t == 1 || j + 1 >= r.nt[1]);
+    }
+  }
+  if (lane == 0) umma_commit(smem_u32(&ms->mma_done));
+  __syncwarp();
+}
+
+// ------------------------------------------------------------ softmax
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, uint32_t tmem, const Range& r,
+                                            int32_t head, int32_t split, int t) {
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const int row = quad * 32 + lane;                  // of the tile
+  const int qi = t * kTile + row;                    // of the block
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t s_addr = tmem + lanes + kColS + 128 * t, o_addr = tmem + lanes + kColO + 128 * t;
+  const int32_t n = t ? r.nt[1] : r.nt[0];
+  const float sl = p.scale * 1.4426950408889634f;    // scores to powers of two
+  // keys that this row, and the warp's first row, see
+  const int32_t sees = p.causal ? min(ms->len, ms->see + qi) : ms->len;
+  const int32_t warp_sees = p.causal ? min(ms->len, ms->see + t * kTile + quad * 32) : ms->len;
+  float ref = -INFINITY, sum = 0.0f;
+  for (int32_t j = 0; j < n; ++j) {
+    if (!warp_wait_on(&ms->s_full[t], j & 1, ms, p.err)) return;
+    tc_fence_after();
+    uint32_t raw[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, raw[c]);
+    tmem_wait_ld();
+    const int32_t key0 = (r.j0 + j) * kTile;
+    if (warp_sees - key0 < kTile) {
+      const int32_t lim = sees - key0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (32 * c + i >= lim) raw[c][i] = 0xFF800000u;  // -inf
+    }
+    float top[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      top[c] = __uint_as_float(raw[c][0]);
+#pragma unroll
+      for (int i = 1; i < 32; ++i) top[c] = fmaxf(top[c], __uint_as_float(raw[c][i]));
+    }
+    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    // (a first finite maximum is infinitely far above -inf; two -inf are not apart)
+    const bool moves = high > ref && (high - ref) * sl > kRescaleThreshold;
+    if (__any_sync(0xffffffffu, moves)) {
+      const float alpha = moves ? ex2((ref - high) * sl) : 1.0f;
+      if (moves) ref = high;
+      sum *= alpha;
+      if (j > 0) {  // O_t's last product is complete: S_t(j) was issued after it
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[16];
+          tmem_ld16(o_addr + 16 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(o_addr + 16 * c, o);
+        }
+      }
+    }
+    const float off = ref == -INFINITY ? 0.0f : -ref * sl;
+    const uint64_t sl2 = pack2(sl, sl), off2 = pack2(off, off);
+    uint64_t part[2] = {0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int e = 2 * i;
+        float x, y;
+        unpack2(fma2(pack2(__uint_as_float(raw[c][e]), __uint_as_float(raw[c][e + 1])), sl2, off2), x, y);
+        x = ex2(x);
+        y = ex2(y);
+        part[i & 1] = add2(part[i & 1], pack2(x, y));
+        pk[i] = bf16x2(x, y);
+      }
+      tmem_st16(s_addr + 16 * c, pk);
+    }
+    float s0, s1, s2, s3;
+    unpack2(part[0], s0, s1);
+    unpack2(part[1], s2, s3);
+    sum += (s0 + s1) + (s2 + s3);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[t]));
+  }
+
+  // Epilogue.  A row that saw no key has sum 0.
+  if (n > 0 && !warp_wait_on(&ms->o_full[t], 0, ms, p.err)) return;
+  tc_fence_after();
+  const bool live = qi < ms->nq;
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const int64_t at = static_cast<int64_t>(ms->q0 + qi) * p.heads + head;
+  const int64_t part_at = static_cast<int64_t>(split) * p.total_q * p.heads + at;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    if (n > 0) {
+      tmem_ld32(o_addr + 32 * c, o);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0;
+    }
+    if (!live) continue;
+    if (p.splits == 1) {
+      uint4* dst = reinterpret_cast<uint4*>(p.out + at * kPrefillV + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                             __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+    }
+  }
+  if (live) {
+    const float lse = sum > 0.0f ? ref * p.scale + logf(sum) : -INFINITY;
+    if (p.splits > 1)
+      p.part_lse[part_at] = lse;
+    else if (p.lse != nullptr)
+      p.lse[at] = lse;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Misc* ms = reinterpret_cast<Misc*>(smem + kOffMisc);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // heads fastest: the blocks of one rank read different heads' keys, and the
+  // ranks of a row run near one another in time, so its keys stay in L2.
+  const int32_t head = static_cast<int32_t>(blockIdx.x % p.heads);
+  const int32_t rest = static_cast<int32_t>(blockIdx.x / p.heads);
+  const int32_t split = rest % p.splits, rank = rest / p.splits;
+
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
+  if (tid == kProducerWarp * 32) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(smem_u32(&ms->full[s]), 1);
+      mbar_init(smem_u32(&ms->empty[s]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&ms->q_full[t]), 1);
+      mbar_init(smem_u32(&ms->s_full[t]), 1);
+      mbar_init(smem_u32(&ms->p_full[t]), 4);
+      mbar_init(smem_u32(&ms->o_full[t]), 1);
+    }
+    mbar_init(smem_u32(&ms->mma_done), 1);
+    ms->abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&maps.q);
+    prefetch_tensormap(&maps.k_nope);
+    prefetch_tensormap(&maps.k_rope);
+    prefetch_tensormap(&maps.v);
+  }
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (warp == 0) find_work(p, rank, blockIdx.x == 0, ms);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem_base;
+  const Range r = key_range(p, ms, split);  // empty when the block has no queries
+  if (warp < 8) {
+    setmaxnreg_inc<kSoftmaxRegs>();
+    if (ms->nq > (warp >> 2) * kTile) run_softmax(p, ms, tmem, r, head, split, warp >> 2);
+  } else {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp == kProducerWarp) {
+      if (lane == 0) run_producer(p, maps, ms, sbase, r, head);
+    } else if (warp == kMmaWarp) {
+      run_mma(p, ms, smem, sbase, tmem, r);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    if (lane == 0) drain(&ms->mma_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+size_t prefill_smem_bytes() { return kSmemBytes; }
+
+cudaError_t prefill_prepare() {
+  return cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+}
+
+cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream) {
+  const int64_t grid = static_cast<int64_t>(p.tiles) * p.heads * p.splits;
+  if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  return launch_dependent(prefill_kernel, static_cast<unsigned>(grid), kThreads, kSmemBytes, stream,
+                          maps, p);
+}
+
+}  // namespace mla
