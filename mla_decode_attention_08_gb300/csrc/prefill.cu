@@ -33,14 +33,14 @@ constexpr int kSlots = 8;
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQPanels * kPanelBytes;
 constexpr int kOffMisc = kOffRing + kSlots * kPanelBytes;
-// Three warpgroups: two of softmax, one with the producer, the MMA issuer and
-// two idle warps, whose registers go to the softmax (a row of 128 scores stays
-// in registers).
+// Three warpgroups: two of softmax, one with the producer, the MMA issuer, the
+// cleaner and an idle warp, whose registers go to the softmax (a row of 128
+// scores stays in registers).
 constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
               "register split exceeds the launch allocation");
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kCleanerWarp = 10;
 constexpr uint32_t kLayoutSw128 = 2;
 constexpr uint32_t kColS = 0, kColO = 256;             // + 128 t
 constexpr uint32_t kTmemCols = 512;
@@ -57,6 +57,8 @@ struct Misc {
   uint64_t s_full[2];   // S_t(j) complete, and with it every product before it
   uint64_t p_full[2];   // P_t(j) written (and O_t rescaled)
   uint64_t o_full[2];   // the last product of tile t complete
+  uint64_t v_last;      // the copies of the tile that holds the row's end are issued
+  uint64_t v_clean;     // V behind the row's end is zeroed
   uint64_t mma_done;
   uint32_t tmem_base;
   volatile int32_t abort_flag;
@@ -174,6 +176,14 @@ __device__ __forceinline__ Range key_range(const PrefillParams& p, const Misc* m
   return r;
 }
 
+// ------------------------------------------------------------ V behind the row's end (a warp of its own)
+// The row's last key tile may end inside the tile.  The rows of V behind it are
+// another row's, or never written: their probabilities are zero, but zero times
+// NaN is NaN, so they are zeroed in shared memory before the product reads them.
+__device__ __forceinline__ int32_t partial_tile(const Misc* ms, const Range& r) {
+  const int32_t j = ms->len / kTile - r.j0;  // the tile that holds the row's end
+  return ms->len % kTile != 0 && j >= 0 && j < max(r.nt[0], r.nt[1]) ? j : -1;
+}
 // ------------------------------------------------------------ producer (one thread)
 __device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms,
                                              uint32_t sbase, const Range& r, int32_t head) {
@@ -187,7 +197,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
     for (int c = 0; c < kQPanels; ++c)
       tma_load_3d(sbase + kOffQ + (t * kQPanels + c) * kPanelBytes, &m.q, 64 * c, head, ms->q0 + t * kTile, bar, keep);
   }
-  const int32_t fills = n * kFillsPerTile;
+  const int32_t fills = n * kFillsPerTile, clean = partial_tile(ms, r);
   int32_t f = 0;
   bool ok = true;
   for (int32_t j = 0; j < n && ok; ++j) {
@@ -210,6 +220,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
         tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, head, key + 64 * (c - 3), bar, keep);
       }
     }
+    if (ok && j == clean) mbar_arrive(smem_u32(&ms->v_last));
   }
   if (!ms->abort_flag && f == fills) return;  // the MMA issuer waits for every panel
   // Abandoned: the copies in flight land before the block's memory is given up.
@@ -218,78 +229,103 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
   for (int32_t g = max(0, f - kSlots); g < f; ++g) drain(&ms->full[g % kSlots], (g / kSlots) & 1);
 }
 
-// ------------------------------------------------------------ MMA issuer (one warp, lane 0 issues)
-__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_t* smem, uint32_t sbase,
-                                        uint32_t tmem, const Range& r) {
+__device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, uint8_t* smem, const Range& r) {
   const int lane = threadIdx.x & 31;
-  const int32_t n = max(r.nt[0], r.nt[1]);
-  auto panel = [&](int32_t f) { return warp_wait_on(&ms->full[f % kSlots], (f / kSlots) & 1, ms, p.err); };
-  // S_t = Q_t . K(j)^T; releases K(j)'s slots after the last tile that reads it.
-  auto qk = [&](int t, int32_t j, bool last) {
-    const int32_t f0 = j * kFillsPerTile;
-    for (int c = 0; c < kKPanels; ++c) {
-      if (!panel(f0 + c)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t q = sbase + kOffQ + (t * kQPanels + c) * kPanelBytes;
-        const uint32_t k = sbase + kOffRing + ((f0 + c) % kSlots) * kPanelBytes;
+  const int32_t j = partial_tile(ms, r);
+  if (j < 0) return;
+  const int32_t f = j * kFillsPerTile + kKPanels;
+  // (a slot's barrier can be waited on for its fill f / 8 once that is under way)
+  if (!warp_wait_on(&ms->v_last, 0, ms, p.err)) return;
+  for (int h = 0; h < kVPanels; ++h)
+    if (!warp_wait_on(&ms->full[(f + h) % kSlots], ((f + h) / kSlots) & 1, ms, p.err)) return;
+  for (int32_t i = (ms->len % kTile) * 16 + lane; i < kTile * 16; i += 32) {
+    const int32_t key = i >> 4, piece = i & 15;
+    *reinterpret_cast<uint4*>(smem + kOffRing + ((f + (key >> 6)) % kSlots) * kPanelBytes +
+                              (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
+}
+
+// ------------------------------------------------------------ MMA issuer (one warp, an elected lane issues)
+// The tensor pipe takes about four of these products ahead (measured: 48
+// issued back to back block the issuer after ~250 cycles of work, and run at 64
+// cycles each), so what stands between two products has to be short: each wait
+// is made once, by the first tile that needs it.
+__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem,
+                                        const Range& r) {
+  const int32_t nt0 = r.nt[0], nt1 = r.nt[1], n = max(nt0, nt1);
+  const int32_t clean = partial_tile(ms, r);
+  const uint64_t q_desc = smem_desc(sbase + kOffQ, 1024, 1024, kLayoutSw128);
+  const uint64_t k_desc = smem_desc(sbase + kOffRing, 1024, 1024, kLayoutSw128);
+  const uint64_t v_desc = smem_desc(sbase + kOffRing, kPanelBytes / 2, 1024, kLayoutSw128);
+  constexpr uint32_t kPanel = kPanelBytes >> 4;  // a panel, in descriptor address units
+  const uint32_t empty0 = smem_u32(&ms->empty[0]);
+  auto panel = [&](uint32_t f) { return warp_wait_on(&ms->full[f % kSlots], (f / kSlots) & 1, ms, p.err); };
+  // S_t = Q_t . K(j)^T, releasing K(j)'s slots after the last tile that reads it.
+  auto qk = [&](int t, uint32_t f, bool last) {
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < kKPanels; ++c) {
+        const uint32_t slot = (f + c) % kSlots;
+        const uint64_t a = q_desc + (t * kQPanels + c) * kPanel, b = k_desc + slot * kPanel;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16(tmem + kColS + 128 * t, smem_desc(q + 32 * kk, 1024, 1024, kLayoutSw128),
-                   smem_desc(k + 32 * kk, 1024, 1024, kLayoutSw128), kIdescQK, c != 0 || kk != 0);
-        if (last) umma_commit(smem_u32(&ms->empty[(f0 + c) % kSlots]));
+          umma_f16(tmem + kColS + 128 * t, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
+        if (last) umma_commit(empty0 + 8 * slot);
       }
+      umma_commit(smem_u32(&ms->s_full[t]));
     }
-    if (lane == 0) umma_commit(smem_u32(&ms->s_full[t]));
-    return true;
+    __syncwarp();
   };
   bool ok = true;
-  for (int t = 0; t < 2 && ok; ++t) {
-    if (r.nt[t] == 0) continue;
-    ok = warp_wait_on(&ms->q_full[t], 0, ms, p.err) && qk(t, 0, t == 1 || r.nt[1] == 0);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    if (!ok || (t ? nt1 : nt0) == 0) continue;
+    ok = warp_wait_on(&ms->q_full[t], 0, ms, p.err) && panel(0) && panel(1) && panel(2);
+    if (!ok) break;
+    tc_fence_after();
+    qk(t, 0, t == 1 || nt1 == 0);
   }
   for (int32_t j = 0; j < n && ok; ++j) {
-    const int32_t f0 = j * kFillsPerTile + kKPanels;
-    bool cleared = false;
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (j >= r.nt[t]) continue;
-      const bool last_v = t == 1 || j >= r.nt[1];
-      ok = panel(f0) && panel(f0 + 1);
-      if (!ok) break;
-      // The row's last tile: rows of V behind the row's end are another row's, or
-      // never written; P is zero there, but zero times NaN is NaN.
-      const int32_t valid = ms->len - (r.j0 + j) * kTile;
-      if (valid < kTile && !cleared) {
-        cleared = true;
-        for (int32_t i = lane; i < (kTile - valid) * 16; i += 32) {
-          const int32_t key = valid + i / 16, piece = i % 16;
-          *reinterpret_cast<uint4*>(smem + kOffRing + ((f0 + (key >> 6)) % kSlots) * kPanelBytes +
-                                    (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+    const uint32_t fv = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels, fk = fv + kVPanels;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int32_t nt = t ? nt1 : nt0;
+      if (!ok || j >= nt) continue;
+      if (t == 0 || j >= nt0) {
+        ok = panel(fv) && panel(fv + 1);
+        if (ok && j == clean) ok = warp_wait_on(&ms->v_clean, 0, ms, p.err);
       }
-      ok = warp_wait_on(&ms->p_full[t], j & 1, ms, p.err);
+      ok = ok && warp_wait_on(&ms->p_full[t], j & 1, ms, p.err);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
+        const uint32_t s0 = fv % kSlots, s1 = (fv + 1) % kSlots;
+        const uint64_t v0 = v_desc + s0 * kPanel, v1 = v_desc + s1 * kPanel;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t v = sbase + kOffRing + ((f0 + (kk >> 2)) % kSlots) * kPanelBytes + (kk & 3) * 2048;
+        for (int kk = 0; kk < 8; ++kk)
           umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk,
-                      smem_desc(v, kPanelBytes / 2, 1024, kLayoutSw128), kIdescPV, j != 0 || kk != 0);
+                      (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
+        if (t == 1 || j >= nt1) {
+          umma_commit(empty0 + 8 * s0);
+          umma_commit(empty0 + 8 * s1);
         }
-        if (last_v) {
-          umma_commit(smem_u32(&ms->empty[f0 % kSlots]));
-          umma_commit(smem_u32(&ms->empty[(f0 + 1) % kSlots]));
-        }
-        if (j + 1 == r.nt[t]) umma_commit(smem_u32(&ms->o_full[t]));
+        if (j + 1 == nt) umma_commit(smem_u32(&ms->o_full[t]));
       }
-      if (j + 1 < r.nt[t]) ok = qk(t, j + 1, t == 1 || j + 1 >= r.nt[1]);
+      __syncwarp();
+      if (j + 1 >= nt) continue;
+      if (t == 0 || j + 1 >= nt0) {
+        ok = panel(fk) && panel(fk + 1) && panel(fk + 2);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      qk(t, fk, t == 1 || j + 1 >= nt1);
     }
   }
-  if (lane == 0) umma_commit(smem_u32(&ms->mma_done));
+  if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
   __syncwarp();
 }
 
@@ -477,6 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ms->p_full[t]), 4);
       mbar_init(smem_u32(&ms->o_full[t]), 1);
     }
+    mbar_init(smem_u32(&ms->v_last), 1);
+    mbar_init(smem_u32(&ms->v_clean), 1);
     mbar_init(smem_u32(&ms->mma_done), 1);
     ms->abort_flag = 0;
     fence_mbar_init();
@@ -501,7 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) {
       if (lane == 0) run_producer(p, maps, ms, sbase, r, head);
     } else if (warp == kMmaWarp) {
-      run_mma(p, ms, smem, sbase, tmem, r);
+      run_mma(p, ms, sbase, tmem, r);
+    } else if (warp == kCleanerWarp) {
+      run_cleaner(p, ms, smem, r);
     }
   }
   __syncwarp();
