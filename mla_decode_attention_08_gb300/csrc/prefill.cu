@@ -4,11 +4,11 @@
 //
 // A block owns 256 queries of one row and head as two tiles of 128 (t = 0, 1)
 // and walks the row's keys in tiles of 128 (j):
-//   * warp 8 streams K(j) (three 64-dim panels of 128 keys) and V(j) (two panels
+//   * warp 2 streams K(j) (three 64-dim panels of 128 keys) and V(j) (two panels
 //     of 64 keys x 128 dims) by TMA into a ring of eight 16 KB slots,
-//   * warp 9 issues S_t = Q_t . K(j)^T and O_t += P_t . V(j) (tcgen05, float32
-//     accumulators in TMEM, P_t read from TMEM),
-//   * warps 0-3 and 4-7 run the online softmax of tile t, a thread a row: S out
+//   * warps 0 and 1 issue S_t = Q_t . K(j)^T and O_t += P_t . V(j) of a tile each
+//     (tcgen05, float32 accumulators in TMEM, P_t read from TMEM),
+//   * warps 4-7 and 8-11 run the online softmax of tile t, a thread a row: S out
 //     of TMEM, running maximum and sum in registers, P back over S as bf16.
 // TMEM is full: S_0 | S_1 | O_0 | O_1, 128 columns each, P_t in S_t's first 64.
 // The two tiles alternate: while the tensor cores work on one tile's products
@@ -33,14 +33,14 @@ constexpr int kSlots = 8;
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQPanels * kPanelBytes;
 constexpr int kOffMisc = kOffRing + kSlots * kPanelBytes;
-// Three warpgroups: two of softmax, one with the producer, the MMA issuer, the
-// cleaner and an idle warp, whose registers go to the softmax (a row of 128
-// scores stays in registers).
+// Three warpgroups: two of softmax, one with the MMA issuers, the producer and
+// the cleaner, whose registers go to the softmax (a row of 128 scores stays in
+// registers).
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
               "register split exceeds the launch allocation");
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kCleanerWarp = 10;
+constexpr int kMmaWarp = 0, kProducerWarp = 2, kCleanerWarp = 3, kFirstSoftmaxWarp = 4;  // issuers 0 and 1
 constexpr uint32_t kLayoutSw128 = 2;
 constexpr uint32_t kColS = 0, kColO = 256;             // + 128 t
 constexpr uint32_t kTmemCols = 512;
@@ -53,10 +53,12 @@ constexpr float kRescaleThreshold = 8.0f;
 
 struct Misc {
   uint64_t q_full[2];
-  uint64_t full[kSlots], empty[kSlots];
+  // Of tile j's K and V, j & 1: landed, and released by both issuers.
+  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
   uint64_t s_full[2];   // S_t(j) complete, and with it every product before it
   uint64_t p_full[2];   // P_t(j) written (and O_t rescaled)
   uint64_t o_full[2];   // the last product of tile t complete
+  uint64_t turn[2];     // the other tile's products are issued
   uint64_t v_last;      // the copies of the tile that holds the row's end are issued
   uint64_t v_clean;     // V behind the row's end is zeroed
   uint64_t mma_done;
@@ -185,62 +187,76 @@ __device__ __forceinline__ int32_t partial_tile(const Misc* ms, const Range& r) 
   return ms->len % kTile != 0 && j >= 0 && j < max(r.nt[0], r.nt[1]) ? j : -1;
 }
 // ------------------------------------------------------------ producer (one thread)
+// K(j) is the ring's fills 5 j .. 5 j + 2 and V(j) 5 j + 3 and 5 j + 4, fill f in
+// slot f % 8: K(j) takes the slots of K(j - 2)'s last panel and V(j - 2), V(j)
+// those of K(j - 1)'s first two.
+__device__ __forceinline__ uint32_t ring_slot(uint32_t f) { return f % kSlots; }
 __device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms,
                                              uint32_t sbase, const Range& r, int32_t head) {
   const int32_t n = max(r.nt[0], r.nt[1]);
   if (n == 0 || p.stall_stream) return;
   const uint64_t keep = l2_policy_evict_normal();
-  for (int t = 0; t < 2; ++t) {
-    if (r.nt[t] == 0) continue;
+  const uint32_t ring = sbase + kOffRing;
+  const int32_t clean = partial_tile(ms, r);
+  int32_t ks = 0, vs = 0;  // tiles whose K, V copies are issued
+  bool ok = true;
+  auto load_k = [&](int32_t j) {
+    const uint32_t bar = smem_u32(&ms->k_full[j & 1]), f = static_cast<uint32_t>(j) * kFillsPerTile;
+    const int32_t key = ms->k0 + (r.j0 + j) * kTile;
+    mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
+    tma_load_3d(ring + ring_slot(f) * kPanelBytes, &m.k_nope, 0, head, key, bar, keep);
+    tma_load_3d(ring + ring_slot(f + 1) * kPanelBytes, &m.k_nope, 64, head, key, bar, keep);
+    tma_load_2d(ring + ring_slot(f + 2) * kPanelBytes, &m.k_rope, 0, key, bar, keep);
+    ++ks;
+  };
+  auto load_q = [&](int t) {
+    if ((t ? r.nt[1] : r.nt[0]) == 0) return;
     const uint32_t bar = smem_u32(&ms->q_full[t]);
     mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
     for (int c = 0; c < kQPanels; ++c)
       tma_load_3d(sbase + kOffQ + (t * kQPanels + c) * kPanelBytes, &m.q, 64 * c, head, ms->q0 + t * kTile, bar, keep);
-  }
-  const int32_t fills = n * kFillsPerTile, clean = partial_tile(ms, r);
-  int32_t f = 0;
-  bool ok = true;
+  };
+  load_q(0);
+  load_k(0);
+  load_q(1);
   for (int32_t j = 0; j < n && ok; ++j) {
-    const int32_t key = ms->k0 + (r.j0 + j) * kTile;
-#pragma unroll
-    for (int c = 0; c < kFillsPerTile; ++c, ++f) {
-      const int slot = f % kSlots;
-      if (f >= kSlots) {
-        ok = wait_on(&ms->empty[slot], (f / kSlots - 1) & 1, ms, p.err);
-        if (!ok) break;
-      }
-      const uint32_t bar = smem_u32(&ms->full[slot]), dst = sbase + kOffRing + slot * kPanelBytes;
-      mbar_arrive_expect_tx(bar, kPanelBytes);
-      if (c < 2) {
-        tma_load_3d(dst, &m.k_nope, 64 * c, head, key, bar, keep);
-      } else if (c == 2) {
-        tma_load_2d(dst, &m.k_rope, 0, key, bar, keep);
-      } else {
-        tma_load_3d(dst, &m.v, 0, head, key + 64 * (c - 3), bar, keep);
-        tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, head, key + 64 * (c - 3), bar, keep);
-      }
+    if (j > 0) {
+      if (j > 1) ok = wait_on(&ms->v_empty[j & 1], (j / 2 - 1) & 1, ms, p.err);
+      if (!ok) break;
+      load_k(j);
+      ok = wait_on(&ms->k_empty[(j - 1) & 1], ((j - 1) / 2) & 1, ms, p.err);
+      if (!ok) break;
     }
-    if (ok && j == clean) mbar_arrive(smem_u32(&ms->v_last));
+    const uint32_t bar = smem_u32(&ms->v_full[j & 1]), f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
+    const int32_t key = ms->k0 + (r.j0 + j) * kTile;
+    mbar_arrive_expect_tx(bar, kVPanels * kPanelBytes);
+#pragma unroll
+    for (int h = 0; h < kVPanels; ++h) {
+      const uint32_t dst = ring + ring_slot(f + h) * kPanelBytes;
+      tma_load_3d(dst, &m.v, 0, head, key + 64 * h, bar, keep);
+      tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, head, key + 64 * h, bar, keep);
+    }
+    ++vs;
+    if (j == clean) mbar_arrive(smem_u32(&ms->v_last));
   }
-  if (!ms->abort_flag && f == fills) return;  // the MMA issuer waits for every panel
+  if (ok && !ms->abort_flag) return;  // the issuers wait for every panel
   // Abandoned: the copies in flight land before the block's memory is given up.
-  for (int t = 0; t < 2; ++t)
-    if (r.nt[t] > 0) drain(&ms->q_full[t], 0);
-  for (int32_t g = max(0, f - kSlots); g < f; ++g) drain(&ms->full[g % kSlots], (g / kSlots) & 1);
+  if (r.nt[0] > 0) drain(&ms->q_full[0], 0);
+  if (r.nt[1] > 0) drain(&ms->q_full[1], 0);
+  for (int32_t j = max(0, ks - 2); j < ks; ++j) drain(&ms->k_full[j & 1], (j / 2) & 1);
+  for (int32_t j = max(0, vs - 2); j < vs; ++j) drain(&ms->v_full[j & 1], (j / 2) & 1);
 }
 
 __device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, uint8_t* smem, const Range& r) {
   const int lane = threadIdx.x & 31;
   const int32_t j = partial_tile(ms, r);
   if (j < 0) return;
-  const int32_t f = j * kFillsPerTile + kKPanels;
-  // (a slot's barrier can be waited on for its fill f / 8 once that is under way)
-  if (!warp_wait_on(&ms->v_last, 0, ms, p.err)) return;
-  for (int h = 0; h < kVPanels; ++h)
-    if (!warp_wait_on(&ms->full[(f + h) % kSlots], ((f + h) / kSlots) & 1, ms, p.err)) return;
+  const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
+  // (a barrier can be waited on for its fill j / 2 once that is under way)
+  if (!warp_wait_on(&ms->v_last, 0, ms, p.err) || !warp_wait_on(&ms->v_full[j & 1], (j / 2) & 1, ms, p.err)) return;
   for (int32_t i = (ms->len % kTile) * 16 + lane; i < kTile * 16; i += 32) {
     const int32_t key = i >> 4, piece = i & 15;
-    *reinterpret_cast<uint4*>(smem + kOffRing + ((f + (key >> 6)) % kSlots) * kPanelBytes +
+    *reinterpret_cast<uint4*>(smem + kOffRing + ring_slot(f + (key >> 6)) * kPanelBytes +
                               (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
         make_uint4(0, 0, 0, 0);
   }
@@ -249,81 +265,85 @@ __device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, ui
   if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
 }
 
-// ------------------------------------------------------------ MMA issuer (one warp, an elected lane issues)
-// The tensor pipe takes about four of these products ahead (measured: 48
-// issued back to back block the issuer after ~250 cycles of work, and run at 64
-// cycles each), so what stands between two products has to be short: each wait
-// is made once, by the first tile that needs it.
+// ------------------------------------------------------------ MMA issuers (a warp a tile, an elected lane issues)
+// The tensor pipe takes hardly more than one of these products ahead (measured:
+// 48 of 128 x 128 x 16 issued back to back block the issuer until ~100 cycles
+// before they end, 64 cycles each), and a look at a barrier takes 100 to 150
+// cycles beside the products' own reads of shared memory.  So each tile has its
+// own issuer, which waits for what its next products need while the other
+// tile's run, and they take turns: P_t(j) . V(j) and Q_t . K(j + 1)^T are issued
+// together, the turn handed over a few products before their end.
 __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem,
-                                        const Range& r) {
-  const int32_t nt0 = r.nt[0], nt1 = r.nt[1], n = max(nt0, nt1);
+                                        const Range& r, int t) {
+  const int32_t nt = t ? r.nt[1] : r.nt[0], n = max(r.nt[0], r.nt[1]);
   const int32_t clean = partial_tile(ms, r);
-  const uint64_t q_desc = smem_desc(sbase + kOffQ, 1024, 1024, kLayoutSw128);
+  const uint64_t q_desc = smem_desc(sbase + kOffQ + t * kQPanels * kPanelBytes, 1024, 1024, kLayoutSw128);
   const uint64_t k_desc = smem_desc(sbase + kOffRing, 1024, 1024, kLayoutSw128);
   const uint64_t v_desc = smem_desc(sbase + kOffRing, kPanelBytes / 2, 1024, kLayoutSw128);
   constexpr uint32_t kPanel = kPanelBytes >> 4;  // a panel, in descriptor address units
-  const uint32_t empty0 = smem_u32(&ms->empty[0]);
-  auto panel = [&](uint32_t f) { return warp_wait_on(&ms->full[f % kSlots], (f / kSlots) & 1, ms, p.err); };
-  // S_t = Q_t . K(j)^T, releasing K(j)'s slots after the last tile that reads it.
-  auto qk = [&](int t, uint32_t f, bool last) {
+  const uint32_t other_turn = smem_u32(&ms->turn[t ^ 1]);
+  const uint32_t d_s = tmem + kColS + 128 * t, d_o = tmem + kColO + 128 * t;
+  // A wait of this warp; tile 0 starts, so its first turn is the phase before the first.
+  auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
+  uint32_t turns = t;
+  // S_t = Q_t . K(j)^T (one lane), handing over the turn four products before its end
+  auto qk = [&](int32_t j) {
+    const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile;
+#pragma unroll
+    for (int c = 0; c < kKPanels; ++c) {
+      const uint64_t a = q_desc + c * kPanel, b = k_desc + ring_slot(f + c) * kPanel;
+      if (c == kKPanels - 1) mbar_arrive(other_turn);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) umma_f16(d_s, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
+    }
+    umma_commit(smem_u32(&ms->s_full[t]));
+    umma_commit(smem_u32(&ms->k_empty[j & 1]));
+  };
+  bool ok = n > 0 && (nt == 0 || on(&ms->q_full[t], 0)) && on(&ms->k_full[0], 0) && on(&ms->turn[t], ++turns);
+  if (ok) {
+    tc_fence_after();
     if (elect_one()) {
-#pragma unroll
-      for (int c = 0; c < kKPanels; ++c) {
-        const uint32_t slot = (f + c) % kSlots;
-        const uint64_t a = q_desc + (t * kQPanels + c) * kPanel, b = k_desc + slot * kPanel;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16(tmem + kColS + 128 * t, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
-        if (last) umma_commit(empty0 + 8 * slot);
+      if (nt > 0) {
+        qk(0);
+      } else {  // the other tile alone reads K(0)
+        mbar_arrive(smem_u32(&ms->k_empty[0]));
+        mbar_arrive(other_turn);
       }
-      umma_commit(smem_u32(&ms->s_full[t]));
     }
     __syncwarp();
-  };
-  bool ok = true;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    if (!ok || (t ? nt1 : nt0) == 0) continue;
-    ok = warp_wait_on(&ms->q_full[t], 0, ms, p.err) && panel(0) && panel(1) && panel(2);
-    if (!ok) break;
-    tc_fence_after();
-    qk(t, 0, t == 1 || nt1 == 0);
   }
   for (int32_t j = 0; j < n && ok; ++j) {
-    const uint32_t fv = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels, fk = fv + kVPanels;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int32_t nt = t ? nt1 : nt0;
-      if (!ok || j >= nt) continue;
-      if (t == 0 || j >= nt0) {
-        ok = panel(fv) && panel(fv + 1);
-        if (ok && j == clean) ok = warp_wait_on(&ms->v_clean, 0, ms, p.err);
-      }
-      ok = ok && warp_wait_on(&ms->p_full[t], j & 1, ms, p.err);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint32_t s0 = fv % kSlots, s1 = (fv + 1) % kSlots;
-        const uint64_t v0 = v_desc + s0 * kPanel, v1 = v_desc + s1 * kPanel;
+    const bool here = j < nt, next = j + 1 < nt;
+    ok = on(&ms->v_full[j & 1], j >> 1) && (j != clean || on(&ms->v_clean, 0)) &&
+         (!here || on(&ms->p_full[t], j)) && on(&ms->turn[t], ++turns);
+    if (!ok) break;
+    tc_fence_after();
+    if (elect_one()) {
+      if (here) {
+        const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
+        const uint64_t v0 = v_desc + ring_slot(f) * kPanel, v1 = v_desc + ring_slot(f + 1) * kPanel;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk,
-                      (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
-        if (t == 1 || j >= nt1) {
-          umma_commit(empty0 + 8 * s0);
-          umma_commit(empty0 + 8 * s1);
-        }
-        if (j + 1 == nt) umma_commit(smem_u32(&ms->o_full[t]));
+          umma_f16_ts(d_o, d_s + 8 * kk, (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
+        if (!next) umma_commit(smem_u32(&ms->o_full[t]));
+        umma_commit(smem_u32(&ms->v_empty[j & 1]));
+      } else {
+        mbar_arrive(smem_u32(&ms->v_empty[j & 1]));
       }
-      __syncwarp();
-      if (j + 1 >= nt) continue;
-      if (t == 0 || j + 1 >= nt0) {
-        ok = panel(fk) && panel(fk + 1) && panel(fk + 2);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      qk(t, fk, t == 1 || j + 1 >= nt1);
+      if (!next) mbar_arrive(other_turn);
     }
+    __syncwarp();
+    if (j + 1 == n) break;
+    ok = on(&ms->k_full[(j + 1) & 1], (j + 1) >> 1);
+    if (!ok) break;
+    tc_fence_after();
+    if (elect_one()) {
+      if (next)
+        qk(j + 1);
+      else
+        mbar_arrive(smem_u32(&ms->k_empty[(j + 1) & 1]));
+    }
+    __syncwarp();
   }
   if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
   __syncwarp();
@@ -503,19 +523,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
   if (tid == kProducerWarp * 32) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(smem_u32(&ms->full[s]), 1);
-      mbar_init(smem_u32(&ms->empty[s]), 1);
-    }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&ms->k_full[t]), 1);
+      mbar_init(smem_u32(&ms->v_full[t]), 1);
+      mbar_init(smem_u32(&ms->k_empty[t]), 2);
+      mbar_init(smem_u32(&ms->v_empty[t]), 2);
       mbar_init(smem_u32(&ms->q_full[t]), 1);
       mbar_init(smem_u32(&ms->s_full[t]), 1);
       mbar_init(smem_u32(&ms->p_full[t]), 4);
       mbar_init(smem_u32(&ms->o_full[t]), 1);
+      mbar_init(smem_u32(&ms->turn[t]), 1);
     }
     mbar_init(smem_u32(&ms->v_last), 1);
     mbar_init(smem_u32(&ms->v_clean), 1);
-    mbar_init(smem_u32(&ms->mma_done), 1);
+    mbar_init(smem_u32(&ms->mma_done), 2);
     ms->abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&maps.q);
@@ -525,23 +546,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (warp == 0) find_work(p, rank, blockIdx.x == 0, ms);
+  if (warp == kFirstSoftmaxWarp) find_work(p, rank, blockIdx.x == 0, ms);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
   const Range r = key_range(p, ms, split);  // empty when the block has no queries
-  if (warp < 8) {
+  if (warp >= kFirstSoftmaxWarp) {
     setmaxnreg_inc<kSoftmaxRegs>();
-    if (ms->nq > (warp >> 2) * kTile) run_softmax(p, ms, tmem, r, head, split, warp >> 2);
+    const int t = (warp - kFirstSoftmaxWarp) >> 2;
+    if (ms->nq > t * kTile) run_softmax(p, ms, tmem, r, head, split, t);
   } else {
     setmaxnreg_dec<kOtherRegs>();
     if (warp == kProducerWarp) {
       if (lane == 0) run_producer(p, maps, ms, sbase, r, head);
-    } else if (warp == kMmaWarp) {
-      run_mma(p, ms, sbase, tmem, r);
     } else if (warp == kCleanerWarp) {
       run_cleaner(p, ms, smem, r);
+    } else {
+      run_mma(p, ms, sbase, tmem, r, warp - kMmaWarp);
     }
   }
   __syncwarp();
