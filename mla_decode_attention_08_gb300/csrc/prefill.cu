@@ -56,7 +56,8 @@ struct Misc {
   // Of tile j's K and V, j & 1: landed, and released by both issuers.
   uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
   uint64_t s_full[2];   // S_t(j) complete, and with it every product before it
-  uint64_t p_full[2];   // P_t(j) written (and O_t rescaled)
+  uint64_t p_head[2];   // the first three quarters of P_t(j) written (and O_t rescaled)
+  uint64_t p_full[2];   // all of it
   uint64_t o_full[2];   // the last product of tile t complete
   uint64_t turn[2];     // the other tile's products are issued
   uint64_t v_last;      // the copies of the tile that holds the row's end are issued
@@ -283,6 +284,7 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
   constexpr uint32_t kPanel = kPanelBytes >> 4;  // a panel, in descriptor address units
   const uint32_t other_turn = smem_u32(&ms->turn[t ^ 1]);
   const uint32_t d_s = tmem + kColS + 128 * t, d_o = tmem + kColO + 128 * t;
+  constexpr int kHeadSteps = 6;  // k-steps of 16 keys in p_head
   // A wait of this warp; tile 0 starts, so its first turn is the phase before the first.
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
   uint32_t turns = t;
@@ -315,16 +317,26 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
   for (int32_t j = 0; j < n && ok; ++j) {
     const bool here = j < nt, next = j + 1 < nt;
     ok = on(&ms->v_full[j & 1], j >> 1) && (j != clean || on(&ms->v_clean, 0)) &&
-         (!here || on(&ms->p_full[t], j)) && on(&ms->turn[t], ++turns);
+         on(&ms->turn[t], ++turns) && (!here || on(&ms->p_head[t], j));
     if (!ok) break;
     tc_fence_after();
+    const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
+    const uint64_t v0 = v_desc + ring_slot(f) * kPanel, v1 = v_desc + ring_slot(f + 1) * kPanel;
+    if (here) {
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kHeadSteps; ++kk)
+          umma_f16_ts(d_o, d_s + 8 * kk, (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
+      }
+      __syncwarp();
+      ok = on(&ms->p_full[t], j);
+      if (!ok) break;
+      tc_fence_after();
+    }
     if (elect_one()) {
       if (here) {
-        const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
-        const uint64_t v0 = v_desc + ring_slot(f) * kPanel, v1 = v_desc + ring_slot(f + 1) * kPanel;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts(d_o, d_s + 8 * kk, (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
+        for (int kk = kHeadSteps; kk < 8; ++kk) umma_f16_ts(d_o, d_s + 8 * kk, v1 + (kk & 3) * 128, kIdescPV, 1);
         if (!next) umma_commit(smem_u32(&ms->o_full[t]));
         umma_commit(smem_u32(&ms->v_empty[j & 1]));
       } else {
@@ -451,15 +463,21 @@ __device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, ui
         pk[i] = bf16x2(x, y);
       }
       tmem_st16(s_addr + 16 * c, pk);
+      if (c == 2) {  // the products of the first 96 keys may start
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->p_head[t]));
+      }
     }
-    float s0, s1, s2, s3;
-    unpack2(part[0], s0, s1);
-    unpack2(part[1], s2, s3);
-    sum += (s0 + s1) + (s2 + s3);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[t]));
+    float s0, s1, s2, s3;
+    unpack2(part[0], s0, s1);
+    unpack2(part[1], s2, s3);
+    sum += (s0 + s1) + (s2 + s3);
   }
 
   // Epilogue.  A row that saw no key has sum 0.
@@ -530,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ms->v_empty[t]), 2);
       mbar_init(smem_u32(&ms->q_full[t]), 1);
       mbar_init(smem_u32(&ms->s_full[t]), 1);
+      mbar_init(smem_u32(&ms->p_head[t]), 4);
       mbar_init(smem_u32(&ms->p_full[t]), 4);
       mbar_init(smem_u32(&ms->o_full[t]), 1);
       mbar_init(smem_u32(&ms->turn[t]), 1);
