@@ -167,7 +167,7 @@ def _e4m3_cache(kv_fp8) -> torch.Tensor:
         raise TypeError(f"kv_fp8 must hold e4m3fn codes (uint8 or float8_e4m3fn), got {kv_fp8.dtype}")
     if kv_fp8.dim() not in (2, 3) or kv_fp8.numel() != kv_fp8.shape[0] * QK_HEAD_DIM:
         raise ValueError(f"kv_fp8 must be [rows, 576] or [rows, 1, 576], got {tuple(kv_fp8.shape)}")
-    return kv_fp8.reshape(kv_fp8.shape[0], QK_HEAD_DIM)
+    return kv_fp8 if kv_fp8.dim() == 2 else kv_fp8.reshape(kv_fp8.shape[0], QK_HEAD_DIM)
 
 
 def _fwd_args(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream, plan, kv_indices,
@@ -324,53 +324,83 @@ def mla_fp8_quantize_per_tensor(src_bf16, dst_fp8, scale_out, tmp, stream=None) 
 
 
 # ---------------------------------------------------------------- around the decode step
-def _operands(fn: str, *named) -> torch.device:
-    """The one CUDA device of (name, tensor, dtype) operands of ``fn`` (None tensors are skipped)."""
-    dev = None
-    for name, t, dtype in named:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, the other tensors on {dev}")
-    return dev
+# A step makes several of these small calls, so their host time counts: operands
+# are checked in one pass each, by the tensors' cheap accessors.
+_BF16, _F32T, _I32T = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _dense(*named) -> None:
-    for name, t in named:
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _device_of(t, name: str) -> int:
+    """Index of the CUDA device that a call's first operand, and so every other one, is on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.get_device()
 
 
-def _shape(name: str, t: torch.Tensor, *dims) -> None:
-    """``t`` must have these sizes (None: any)."""
-    if t.dim() != len(dims) or any(d is not None and d != n for d, n in zip(dims, t.shape)):
-        want = ", ".join("*" if d is None else str(d) for d in dims)
-        raise ValueError(f"{name} must be [{want}], got {list(t.shape)}")
+def _view_ptr(t, name: str, dtype, dev: int) -> int:
+    """Address of an operand on device ``dev`` that may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _strides(name: str, t: torch.Tensor):
-    """Element strides of the leading dims of a tensor whose last dim is dense."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _ptr(t, name: str, dtype, dev: int) -> int:
+    """Address of a contiguous operand on device ``dev``."""
+    p = _view_ptr(t, name, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def _expect(name: str, t, shape) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _strides2(name: str, t):
+    """(token, head) strides of a [tokens, heads, dim] operand; a dimension of size one has
+    no stride of its own (torch may report any value)."""
+    a, b, c = t.stride()
+    n, h, d = t.shape
+    if c != 1 and d > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    # a dimension of size one has no stride of its own (torch may report any value)
-    return [s if n > 1 else t.shape[-1] for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+    return (a if n > 1 else d), (b if h > 1 else d)
 
 
-def _launch(fn: str, device: torch.device, stream, make_args) -> None:
-    """Call ``fn`` with ``device`` current, on ``stream`` or that device's current stream."""
-    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            _check(fn, getattr(load_library(), fn)(*make_args(_stream(stream))))
+def _stride1(name: str, t) -> int:
+    """Row stride of a [tokens, dim] operand."""
+    a, c = t.stride()
+    n, d = t.shape
+    if c != 1 and d > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return a if n > 1 else d
+
+
+def _on(fn: str, stream, dev: int) -> Optional[int]:
+    """The stream's handle: ``stream``, or device ``dev``'s current one."""
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{dev}")
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _call(fn: str, dev: int, *args) -> None:
+    """Call entry point ``fn`` with device ``dev`` current."""
+    entry = getattr(_lib or load_library(), fn)
+    if torch.cuda.current_device() == dev:
+        status = entry(*args)
     else:
-        _check(fn, getattr(load_library(), fn)(*make_args(_stream(stream))))
+        with torch.cuda.device(dev):
+            status = entry(*args)
+    if status != 0:
+        raise MlaError(fn, status)
 
 
 def mla_page_map(kv_lens, new_lens, block_table, free_pages, qo_indptr, kv_indptr, kv_indices, slots,
@@ -384,19 +414,21 @@ def mla_page_map(kv_lens, new_lens, block_table, free_pages, qo_indptr, kv_indpt
     ``kv_indptr`` int32 [B + 1], ``kv_indices`` int32, ``slots`` and ``positions``
     int32 of one length (or both None), ``pages_used`` int32 [1].  ``workspace``:
     STEP_WORKSPACE_BYTES, zeroed once; errors are read by mla_decode_read_error."""
-    i32 = torch.int32
-    dev = _operands("mla_page_map", ("kv_lens", kv_lens, i32), ("new_lens", new_lens, i32),
-                    ("block_table", block_table, i32), ("free_pages", free_pages, i32),
-                    ("qo_indptr", qo_indptr, i32), ("kv_indptr", kv_indptr, i32),
-                    ("kv_indices", kv_indices, i32), ("slots", slots, i32),
-                    ("positions", positions, i32), ("pages_used", pages_used, i32),
-                    ("workspace", workspace, None))
-    _dense(("kv_lens", kv_lens), ("new_lens", new_lens), ("free_pages", free_pages),
-           ("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("kv_indices", kv_indices),
-           ("slots", slots), ("positions", positions), ("pages_used", pages_used),
-           ("workspace", workspace))
+    dev = _device_of(kv_lens, "kv_lens")
+    p_len = _ptr(kv_lens, "kv_lens", _I32T, dev)
+    p_new = _ptr(new_lens, "new_lens", _I32T, dev)
+    p_table = _view_ptr(block_table, "block_table", _I32T, dev)
+    p_free = None if free_pages is None else _ptr(free_pages, "free_pages", _I32T, dev)
+    p_qo = _ptr(qo_indptr, "qo_indptr", _I32T, dev)
+    p_kv = _ptr(kv_indptr, "kv_indptr", _I32T, dev)
+    p_idx = _ptr(kv_indices, "kv_indices", _I32T, dev)
+    p_slots = None if slots is None else _ptr(slots, "slots", _I32T, dev)
+    p_pos = None if positions is None else _ptr(positions, "positions", _I32T, dev)
+    p_used = _ptr(pages_used, "pages_used", _I32T, dev)
+    p_ws = _ptr(workspace, "workspace", None, dev)
     b = kv_lens.numel()
-    _shape("block_table", block_table, b, None)
+    if block_table.dim() != 2 or block_table.shape[0] != b:
+        raise ValueError(f"block_table must be [{b}, max_pages], got {list(block_table.shape)}")
     if (new_lens.numel() != b or qo_indptr.numel() != b + 1 or kv_indptr.numel() != b + 1
             or pages_used.numel() != 1):
         raise ValueError("new_lens must hold B entries, the indptrs B + 1, pages_used one")
@@ -404,53 +436,48 @@ def mla_page_map(kv_lens, new_lens, block_table, free_pages, qo_indptr, kv_indpt
     if n_slots != (0 if positions is None else positions.numel()):
         raise ValueError("slots and positions must have one length")
     width = block_table.shape[1]
-    if width > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table's rows must be contiguous")
-    if b > 1 and block_table.stride(0) < width:
+    row = _stride1("block_table", block_table)
+    if row < width:
         raise ValueError("block_table's rows must not overlap")
-    _launch("mla_page_map", dev, stream, lambda s: (
-        kv_lens.data_ptr(), new_lens.data_ptr(), b, block_table.data_ptr(),
-        block_table.stride(0) if b > 1 else width, width, int(page_size), int(num_pages),
-        None if free_pages is None else free_pages.data_ptr(),
-        0 if free_pages is None else free_pages.numel(), qo_indptr.data_ptr(), kv_indptr.data_ptr(),
-        kv_indices.data_ptr(), kv_indices.numel(), None if slots is None else slots.data_ptr(),
-        None if positions is None else positions.data_ptr(), n_slots, pages_used.data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    _call("mla_page_map", dev, p_len, p_new, b, p_table, row, width, page_size, num_pages, p_free,
+          0 if free_pages is None else free_pages.numel(), p_qo, p_kv, p_idx, kv_indices.numel(),
+          p_slots, p_pos, n_slots, p_used, p_ws, workspace.nbytes, _on("mla_page_map", stream, dev))
 
 
 def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, stream, workspace,
             eps, interleaved, q_pe, q_out, latent_out):
-    bf16, i32 = torch.bfloat16, torch.int32
-    if (q_pe is None) != (q_out is None):
-        raise ValueError("q_pe and q_out come together")
-    dev = _operands(fn, ("kv", kv, bf16), ("norm_weight", norm_weight, bf16),
-                    ("rope_table", rope_table, torch.float32), ("positions", positions, i32),
-                    ("slots", slots, i32), ("cache", cache, None), ("kv_scale", kv_scale, torch.float32),
-                    ("q_pe", q_pe, bf16), ("q_out", q_out, bf16), ("latent_out", latent_out, bf16),
-                    ("workspace", workspace, None))
-    _dense(("norm_weight", norm_weight), ("rope_table", rope_table), ("positions", positions),
-           ("slots", slots), ("cache", cache), ("latent_out", latent_out), ("workspace", workspace))
+    dev = _device_of(kv, "kv")
+    p_kv = _view_ptr(kv, "kv", _BF16, dev)
+    p_weight = _ptr(norm_weight, "norm_weight", _BF16, dev)
+    p_table = _ptr(rope_table, "rope_table", _F32T, dev)
+    p_pos = _ptr(positions, "positions", _I32T, dev)
+    p_slots = _ptr(slots, "slots", _I32T, dev)
+    p_cache = _ptr(cache, "cache", None, dev)
+    scale = () if kv_scale is None else (_ptr(kv_scale, "kv_scale", _F32T, dev),)
+    p_dense = None if latent_out is None else _ptr(latent_out, "latent_out", _BF16, dev)
+    p_ws = _ptr(workspace, "workspace", None, dev)
+    if kv.dim() != 2 or kv.shape[1] != QK_HEAD_DIM:
+        raise ValueError(f"kv must be [tokens, {QK_HEAD_DIM}], got {list(kv.shape)}")
+    if rope_table.dim() != 2 or rope_table.shape[1] != ROPE_DIM:
+        raise ValueError(f"rope_table must be [positions, {ROPE_DIM}], got {list(rope_table.shape)}")
     t = kv.shape[0]
-    _shape("kv", kv, None, QK_HEAD_DIM)
-    _shape("rope_table", rope_table, None, ROPE_DIM)
     if norm_weight.numel() != V_HEAD_DIM or positions.numel() != t or slots.numel() != t:
         raise ValueError("norm_weight must hold 512 values, positions and slots one entry a token")
     if latent_out is not None:
-        _shape("latent_out", latent_out, t, QK_HEAD_DIM)
-    heads, qs, os_ = 0, (0, 0), (0, 0)
-    if q_pe is not None:
-        heads = q_pe.shape[1] if q_pe.dim() == 3 else -1
-        _shape("q_pe", q_pe, t, heads, ROPE_DIM)
-        _shape("q_out", q_out, t, heads, ROPE_DIM)
-        qs, os_ = _strides("q_pe", q_pe), _strides("q_out", q_out)
-    ks = _strides("kv", kv)[0]
-    scale = () if kv_scale is None else (kv_scale.data_ptr(),)
-    _launch(fn, dev, stream, lambda s: (
-        kv.data_ptr(), ks, norm_weight.data_ptr(), float(eps), rope_table.data_ptr(),
-        rope_table.shape[0], int(interleaved), positions.data_ptr(), slots.data_ptr(), t,
-        cache.data_ptr(), *scale, cache.shape[0], None if latent_out is None else latent_out.data_ptr(),
-        None if q_pe is None else q_pe.data_ptr(), *qs, None if q_out is None else q_out.data_ptr(),
-        *os_, heads, workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+        _expect("latent_out", latent_out, (t, QK_HEAD_DIM))
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out come together")
+    if q_pe is None:
+        queries = (None, 0, 0, None, 0, 0, 0)
+    else:
+        p_q, p_out = _view_ptr(q_pe, "q_pe", _BF16, dev), _view_ptr(q_out, "q_out", _BF16, dev)
+        if q_pe.dim() != 3 or q_pe.shape[0] != t or q_pe.shape[2] != ROPE_DIM:
+            raise ValueError(f"q_pe must be [{t}, heads, {ROPE_DIM}], got {list(q_pe.shape)}")
+        _expect("q_out", q_out, q_pe.shape)
+        queries = (p_q, *_strides2("q_pe", q_pe), p_out, *_strides2("q_out", q_out), q_pe.shape[1])
+    _call(fn, dev, p_kv, _stride1("kv", kv), p_weight, eps, p_table, rope_table.shape[0],
+          1 if interleaved else 0, p_pos, p_slots, t, p_cache, *scale, cache.shape[0], p_dense,
+          *queries, p_ws, workspace.nbytes, _on(fn, stream, dev))
 
 
 def mla_kv_append(kv, norm_weight, rope_table, positions, slots, kv_fp8, kv_scale, stream=None, *,
@@ -493,32 +520,29 @@ def mla_prefill_plan(batch: int, total_q: int, max_kv_len: int, num_heads: int =
 
 def _prefill(fn, q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream, plan, workspace, scale,
              causal, lse):
-    bf16, i32 = torch.bfloat16, torch.int32
-    dev = _operands(fn, ("q", q, bf16), ("k_nope", k_nope, bf16), ("k_rope", k_rope, bf16),
-                    ("v", v, bf16), ("qo_indptr", qo_indptr, i32), ("kv_indptr", kv_indptr, i32),
-                    ("out", out, bf16), ("lse", lse, torch.float32), ("workspace", workspace, None))
-    _dense(("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("out", out), ("lse", lse),
-           ("workspace", workspace))
-    t, h, b = int(plan.total_q), int(plan.num_heads), int(plan.batch)
+    dev = _device_of(q, "q")
+    p_q, p_kn = _view_ptr(q, "q", _BF16, dev), _view_ptr(k_nope, "k_nope", _BF16, dev)
+    p_kr, p_v = _view_ptr(k_rope, "k_rope", _BF16, dev), _view_ptr(v, "v", _BF16, dev)
+    p_qo = _ptr(qo_indptr, "qo_indptr", _I32T, dev)
+    p_kv = _ptr(kv_indptr, "kv_indptr", _I32T, dev)
+    p_out = _ptr(out, "out", _BF16, dev)
+    p_lse = None if lse is None else _ptr(lse, "lse", _F32T, dev)
+    p_ws = _ptr(workspace, "workspace", None, dev)
+    t, h, b = plan.total_q, plan.num_heads, plan.batch
     n = k_nope.shape[0]
-    _shape("q", q, t, h, PREFILL_QK_DIM)
-    _shape("k_nope", k_nope, n, h, PREFILL_NOPE_DIM)
-    _shape("k_rope", k_rope, n, PREFILL_QK_DIM - PREFILL_NOPE_DIM)
-    _shape("v", v, n, h, PREFILL_V_DIM)
-    _shape("out", out, t, h, PREFILL_V_DIM)
+    _expect("q", q, (t, h, PREFILL_QK_DIM))
+    _expect("k_nope", k_nope, (n, h, PREFILL_NOPE_DIM))
+    _expect("k_rope", k_rope, (n, PREFILL_QK_DIM - PREFILL_NOPE_DIM))
+    _expect("v", v, (n, h, PREFILL_V_DIM))
+    _expect("out", out, (t, h, PREFILL_V_DIM))
     if lse is not None:
-        _shape("lse", lse, t, h)
+        _expect("lse", lse, (t, h))
     if qo_indptr.numel() != b + 1 or kv_indptr.numel() != b + 1:
         raise ValueError("qo_indptr and kv_indptr must hold plan.batch + 1 entries")
-    qs, ns, rs, vs = (_strides("q", q), _strides("k_nope", k_nope), _strides("k_rope", k_rope),
-                      _strides("v", v))
-    if scale is None:
-        scale = PREFILL_QK_DIM ** -0.5
-    _launch(fn, dev, stream, lambda s: (
-        q.data_ptr(), *qs, k_nope.data_ptr(), *ns, k_rope.data_ptr(), *rs, v.data_ptr(), *vs, n,
-        qo_indptr.data_ptr(), kv_indptr.data_ptr(), float(scale), int(causal), out.data_ptr(),
-        None if lse is None else lse.data_ptr(), s, ctypes.byref(plan), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size()))
+    _call(fn, dev, p_q, *_strides2("q", q), p_kn, *_strides2("k_nope", k_nope), p_kr,
+          _stride1("k_rope", k_rope), p_v, *_strides2("v", v), n, p_qo, p_kv,
+          PREFILL_QK_DIM ** -0.5 if scale is None else scale, 1 if causal else 0, p_out, p_lse,
+          _on(fn, stream, dev), ctypes.byref(plan), p_ws, workspace.nbytes)
 
 
 def mla_prefill_fwd(q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream=None, *, plan, workspace,
@@ -546,17 +570,17 @@ def mla_attn_merge(parts, lses, out, stream=None, *, lse_out=None) -> torch.Tens
     """Join attention over disjoint keys: ``parts`` bf16 [S, ..., dim] with natural
     log-sum-exps ``lses`` float32 [S, ...] into ``out`` bf16 [..., dim] (and ``lse_out``
     float32 [...]); returns ``out`` (see the C header)."""
-    dev = _operands("mla_attn_merge", ("parts", parts, torch.bfloat16), ("lses", lses, torch.float32),
-                    ("out", out, torch.bfloat16), ("lse_out", lse_out, torch.float32))
-    _dense(("parts", parts), ("lses", lses), ("out", out), ("lse_out", lse_out))
-    rows = parts.shape[1:-1]
-    if parts.dim() < 2 or lses.shape != parts.shape[:-1] or out.shape != parts.shape[1:]:
+    dev = _device_of(parts, "parts")
+    p_parts, p_lses = _ptr(parts, "parts", _BF16, dev), _ptr(lses, "lses", _F32T, dev)
+    p_out = _ptr(out, "out", _BF16, dev)
+    p_lse = None if lse_out is None else _ptr(lse_out, "lse_out", _F32T, dev)
+    shape = parts.shape
+    if len(shape) < 2 or lses.shape != shape[:-1] or out.shape != shape[1:]:
         raise ValueError("parts must be [S, ..., dim], lses [S, ...], out [..., dim]")
-    if lse_out is not None and lse_out.shape != rows:
+    if lse_out is not None and lse_out.shape != shape[1:-1]:
         raise ValueError("lse_out must have one entry a row")
-    _launch("mla_attn_merge", dev, stream, lambda s: (
-        parts.data_ptr(), lses.data_ptr(), parts.shape[0], rows.numel(), parts.shape[-1],
-        out.data_ptr(), None if lse_out is None else lse_out.data_ptr(), s))
+    _call("mla_attn_merge", dev, p_parts, p_lses, shape[0], shape[1:-1].numel(), shape[-1], p_out, p_lse,
+          _on("mla_attn_merge", stream, dev))
     return out
 
 
