@@ -13,6 +13,7 @@
 namespace {
 
 constexpr uint64_t kAlign = 256;
+constexpr uint64_t kSchedOffset = 64;  // in a workspace's first 256 bytes, behind the error word
 uint64_t round_up(uint64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -233,11 +234,13 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   p.part = reinterpret_cast<float*>(ws + plan->ws_partial_offset);
   p.part_lse = reinterpret_cast<float*>(ws + plan->ws_lse_offset);
   p.err = reinterpret_cast<int32_t*>(ws);
+  p.sched = reinterpret_cast<uint32_t*>(ws + kSchedOffset);
   p.scale = scale;
   p.batch = plan->batch;
   p.heads = heads;
   p.total_q = plan->total_q;
   p.tiles = plan->tiles;
+  p.num_sms = plan->num_sms;
   p.splits = plan->splits;
   p.causal = causal != 0;
   p.total_kv = total_kv;

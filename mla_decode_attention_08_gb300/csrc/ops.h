@@ -87,7 +87,8 @@ struct MergeParams {
 };
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
 
-// mla_prefill_fwd: one block per (256 queries of a row, head, split).
+// mla_prefill_fwd: a persistent block an SM; a job is up to 256 queries of a row
+// and head over one split of its keys.
 struct PrefillParams {
   const int32_t* qo_indptr;
   const int32_t* kv_indptr;
@@ -96,8 +97,9 @@ struct PrefillParams {
   float* part;             // splits > 1: [splits][total_q][heads][128]
   float* part_lse;         // splits > 1: [splits][total_q][heads]
   int32_t* err;
+  uint32_t* sched;         // jobs handed out, blocks done: both zero between calls
   float scale;
-  int32_t batch, heads, total_q, tiles, splits, causal;
+  int32_t batch, heads, total_q, tiles, splits, causal, num_sms;
   int64_t total_kv;
   int32_t stall_stream;    // test hook: no copies are issued, so the waits run out
 };
@@ -106,7 +108,7 @@ struct PrefillMaps {
 };
 constexpr int kPrefillQk = MLA_PREFILL_QK_DIM, kPrefillNope = MLA_PREFILL_NOPE_DIM;
 constexpr int kPrefillRope = kPrefillQk - kPrefillNope, kPrefillV = MLA_PREFILL_V_DIM;
-constexpr int kPrefillRows = 256;  // query rows of a block: two tiles of 128
+constexpr int kPrefillRows = 256;  // query rows of a job: two tiles of 128
 size_t prefill_smem_bytes();
 cudaError_t prefill_prepare();
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream);

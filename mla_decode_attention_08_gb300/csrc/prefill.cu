@@ -51,26 +51,44 @@ constexpr uint32_t kIdescPV = idesc_bf16(kTile, kPrefillV, false, true);
 // costs bf16 nothing, and most tiles rescale nothing.
 constexpr float kRescaleThreshold = 8.0f;
 
+// One job: up to 256 queries of a row and head over a part of the row's keys.
+struct Job {
+  int32_t q0, nq;       // first query token (of the batch) and number of queries
+  int32_t k0, len;      // the row's first key and number of keys
+  int32_t see;          // keys that the first query sees, when causal
+  int32_t head, split;
+  int32_t j0, nt0, nt1; // first key tile, and key tiles of query tiles 0 and 1
+  int32_t live;         // 0: no more jobs
+  __device__ __forceinline__ int32_t tiles() const { return max(nt0, nt1); }
+  // The tile (counted from j0) that the row's end cuts, or -1.
+  __device__ __forceinline__ int32_t partial() const {
+    const int32_t j = len / kTile - j0;
+    return len % kTile != 0 && j >= 0 && j < tiles() ? j : -1;
+  }
+};
+
+// The block works through jobs; key tiles are numbered through all of them (T),
+// and so are each query tile's tiles and jobs: the numbers give the phases.
 struct Misc {
-  uint64_t q_full[2];
-  // Of tile j's K and V, j & 1: landed, and released by both issuers.
+  uint64_t job_full[2], job_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  // Of key tile T's K and V, T & 1: landed, and released by both issuers.
   uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
-  uint64_t s_full[2];   // S_t(j) complete, and with it every product before it
-  uint64_t p_head[2];   // the first three quarters of P_t(j) written (and O_t rescaled)
+  uint64_t s_full[2];   // S_t complete, and with it every product before it
+  uint64_t p_head[2];   // the first three quarters of P_t written (and O_t rescaled)
   uint64_t p_full[2];   // all of it
-  uint64_t o_full[2];   // the last product of tile t complete
+  uint64_t o_full[2];   // the job's last product of tile t complete
+  uint64_t o_free[2];   // the job's O_t read out
   uint64_t turn[2];     // the other tile's products are issued
   uint64_t v_last;      // the copies of the tile that holds the row's end are issued
   uint64_t v_clean;     // V behind the row's end is zeroed
   uint64_t mma_done;
   uint32_t tmem_base;
   volatile int32_t abort_flag;
-  // This block's work.
-  int32_t q0;           // first query token (of the batch)
-  int32_t nq;           // queries of this block, 0: nothing to do
-  int32_t k0, len;      // the row's first key and number of keys
-  int32_t see;          // keys that the block's first query sees, when causal
+  Job job[2];
 };
+// What reads a job: two issuers, the cleaner and eight softmax warps.
+constexpr uint32_t kJobReaders = 11;
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one block");
 static_assert(kPrefillV == 128 && kPrefillNope == 128 && kPrefillRope == 64, "tile layout");
@@ -111,159 +129,211 @@ __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
 
 __device__ __forceinline__ int32_t tiles_256(int32_t n) { return n / kPrefillRows + (n % kPrefillRows != 0); }
 
-// Finds block `rank`'s row and queries (one warp).  The rows' blocks of 256
-// queries, in order, are handed out from the last one: with causal rows a
-// row's later queries see more keys, so its long blocks start first.
-__device__ __forceinline__ void find_work(const PrefillParams& p, int32_t rank, bool report, Misc* ms) {
+// The rows' blocks of 256 queries, counted over the batch: each lane of the
+// producer warp a run of consecutive rows.
+struct RowRuns {
+  int32_t b0, b1, first, count, total;  // rows [b0, b1), their blocks, all rows' blocks
+};
+__device__ __forceinline__ int32_t row_blocks(const PrefillParams& p, int32_t b, bool report) {
+  const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
+  const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
+  const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || ke < ks || ke > p.total_kv;
+  if (report && (bad_q || bad_k))
+    atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
+  return bad_q || bad_k ? 0 : tiles_256(qe - qs);
+}
+__device__ __forceinline__ RowRuns count_rows(const PrefillParams& p) {
   const int lane = threadIdx.x & 31;
   const int32_t run = (p.batch + 31) / 32;
-  const int32_t b0 = min(p.batch, lane * run), b1 = min(p.batch, b0 + run);
-  auto row_tiles = [&](int32_t b, bool tell) {
-    const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
-    const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
-    const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || ke < ks || ke > p.total_kv;
-    if (tell && (bad_q || bad_k))
-      atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
-    return bad_q || bad_k ? 0 : tiles_256(qe - qs);
-  };
-  int32_t mine = 0;
-  for (int32_t b = b0; b < b1; ++b) mine += row_tiles(b, report);
-  int32_t incl = mine;
+  RowRuns r;
+  r.b0 = min(p.batch, lane * run);
+  r.b1 = min(p.batch, r.b0 + run);
+  r.count = 0;
+  for (int32_t b = r.b0; b < r.b1; ++b) r.count += row_blocks(p, b, blockIdx.x == 0);
+  int32_t incl = r.count;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
-  const int32_t total = __shfl_sync(0xffffffffu, incl, 31);
-  int32_t target = total - 1 - rank;
-  if (target < 0) {
-    if (lane == 0) ms->nq = 0;
-    return;
-  }
-  if (target < incl - mine || target >= incl) return;
-  target -= incl - mine;
-  for (int32_t b = b0; b < b1; ++b) {
-    const int32_t nt = row_tiles(b, false);
-    if (target < nt) {
-      const int32_t qs = __ldg(p.qo_indptr + b), n = __ldg(p.qo_indptr + b + 1) - qs;
-      const int32_t ks = __ldg(p.kv_indptr + b), len = __ldg(p.kv_indptr + b + 1) - ks;
-      const int32_t i0 = target * kPrefillRows;
-      ms->q0 = qs + i0;
-      ms->nq = min(kPrefillRows, n - i0);
-      ms->k0 = ks;
-      ms->len = len;
-      ms->see = len - n + i0 + 1;
-      return;
-    }
-    target -= nt;
-  }
-}
-
-// A block's key tiles: [j0, j1) of the row for its split, and how many of them
-// query tile t needs.
-struct Range {
-  int32_t j0, nt[2];
-};
-__device__ __forceinline__ Range key_range(const PrefillParams& p, const Misc* ms, int32_t split) {
-  Range r;
-  auto tiles = [&](int32_t last) {  // key tiles up to the block's query `last`
-    const int32_t keys = p.causal ? max(0, min(ms->len, ms->see + last)) : ms->len;
-    return keys / kTile + (keys % kTile != 0);
-  };
-  const int32_t all = ms->nq > 0 ? tiles(ms->nq - 1) : 0;
-  const int32_t share = (all + p.splits - 1) / p.splits;
-  r.j0 = min(all, split * share);
-  const int32_t j1 = min(all, r.j0 + share);
-  r.nt[0] = all > 0 ? max(0, min(j1, tiles(min(ms->nq, kTile) - 1)) - r.j0) : 0;
-  r.nt[1] = ms->nq > kTile ? j1 - r.j0 : 0;
+  r.first = incl - r.count;
+  r.total = __shfl_sync(0xffffffffu, incl, 31);
   return r;
 }
 
-// ------------------------------------------------------------ V behind the row's end (a warp of its own)
-// The row's last key tile may end inside the tile.  The rows of V behind it are
-// another row's, or never written: their probabilities are zero, but zero times
-// NaN is NaN, so they are zeroed in shared memory before the product reads them.
-__device__ __forceinline__ int32_t partial_tile(const Misc* ms, const Range& r) {
-  const int32_t j = ms->len / kTile - r.j0;  // the tile that holds the row's end
-  return ms->len % kTile != 0 && j >= 0 && j < max(r.nt[0], r.nt[1]) ? j : -1;
+// Job `index` into `job` (one warp).  Heads run fastest, so that the blocks at
+// work read the same keys' neighbourhood for all heads and it stays in L2; the
+// blocks of queries are handed out from the last one, so that with causal rows
+// the long jobs start first.
+__device__ __forceinline__ void find_job(const PrefillParams& p, const RowRuns& r, uint32_t index, Job* job) {
+  const uint32_t rest = index / p.heads, rank = rest / p.splits;
+  const int32_t target = r.total - 1 - static_cast<int32_t>(min(rank, 0x7FFFFFFFu));
+  if (target < 0) {
+    if ((threadIdx.x & 31) == 0) {
+      job->live = job->nq = job->nt0 = job->nt1 = 0;
+    }
+  } else if (target >= r.first && target < r.first + r.count) {
+    int32_t i = target - r.first;
+    for (int32_t b = r.b0; b < r.b1; ++b) {
+      const int32_t blocks = row_blocks(p, b, false);
+      if (i >= blocks) {
+        i -= blocks;
+        continue;
+      }
+      const int32_t qs = __ldg(p.qo_indptr + b), n = __ldg(p.qo_indptr + b + 1) - qs;
+      const int32_t ks = __ldg(p.kv_indptr + b), len = __ldg(p.kv_indptr + b + 1) - ks;
+      const int32_t i0 = i * kPrefillRows, nq = min(kPrefillRows, n - i0), see = len - n + i0 + 1;
+      auto tiles = [&](int32_t last) {  // key tiles up to the job's query `last`
+        const int32_t keys = p.causal ? max(0, min(len, see + last)) : len;
+        return keys / kTile + (keys % kTile != 0);
+      };
+      const int32_t split = static_cast<int32_t>(rest % p.splits);
+      const int32_t all = tiles(nq - 1), share = (all + p.splits - 1) / p.splits;
+      const int32_t j0 = min(all, split * share), j1 = min(all, j0 + share);
+      job->q0 = qs + i0;
+      job->nq = nq;
+      job->k0 = ks;
+      job->len = len;
+      job->see = see;
+      job->head = static_cast<int32_t>(index % p.heads);
+      job->split = split;
+      job->j0 = j0;
+      job->nt0 = max(0, min(j1, tiles(min(nq, kTile) - 1)) - j0);
+      job->nt1 = nq > kTile ? j1 - j0 : 0;
+      job->live = 1;
+      break;
+    }
+  }
+  __syncwarp();
 }
-// ------------------------------------------------------------ producer (one thread)
-// K(j) is the ring's fills 5 j .. 5 j + 2 and V(j) 5 j + 3 and 5 j + 4, fill f in
-// slot f % 8: K(j) takes the slots of K(j - 2)'s last panel and V(j - 2), V(j)
-// those of K(j - 1)'s first two.
+
+// Job number `k` of this block, for one of its readers (a whole warp).
+__device__ __forceinline__ bool next_job(const PrefillParams& p, Misc* ms, uint32_t k, Job& job) {
+  if (!warp_wait_on(&ms->job_full[k & 1], (k >> 1) & 1, ms, p.err)) return false;
+  job = ms->job[k & 1];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms->job_empty[k & 1]));
+  return job.live != 0;
+}
+
+// ------------------------------------------------------------ producer (one warp, lane 0 copies)
+// K(T) is the ring's fills 5 T .. 5 T + 2 and V(T) 5 T + 3 and 5 T + 4, fill f in
+// slot f % 8: K(T) takes the slots of K(T - 2)'s last panel and V(T - 2), V(T)
+// those of K(T - 1)'s first two.
 __device__ __forceinline__ uint32_t ring_slot(uint32_t f) { return f % kSlots; }
-__device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms,
-                                             uint32_t sbase, const Range& r, int32_t head) {
-  const int32_t n = max(r.nt[0], r.nt[1]);
-  if (n == 0 || p.stall_stream) return;
-  const uint64_t keep = l2_policy_evict_normal();
+
+struct Loads {
+  uint32_t k = 0, v = 0, q0 = 0, q1 = 0;  // copies issued: key tiles, and query tiles 0 and 1
+};
+
+// The copies of one job (lane 0).
+__device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase,
+                                         const Job& job, Loads& l, uint64_t keep) {
   const uint32_t ring = sbase + kOffRing;
-  const int32_t clean = partial_tile(ms, r);
-  int32_t ks = 0, vs = 0;  // tiles whose K, V copies are issued
-  bool ok = true;
-  auto load_k = [&](int32_t j) {
-    const uint32_t bar = smem_u32(&ms->k_full[j & 1]), f = static_cast<uint32_t>(j) * kFillsPerTile;
-    const int32_t key = ms->k0 + (r.j0 + j) * kTile;
-    mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
-    tma_load_3d(ring + ring_slot(f) * kPanelBytes, &m.k_nope, 0, head, key, bar, keep);
-    tma_load_3d(ring + ring_slot(f + 1) * kPanelBytes, &m.k_nope, 64, head, key, bar, keep);
-    tma_load_2d(ring + ring_slot(f + 2) * kPanelBytes, &m.k_rope, 0, key, bar, keep);
-    ++ks;
-  };
-  auto load_q = [&](int t) {
-    if ((t ? r.nt[1] : r.nt[0]) == 0) return;
+  const int32_t n = job.tiles(), clean = job.partial();
+  auto load_q = [&](int t, uint32_t& count) {
+    if (!wait_on(&ms->q_empty[t], (count + 1) & 1, ms, p.err)) return false;  // (the first passes)
+    ++count;
     const uint32_t bar = smem_u32(&ms->q_full[t]);
     mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
     for (int c = 0; c < kQPanels; ++c)
-      tma_load_3d(sbase + kOffQ + (t * kQPanels + c) * kPanelBytes, &m.q, 64 * c, head, ms->q0 + t * kTile, bar, keep);
+      tma_load_3d(sbase + kOffQ + (t * kQPanels + c) * kPanelBytes, &m.q, 64 * c, job.head, job.q0 + t * kTile,
+                  bar, keep);
+    return true;
   };
-  load_q(0);
-  load_k(0);
-  load_q(1);
-  for (int32_t j = 0; j < n && ok; ++j) {
-    if (j > 0) {
-      if (j > 1) ok = wait_on(&ms->v_empty[j & 1], (j / 2 - 1) & 1, ms, p.err);
-      if (!ok) break;
-      load_k(j);
-      ok = wait_on(&ms->k_empty[(j - 1) & 1], ((j - 1) / 2) & 1, ms, p.err);
-      if (!ok) break;
-    }
-    const uint32_t bar = smem_u32(&ms->v_full[j & 1]), f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
-    const int32_t key = ms->k0 + (r.j0 + j) * kTile;
+  for (int32_t j = 0; j < n; ++j) {
+    const uint32_t T = l.k, f = T * kFillsPerTile;
+    const int32_t key = job.k0 + (job.j0 + j) * kTile;
+    if (j == 0 && job.nt0 > 0 && !load_q(0, l.q0)) return false;
+    if (T > 1 && !wait_on(&ms->v_empty[T & 1], ((T >> 1) + 1) & 1, ms, p.err)) return false;
+    uint32_t bar = smem_u32(&ms->k_full[T & 1]);
+    mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
+    tma_load_3d(ring + ring_slot(f) * kPanelBytes, &m.k_nope, 0, job.head, key, bar, keep);
+    tma_load_3d(ring + ring_slot(f + 1) * kPanelBytes, &m.k_nope, 64, job.head, key, bar, keep);
+    tma_load_2d(ring + ring_slot(f + 2) * kPanelBytes, &m.k_rope, 0, key, bar, keep);
+    ++l.k;
+    if (j == 0 && job.nt1 > 0 && !load_q(1, l.q1)) return false;
+    if (T > 0 && !wait_on(&ms->k_empty[(T - 1) & 1], ((T - 1) >> 1) & 1, ms, p.err)) return false;
+    bar = smem_u32(&ms->v_full[T & 1]);
     mbar_arrive_expect_tx(bar, kVPanels * kPanelBytes);
 #pragma unroll
     for (int h = 0; h < kVPanels; ++h) {
-      const uint32_t dst = ring + ring_slot(f + h) * kPanelBytes;
-      tma_load_3d(dst, &m.v, 0, head, key + 64 * h, bar, keep);
-      tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, head, key + 64 * h, bar, keep);
+      const uint32_t dst = ring + ring_slot(f + kKPanels + h) * kPanelBytes;
+      tma_load_3d(dst, &m.v, 0, job.head, key + 64 * h, bar, keep);
+      tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, job.head, key + 64 * h, bar, keep);
     }
-    ++vs;
+    ++l.v;
     if (j == clean) mbar_arrive(smem_u32(&ms->v_last));
   }
-  if (ok && !ms->abort_flag) return;  // the issuers wait for every panel
-  // Abandoned: the copies in flight land before the block's memory is given up.
-  if (r.nt[0] > 0) drain(&ms->q_full[0], 0);
-  if (r.nt[1] > 0) drain(&ms->q_full[1], 0);
-  for (int32_t j = max(0, ks - 2); j < ks; ++j) drain(&ms->k_full[j & 1], (j / 2) & 1);
-  for (int32_t j = max(0, vs - 2); j < vs; ++j) drain(&ms->v_full[j & 1], (j / 2) & 1);
+  return true;
 }
 
-__device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, uint8_t* smem, const Range& r) {
+// Finds the block's jobs and loads them.  The first is the block's own, the
+// others are taken from a counter when the last copies of the job before are
+// issued, about two key tiles before its end: late enough that no block sits
+// on a job that another could start, early enough to hide the search.
+__device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase) {
   const int lane = threadIdx.x & 31;
-  const int32_t j = partial_tile(ms, r);
-  if (j < 0) return;
-  const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
-  // (a barrier can be waited on for its fill j / 2 once that is under way)
-  if (!warp_wait_on(&ms->v_last, 0, ms, p.err) || !warp_wait_on(&ms->v_full[j & 1], (j / 2) & 1, ms, p.err)) return;
-  for (int32_t i = (ms->len % kTile) * 16 + lane; i < kTile * 16; i += 32) {
-    const int32_t key = i >> 4, piece = i & 15;
-    *reinterpret_cast<uint4*>(smem + kOffRing + ring_slot(f + (key >> 6)) * kPanelBytes +
-                              (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
-        make_uint4(0, 0, 0, 0);
+  const uint64_t keep = l2_policy_evict_normal();
+  const RowRuns rows = count_rows(p);
+  Loads l;
+  uint32_t index = blockIdx.x;
+  bool ok = true;
+  for (uint32_t k = 0;; ++k) {
+    Job* job = &ms->job[k & 1];
+    ok = warp_wait_on(&ms->job_empty[k & 1], ((k >> 1) + 1) & 1, ms, p.err);  // (the first two pass)
+    if (!ok) break;
+    find_job(p, rows, index, job);
+    const Job mine = *job;
+    if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
+    if (mine.live == 0) break;
+    if (!p.stall_stream) {
+      if (lane == 0) ok = load_job(p, m, ms, sbase, mine, l, keep);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+    }
+    if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
+    index = __shfl_sync(0xffffffffu, index, 0);
   }
-  fence_proxy_async_smem();
+  if (ok && !ms->abort_flag) return;  // the issuers wait for every copy
+  // Abandoned: the copies in flight land before the block's memory is given up.
+  if (lane == 0) {
+    if (l.q0 > 0) drain(&ms->q_full[0], (l.q0 - 1) & 1);
+    if (l.q1 > 0) drain(&ms->q_full[1], (l.q1 - 1) & 1);
+    for (uint32_t T = l.k > 2 ? l.k - 2 : 0; T < l.k; ++T) drain(&ms->k_full[T & 1], (T >> 1) & 1);
+    for (uint32_t T = l.v > 2 ? l.v - 2 : 0; T < l.v; ++T) drain(&ms->v_full[T & 1], (T >> 1) & 1);
+  }
   __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
+}
+
+// ------------------------------------------------------------ V behind the row's end (one warp)
+// The row's last key tile may end inside the tile.  The rows of V behind it are
+// another row's, or never written: their probabilities are zero, but zero times
+// NaN is NaN, so they are zeroed in shared memory before the product reads them.
+__device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, uint8_t* smem) {
+  const int lane = threadIdx.x & 31;
+  uint32_t base = 0, cleans = 0;
+  Job job;
+  for (uint32_t k = 0; next_job(p, ms, k, job); ++k) {
+    const int32_t j = job.partial();
+    const uint32_t T = base + j, f = T * kFillsPerTile + kKPanels;
+    base += job.tiles();
+    if (j < 0) continue;
+    // (a barrier can be waited on for its fill T / 2 once that is under way)
+    if (!warp_wait_on(&ms->v_last, cleans & 1, ms, p.err) ||
+        !warp_wait_on(&ms->v_full[T & 1], (T >> 1) & 1, ms, p.err))
+      return;
+    ++cleans;
+    for (int32_t i = (job.len % kTile) * 16 + lane; i < kTile * 16; i += 32) {
+      const int32_t key = i >> 4, piece = i & 15;
+      *reinterpret_cast<uint4*>(smem + kOffRing + ring_slot(f + (key >> 6)) * kPanelBytes +
+                                (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
+  }
 }
 
 // ------------------------------------------------------------ MMA issuers (a warp a tile, an elected lane issues)
@@ -274,10 +344,7 @@ __device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, ui
 // own issuer, which waits for what its next products need while the other
 // tile's run, and they take turns: P_t(j) . V(j) and Q_t . K(j + 1)^T are issued
 // together, the turn handed over a few products before their end.
-__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem,
-                                        const Range& r, int t) {
-  const int32_t nt = t ? r.nt[1] : r.nt[0], n = max(r.nt[0], r.nt[1]);
-  const int32_t clean = partial_tile(ms, r);
+__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int t) {
   const uint64_t q_desc = smem_desc(sbase + kOffQ + t * kQPanels * kPanelBytes, 1024, 1024, kLayoutSw128);
   const uint64_t k_desc = smem_desc(sbase + kOffRing, 1024, 1024, kLayoutSw128);
   const uint64_t v_desc = smem_desc(sbase + kOffRing, kPanelBytes / 2, 1024, kLayoutSw128);
@@ -287,10 +354,10 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
   constexpr int kHeadSteps = 6;  // k-steps of 16 keys in p_head
   // A wait of this warp; tile 0 starts, so its first turn is the phase before the first.
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
-  uint32_t turns = t;
-  // S_t = Q_t . K(j)^T (one lane), handing over the turn four products before its end
-  auto qk = [&](int32_t j) {
-    const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile;
+  uint32_t turns = t, T = 0, mine = 0, jobs = 0, cleans = 0;
+  // S_t = Q_t . K(T)^T (one lane), handing over the turn four products before its end
+  auto qk = [&](uint32_t tile, bool last) {
+    const uint32_t f = tile * kFillsPerTile;
 #pragma unroll
     for (int c = 0; c < kKPanels; ++c) {
       const uint64_t a = q_desc + c * kPanel, b = k_desc + ring_slot(f + c) * kPanel;
@@ -299,63 +366,72 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
       for (int kk = 0; kk < 4; ++kk) umma_f16(d_s, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
     }
     umma_commit(smem_u32(&ms->s_full[t]));
-    umma_commit(smem_u32(&ms->k_empty[j & 1]));
+    umma_commit(smem_u32(&ms->k_empty[tile & 1]));
+    if (last) umma_commit(smem_u32(&ms->q_empty[t]));
   };
-  bool ok = n > 0 && (nt == 0 || on(&ms->q_full[t], 0)) && on(&ms->k_full[0], 0) && on(&ms->turn[t], ++turns);
-  if (ok) {
+  Job job;
+  bool ok = true;
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    const int32_t nt = t ? job.nt1 : job.nt0, n = job.tiles(), clean = job.partial();
+    if (n == 0) continue;
+    ok = (nt == 0 || on(&ms->q_full[t], jobs)) && on(&ms->k_full[T & 1], T >> 1) && on(&ms->turn[t], ++turns);
+    if (!ok) break;
     tc_fence_after();
     if (elect_one()) {
       if (nt > 0) {
-        qk(0);
-      } else {  // the other tile alone reads K(0)
-        mbar_arrive(smem_u32(&ms->k_empty[0]));
+        qk(T, nt == 1);
+      } else {  // the other tile alone reads this K
+        mbar_arrive(smem_u32(&ms->k_empty[T & 1]));
         mbar_arrive(other_turn);
       }
     }
     __syncwarp();
-  }
-  for (int32_t j = 0; j < n && ok; ++j) {
-    const bool here = j < nt, next = j + 1 < nt;
-    ok = on(&ms->v_full[j & 1], j >> 1) && (j != clean || on(&ms->v_clean, 0)) &&
-         on(&ms->turn[t], ++turns) && (!here || on(&ms->p_head[t], j));
-    if (!ok) break;
-    tc_fence_after();
-    const uint32_t f = static_cast<uint32_t>(j) * kFillsPerTile + kKPanels;
-    const uint64_t v0 = v_desc + ring_slot(f) * kPanel, v1 = v_desc + ring_slot(f + 1) * kPanel;
-    if (here) {
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < kHeadSteps; ++kk)
-          umma_f16_ts(d_o, d_s + 8 * kk, (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
-      }
-      __syncwarp();
-      ok = on(&ms->p_full[t], j);
+    for (int32_t j = 0; j < n && ok; ++j, ++T) {
+      const bool here = j < nt, next = j + 1 < nt;
+      ok = on(&ms->v_full[T & 1], T >> 1) && (j != clean || on(&ms->v_clean, cleans)) &&
+           (j != 0 || nt == 0 || on(&ms->o_free[t], jobs + 1)) && on(&ms->turn[t], ++turns) &&
+           (!here || on(&ms->p_head[t], mine));
       if (!ok) break;
       tc_fence_after();
-    }
-    if (elect_one()) {
+      const uint32_t f = T * kFillsPerTile + kKPanels;
+      const uint64_t v0 = v_desc + ring_slot(f) * kPanel, v1 = v_desc + ring_slot(f + 1) * kPanel;
       if (here) {
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = kHeadSteps; kk < 8; ++kk) umma_f16_ts(d_o, d_s + 8 * kk, v1 + (kk & 3) * 128, kIdescPV, 1);
-        if (!next) umma_commit(smem_u32(&ms->o_full[t]));
-        umma_commit(smem_u32(&ms->v_empty[j & 1]));
-      } else {
-        mbar_arrive(smem_u32(&ms->v_empty[j & 1]));
+          for (int kk = 0; kk < kHeadSteps; ++kk)
+            umma_f16_ts(d_o, d_s + 8 * kk, (kk < 4 ? v0 : v1) + (kk & 3) * 128, kIdescPV, j != 0 || kk != 0);
+        }
+        __syncwarp();
+        ok = on(&ms->p_full[t], mine++);
+        if (!ok) break;
+        tc_fence_after();
       }
-      if (!next) mbar_arrive(other_turn);
+      if (elect_one()) {
+        if (here) {
+#pragma unroll
+          for (int kk = kHeadSteps; kk < 8; ++kk) umma_f16_ts(d_o, d_s + 8 * kk, v1 + (kk & 3) * 128, kIdescPV, 1);
+          if (!next) umma_commit(smem_u32(&ms->o_full[t]));
+          umma_commit(smem_u32(&ms->v_empty[T & 1]));
+        } else {
+          mbar_arrive(smem_u32(&ms->v_empty[T & 1]));
+        }
+        if (!next) mbar_arrive(other_turn);
+      }
+      __syncwarp();
+      if (j + 1 == n) continue;
+      ok = on(&ms->k_full[(T + 1) & 1], (T + 1) >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        if (next)
+          qk(T + 1, j + 2 == nt);
+        else
+          mbar_arrive(smem_u32(&ms->k_empty[(T + 1) & 1]));
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    if (j + 1 == n) break;
-    ok = on(&ms->k_full[(j + 1) & 1], (j + 1) >> 1);
-    if (!ok) break;
-    tc_fence_after();
-    if (elect_one()) {
-      if (next)
-        qk(j + 1);
-      else
-        mbar_arrive(smem_u32(&ms->k_empty[(j + 1) & 1]));
-    }
-    __syncwarp();
+    jobs += nt > 0;
+    cleans += clean >= 0;
   }
   if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
   __syncwarp();
@@ -391,27 +467,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-__device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, uint32_t tmem, const Range& r,
-                                            int32_t head, int32_t split, int t) {
+// One job of query tile t (a warpgroup); `tiles` and `jobs` count what it has done before.
+__device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, uint32_t tmem, const Job& job, int t,
+                                            uint32_t& tiles, uint32_t& jobs) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
-  const int row = quad * 32 + lane;                  // of the tile
-  const int qi = t * kTile + row;                    // of the block
+  const int qi = t * kTile + quad * 32 + lane;       // this thread's query of the job
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t s_addr = tmem + lanes + kColS + 128 * t, o_addr = tmem + lanes + kColO + 128 * t;
-  const int32_t n = t ? r.nt[1] : r.nt[0];
+  const int32_t n = t ? job.nt1 : job.nt0;
   const float sl = p.scale * 1.4426950408889634f;    // scores to powers of two
   // keys that this row, and the warp's first row, see
-  const int32_t sees = p.causal ? min(ms->len, ms->see + qi) : ms->len;
-  const int32_t warp_sees = p.causal ? min(ms->len, ms->see + t * kTile + quad * 32) : ms->len;
+  const int32_t sees = p.causal ? min(job.len, job.see + qi) : job.len;
+  const int32_t warp_sees = p.causal ? min(job.len, job.see + t * kTile + quad * 32) : job.len;
   float ref = -INFINITY, sum = 0.0f;
-  for (int32_t j = 0; j < n; ++j) {
-    if (!warp_wait_on(&ms->s_full[t], j & 1, ms, p.err)) return;
+  for (int32_t j = 0; j < n; ++j, ++tiles) {
+    if (!warp_wait_on(&ms->s_full[t], tiles & 1, ms, p.err)) return false;
     tc_fence_after();
     uint32_t raw[4][32];
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, raw[c]);
     tmem_wait_ld();
-    const int32_t key0 = (r.j0 + j) * kTile;
+    const int32_t key0 = (job.j0 + j) * kTile;
     if (warp_sees - key0 < kTile) {
       const int32_t lim = sees - key0;
 #pragma unroll
@@ -481,40 +557,50 @@ __device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, ui
   }
 
   // Epilogue.  A row that saw no key has sum 0.
-  if (n > 0 && !warp_wait_on(&ms->o_full[t], 0, ms, p.err)) return;
-  tc_fence_after();
-  const bool live = qi < ms->nq;
+  if (n > 0) {
+    if (!warp_wait_on(&ms->o_full[t], jobs & 1, ms, p.err)) return false;
+    ++jobs;
+    tc_fence_after();
+  }
+  const bool live = qi < job.nq;
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  const int64_t at = static_cast<int64_t>(ms->q0 + qi) * p.heads + head;
-  const int64_t part_at = static_cast<int64_t>(split) * p.total_q * p.heads + at;
+  const int64_t at = static_cast<int64_t>(job.q0 + qi) * p.heads + job.head;
+  const int64_t part_at = static_cast<int64_t>(job.split) * p.total_q * p.heads + at;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t o[32];
     if (n > 0) {
       tmem_ld32(o_addr + 32 * c, o);
       tmem_wait_ld();
+      if (c == 3) {  // the next job's products may overwrite O_t
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[t]));
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] = 0;
     }
-    if (!live) continue;
-    if (p.splits == 1) {
-      uint4* dst = reinterpret_cast<uint4*>(p.out + at * kPrefillV + 32 * c);
+    if (live) {
+      if (p.splits == 1) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kPrefillV + 32 * c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k)
+            w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV + 32 * c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                               __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
       }
-    } else {
-      float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV + 32 * c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                             __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
     }
+    __syncwarp();
   }
   if (live) {
     const float lse = sum > 0.0f ? ref * p.scale + logf(sum) : -INFINITY;
@@ -523,6 +609,15 @@ __device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, ui
     else if (p.lse != nullptr)
       p.lse[at] = lse;
   }
+  __syncwarp();
+  return true;
+}
+
+__device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, uint32_t tmem, int t) {
+  uint32_t tiles = 0, jobs = 0;
+  Job job;
+  for (uint32_t k = 0; next_job(p, ms, k, job); ++k)
+    if (job.nq > t * kTile && !softmax_job(p, ms, tmem, job, t, tiles, jobs)) return;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -533,12 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   Misc* ms = reinterpret_cast<Misc*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // heads fastest: the blocks of one rank read different heads' keys, and the
-  // ranks of a row run near one another in time, so its keys stay in L2.
-  const int32_t head = static_cast<int32_t>(blockIdx.x % p.heads);
-  const int32_t rest = static_cast<int32_t>(blockIdx.x / p.heads);
-  const int32_t split = rest % p.splits, rank = rest / p.splits;
-
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
   if (tid == kProducerWarp * 32) {
     for (int t = 0; t < 2; ++t) {
@@ -551,6 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ms->p_head[t]), 4);
       mbar_init(smem_u32(&ms->p_full[t]), 4);
       mbar_init(smem_u32(&ms->o_full[t]), 1);
+      mbar_init(smem_u32(&ms->o_free[t]), 4);
+      mbar_init(smem_u32(&ms->q_empty[t]), 1);
+      mbar_init(smem_u32(&ms->job_full[t]), 1);
+      mbar_init(smem_u32(&ms->job_empty[t]), kJobReaders);
       mbar_init(smem_u32(&ms->turn[t]), 1);
     }
     mbar_init(smem_u32(&ms->v_last), 1);
@@ -565,25 +658,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (warp == kFirstSoftmaxWarp) find_work(p, rank, blockIdx.x == 0, ms);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
-  const Range r = key_range(p, ms, split);  // empty when the block has no queries
   if (warp >= kFirstSoftmaxWarp) {
     setmaxnreg_inc<kSoftmaxRegs>();
-    const int t = (warp - kFirstSoftmaxWarp) >> 2;
-    if (ms->nq > t * kTile) run_softmax(p, ms, tmem, r, head, split, t);
+    run_softmax(p, ms, tmem, (warp - kFirstSoftmaxWarp) >> 2);
   } else {
     setmaxnreg_dec<kOtherRegs>();
-    if (warp == kProducerWarp) {
-      if (lane == 0) run_producer(p, maps, ms, sbase, r, head);
-    } else if (warp == kCleanerWarp) {
-      run_cleaner(p, ms, smem, r);
-    } else {
-      run_mma(p, ms, sbase, tmem, r, warp - kMmaWarp);
-    }
+    if (warp == kProducerWarp)
+      run_producer(p, maps, ms, sbase);
+    else if (warp == kCleanerWarp)
+      run_cleaner(p, ms, smem);
+    else
+      run_mma(p, ms, sbase, tmem, warp - kMmaWarp);
   }
   __syncwarp();
   tc_fence_before();
@@ -593,6 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
+    // The last block leaves the counters zero for the workspace's next call.
+    if (lane == 0 && atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
+      p.sched[0] = 0;
+      p.sched[1] = 0;
+    }
   }
 }
 
@@ -605,8 +699,9 @@ cudaError_t prefill_prepare() {
 }
 
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream) {
-  const int64_t grid = static_cast<int64_t>(p.tiles) * p.heads * p.splits;
-  if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.heads * p.splits;
+  if (jobs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  const int64_t grid = jobs < p.num_sms ? jobs : p.num_sms;
   return launch_dependent(prefill_kernel, static_cast<unsigned>(grid), kThreads, kSmemBytes, stream,
                           maps, p);
 }

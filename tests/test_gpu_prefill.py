@@ -277,3 +277,18 @@ def test_binding_refusals():
     with pytest.raises(binding.MlaError):                            # one tensor for all heads: stride 0
         c.v = c.v[:, :1].expand(-1, 2, -1)
         c.run()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("sms", [1, 2, 7])
+def test_a_block_works_through_many_jobs(sms, causal):
+    """A plan for few SMs: each persistent block takes rows of every shape in turn, among
+    them queries that see nothing and rows that end inside a key tile."""
+    q = [5, 300, 0, 128, 129, 77, 260, 513, 2, 1, 400]
+    kv = [5, 300, 70, 500, 0, 80, 30, 513, 700, 128, 401]
+    c = Case(q, kv, heads=3, causal=causal, lead=2, tail=3, seed=sms, sms=sms)
+    for _ in range(2):                      # the second call finds the counters as the first did
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        c.run()
+        c.check()
