@@ -244,6 +244,7 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   p.splits = plan->splits;
   p.causal = causal != 0;
   p.total_kv = total_kv;
+  p.wide_out = aligned(out, 32) ? 1 : 0;
   p.stall_stream = stall_stream ? 1 : 0;
   st = launched(mla::launch_prefill(p, m, stream));
   if (st != MLA_OK || plan->splits == 1) return st;

@@ -101,6 +101,7 @@ struct PrefillParams {
   float scale;
   int32_t batch, heads, total_q, tiles, splits, causal, num_sms;
   int64_t total_kv;
+  int32_t wide_out;        // out is 32-byte aligned
   int32_t stall_stream;    // test hook: no copies are issued, so the waits run out
 };
 struct PrefillMaps {

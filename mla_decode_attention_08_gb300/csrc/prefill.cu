@@ -467,6 +467,21 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// 32 bytes of a row.  A warp's lanes write 32 different rows, one cache line each,
+// which holds up the other warps' barriers while it lasts: whole 32-byte sectors
+// take half the instructions of 16-byte pieces (which an output that is only
+// 16-byte aligned gets).
+__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t* w, int32_t wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // One job of query tile t (a warpgroup); `tiles` and `jobs` count what it has done before.
 __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, uint32_t tmem, const Job& job, int t,
                                             uint32_t& tiles, uint32_t& jobs) {
@@ -566,41 +581,39 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   const int64_t at = static_cast<int64_t>(job.q0 + qi) * p.heads + job.head;
   const int64_t part_at = static_cast<int64_t>(job.split) * p.total_q * p.heads + at;
+  uint32_t o[4][32];
+  if (n > 0) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t o[32];
-    if (n > 0) {
-      tmem_ld32(o_addr + 32 * c, o);
-      tmem_wait_ld();
-      if (c == 3) {  // the next job's products may overwrite O_t
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[t]));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = 0;
-    }
-    if (live) {
-      if (p.splits == 1) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kPrefillV + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      } else {
-        float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV + 32 * c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                               __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-      }
-    }
+    for (int c = 0; c < 4; ++c) tmem_ld32(o_addr + 32 * c, o[c]);
+    tmem_wait_ld();
+    tc_fence_before();
     __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[t]));  // the next job's products may overwrite O_t
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[c][i] = 0;
+  }
+  if (live && p.splits == 1) {
+    uint16_t* dst = p.out + at * kPrefillV;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = bf16x2(__uint_as_float(o[c][2 * i]) * inv, __uint_as_float(o[c][2 * i + 1]) * inv);
+      store_row32(dst + 32 * c, w, p.wide_out);
+      store_row32(dst + 32 * c + 16, w + 8, p.wide_out);
+    }
+  } else if (live) {
+    float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        dst[8 * c + i] = make_float4(__uint_as_float(o[c][4 * i]) * inv, __uint_as_float(o[c][4 * i + 1]) * inv,
+                                     __uint_as_float(o[c][4 * i + 2]) * inv, __uint_as_float(o[c][4 * i + 3]) * inv);
   }
   if (live) {
     const float lse = sum > 0.0f ? ref * p.scale + logf(sum) : -INFINITY;

@@ -292,3 +292,12 @@ def test_a_block_works_through_many_jobs(sms, causal):
         c.lse.fill_(7.0)
         c.run()
         c.check()
+
+
+def test_output_aligned_to_16_bytes_only():
+    c = Case([300], [300], heads=1)
+    flat = torch.full((300 * 128 + 8,), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.out = flat[8:].view(300, 1, 128)
+    assert c.out.data_ptr() % 32 == 16
+    c.run()
+    c.check()
