@@ -34,13 +34,13 @@ constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQPanels * kPanelBytes;
 constexpr int kOffMisc = kOffRing + kSlots * kPanelBytes;
 // Three warpgroups: two of softmax, one with the MMA issuers, the producer and
-// the cleaner, whose registers go to the softmax (a row of 128 scores stays in
+// the scheduler, whose registers go to the softmax (a row of 128 scores stays in
 // registers).
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
               "register split exceeds the launch allocation");
-constexpr int kMmaWarp = 0, kProducerWarp = 2, kCleanerWarp = 3, kFirstSoftmaxWarp = 4;  // issuers 0 and 1
+constexpr int kMmaWarp = 0, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;  // issuers 0 and 1
 constexpr uint32_t kLayoutSw128 = 2;
 constexpr uint32_t kColS = 0, kColO = 256;             // + 128 t
 constexpr uint32_t kTmemCols = 512;
@@ -71,6 +71,7 @@ struct Job {
 // and so are each query tile's tiles and jobs: the numbers give the phases.
 struct Misc {
   uint64_t job_full[2], job_empty[2];
+  uint64_t claim;       // the copies of a job's last tiles are due: take the next job
   uint64_t q_full[2], q_empty[2];
   // Of key tile T's K and V, T & 1: landed, and released by both issuers.
   uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];
@@ -80,14 +81,13 @@ struct Misc {
   uint64_t o_full[2];   // the job's last product of tile t complete
   uint64_t o_free[2];   // the job's O_t read out
   uint64_t turn[2];     // the other tile's products are issued
-  uint64_t v_last;      // the copies of the tile that holds the row's end are issued
   uint64_t v_clean;     // V behind the row's end is zeroed
   uint64_t mma_done;
   uint32_t tmem_base;
   volatile int32_t abort_flag;
   Job job[2];
 };
-// What reads a job: two issuers, the cleaner and eight softmax warps.
+// What reads a job: two issuers, the producer and eight softmax warps.
 constexpr uint32_t kJobReaders = 11;
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one block");
@@ -130,7 +130,7 @@ __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ int32_t tiles_256(int32_t n) { return n / kPrefillRows + (n % kPrefillRows != 0); }
 
 // The rows' blocks of 256 queries, counted over the batch: each lane of the
-// producer warp a run of consecutive rows.
+// scheduler warp a run of consecutive rows.
 struct RowRuns {
   int32_t b0, b1, first, count, total;  // rows [b0, b1), their blocks, all rows' blocks
 };
@@ -226,11 +226,17 @@ struct Loads {
   uint32_t k = 0, v = 0, q0 = 0, q1 = 0;  // copies issued: key tiles, and query tiles 0 and 1
 };
 
+// The next job is taken when this many key tiles of the present one are still to
+// be copied: late enough that no block sits on a job that another could start,
+// early enough to hide the counter and the search.
+constexpr int32_t kClaimTiles = 4;
+
 // The copies of one job (lane 0).
 __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase,
                                          const Job& job, Loads& l, uint64_t keep) {
   const uint32_t ring = sbase + kOffRing;
-  const int32_t n = job.tiles(), clean = job.partial();
+  const int32_t n = job.tiles(), claim = max(0, n - kClaimTiles);
+  if (n == 0) mbar_arrive(smem_u32(&ms->claim));
   auto load_q = [&](int t, uint32_t& count) {
     if (!wait_on(&ms->q_empty[t], (count + 1) & 1, ms, p.err)) return false;  // (the first passes)
     ++count;
@@ -244,7 +250,7 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
   for (int32_t j = 0; j < n; ++j) {
     const uint32_t T = l.k, f = T * kFillsPerTile;
     const int32_t key = job.k0 + (job.j0 + j) * kTile;
-    if (j == 0 && job.nt0 > 0 && !load_q(0, l.q0)) return false;
+    if (j == claim) mbar_arrive(smem_u32(&ms->claim));
     if (T > 1 && !wait_on(&ms->v_empty[T & 1], ((T >> 1) + 1) & 1, ms, p.err)) return false;
     uint32_t bar = smem_u32(&ms->k_full[T & 1]);
     mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
@@ -252,6 +258,7 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
     tma_load_3d(ring + ring_slot(f + 1) * kPanelBytes, &m.k_nope, 64, job.head, key, bar, keep);
     tma_load_2d(ring + ring_slot(f + 2) * kPanelBytes, &m.k_rope, 0, key, bar, keep);
     ++l.k;
+    if (j == 0 && job.nt0 > 0 && !load_q(0, l.q0)) return false;
     if (j == 0 && job.nt1 > 0 && !load_q(1, l.q1)) return false;
     if (T > 0 && !wait_on(&ms->k_empty[(T - 1) & 1], ((T - 1) >> 1) & 1, ms, p.err)) return false;
     bar = smem_u32(&ms->v_full[T & 1]);
@@ -263,39 +270,26 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
       tma_load_3d(dst + kPanelBytes / 2, &m.v, 64, job.head, key + 64 * h, bar, keep);
     }
     ++l.v;
-    if (j == clean) mbar_arrive(smem_u32(&ms->v_last));
   }
   return true;
 }
 
-// Finds the block's jobs and loads them.  The first is the block's own, the
-// others are taken from a counter when the last copies of the job before are
-// issued, about two key tiles before its end: late enough that no block sits
-// on a job that another could start, early enough to hide the search.
 __device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase) {
   const int lane = threadIdx.x & 31;
   const uint64_t keep = l2_policy_evict_normal();
-  const RowRuns rows = count_rows(p);
   Loads l;
-  uint32_t index = blockIdx.x;
+  Job job;
   bool ok = true;
-  for (uint32_t k = 0;; ++k) {
-    Job* job = &ms->job[k & 1];
-    ok = warp_wait_on(&ms->job_empty[k & 1], ((k >> 1) + 1) & 1, ms, p.err);  // (the first two pass)
-    if (!ok) break;
-    find_job(p, rows, index, job);
-    const Job mine = *job;
-    if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
-    if (mine.live == 0) break;
-    if (!p.stall_stream) {
-      if (lane == 0) ok = load_job(p, m, ms, sbase, mine, l, keep);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    if (lane == 0) {
+      if (p.stall_stream)
+        mbar_arrive(smem_u32(&ms->claim));
+      else
+        ok = load_job(p, m, ms, sbase, job, l, keep);
     }
-    if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
-    index = __shfl_sync(0xffffffffu, index, 0);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
   }
-  if (ok && !ms->abort_flag) return;  // the issuers wait for every copy
+  if (!ms->abort_flag) return;  // the issuers wait for every copy
   // Abandoned: the copies in flight land before the block's memory is given up.
   if (lane == 0) {
     if (l.q0 > 0) drain(&ms->q_full[0], (l.q0 - 1) & 1);
@@ -306,34 +300,43 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
   __syncwarp();
 }
 
-// ------------------------------------------------------------ V behind the row's end (one warp)
+// ------------------------------------------------------------ scheduler (one warp)
+// The first job is the block's own, the others are taken from a counter.
+__device__ __forceinline__ void run_scheduler(const PrefillParams& p, Misc* ms) {
+  const int lane = threadIdx.x & 31;
+  const RowRuns rows = count_rows(p);
+  uint32_t index = blockIdx.x;
+  for (uint32_t k = 0;; ++k) {
+    Job* job = &ms->job[k & 1];
+    if (!warp_wait_on(&ms->job_empty[k & 1], ((k >> 1) + 1) & 1, ms, p.err)) return;  // (the first two pass)
+    find_job(p, rows, index, job);
+    const int32_t live = job->live;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
+    if (live == 0 || !warp_wait_on(&ms->claim, k & 1, ms, p.err)) return;
+    if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
+    index = __shfl_sync(0xffffffffu, index, 0);
+  }
+}
+
+// ------------------------------------------------------------ V behind the row's end
 // The row's last key tile may end inside the tile.  The rows of V behind it are
 // another row's, or never written: their probabilities are zero, but zero times
-// NaN is NaN, so they are zeroed in shared memory before the product reads them.
-__device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, uint8_t* smem) {
+// NaN is NaN, so issuer 0 zeroes them in shared memory (while the tile's softmax
+// runs) before either product reads them.
+__device__ __forceinline__ void clean_v(Misc* ms, uint8_t* smem, uint32_t T, int32_t keys) {
   const int lane = threadIdx.x & 31;
-  uint32_t base = 0, cleans = 0;
-  Job job;
-  for (uint32_t k = 0; next_job(p, ms, k, job); ++k) {
-    const int32_t j = job.partial();
-    const uint32_t T = base + j, f = T * kFillsPerTile + kKPanels;
-    base += job.tiles();
-    if (j < 0) continue;
-    // (a barrier can be waited on for its fill T / 2 once that is under way)
-    if (!warp_wait_on(&ms->v_last, cleans & 1, ms, p.err) ||
-        !warp_wait_on(&ms->v_full[T & 1], (T >> 1) & 1, ms, p.err))
-      return;
-    ++cleans;
-    for (int32_t i = (job.len % kTile) * 16 + lane; i < kTile * 16; i += 32) {
-      const int32_t key = i >> 4, piece = i & 15;
-      *reinterpret_cast<uint4*>(smem + kOffRing + ring_slot(f + (key >> 6)) * kPanelBytes +
-                                (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
-          make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
+  const uint32_t f = T * kFillsPerTile + kKPanels;
+#pragma unroll 1
+  for (int32_t i = keys * 16 + lane; i < kTile * 16; i += 32) {
+    const int32_t key = i >> 4, piece = i & 15;
+    *reinterpret_cast<uint4*>(smem + kOffRing + ring_slot(f + (key >> 6)) * kPanelBytes +
+                              (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
+        make_uint4(0, 0, 0, 0);
   }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
 }
 
 // ------------------------------------------------------------ MMA issuers (a warp a tile, an elected lane issues)
@@ -344,7 +347,8 @@ __device__ __forceinline__ void run_cleaner(const PrefillParams& p, Misc* ms, ui
 // own issuer, which waits for what its next products need while the other
 // tile's run, and they take turns: P_t(j) . V(j) and Q_t . K(j + 1)^T are issued
 // together, the turn handed over a few products before their end.
-__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int t) {
+__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_t* smem, uint32_t sbase,
+                                        uint32_t tmem, int t) {
   const uint64_t q_desc = smem_desc(sbase + kOffQ + t * kQPanels * kPanelBytes, 1024, 1024, kLayoutSw128);
   const uint64_t k_desc = smem_desc(sbase + kOffRing, 1024, 1024, kLayoutSw128);
   const uint64_t v_desc = smem_desc(sbase + kOffRing, kPanelBytes / 2, 1024, kLayoutSw128);
@@ -388,8 +392,12 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
     __syncwarp();
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
       const bool here = j < nt, next = j + 1 < nt;
-      ok = on(&ms->v_full[T & 1], T >> 1) && (j != clean || on(&ms->v_clean, cleans)) &&
-           (j != 0 || nt == 0 || on(&ms->o_free[t], jobs + 1)) && on(&ms->turn[t], ++turns) &&
+      ok = on(&ms->v_full[T & 1], T >> 1);
+      if (ok && j == clean) {
+        if (t == 0) clean_v(ms, smem, T, job.len % kTile);
+        ok = t == 0 || on(&ms->v_clean, cleans);
+      }
+      ok = ok && (j != 0 || nt == 0 || on(&ms->o_free[t], jobs + 1)) && on(&ms->turn[t], ++turns) &&
            (!here || on(&ms->p_head[t], mine));
       if (!ok) break;
       tc_fence_after();
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ms->job_empty[t]), kJobReaders);
       mbar_init(smem_u32(&ms->turn[t]), 1);
     }
-    mbar_init(smem_u32(&ms->v_last), 1);
+    mbar_init(smem_u32(&ms->claim), 1);
     mbar_init(smem_u32(&ms->v_clean), 1);
     mbar_init(smem_u32(&ms->mma_done), 2);
     ms->abort_flag = 0;
@@ -682,10 +690,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_dec<kOtherRegs>();
     if (warp == kProducerWarp)
       run_producer(p, maps, ms, sbase);
-    else if (warp == kCleanerWarp)
-      run_cleaner(p, ms, smem);
+    else if (warp == kSchedulerWarp)
+      run_scheduler(p, ms);
     else
-      run_mma(p, ms, sbase, tmem, warp - kMmaWarp);
+      run_mma(p, ms, smem, sbase, tmem, warp - kMmaWarp);
   }
   __syncwarp();
   tc_fence_before();
