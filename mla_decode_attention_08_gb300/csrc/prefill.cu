@@ -129,27 +129,62 @@ __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
 
 __device__ __forceinline__ int32_t tiles_256(int32_t n) { return n / kPrefillRows + (n % kPrefillRows != 0); }
 
-// The rows' blocks of 256 queries, counted over the batch: each lane of the
-// scheduler warp a run of consecutive rows.
-struct RowRuns {
-  int32_t b0, b1, first, count, total;  // rows [b0, b1), their blocks, all rows' blocks
+// A row, its queries in `blocks` of up to 256.
+struct Row {
+  int32_t qs, n, ks, len, blocks;
+  // Key tiles that block i's last query reaches.
+  __device__ __forceinline__ int32_t tiles(bool causal, int32_t last) const {
+    const int32_t keys = causal ? max(0, min(len, len - n + 1 + last)) : len;
+    return keys / kTile + (keys % kTile != 0);
+  }
+  __device__ __forceinline__ int32_t block_tiles(bool causal, int32_t i) const {
+    return tiles(causal, min(n, (i + 1) * kPrefillRows) - 1);
+  }
+  // Blocks with at least c key tiles: the row's last ones.
+  __device__ __forceinline__ int32_t at_least(bool causal, int32_t c) const {
+    if (c <= 0 || blocks == 0) return blocks;
+    if (block_tiles(causal, blocks - 1) < c) return 0;
+    if (!causal) return blocks;
+    // the first block whose last query, counted (i + 1) * 256, sees a key of tile c - 1
+    const int32_t need = (c - 1) * kTile + 1 - (len - n);
+    const int32_t first = need <= 0 ? 0 : (need + kPrefillRows - 1) / kPrefillRows - 1;
+    return blocks - min(first, blocks - 1);
+  }
 };
-__device__ __forceinline__ int32_t row_blocks(const PrefillParams& p, int32_t b, bool report) {
+__device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool report) {
+  Row r = {0, 0, 0, 0, 0};
+  if (b >= p.batch) return r;
   const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
   const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
   const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || ke < ks || ke > p.total_kv;
   if (report && (bad_q || bad_k))
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
-  return bad_q || bad_k ? 0 : tiles_256(qe - qs);
+  if (!bad_q && !bad_k) r = Row{qs, qe - qs, ks, ke - ks, tiles_256(qe - qs)};
+  return r;
 }
-__device__ __forceinline__ RowRuns count_rows(const PrefillParams& p) {
+
+// The batch as the scheduler warp holds it.  Up to 32 rows: a row a lane, and the
+// blocks of queries are handed out by falling number of key tiles, so that the
+// last jobs to start are the short ones.  (12 prompts of up to 2047 tokens: the
+// blocks of an SM ended between 86 and 102 us in plain order.)  More rows: a run
+// of consecutive rows a lane, and blocks from the batch's last one on, which with
+// causal rows starts a row's long jobs first; that many rows even out.
+struct Batch {
+  Row row;
+  int32_t b0, b1, first, count, total;
+};
+__device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
   const int lane = threadIdx.x & 31;
   const int32_t run = (p.batch + 31) / 32;
-  RowRuns r;
+  Batch r;
   r.b0 = min(p.batch, lane * run);
   r.b1 = min(p.batch, r.b0 + run);
   r.count = 0;
-  for (int32_t b = r.b0; b < r.b1; ++b) r.count += row_blocks(p, b, blockIdx.x == 0);
+  r.row = Row{0, 0, 0, 0, 0};
+  for (int32_t b = r.b0; b < r.b1; ++b) {
+    r.row = load_row(p, b, blockIdx.x == 0);
+    r.count += r.row.blocks;
+  }
   int32_t incl = r.count;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -162,47 +197,65 @@ __device__ __forceinline__ RowRuns count_rows(const PrefillParams& p) {
 }
 
 // Job `index` into `job` (one warp).  Heads run fastest, so that the blocks at
-// work read the same keys' neighbourhood for all heads and it stays in L2; the
-// blocks of queries are handed out from the last one, so that with causal rows
-// the long jobs start first.
-__device__ __forceinline__ void find_job(const PrefillParams& p, const RowRuns& r, uint32_t index, Job* job) {
-  const uint32_t rest = index / p.heads, rank = rest / p.splits;
-  const int32_t target = r.total - 1 - static_cast<int32_t>(min(rank, 0x7FFFFFFFu));
-  if (target < 0) {
-    if ((threadIdx.x & 31) == 0) {
-      job->live = job->nq = job->nt0 = job->nt1 = 0;
+// work read the same keys' neighbourhood for all heads and it stays in L2.
+__device__ __forceinline__ void find_job(const PrefillParams& p, const Batch& r, uint32_t index, Job* job) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t rest = index / p.heads, order = rest / p.splits;
+  const bool causal = p.causal != 0;
+  if (order >= static_cast<uint32_t>(r.total)) {
+    if (lane == 0) job->live = job->nq = job->nt0 = job->nt1 = 0;
+    __syncwarp();
+    return;
+  }
+  const int32_t rank = static_cast<int32_t>(order);
+  Row row = r.row;
+  int32_t block = -1;  // of `row`, in the lane that has it
+  if (p.batch <= 32) {
+    int32_t lo = 0;  // the largest c with more than `rank` blocks of at least c tiles
+    int32_t hi = __reduce_max_sync(0xffffffffu, row.blocks > 0 ? row.block_tiles(causal, row.blocks - 1) : 0) + 1;
+    while (hi - lo > 1) {
+      const int32_t mid = lo + (hi - lo) / 2;
+      if (__reduce_add_sync(0xffffffffu, row.at_least(causal, mid)) > rank)
+        lo = mid;
+      else
+        hi = mid;
     }
-  } else if (target >= r.first && target < r.first + r.count) {
-    int32_t i = target - r.first;
-    for (int32_t b = r.b0; b < r.b1; ++b) {
-      const int32_t blocks = row_blocks(p, b, false);
-      if (i >= blocks) {
-        i -= blocks;
-        continue;
+    const int32_t longer = row.at_least(causal, lo + 1), same = row.at_least(causal, lo) - longer;
+    int32_t incl = same;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    const int32_t k = rank - __reduce_add_sync(0xffffffffu, longer) - (incl - same);
+    if (k >= 0 && k < same) block = row.blocks - longer - 1 - k;
+  } else {
+    int32_t i = r.total - 1 - rank - r.first;
+    if (i >= 0 && i < r.count) {
+      for (int32_t b = r.b0; b < r.b1; ++b) {
+        row = load_row(p, b, false);
+        if (i < row.blocks) break;
+        i -= row.blocks;
       }
-      const int32_t qs = __ldg(p.qo_indptr + b), n = __ldg(p.qo_indptr + b + 1) - qs;
-      const int32_t ks = __ldg(p.kv_indptr + b), len = __ldg(p.kv_indptr + b + 1) - ks;
-      const int32_t i0 = i * kPrefillRows, nq = min(kPrefillRows, n - i0), see = len - n + i0 + 1;
-      auto tiles = [&](int32_t last) {  // key tiles up to the job's query `last`
-        const int32_t keys = p.causal ? max(0, min(len, see + last)) : len;
-        return keys / kTile + (keys % kTile != 0);
-      };
-      const int32_t split = static_cast<int32_t>(rest % p.splits);
-      const int32_t all = tiles(nq - 1), share = (all + p.splits - 1) / p.splits;
-      const int32_t j0 = min(all, split * share), j1 = min(all, j0 + share);
-      job->q0 = qs + i0;
-      job->nq = nq;
-      job->k0 = ks;
-      job->len = len;
-      job->see = see;
-      job->head = static_cast<int32_t>(index % p.heads);
-      job->split = split;
-      job->j0 = j0;
-      job->nt0 = max(0, min(j1, tiles(min(nq, kTile) - 1)) - j0);
-      job->nt1 = nq > kTile ? j1 - j0 : 0;
-      job->live = 1;
-      break;
+      block = i;
     }
+  }
+  if (block >= 0) {
+    const int32_t i0 = block * kPrefillRows, nq = min(kPrefillRows, row.n - i0);
+    const int32_t split = static_cast<int32_t>(rest % p.splits);
+    const int32_t all = row.block_tiles(causal, block), share = (all + p.splits - 1) / p.splits;
+    const int32_t j0 = min(all, split * share), j1 = min(all, j0 + share);
+    job->q0 = row.qs + i0;
+    job->nq = nq;
+    job->k0 = row.ks;
+    job->len = row.len;
+    job->see = row.len - row.n + i0 + 1;
+    job->head = static_cast<int32_t>(index % p.heads);
+    job->split = split;
+    job->j0 = j0;
+    job->nt0 = max(0, min(j1, row.tiles(causal, i0 + min(nq, kTile) - 1)) - j0);
+    job->nt1 = nq > kTile ? j1 - j0 : 0;
+    job->live = 1;
   }
   __syncwarp();
 }
@@ -304,7 +357,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
 // The first job is the block's own, the others are taken from a counter.
 __device__ __forceinline__ void run_scheduler(const PrefillParams& p, Misc* ms) {
   const int lane = threadIdx.x & 31;
-  const RowRuns rows = count_rows(p);
+  const Batch rows = count_rows(p);
   uint32_t index = blockIdx.x;
   for (uint32_t k = 0;; ++k) {
     Job* job = &ms->job[k & 1];
@@ -359,13 +412,14 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
   // A wait of this warp; tile 0 starts, so its first turn is the phase before the first.
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
   uint32_t turns = t, T = 0, mine = 0, jobs = 0, cleans = 0;
+  bool duo = false;  // both tiles have keys: they take turns
   // S_t = Q_t . K(T)^T (one lane), handing over the turn four products before its end
   auto qk = [&](uint32_t tile, bool last) {
     const uint32_t f = tile * kFillsPerTile;
 #pragma unroll
     for (int c = 0; c < kKPanels; ++c) {
       const uint64_t a = q_desc + c * kPanel, b = k_desc + ring_slot(f + c) * kPanel;
-      if (c == kKPanels - 1) mbar_arrive(other_turn);
+      if (c == kKPanels - 1 && duo) mbar_arrive(other_turn);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) umma_f16(d_s, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
     }
@@ -378,7 +432,9 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t nt = t ? job.nt1 : job.nt0, n = job.tiles(), clean = job.partial();
     if (n == 0) continue;
-    ok = (nt == 0 || on(&ms->q_full[t], jobs)) && on(&ms->k_full[T & 1], T >> 1) && on(&ms->turn[t], ++turns);
+    duo = job.nt0 > 0 && job.nt1 > 0;
+    ok = (nt == 0 || on(&ms->q_full[t], jobs)) && on(&ms->k_full[T & 1], T >> 1) &&
+         (!duo || on(&ms->turn[t], ++turns));
     if (!ok) break;
     tc_fence_after();
     if (elect_one()) {
@@ -386,7 +442,6 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
         qk(T, nt == 1);
       } else {  // the other tile alone reads this K
         mbar_arrive(smem_u32(&ms->k_empty[T & 1]));
-        mbar_arrive(other_turn);
       }
     }
     __syncwarp();
@@ -397,7 +452,7 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
         if (t == 0) clean_v(ms, smem, T, job.len % kTile);
         ok = t == 0 || on(&ms->v_clean, cleans);
       }
-      ok = ok && (j != 0 || nt == 0 || on(&ms->o_free[t], jobs + 1)) && on(&ms->turn[t], ++turns) &&
+      ok = ok && (j != 0 || nt == 0 || on(&ms->o_free[t], jobs + 1)) && (!duo || on(&ms->turn[t], ++turns)) &&
            (!here || on(&ms->p_head[t], mine));
       if (!ok) break;
       tc_fence_after();
@@ -423,7 +478,7 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
         } else {
           mbar_arrive(smem_u32(&ms->v_empty[T & 1]));
         }
-        if (!next) mbar_arrive(other_turn);
+        if (!next && duo) mbar_arrive(other_turn);
       }
       __syncwarp();
       if (j + 1 == n) continue;
@@ -589,39 +644,39 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   const int64_t at = static_cast<int64_t>(job.q0 + qi) * p.heads + job.head;
   const int64_t part_at = static_cast<int64_t>(job.split) * p.total_q * p.heads + at;
-  uint32_t o[4][32];
-  if (n > 0) {
+  // (one copy of a chunk's code: it runs once a job, and unrolled it is fetched
+  // from far away every time)
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[32];
+    if (n > 0) {
+      tmem_ld32(o_addr + 32 * c, o);
+      tmem_wait_ld();
+      if (c == 3) {  // the next job's products may overwrite O_t
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[t]));
+      }
+    } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32(o_addr + 32 * c, o[c]);
-    tmem_wait_ld();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[t]));  // the next job's products may overwrite O_t
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[c][i] = 0;
-  }
-  if (live && p.splits == 1) {
-    uint16_t* dst = p.out + at * kPrefillV;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+      for (int i = 0; i < 32; ++i) o[i] = 0;
+    }
+    if (live && p.splits == 1) {
+      uint16_t* dst = p.out + at * kPrefillV + 32 * c;
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        w[i] = bf16x2(__uint_as_float(o[c][2 * i]) * inv, __uint_as_float(o[c][2 * i + 1]) * inv);
-      store_row32(dst + 32 * c, w, p.wide_out);
-      store_row32(dst + 32 * c + 16, w + 8, p.wide_out);
-    }
-  } else if (live) {
-    float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
+        w[i] = bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+      store_row32(dst, w, p.wide_out);
+      store_row32(dst + 16, w + 8, p.wide_out);
+    } else if (live) {
+      float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV + 32 * c);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        dst[8 * c + i] = make_float4(__uint_as_float(o[c][4 * i]) * inv, __uint_as_float(o[c][4 * i + 1]) * inv,
-                                     __uint_as_float(o[c][4 * i + 2]) * inv, __uint_as_float(o[c][4 * i + 3]) * inv);
+        dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                             __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+    }
+    __syncwarp();
   }
   if (live) {
     const float lse = sum > 0.0f ? ref * p.scale + logf(sum) : -INFINITY;
