@@ -408,20 +408,23 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
   constexpr uint32_t kPanel = kPanelBytes >> 4;  // a panel, in descriptor address units
   const uint32_t other_turn = smem_u32(&ms->turn[t ^ 1]);
   const uint32_t d_s = tmem + kColS + 128 * t, d_o = tmem + kColO + 128 * t;
+  constexpr int kHandover = 1;   // products issued after the turn is handed over
   constexpr int kHeadSteps = 6;  // k-steps of 16 keys in p_head
   // A wait of this warp; tile 0 starts, so its first turn is the phase before the first.
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
   uint32_t turns = t, T = 0, mine = 0, jobs = 0, cleans = 0;
   bool duo = false;  // both tiles have keys: they take turns
   // S_t = Q_t . K(T)^T (one lane), handing over the turn four products before its end
-  auto qk = [&](uint32_t tile, bool last) {
+  auto qk = [&](uint32_t tile, bool last, bool hand_over) {
     const uint32_t f = tile * kFillsPerTile;
 #pragma unroll
     for (int c = 0; c < kKPanels; ++c) {
       const uint64_t a = q_desc + c * kPanel, b = k_desc + ring_slot(f + c) * kPanel;
-      if (c == kKPanels - 1 && duo) mbar_arrive(other_turn);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) umma_f16(d_s, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
+      for (int kk = 0; kk < 4; ++kk) {
+        if (4 * c + kk == 4 * kKPanels - kHandover && hand_over) mbar_arrive(other_turn);
+        umma_f16(d_s, a + 2 * kk, b + 2 * kk, kIdescQK, c != 0 || kk != 0);
+      }
     }
     umma_commit(smem_u32(&ms->s_full[t]));
     umma_commit(smem_u32(&ms->k_empty[tile & 1]));
@@ -433,13 +436,12 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
     const int32_t nt = t ? job.nt1 : job.nt0, n = job.tiles(), clean = job.partial();
     if (n == 0) continue;
     duo = job.nt0 > 0 && job.nt1 > 0;
-    ok = (nt == 0 || on(&ms->q_full[t], jobs)) && on(&ms->k_full[T & 1], T >> 1) &&
-         (!duo || on(&ms->turn[t], ++turns));
+    ok = (nt == 0 || on(&ms->q_full[t], jobs)) && on(&ms->k_full[T & 1], T >> 1);
     if (!ok) break;
     tc_fence_after();
     if (elect_one()) {
       if (nt > 0) {
-        qk(T, nt == 1);
+        qk(T, nt == 1, false);  // beside the other tile's last products of the job before
       } else {  // the other tile alone reads this K
         mbar_arrive(smem_u32(&ms->k_empty[T & 1]));
       }
@@ -452,6 +454,10 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
         if (t == 0) clean_v(ms, smem, T, job.len % kTile);
         ok = t == 0 || on(&ms->v_clean, cleans);
       }
+      // K(T + 1) has mostly landed too; looked at here, it costs no pause between
+      // the products.
+      const bool k_ready = ok && j + 1 < n &&
+                           __all_sync(0xffffffffu, mbar_test_wait(smem_u32(&ms->k_full[(T + 1) & 1]), ((T + 1) >> 1) & 1));
       ok = ok && (j != 0 || nt == 0 || on(&ms->o_free[t], jobs + 1)) && (!duo || on(&ms->turn[t], ++turns)) &&
            (!here || on(&ms->p_head[t], mine));
       if (!ok) break;
@@ -482,12 +488,12 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
       }
       __syncwarp();
       if (j + 1 == n) continue;
-      ok = on(&ms->k_full[(T + 1) & 1], (T + 1) >> 1);
+      ok = k_ready || on(&ms->k_full[(T + 1) & 1], (T + 1) >> 1);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
         if (next)
-          qk(T + 1, j + 2 == nt);
+          qk(T + 1, j + 2 == nt, duo);
         else
           mbar_arrive(smem_u32(&ms->k_empty[(T + 1) & 1]));
       }
