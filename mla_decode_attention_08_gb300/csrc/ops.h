@@ -46,6 +46,7 @@ struct PageMapParams {
   int64_t table_stride;
   int32_t kv_indices_len, slots_len;
   int32_t batch, max_pages, page_size, num_pages, num_free;
+  int32_t page_shift;      // set by the launch: log2 of page_size, or -1
 };
 
 struct KvAppendParams {
@@ -67,7 +68,7 @@ struct KvAppendParams {
 };
 
 cudaError_t page_map_prepare();
-cudaError_t launch_page_map(const PageMapParams& p, int32_t num_sms, cudaStream_t stream);
+cudaError_t launch_page_map(PageMapParams p, int32_t num_sms, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendParams& p, bool e4m3, bool interleaved,
                              cudaStream_t stream);
 

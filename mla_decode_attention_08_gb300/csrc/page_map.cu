@@ -1,5 +1,9 @@
 // mla_page_map: tables and maps of one step from the rows' lengths.
 //
+// Bound by latency: two trips to L2 for the lengths and a table entry, and the
+// launch; 256 rows of 8192 tokens are 8.4 MB of indices (1.3 us of traffic) in
+// 6.4 us, four short rows 3.3 us.
+//
 // The three prefix sums over rows (cached tokens after the step, new tokens,
 // new pages) are small: every block computes all of them into its shared
 // memory, so no block waits for another and one launch does the whole step.
@@ -14,9 +18,18 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kSaturated = 0x7FFFFFFFu;
+
+// t / page_size: pages are mostly a power of two long.
+__device__ __forceinline__ uint32_t page_of(const PageMapParams& p, uint32_t t) {
+  return p.page_shift >= 0 ? t >> p.page_shift : t / static_cast<uint32_t>(p.page_size);
+}
+__device__ __forceinline__ uint32_t pages_for(const PageMapParams& p, uint32_t tokens) {
+  const uint32_t n = page_of(p, tokens);
+  return n + (tokens != n * static_cast<uint32_t>(p.page_size));
+}
 
 // Saturating sums of values <= kSaturated: associative, so a prefix either is
 // exact or reads kSaturated, which no accepted total reaches.
@@ -42,14 +55,14 @@ __device__ __forceinline__ RowShape row_shape(const PageMapParams& p, int32_t b)
           static_cast<uint64_t>(static_cast<uint32_t>(len)) + static_cast<uint32_t>(add) > min(cap, static_cast<uint64_t>(kSaturated));
   r.before = r.bad ? 0u : static_cast<uint32_t>(len);
   r.total = r.bad ? 0u : static_cast<uint32_t>(len) + static_cast<uint32_t>(add);
-  r.pages_before = r.before / page + (r.before % page != 0);
-  r.pages_new = r.total / page + (r.total % page != 0) - r.pages_before;
+  r.pages_before = pages_for(p, r.before);
+  r.pages_new = pages_for(p, r.total) - r.pages_before;
   return r;
 }
 
 // The last row whose prefix is <= at (empty rows before it are passed over).
-__device__ __forceinline__ int32_t row_of(const uint32_t* prefix, int32_t batch, uint32_t at) {
-  int32_t lo = 0, hi = batch;  // prefix[lo] <= at < prefix[hi]
+__device__ __forceinline__ int32_t row_of(const uint32_t* prefix, int32_t lo, int32_t hi, uint32_t at) {
+  // prefix[lo] <= at < prefix[hi]
   while (hi - lo > 1) {
     const int32_t mid = (lo + hi) >> 1;
     if (prefix[mid] <= at) lo = mid;
@@ -66,12 +79,11 @@ struct RowView {
 
 __device__ __forceinline__ RowView view_row(const PageMapParams& p, const uint32_t* kv,
                                             const uint32_t* fresh, const uint32_t* pages, int32_t b) {
-  const uint32_t page = static_cast<uint32_t>(p.page_size);
   RowView r;
   r.kv0 = kv[b];
   r.kv1 = kv[b + 1];
   r.before = r.kv1 - r.kv0 - (fresh[b + 1] - fresh[b]);
-  r.pages_before = r.before / page + (r.before % page != 0);
+  r.pages_before = pages_for(p, r.before);
   r.need0 = pages[b];
   r.table = p.block_table + static_cast<int64_t>(b) * p.table_stride;
   return r;
@@ -184,10 +196,10 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapParams 
   for (uint32_t i = gtid; i < static_cast<uint32_t>(p.slots_len); i += gthreads) {
     int32_t slot = -1, pos = 0;
     if (i < total.fresh) {
-      const int32_t b = row_of(fresh, n, i);
+      const int32_t b = row_of(fresh, 0, n, i);
       const RowView r = view_row(p, kv, fresh, pages, b);
       const uint32_t t = r.before + (i - fresh[b]);
-      const uint32_t pg = t / page;
+      const uint32_t pg = page_of(p, t);
       const int32_t id = page_id(p, r, pg);
       pos = static_cast<int32_t>(t);
       if (id >= 0) slot = id * p.page_size + static_cast<int32_t>(t - pg * page);
@@ -197,21 +209,29 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapParams 
   }
   // New pages into the table.
   for (uint32_t i = gtid; i < total.pages; i += gthreads) {
-    const int32_t b = row_of(pages, n, i);
+    const int32_t b = row_of(pages, 0, n, i);
     const RowView r = view_row(p, kv, fresh, pages, b);
     p.block_table[static_cast<int64_t>(b) * p.table_stride + r.pages_before + (i - r.need0)] =
         __ldg(p.free_pages + i);
   }
   // The index of every cached token, four at a time: each block a contiguous
-  // share, so that a warp's searches and table entries fall together.
+  // share, whose rows are found first, so that a thread searches among those.
   const uint32_t units = total.kv / 4 + (total.kv % 4 != 0);
   const uint32_t share = (units + gridDim.x - 1) / gridDim.x;
-  const uint32_t u1 = min(units, (blockIdx.x + 1) * share);
-  for (uint32_t u = blockIdx.x * share + tid; u < u1; u += kThreads) {
+  const uint32_t u0 = min(units, blockIdx.x * share), u1 = min(units, u0 + share);
+  __shared__ int32_t ends[2];
+  int32_t first_row = 0, last_row = n - 1;
+  if (gridDim.x > 1) {
+    if (u0 < u1 && tid < 2) ends[tid] = row_of(kv, 0, n, tid == 0 ? 4 * u0 : min(total.kv, 4 * u1) - 1);
+    __syncthreads();
+    first_row = ends[0];
+    last_row = ends[1];
+  }
+  for (uint32_t u = u0 + tid; u < u1; u += kThreads) {
     uint32_t t = 4 * u;
-    int32_t b = row_of(kv, n, t);
+    int32_t b = row_of(kv, first_row, last_row + 1, t);
     RowView r = view_row(p, kv, fresh, pages, b);
-    uint32_t j = t - r.kv0, pg = j / page, off = j - pg * page;
+    uint32_t j = t - r.kv0, pg = page_of(p, j), off = j - pg * page;
     int32_t id = page_id(p, r, pg);
     int32_t v[4];
 #pragma unroll
@@ -250,9 +270,14 @@ cudaError_t page_map_prepare() {
                               static_cast<int>(smem_of(MLA_MAX_MAP_ROWS)));
 }
 
-cudaError_t launch_page_map(const PageMapParams& p, int32_t num_sms, cudaStream_t stream) {
-  // One block for every 2048 entries that the outputs have room for, at most
-  // two an SM: each repeats the prefix sums, so more blocks only add those.
+cudaError_t launch_page_map(PageMapParams p, int32_t num_sms, cudaStream_t stream) {
+  p.page_shift = -1;
+  for (int32_t k = 0; k < 31; ++k)
+    if (p.page_size == 1 << k) p.page_shift = k;
+  // One block for every 1024 indices and 256 slots that the outputs have room for,
+  // at most two an SM: each repeats the prefix sums, so more blocks only add
+  // those (256 rows of 8192 tokens: 6.4 us with two blocks an SM, 7.4 with four;
+  // blocks of 512 threads 7.7, and 3.9 against 3.3 us for four short rows).
   const int64_t room = static_cast<int64_t>(p.kv_indices_len) / 4 + p.slots_len;
   int64_t blocks = (room + kThreads - 1) / kThreads;
   if (blocks > 2 * num_sms) blocks = 2 * num_sms;
