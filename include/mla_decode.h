@@ -498,7 +498,9 @@ mla_status_t mla_page_map(const int32_t* kv_lens, const int32_t* new_lens, int32
  * All in float32, rounded once.  A negative slot marks a padding token: nothing
  * is written for it, neither its queries nor its latent_out row.  A slot outside
  * the pool (MLA_DERR_KV_INDEX) or a position outside the table
- * (MLA_DERR_POSITION) skips its token the same way.  Inputs must be finite.
+ * (MLA_DERR_POSITION) skips its token the same way.  Inputs must be finite, the
+ * latent's magnitudes below 2^59 (its squares are summed in float32); eps may be
+ * 0 for rows that are not all zero.
  * Slots must be distinct: of two tokens with one slot, each 8- or 16-byte piece
  * of the cache row comes from either.
  *   kv_bf16     device bf16, token t at kv_bf16 + t * kv_stride (>= 576).
@@ -562,14 +564,17 @@ mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const 
  *           once.  Calls sharing a workspace must not overlap on the GPU.
  * Base pointers are 16-byte aligned; strides are in elements, multiples of 8, at
  * least the row's dims, below 2^36 (tokens or heads outermost; the stride of a
- * single token or head is not used).  Values of the rows' own tokens must be finite; what lies outside
+ * single token or head is not used).  Values of the rows' own tokens and their scores must be finite; what lies outside
  * the rows (padding, other rows' tokens) may hold anything.  No output may
- * overlap an input.  Rows outside total_q or total_kv set MLA_DERR_QO_INDPTR /
- * MLA_DERR_KV_INDPTR and are not written.  Deterministic for a given plan.
+ * overlap an input.  Rows outside total_q or total_kv, or with more than
+ * MLA_PREFILL_MAX_ROW_KEYS keys, set MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and
+ * are not written.  Deterministic for a given plan.
  */
 #define MLA_PREFILL_QK_DIM 192
 #define MLA_PREFILL_NOPE_DIM 128
 #define MLA_PREFILL_V_DIM 128
+#define MLA_PREFILL_MAX_ROWS 65536
+#define MLA_PREFILL_MAX_ROW_KEYS (1 << 25) /* half a second of one block's work: the waits are bounded */
 typedef struct {
   int32_t batch;       /* rows                                                        */
   int32_t total_q;     /* query tokens that q and out have room for (0 allowed)        */
@@ -585,7 +590,7 @@ typedef struct {
   uint64_t ws_partial_offset; /* float[splits][total_q][num_heads][128] when splits > 1 */
 } mla_prefill_plan_t;
 
-/* Pure host.  batch 1 .. 2^20, total_q and max_kv_len >= 0; num_sms <= 0 asks the device. */
+/* Pure host.  batch 1 .. MLA_PREFILL_MAX_ROWS, total_q and max_kv_len >= 0; num_sms <= 0 asks the device. */
 mla_status_t mla_prefill_plan(int32_t batch, int32_t total_q, int32_t max_kv_len,
                               int32_t num_heads, int32_t num_sms, mla_prefill_plan_t* plan);
 

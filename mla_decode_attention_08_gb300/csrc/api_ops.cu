@@ -185,7 +185,7 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
                          bool stall_stream) {
   mla_prefill_plan_t want;
   if (plan == nullptr || plan->abi_version != MLA_ABI_VERSION || plan->batch < 1 ||
-      plan->batch > (1 << 20) || plan->total_q < 0 || plan->max_kv_len < 0 || plan->num_heads < 1 ||
+      plan->batch > MLA_PREFILL_MAX_ROWS || plan->total_q < 0 || plan->max_kv_len < 0 || plan->num_heads < 1 ||
       plan->num_heads > 1024 || plan->num_sms < 1 ||
       !plan_fields(plan->batch, plan->total_q, plan->max_kv_len, plan->num_heads, plan->num_sms, &want) ||
       std::memcmp(&want, plan, sizeof(want)) != 0)
@@ -256,9 +256,12 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   g.rows = static_cast<int64_t>(plan->total_q) * heads;
   g.pieces = plan->splits;
   g.dim = mla::kPrefillV;
-  g.indptr = qo_indptr;
+  g.qo_indptr = qo_indptr;
+  g.kv_indptr = kv_indptr;
+  g.total_kv = total_kv;
   g.batch = plan->batch;
   g.heads = heads;
+  g.total_q = plan->total_q;
   return launched(mla::launch_attn_merge(g, true, stream));
 }
 
@@ -350,7 +353,7 @@ mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const 
 
 mla_status_t mla_prefill_plan(int32_t batch, int32_t total_q, int32_t max_kv_len,
                               int32_t num_heads, int32_t num_sms, mla_prefill_plan_t* plan) {
-  if (plan == nullptr || batch < 1 || batch > (1 << 20) || total_q < 0 || max_kv_len < 0 ||
+  if (plan == nullptr || batch < 1 || batch > MLA_PREFILL_MAX_ROWS || total_q < 0 || max_kv_len < 0 ||
       num_heads < 1 || num_heads > 1024)
     return MLA_ERR_INVALID_ARG;
   if (num_sms <= 0) {
@@ -411,8 +414,9 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
   p.rows = rows;
   p.pieces = num_parts;
   p.dim = dim;
-  p.indptr = nullptr;
-  p.batch = p.heads = 0;
+  p.qo_indptr = p.kv_indptr = nullptr;
+  p.total_kv = 0;
+  p.batch = p.heads = p.total_q = 0;
   return launched(mla::launch_attn_merge(p, false, stream));
 }
 

@@ -47,6 +47,21 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
+// Whether `token` is one that mla_prefill_fwd has computed: it belongs to a row,
+// and the row's tokens and keys lie in their tensors.  (A batch whose keys are
+// split has few rows.)
+__device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
+  for (int32_t b = 0; b < p.batch; ++b) {
+    const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
+    if (token < qs || token >= qe) continue;
+    const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
+    if (qs >= 0 && qe <= p.total_q && ks >= 0 && ke >= ks && ke <= p.total_kv &&
+        ke - ks <= MLA_PREFILL_MAX_ROW_KEYS)
+      return true;
+  }
+  return false;
+}
+
 // The first pieces' values are loaded beside the log-sum-exps, before it is known
 // which of them count: one trip to memory instead of two.  Four pieces of 16384 x
 // 16 rows of 128: 67 -> 55 us, 6.1 TB/s of a measured 6.7.
@@ -59,10 +74,7 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
   pdl_wait_primary();
   pdl_launch_dependents();
   if (row >= p.rows) return;
-  if (p.indptr != nullptr) {
-    const int64_t lo = __ldg(p.indptr), hi = __ldg(p.indptr + p.batch);
-    if (row < lo * p.heads || row >= hi * p.heads) return;
-  }
+  if (p.qo_indptr != nullptr && !in_a_row(p, row / p.heads)) return;
   const float* lses = p.lses + row;
   Piece<kF32> x[kGroup];
 #pragma unroll

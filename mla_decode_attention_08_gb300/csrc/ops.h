@@ -74,8 +74,8 @@ cudaError_t launch_kv_append(const KvAppendParams& p, bool e4m3, bool interleave
 
 // Joins `pieces` outputs [pieces][rows][dim] by their log-sum-exps
 // [pieces][rows].  bf16 pieces (the public operator) or float ones (the split
-// of mla_prefill_fwd, whose rows in use are tokens [indptr[0], indptr[batch])
-// of `heads` rows each; other rows are left alone).
+// of mla_prefill_fwd, a row for each token and head; tokens that it has not
+// computed are left alone).
 struct MergeParams {
   const void* parts;
   const float* lses;
@@ -83,8 +83,10 @@ struct MergeParams {
   float* lse_out;          // or null
   int64_t rows;
   int32_t pieces, dim;
-  const int32_t* indptr;   // or null: every row
-  int32_t batch, heads;
+  const int32_t* qo_indptr;  // or null: every row
+  const int32_t* kv_indptr;
+  int64_t total_kv;
+  int32_t batch, heads, total_q;
 };
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
 

@@ -156,7 +156,8 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
   if (b >= p.batch) return r;
   const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
   const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
-  const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || ke < ks || ke > p.total_kv;
+  const bool bad_q = qs < 0 || qe < qs || qe > p.total_q;
+  const bool bad_k = ks < 0 || ke < ks || ke > p.total_kv || ke - ks > MLA_PREFILL_MAX_ROW_KEYS;
   if (report && (bad_q || bad_k))
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
   if (!bad_q && !bad_k) r = Row{qs, qe - qs, ks, ke - ks, tiles_256(qe - qs)};
@@ -172,6 +173,10 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 struct Batch {
   Row row;
   int32_t b0, b1, first, count, total;
+  // More than 32 rows: the row before which the lane's search stands, and the
+  // blocks of its run before that row.  A block's jobs come in falling order, so
+  // the search only moves back.
+  int32_t at, before;
 };
 __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
   const int lane = threadIdx.x & 31;
@@ -192,13 +197,15 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     if (lane >= d) incl += v;
   }
   r.first = incl - r.count;
+  r.at = r.b1;
+  r.before = r.count;
   r.total = __shfl_sync(0xffffffffu, incl, 31);
   return r;
 }
 
 // Job `index` into `job` (one warp).  Heads run fastest, so that the blocks at
 // work read the same keys' neighbourhood for all heads and it stays in L2.
-__device__ __forceinline__ void find_job(const PrefillParams& p, const Batch& r, uint32_t index, Job* job) {
+__device__ __forceinline__ void find_job(const PrefillParams& p, Batch& r, uint32_t index, Job* job) {
   const int lane = threadIdx.x & 31;
   const uint32_t rest = index / p.heads, order = rest / p.splits;
   const bool causal = p.causal != 0;
@@ -230,14 +237,14 @@ __device__ __forceinline__ void find_job(const PrefillParams& p, const Batch& r,
     const int32_t k = rank - __reduce_add_sync(0xffffffffu, longer) - (incl - same);
     if (k >= 0 && k < same) block = row.blocks - longer - 1 - k;
   } else {
-    int32_t i = r.total - 1 - rank - r.first;
+    const int32_t i = r.total - 1 - rank - r.first;
     if (i >= 0 && i < r.count) {
-      for (int32_t b = r.b0; b < r.b1; ++b) {
-        row = load_row(p, b, false);
-        if (i < row.blocks) break;
-        i -= row.blocks;
+      while (i < r.before) {
+        r.row = load_row(p, --r.at, false);
+        r.before -= r.row.blocks;
       }
-      block = i;
+      row = r.row;
+      block = i - r.before;
     }
   }
   if (block >= 0) {
@@ -357,7 +364,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
 // The first job is the block's own, the others are taken from a counter.
 __device__ __forceinline__ void run_scheduler(const PrefillParams& p, Misc* ms) {
   const int lane = threadIdx.x & 31;
-  const Batch rows = count_rows(p);
+  Batch rows = count_rows(p);
   uint32_t index = blockIdx.x;
   for (uint32_t k = 0;; ++k) {
     Job* job = &ms->job[k & 1];

@@ -301,3 +301,35 @@ def test_output_aligned_to_16_bytes_only():
     assert c.out.data_ptr() % 32 == 16
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("batch,sms", [(33, 152), (40, 3), (200, 152), (1000, 152), (130, 1)])
+def test_many_rows(batch, sms):
+    """More rows than lanes of the scheduler's warp: runs of rows, walked from the last."""
+    rng = np.random.default_rng(batch)
+    q = rng.integers(0, 5, batch) * (rng.random(batch) > 0.3)
+    q[rng.integers(0, batch, 3)] = [300, 140, 1]
+    kv = q + rng.integers(0, 200, batch)
+    c = Case(q.tolist(), kv.tolist(), heads=2, seed=batch, sms=sms, lead=1, tail=1)
+    c.run()
+    c.check()
+
+
+def test_rows_outside_the_tensors_are_not_written_by_the_joining_kernel():
+    c = Case([2, 3, 4], [2000, 1500, 3000], heads=1)
+    assert c.plan.splits > 1
+    c.run()                                       # leaves parts of every row in the workspace
+    c.check()
+    c.out.fill_(7.0)
+    c.lse.fill_(7.0)
+    c.d_kv[3] = c.v.shape[0] + 1
+    c.run()
+    assert binding.mla_decode_read_error(c.ws) == KV_INDPTR
+    assert (c.out[5:] == 7.0).all() and (c.lse[5:] == 7.0).all() and (c.out[:5] != 7.0).all()
+    c.d_kv[3] = c.v.shape[0]
+    c.out.fill_(7.0)
+    c.lse.fill_(7.0)
+    c.d_qo[0] = -1
+    c.run()
+    assert binding.mla_decode_read_error(c.ws) == QO_INDPTR
+    assert (c.out[:2] == 7.0).all() and (c.lse[:2] == 7.0).all() and (c.out[2:] != 7.0).all()

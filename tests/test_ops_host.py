@@ -132,7 +132,7 @@ def test_prefill_plan(lib, batch, total, kv, heads, sms):
 
 def test_prefill_plan_refusals(lib):
     p = ctypes.byref(binding.mla_prefill_plan_t())
-    for args in [(0, 1, 1, 1), (1, -1, 1, 1), (1, 1, -1, 1), (1, 1, 1, 0), (1, 1, 1, 1025), ((1 << 20) + 1, 1, 1, 1)]:
+    for args in [(0, 1, 1, 1), (1, -1, 1, 1), (1, 1, -1, 1), (1, 1, 1, 0), (1, 1, 1, 1025), (65537, 1, 1, 1)]:
         assert lib.mla_prefill_plan(*args, 152, p) == INVALID
     assert lib.mla_prefill_plan(1, 1, 1, 1, 152, None) == INVALID
     assert lib.mla_prefill_plan(1, 2**31 - 1, 1, 1024, 152, p) == INVALID   # blocks past 2^31 - 1 are refused or fit
