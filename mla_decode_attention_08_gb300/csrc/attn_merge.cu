@@ -3,7 +3,7 @@
 //
 // With m = max_s lse_s (0 if every piece is empty) and w_s = exp(lse_s - m):
 // out = sum_s w_s part_s / sum_s w_s and lse = m + log sum_s w_s.  A thread owns
-// eight values of a row: it reads the row's few lses (the row's threads read
+// eight or 16 values of a row: it reads the row's few lses (the row's threads read
 // the same ones) and each piece once.  Bound by the bytes of the pieces.
 #include "ops.h"
 #include "ptx.cuh"
@@ -14,38 +14,43 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroup = 4;  // pieces whose loads are in flight together
 
-template <bool kF32>
-struct Piece;
-template <>
-struct Piece<false> {
-  uint4 v = {};
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
-    v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
-  }
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t w = i < 2 ? v.x : (i < 4 ? v.y : (i < 6 ? v.z : v.w));
-    return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
-  }
-};
-template <>
-struct Piece<true> {
-  float4 a = {}, b = {};
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    a = __ldcs(p);
-    b = __ldcs(p + 1);
-  }
-  __device__ __forceinline__ float get(int i) const {
-    const float4& q = i < 4 ? a : b;
-    return (i & 3) == 0 ? q.x : ((i & 3) == 1 ? q.y : ((i & 3) == 2 ? q.z : q.w));
-  }
-};
-
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// kVec consecutive values of a piece, as loaded; pair(i) are values 2 i, 2 i + 1.
+template <bool kF32, int kVec>
+struct Piece {
+  static constexpr int kWords = kF32 ? kVec : kVec / 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (kF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = __ldcs(p + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (kF32) return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    return pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+};
 
 // Whether `token` is one that mla_prefill_fwd has computed: it belongs to a row,
 // and the row's tokens and keys lie in their tensors.  (A batch whose keys are
@@ -63,27 +68,31 @@ __device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
 }
 
 // The first pieces' values are loaded beside the log-sum-exps, before it is known
-// which of them count: one trip to memory instead of two.  Four pieces of 16384 x
-// 16 rows of 128: 67 -> 55 us, 6.1 TB/s of a measured 6.7.
-template <bool kF32>
+// which of them count: one trip to memory instead of two.  Where a row is a
+// multiple of 16 long a thread takes 16 of its values, which halves what the
+// weights cost (the kernel issues on 8 of 10 cycles with eight).  Four pieces of
+// 16384 x 16 rows of 128: 67 us with eight values and the weights first, 55 with the
+// values beside them, 49.6 us with 16 (6.9 TB/s; a copy reaches 6.7).
+template <bool kF32, int kVec>
 __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams p, int32_t chunk_shift) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t chunks = static_cast<uint32_t>(p.dim) >> 3;
+  const uint32_t chunks = static_cast<uint32_t>(p.dim) / kVec;
   const int64_t row = chunk_shift >= 0 ? i >> chunk_shift : i / chunks;
-  const int dim0 = 8 * static_cast<int>(i - row * chunks);
+  const int dim0 = kVec * static_cast<int>(i - row * chunks);
   pdl_wait_primary();
   pdl_launch_dependents();
   if (row >= p.rows) return;
   if (p.qo_indptr != nullptr && !in_a_row(p, row / p.heads)) return;
   const float* lses = p.lses + row;
-  Piece<kF32> x[kGroup];
+  Piece<kF32, kVec> x[kGroup];
 #pragma unroll
   for (int k = 0; k < kGroup; ++k)
     if (k < p.pieces) x[k].load(p.parts, (k * p.rows + row) * p.dim + dim0);
   float top = -INFINITY;
   for (int s = 0; s < p.pieces; ++s) top = fmaxf(top, lses[s * p.rows]);
   if (top == -INFINITY) top = 0.0f;
-  float acc[8] = {}, sum = 0.0f;
+  uint64_t acc[kVec / 2] = {};
+  float sum = 0.0f;
   for (int s0 = 0; s0 < p.pieces; s0 += kGroup) {
     if (s0 > 0) {
 #pragma unroll
@@ -97,29 +106,41 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
       sum += w;
       // a piece of weight zero may hold anything; a NaN weight reaches the result
       if (w == 0.0f) continue;
+      const uint64_t w2 = pack2(w, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, x[k].get(e), acc[e]);
+      for (int e = 0; e < kVec / 2; ++e) acc[e] = fma2(w2, x[k].pair(e), acc[e]);
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<uint4*>(p.out + row * p.dim + dim0) =
-      make_uint4(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv),
-                 bf16x2(acc[4] * inv, acc[5] * inv), bf16x2(acc[6] * inv, acc[7] * inv));
+  uint32_t out[kVec / 2];
+#pragma unroll
+  for (int e = 0; e < kVec / 2; ++e) {
+    float lo, hi;
+    unpack2(acc[e], lo, hi);
+    out[e] = bf16x2(lo * inv, hi * inv);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.dim + dim0);
+#pragma unroll
+  for (int e = 0; e < kVec / 8; ++e) dst[e] = make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
   if (dim0 == 0 && p.lse_out != nullptr) p.lse_out[row] = top + logf(sum);
+}
+
+template <bool kF32, int kVec>
+cudaError_t launch_vec(const MergeParams& p, cudaStream_t stream) {
+  const int32_t chunks = p.dim / kVec;
+  const int64_t blocks = (p.rows * chunks + kThreads - 1) / kThreads;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  int32_t shift = -1;  // of `chunks`, where that is a power of two
+  for (int32_t k = 0; k < 8; ++k)
+    if (chunks == 1 << k) shift = k;
+  return launch_dependent(attn_merge_kernel<kF32, kVec>, static_cast<unsigned>(blocks), kThreads, 0, stream, p, shift);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream) {
-  const int64_t items = p.rows * (p.dim / 8);
-  const int64_t blocks = (items + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  const unsigned g = static_cast<unsigned>(blocks);
-  int32_t shift = -1;  // of dim / 8, where that is a power of two
-  for (int32_t k = 0; k < 8; ++k)
-    if (p.dim == 8 << k) shift = k;
-  return f32_parts ? launch_dependent(attn_merge_kernel<true>, g, kThreads, 0, stream, p, shift)
-                   : launch_dependent(attn_merge_kernel<false>, g, kThreads, 0, stream, p, shift);
+  if (f32_parts) return launch_vec<true, 8>(p, stream);
+  return p.dim % 16 == 0 ? launch_vec<false, 16>(p, stream) : launch_vec<false, 8>(p, stream);
 }
 
 }  // namespace mla
