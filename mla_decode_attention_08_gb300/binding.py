@@ -326,7 +326,8 @@ def mla_fp8_quantize_per_tensor(src_bf16, dst_fp8, scale_out, tmp, stream=None) 
 # ---------------------------------------------------------------- around the decode step
 # A step makes several of these small calls, so their host time counts: operands
 # are checked in one pass each, by the tensors' cheap accessors.
-_BF16, _F32T, _I32T = torch.bfloat16, torch.float32, torch.int32
+_Tensor, _BF16, _F32T, _I32T = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
+_E4M3_CODES = (torch.uint8, torch.float8_e4m3fn)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -344,28 +345,28 @@ def _refuse(t, name: str, dtype, dev) -> None:
 
 def _device_of(t, name: str) -> int:
     """Index of the CUDA device that a call's first operand, and so every other one, is on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         _refuse(t, name, None, None)
     return t.get_device()
 
 
 def _view_ptr(t, name: str, dtype, dev: int) -> int:
     """Address of an operand on device ``dev`` that may be strided."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
         _refuse(t, name, dtype, dev)
     return t.data_ptr()
 
 
 def _ptr(t, name: str, dtype, dev: int) -> int:
     """Address of a contiguous operand on device ``dev``."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev
+    if (not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev
             or not t.is_contiguous()):
         _refuse(t, name, dtype, dev)
     return t.data_ptr()
 
 
 def _workspace(t, dev: int) -> int:
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, "workspace", None, dev)
     return t.data_ptr()
 
@@ -461,6 +462,9 @@ def mla_page_map(kv_lens, new_lens, block_table, free_pages, qo_indptr, kv_indpt
 def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, stream, workspace,
             eps, interleaved, q_pe, q_out, latent_out):
     dev = _device_of(kv, "kv")
+    rows = cache.shape
+    if rows[-1] != QK_HEAD_DIM or len(rows) != 2 and (len(rows) != 3 or rows[1] != 1):
+        raise ValueError(f"the cache must be [rows, 576] or [rows, 1, 576], got {list(rows)}")
     p_kv = _view_ptr(kv, "kv", _BF16, dev)
     p_weight = _ptr(norm_weight, "norm_weight", _BF16, dev)
     p_table = _ptr(rope_table, "rope_table", _F32T, dev)
@@ -470,11 +474,12 @@ def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, 
     scale = () if kv_scale is None else (_ptr(kv_scale, "kv_scale", _F32T, dev),)
     p_dense = None if latent_out is None else _ptr(latent_out, "latent_out", _BF16, dev)
     p_ws = _workspace(workspace, dev)
-    if kv.dim() != 2 or kv.shape[1] != QK_HEAD_DIM:
-        raise ValueError(f"kv must be [tokens, {QK_HEAD_DIM}], got {list(kv.shape)}")
-    if rope_table.dim() != 2 or rope_table.shape[1] != ROPE_DIM:
-        raise ValueError(f"rope_table must be [positions, {ROPE_DIM}], got {list(rope_table.shape)}")
-    t = kv.shape[0]
+    shape, table = kv.shape, rope_table.shape
+    if len(shape) != 2 or shape[1] != QK_HEAD_DIM:
+        raise ValueError(f"kv must be [tokens, {QK_HEAD_DIM}], got {list(shape)}")
+    if len(table) != 2 or table[1] != ROPE_DIM:
+        raise ValueError(f"rope_table must be [positions, {ROPE_DIM}], got {list(table)}")
+    t = shape[0]
     if norm_weight.numel() != V_HEAD_DIM or positions.numel() != t or slots.numel() != t:
         raise ValueError("norm_weight must hold 512 values, positions and slots one entry a token")
     if latent_out is not None:
@@ -485,12 +490,13 @@ def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, 
         queries = (None, 0, 0, None, 0, 0, 0)
     else:
         p_q, p_out = _view_ptr(q_pe, "q_pe", _BF16, dev), _view_ptr(q_out, "q_out", _BF16, dev)
-        if q_pe.dim() != 3 or q_pe.shape[0] != t or q_pe.shape[2] != ROPE_DIM:
-            raise ValueError(f"q_pe must be [{t}, heads, {ROPE_DIM}], got {list(q_pe.shape)}")
-        _expect("q_out", q_out, q_pe.shape)
-        queries = (p_q, *_strides2("q_pe", q_pe), p_out, *_strides2("q_out", q_out), q_pe.shape[1])
-    _call(fn, dev, p_kv, _stride1("kv", kv), p_weight, eps, p_table, rope_table.shape[0],
-          1 if interleaved else 0, p_pos, p_slots, t, p_cache, *scale, cache.shape[0], p_dense,
+        shape = q_pe.shape
+        if len(shape) != 3 or shape[0] != t or shape[2] != ROPE_DIM:
+            raise ValueError(f"q_pe must be [{t}, heads, {ROPE_DIM}], got {list(shape)}")
+        _expect("q_out", q_out, shape)
+        queries = (p_q, *_strides2("q_pe", q_pe), p_out, *_strides2("q_out", q_out), shape[1])
+    _call(fn, dev, p_kv, _stride1("kv", kv), p_weight, eps, p_table, table[0],
+          1 if interleaved else 0, p_pos, p_slots, t, p_cache, *scale, rows[0], p_dense,
           *queries, p_ws, workspace.nbytes, _on(fn, stream, dev))
 
 
@@ -507,7 +513,9 @@ def mla_kv_append(kv, norm_weight, rope_table, positions, slots, kv_fp8, kv_scal
     bf16 [T, 576].  ``workspace``: STEP_WORKSPACE_BYTES, zeroed once."""
     if kv_scale is None or kv_scale.numel() != 1:
         raise ValueError("kv_scale must be one float32")
-    _append("mla_kv_append", kv, norm_weight, rope_table, positions, slots, _e4m3_cache(kv_fp8),
+    if not isinstance(kv_fp8, _Tensor) or kv_fp8.dtype not in _E4M3_CODES:
+        _e4m3_cache(kv_fp8)  # says what is wrong
+    _append("mla_kv_append", kv, norm_weight, rope_table, positions, slots, kv_fp8,
             kv_scale, stream, workspace, eps, interleaved, q_pe, q_out, latent_out)
 
 
@@ -515,10 +523,8 @@ def mla_kv_append_bf16kv(kv, norm_weight, rope_table, positions, slots, kv_bf16,
                          workspace, eps: float = 1e-6, interleaved: bool = True, q_pe=None,
                          q_out=None, latent_out=None) -> None:
     """mla_kv_append into a bf16 cache ``[rows, 576]`` (no scale)."""
-    if not isinstance(kv_bf16, torch.Tensor) or kv_bf16.dtype != torch.bfloat16:
+    if not isinstance(kv_bf16, _Tensor) or kv_bf16.dtype is not _BF16:
         raise TypeError("kv_bf16 must be a bfloat16 CUDA tensor")
-    if kv_bf16.dim() not in (2, 3) or kv_bf16.numel() != kv_bf16.shape[0] * QK_HEAD_DIM:
-        raise ValueError(f"kv_bf16 must be [rows, 576] or [rows, 1, 576], got {tuple(kv_bf16.shape)}")
     _append("mla_kv_append_bf16kv", kv, norm_weight, rope_table, positions, slots, kv_bf16, None,
             stream, workspace, eps, interleaved, q_pe, q_out, latent_out)
 
