@@ -561,7 +561,9 @@ mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const 
  *   out     device bf16 [total_q][num_heads][128], 16-byte aligned; lse device
  *           float [total_q][num_heads], or NULL.  Tokens of no row are left alone.
  *   plan, workspace  from mla_prefill_plan; workspace 256-byte aligned, zeroed
- *           once.  Calls sharing a workspace must not overlap on the GPU.
+ *           once (it holds the error word, counters that each call leaves zero,
+ *           and the parts of split keys).  Calls sharing a workspace must not
+ *           overlap on the GPU.
  * Base pointers are 16-byte aligned; strides are in elements, multiples of 8, at
  * least the row's dims, below 2^36 (tokens or heads outermost; the stride of a
  * single token or head is not used).  Values of the rows' own tokens and their scores must be finite; what lies outside

@@ -2,8 +2,10 @@
 // head (192-dim queries, keys = 128 dims of the head | 64 rotated dims shared by
 // the heads, 128-dim values).
 //
-// A block owns 256 queries of one row and head as two tiles of 128 (t = 0, 1)
-// and walks the row's keys in tiles of 128 (j):
+// Persistent blocks, one an SM, take jobs from a counter.  A job is up to 256
+// queries of one row and head as two tiles of 128 (t = 0, 1), over the row's keys
+// (or a split of them) in tiles of 128 (j):
+//   * warp 3 takes the jobs, long ones first, and finds their row,
 //   * warp 2 streams K(j) (three 64-dim panels of 128 keys) and V(j) (two panels
 //     of 64 keys x 128 dims) by TMA into a ring of eight 16 KB slots,
 //   * warps 0 and 1 issue S_t = Q_t . K(j)^T and O_t += P_t . V(j) of a tile each
@@ -14,6 +16,13 @@
 // The two tiles alternate: while the tensor cores work on one tile's products
 // the other tile's softmax runs.  K and V are read from shared memory for both
 // tiles, so a block moves 80 KB for 2 x 128 x 128 x 320 multiply-adds.
+//
+// Bound by the chain of one tile (scores 768 cycles of the tensor pipe, softmax
+// ~1250, values 512, and the looks at barriers between them) against the other
+// tile's: ~3300 cycles for a key tile of both where the pipe alone needs 2560,
+// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 776-790 us,
+// 1.75 PFLOP/s, with the SM clock at 1.78 GHz under the power limit (a plain bf16
+// product sustains 1.77 there); 12 prompts of up to 2047 tokens: 105 us.
 #include <cstddef>
 
 #include "ops.h"
@@ -406,7 +415,10 @@ __device__ __forceinline__ void clean_v(Misc* ms, uint8_t* smem, uint32_t T, int
 // cycles beside the products' own reads of shared memory.  So each tile has its
 // own issuer, which waits for what its next products need while the other
 // tile's run, and they take turns: P_t(j) . V(j) and Q_t . K(j + 1)^T are issued
-// together, the turn handed over a few products before their end.
+// together, the turn handed over one product before their end.  (A 16384-token
+// prompt: one issuer for both tiles 913 us, two without turns 1252 us, as both
+// tiles' softmax then fall together, two in turn 776 us.  A single S for both
+// tiles with one issuer for the scores and one for the values: 829 us.)
 __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_t* smem, uint32_t sbase,
                                         uint32_t tmem, int t) {
   const uint64_t q_desc = smem_desc(sbase + kOffQ + t * kQPanels * kPanelBytes, 1024, 1024, kLayoutSw128);
@@ -421,7 +433,7 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
   uint32_t turns = t, T = 0, mine = 0, jobs = 0, cleans = 0;
   bool duo = false;  // both tiles have keys: they take turns
-  // S_t = Q_t . K(T)^T (one lane), handing over the turn four products before its end
+  // S_t = Q_t . K(T)^T (one lane)
   auto qk = [&](uint32_t tile, bool last, bool hand_over) {
     const uint32_t f = tile * kFillsPerTile;
 #pragma unroll

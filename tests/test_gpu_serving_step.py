@@ -170,3 +170,27 @@ def test_expanded_and_absorbed_forms_agree():
     lat = s.decode(one, dq)[0].float()
     got = torch.einsum("hc,hdc->hd", lat, s.w_v.float())
     assert np.linalg.norm(f64(got) - f64(out)) <= 2.0 ** -4 * np.linalg.norm(f64(out))
+
+
+def test_calls_without_tokens_do_nothing():
+    bf16, dev = torch.bfloat16, "cuda"
+    s = Server(seed=3)
+    none = torch.empty(0, dtype=torch.int32, device=dev)
+    before = s.cache.clone()
+    binding.mla_kv_append(torch.empty((0, 576), dtype=bf16, device=dev), s.weight, s.rope, none, none, s.cache, s.scale,
+                          workspace=s.ws, q_pe=torch.empty((0, 16, 64), dtype=bf16, device=dev),
+                          q_out=torch.empty((0, 16, 64), dtype=bf16, device=dev))
+    assert torch.equal(s.cache, before)
+    plan = binding.mla_prefill_plan(2, 0, 100, HEADS)
+    ind = torch.zeros(3, dtype=torch.int32, device=dev)
+    empty = lambda *shape: torch.empty(shape, dtype=bf16, device=dev)  # noqa: E731
+    binding.mla_prefill_fwd(empty(0, HEADS, 192), empty(5, HEADS, 128), empty(5, 64), empty(5, HEADS, 128), ind, ind,
+                            empty(0, HEADS, 128), plan=plan, workspace=binding.new_workspace(plan))
+    # queries without any key tensor rows: zeros
+    plan = binding.mla_prefill_plan(1, 3, 0, HEADS)
+    out = torch.full((3, HEADS, 128), 7.0, dtype=bf16, device=dev)
+    binding.mla_prefill_fwd(s.rand(3, HEADS, 192).bfloat16(), empty(0, HEADS, 128), empty(0, 64), empty(0, HEADS, 128),
+                            torch.tensor([0, 3], dtype=torch.int32, device=dev), ind[:2], out, plan=plan,
+                            workspace=binding.new_workspace(plan))
+    assert (out == 0).all()
+    binding.mla_attn_merge(empty(2, 0, 128), torch.empty((2, 0), device=dev), empty(0, 128))
