@@ -125,7 +125,20 @@ __device__ __forceinline__ bool wait_on(const uint64_t* bar, uint32_t parity, Mi
 }
 // The same by a whole warp, which goes on or gives up together.
 __device__ __forceinline__ bool warp_wait_on(const uint64_t* bar, uint32_t parity, Misc* ms, int32_t* err) {
-  return __all_sync(0xffffffffu, wait_on(bar, parity, ms, err));
+  const uint32_t b = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+  const long long start = clock64();
+  for (uint32_t n = 1;; ++n) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    if ((n & 15) == 0) {
+      const bool late = clock64() - start > kWaitLimitCycles;
+      if (__any_sync(0xffffffffu, late || ms->abort_flag)) {
+        if (late && !ms->abort_flag) atomicOr(err, MLA_DERR_TIMEOUT);
+        ms->abort_flag = 1;
+        return false;
+      }
+    }
+  }
 }
 // Bounded wait while draining at the end of a call.
 __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
