@@ -162,16 +162,6 @@ struct Row {
   __device__ __forceinline__ int32_t block_tiles(bool causal, int32_t i) const {
     return tiles(causal, min(n, (i + 1) * kPrefillRows) - 1);
   }
-  // Blocks with at least c key tiles: the row's last ones.
-  __device__ __forceinline__ int32_t at_least(bool causal, int32_t c) const {
-    if (c <= 0 || blocks == 0) return blocks;
-    if (block_tiles(causal, blocks - 1) < c) return 0;
-    if (!causal) return blocks;
-    // the first block whose last query, counted (i + 1) * 256, sees a key of tile c - 1
-    const int32_t need = (c - 1) * kTile + 1 - (len - n);
-    const int32_t first = need <= 0 ? 0 : (need + kPrefillRows - 1) / kPrefillRows - 1;
-    return blocks - min(first, blocks - 1);
-  }
 };
 __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool report) {
   Row r = {0, 0, 0, 0, 0};
@@ -186,12 +176,12 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
   return r;
 }
 
-// The batch as the scheduler warp holds it.  Up to 32 rows: a row a lane, and the
-// blocks of queries are handed out by falling number of key tiles, so that the
-// last jobs to start are the short ones.  (12 prompts of up to 2047 tokens: the
-// blocks of an SM ended between 86 and 102 us in plain order.)  More rows: a run
-// of consecutive rows a lane, and blocks from the batch's last one on, which with
-// causal rows starts a row's long jobs first; that many rows even out.
+// The batch as the scheduler warp holds it.  Up to 32 rows: a row a lane, handed
+// out from the row with the most key tiles to the one with the fewest, each row's
+// blocks of queries from its last, which sees the most keys: the blocks at work at
+// one time share few rows' keys, which stay in L2, and the last jobs to start are
+// short.  More rows: a run of consecutive rows a lane, and the batch's blocks from
+// the last one on; that many rows even out.
 struct Batch {
   Row row;
   int32_t b0, b1, first, count, total;
@@ -219,6 +209,14 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     if (lane >= d) incl += v;
   }
   r.first = incl - r.count;
+  if (p.batch <= 32) {
+    const int32_t size = r.count > 0 ? r.row.block_tiles(p.causal != 0, r.count - 1) : 0;
+    r.first = 0;
+    for (int l = 0; l < 32; ++l) {
+      const int32_t other = __shfl_sync(0xffffffffu, size, l), blocks = __shfl_sync(0xffffffffu, r.count, l);
+      if (other > size || (other == size && l < lane)) r.first += blocks;
+    }
+  }
   r.at = r.b1;
   r.before = r.count;
   r.total = __shfl_sync(0xffffffffu, incl, 31);
@@ -240,24 +238,8 @@ __device__ __forceinline__ void find_job(const PrefillParams& p, Batch& r, uint3
   Row row = r.row;
   int32_t block = -1;  // of `row`, in the lane that has it
   if (p.batch <= 32) {
-    int32_t lo = 0;  // the largest c with more than `rank` blocks of at least c tiles
-    int32_t hi = __reduce_max_sync(0xffffffffu, row.blocks > 0 ? row.block_tiles(causal, row.blocks - 1) : 0) + 1;
-    while (hi - lo > 1) {
-      const int32_t mid = lo + (hi - lo) / 2;
-      if (__reduce_add_sync(0xffffffffu, row.at_least(causal, mid)) > rank)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int32_t longer = row.at_least(causal, lo + 1), same = row.at_least(causal, lo) - longer;
-    int32_t incl = same;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    const int32_t k = rank - __reduce_add_sync(0xffffffffu, longer) - (incl - same);
-    if (k >= 0 && k < same) block = row.blocks - longer - 1 - k;
+    const int32_t k = rank - r.first;
+    if (k >= 0 && k < r.count) block = r.count - 1 - k;
   } else {
     const int32_t i = r.total - 1 - rank - r.first;
     if (i >= 0 && i < r.count) {
@@ -315,7 +297,7 @@ constexpr int32_t kClaimTiles = 4;
 
 // The copies of one job (lane 0).
 __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase,
-                                         const Job& job, Loads& l, uint64_t keep) {
+                                         const Job& job, Loads& l, uint64_t keep, uint64_t once) {
   const uint32_t ring = sbase + kOffRing;
   const int32_t n = job.tiles(), claim = max(0, n - kClaimTiles);
   if (n == 0) mbar_arrive(smem_u32(&ms->claim));
@@ -326,7 +308,7 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
     mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
     for (int c = 0; c < kQPanels; ++c)
       tma_load_3d(sbase + kOffQ + (t * kQPanels + c) * kPanelBytes, &m.q, 64 * c, job.head, job.q0 + t * kTile,
-                  bar, keep);
+                  bar, once);
     return true;
   };
   for (int32_t j = 0; j < n; ++j) {
@@ -358,7 +340,7 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
 
 __device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase) {
   const int lane = threadIdx.x & 31;
-  const uint64_t keep = l2_policy_evict_normal();
+  const uint64_t keep = l2_policy_evict_normal(), once = l2_policy_evict_first();
   Loads l;
   Job job;
   bool ok = true;
@@ -367,7 +349,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
       if (p.stall_stream)
         mbar_arrive(smem_u32(&ms->claim));
       else
-        ok = load_job(p, m, ms, sbase, job, l, keep);
+        ok = load_job(p, m, ms, sbase, job, l, keep, once);
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
   }
