@@ -20,9 +20,9 @@
 // Bound by the chain of one tile (scores 768 cycles of the tensor pipe, softmax
 // ~1250, values 512, and the looks at barriers between them) against the other
 // tile's: ~3300 cycles for a key tile of both where the pipe alone needs 2560,
-// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 776-790 us,
-// 1.75 PFLOP/s, with the SM clock at 1.78 GHz under the power limit (a plain bf16
-// product sustains 1.77 there); 12 prompts of up to 2047 tokens: 105 us.
+// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 755-765 us,
+// 1.8 PFLOP/s, with the SM clock below 1.8 GHz under the power limit (a plain bf16
+// product sustains 1.77 PFLOP/s there); 12 prompts of up to 2047 tokens: 99 us.
 #include <cstddef>
 
 #include "ops.h"
@@ -123,7 +123,9 @@ __device__ __forceinline__ bool wait_on(const uint64_t* bar, uint32_t parity, Mi
   if (mbar_try_wait(b, parity)) return true;
   return wait_slow(b, parity, ms, err);
 }
-// The same by a whole warp, which goes on or gives up together.
+// The same by a whole warp, which polls and gives up together: no lane runs ahead,
+// so nothing has to be brought together again (16384-token prompt: 766 us; the
+// lanes each on their own, then a vote, 781; one lane for the warp 961).
 __device__ __forceinline__ bool warp_wait_on(const uint64_t* bar, uint32_t parity, Misc* ms, int32_t* err) {
   const uint32_t b = smem_u32(bar);
   if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
@@ -180,8 +182,10 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 // out from the row with the most key tiles to the one with the fewest, each row's
 // blocks of queries from its last, which sees the most keys: the blocks at work at
 // one time share few rows' keys, which stay in L2, and the last jobs to start are
-// short.  More rows: a run of consecutive rows a lane, and the batch's blocks from
-// the last one on; that many rows even out.
+// short.  (12 prompts of up to 2047 tokens: 99 us; blocks by falling length over
+// all rows 102 us, with 331 MB read from DRAM for 184 MB of inputs.)  More rows: a
+// run of consecutive rows a lane, and the batch's blocks from the last one on; that
+// many rows even out.
 struct Batch {
   Row row;
   int32_t b0, b1, first, count, total;
@@ -291,9 +295,12 @@ struct Loads {
 };
 
 // The next job is taken when this many key tiles of the present one are still to
-// be copied: late enough that no block sits on a job that another could start,
-// early enough to hide the counter and the search.
-constexpr int32_t kClaimTiles = 4;
+// be copied: late enough that no block sits on a job that another could start and
+// that the heads of a block of queries stay abreast, early enough to hide the
+// counter and the search, since the copies run two tiles ahead.  (76 rows of up to
+// 256 tokens: 52.3 us, with two tiles 54.1; 12 prompts of up to 2047 tokens: 99 us,
+// and 105 with the next job taken as a job starts.)
+constexpr int32_t kClaimTiles = 1;
 
 // The copies of one job (lane 0).
 __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase,
@@ -412,8 +419,8 @@ __device__ __forceinline__ void clean_v(Misc* ms, uint8_t* smem, uint32_t T, int
 // tile's run, and they take turns: P_t(j) . V(j) and Q_t . K(j + 1)^T are issued
 // together, the turn handed over one product before their end.  (A 16384-token
 // prompt: one issuer for both tiles 913 us, two without turns 1252 us, as both
-// tiles' softmax then fall together, two in turn 776 us.  A single S for both
-// tiles with one issuer for the scores and one for the values: 829 us.)
+// tiles' softmax then fall together, two in turn 776 us at that time.  A single S
+// for both tiles with one issuer for the scores and one for the values: 829 us.)
 __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_t* smem, uint32_t sbase,
                                         uint32_t tmem, int t) {
   const uint64_t q_desc = smem_desc(sbase + kOffQ + t * kQPanels * kPanelBytes, 1024, 1024, kLayoutSw128);
