@@ -17,6 +17,15 @@
 // the other tile's softmax runs.  K and V are read from shared memory for both
 // tiles, so a block moves 80 KB for 2 x 128 x 128 x 320 multiply-adds.
 //
+// When no row of the batch has more than one tile of queries, the key tiles
+// themselves alternate ("pairs" below): tile T goes to issuer and softmax T & 1,
+// each with its own S and O over the same queries, and the second accumulator is
+// joined to the first at the job's end, out of TMEM.  A tile's chain then runs
+// beside the next one's, and the keys stream at nearly the memory's rate.  (64
+// queries over 8256 keys, 16 heads: 22.6 us, one query tile on its own 25.6; 8 rows
+// of up to 64 queries over up to 4000 keys: 42.1 us and 52.5; 24 rows of up to 128
+// over up to 256: 14.4 and 17.9.)
+//
 // Bound by the chain of one tile (scores 768 cycles of the tensor pipe, softmax
 // ~1250, values 512, and the looks at barriers between them) against the other
 // tile's: ~3300 cycles for a key tile of both where the pipe alone needs 2560,
@@ -42,11 +51,17 @@ constexpr int kSlots = 8;
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQPanels * kPanelBytes;
 constexpr int kOffMisc = kOffRing + kSlots * kPanelBytes;
+// Pairs: one query tile, two buffers of K and of V, and the running maximum and
+// sum of the softmax that is joined to the other.
+constexpr int kOffPairK = kOffQ + kQPanels * kPanelBytes;
+constexpr int kOffPairV = kOffPairK + 2 * kKPanels * kPanelBytes;
+constexpr int kOffStats = kOffPairV + 2 * kVPanels * kPanelBytes;
+static_assert(kOffStats + 2 * kTile * static_cast<int>(sizeof(float2)) <= kOffMisc, "room of the pairs' layout");
 // Three warpgroups: two of softmax, one with the MMA issuers, the producer and
 // the scheduler, whose registers go to the softmax (a row of 128 scores stays in
-// registers).
+// registers; 200 and 104 take the same time).
 constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
               "register split exceeds the launch allocation");
 constexpr int kMmaWarp = 0, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;  // issuers 0 and 1
@@ -91,11 +106,18 @@ struct Misc {
   uint64_t o_free[2];   // the job's O_t read out
   uint64_t turn[2];     // the other tile's products are issued
   uint64_t v_clean;     // V behind the row's end is zeroed
+  // Pairs: of buffer b, K and V released; the query tile released by both issuers;
+  // softmax b's maximum and sum written and O_b complete.
+  uint64_t pair_k_empty[2], pair_v_empty[2], pair_q_empty, joined[2];
   uint64_t mma_done;
   uint32_t tmem_base;
+  int32_t pairs;        // no row of the batch has more than one tile of queries
   volatile int32_t abort_flag;
   Job job[2];
 };
+__device__ __forceinline__ uint8_t* block_memory(Misc* ms, int at) {
+  return reinterpret_cast<uint8_t*>(ms) - kOffMisc + at;
+}
 // What reads a job: two issuers, the producer and eight softmax warps.
 constexpr uint32_t kJobReaders = 11;
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
@@ -189,6 +211,7 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 struct Batch {
   Row row;
   int32_t b0, b1, first, count, total;
+  bool pairs;
   // More than 32 rows: the row before which the lane's search stands, and the
   // blocks of its run before that row.  A block's jobs come in falling order, so
   // the search only moves back.
@@ -202,10 +225,13 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
   r.b1 = min(p.batch, r.b0 + run);
   r.count = 0;
   r.row = Row{0, 0, 0, 0, 0};
+  bool one = true;
   for (int32_t b = r.b0; b < r.b1; ++b) {
     r.row = load_row(p, b, blockIdx.x == 0);
     r.count += r.row.blocks;
+    one = one && r.row.n <= kTile;
   }
+  r.pairs = __all_sync(0xffffffffu, one);
   int32_t incl = r.count;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -273,6 +299,11 @@ __device__ __forceinline__ void find_job(const PrefillParams& p, Batch& r, uint3
     job->live = 1;
   }
   __syncwarp();
+}
+
+// Whether the block works in pairs; known with its first job.  (Abandoned: either.)
+__device__ __forceinline__ bool in_pairs(const PrefillParams& p, Misc* ms) {
+  return warp_wait_on(&ms->job_full[0], 0, ms, p.err) && ms->pairs != 0;
 }
 
 // Job number `k` of this block, for one of its readers (a whole warp).
@@ -345,6 +376,43 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
   return true;
 }
 
+// The same for pairs: key tile T's K and V in buffer T & 1.
+__device__ __forceinline__ bool load_pair_job(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase,
+                                              const Job& job, Loads& l, uint64_t keep, uint64_t once) {
+  const int32_t n = job.tiles(), claim = max(0, n - kClaimTiles);
+  if (n == 0) mbar_arrive(smem_u32(&ms->claim));
+  for (int32_t j = 0; j < n; ++j) {
+    const uint32_t b = l.k & 1, before = ((l.k >> 1) + 1) & 1;  // (the first of each pass)
+    const int32_t key = job.k0 + (job.j0 + j) * kTile;
+    if (j == claim) mbar_arrive(smem_u32(&ms->claim));
+    if (!wait_on(&ms->pair_k_empty[b], before, ms, p.err)) return false;
+    uint32_t bar = smem_u32(&ms->k_full[b]), dst = sbase + kOffPairK + b * kKPanels * kPanelBytes;
+    mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
+    tma_load_3d(dst, &m.k_nope, 0, job.head, key, bar, keep);
+    tma_load_3d(dst + kPanelBytes, &m.k_nope, 64, job.head, key, bar, keep);
+    tma_load_2d(dst + 2 * kPanelBytes, &m.k_rope, 0, key, bar, keep);
+    ++l.k;
+    if (j == 0) {
+      if (!wait_on(&ms->pair_q_empty, (l.q0 + 1) & 1, ms, p.err)) return false;
+      ++l.q0;
+      bar = smem_u32(&ms->q_full[0]);
+      mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
+      for (int c = 0; c < kQPanels; ++c)
+        tma_load_3d(sbase + kOffQ + c * kPanelBytes, &m.q, 64 * c, job.head, job.q0, bar, once);
+    }
+    if (!wait_on(&ms->pair_v_empty[b], before, ms, p.err)) return false;
+    bar = smem_u32(&ms->v_full[b]);
+    dst = sbase + kOffPairV + b * kVPanels * kPanelBytes;
+    mbar_arrive_expect_tx(bar, kVPanels * kPanelBytes);
+    for (int h = 0; h < kVPanels; ++h) {
+      tma_load_3d(dst + h * kPanelBytes, &m.v, 0, job.head, key + 64 * h, bar, keep);
+      tma_load_3d(dst + h * kPanelBytes + kPanelBytes / 2, &m.v, 64, job.head, key + 64 * h, bar, keep);
+    }
+    ++l.v;
+  }
+  return true;
+}
+
 __device__ __forceinline__ void run_producer(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase) {
   const int lane = threadIdx.x & 31;
   const uint64_t keep = l2_policy_evict_normal(), once = l2_policy_evict_first();
@@ -356,7 +424,8 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
       if (p.stall_stream)
         mbar_arrive(smem_u32(&ms->claim));
       else
-        ok = load_job(p, m, ms, sbase, job, l, keep, once);
+        ok = ms->pairs ? load_pair_job(p, m, ms, sbase, job, l, keep, once)
+                       : load_job(p, m, ms, sbase, job, l, keep, once);
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
   }
@@ -376,6 +445,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
 __device__ __forceinline__ void run_scheduler(const PrefillParams& p, Misc* ms) {
   const int lane = threadIdx.x & 31;
   Batch rows = count_rows(p);
+  if (lane == 0) ms->pairs = rows.pairs;
   uint32_t index = blockIdx.x;
   for (uint32_t k = 0;; ++k) {
     Job* job = &ms->job[k & 1];
@@ -394,20 +464,17 @@ __device__ __forceinline__ void run_scheduler(const PrefillParams& p, Misc* ms) 
 // The row's last key tile may end inside the tile.  The rows of V behind it are
 // another row's, or never written: their probabilities are zero, but zero times
 // NaN is NaN, so issuer 0 zeroes them in shared memory (while the tile's softmax
-// runs) before either product reads them.
-__device__ __forceinline__ void clean_v(Misc* ms, uint8_t* smem, uint32_t T, int32_t keys) {
+// runs) before either product reads them; of pairs, the issuer whose tile it is.
+__device__ __forceinline__ void clean_v(uint8_t* v0, uint8_t* v1, int32_t keys) {
   const int lane = threadIdx.x & 31;
-  const uint32_t f = T * kFillsPerTile + kKPanels;
 #pragma unroll 1
   for (int32_t i = keys * 16 + lane; i < kTile * 16; i += 32) {
     const int32_t key = i >> 4, piece = i & 15;
-    *reinterpret_cast<uint4*>(smem + kOffRing + ring_slot(f + (key >> 6)) * kPanelBytes +
-                              (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
+    *reinterpret_cast<uint4*>((key < 64 ? v0 : v1) + (piece >> 3) * (kPanelBytes / 2) + (key & 63) * 128 + (piece & 7) * 16) =
         make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0) mbar_arrive(smem_u32(&ms->v_clean));
 }
 
 // ------------------------------------------------------------ MMA issuers (a warp a tile, an elected lane issues)
@@ -421,8 +488,7 @@ __device__ __forceinline__ void clean_v(Misc* ms, uint8_t* smem, uint32_t T, int
 // prompt: one issuer for both tiles 913 us, two without turns 1252 us, as both
 // tiles' softmax then fall together, two in turn 776 us at that time.  A single S
 // for both tiles with one issuer for the scores and one for the values: 829 us.)
-__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_t* smem, uint32_t sbase,
-                                        uint32_t tmem, int t) {
+__device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int t) {
   const uint64_t q_desc = smem_desc(sbase + kOffQ + t * kQPanels * kPanelBytes, 1024, 1024, kLayoutSw128);
   const uint64_t k_desc = smem_desc(sbase + kOffRing, 1024, 1024, kLayoutSw128);
   const uint64_t v_desc = smem_desc(sbase + kOffRing, kPanelBytes / 2, 1024, kLayoutSw128);
@@ -472,7 +538,13 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
       const bool here = j < nt, next = j + 1 < nt;
       ok = on(&ms->v_full[T & 1], T >> 1);
       if (ok && j == clean) {
-        if (t == 0) clean_v(ms, smem, T, job.len % kTile);
+        if (t == 0) {
+          const uint32_t f = T * kFillsPerTile + kKPanels;
+          clean_v(block_memory(ms, kOffRing + ring_slot(f) * kPanelBytes),
+                  block_memory(ms, kOffRing + ring_slot(f + 1) * kPanelBytes), job.len % kTile);
+          if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms->v_clean));
+          __syncwarp();
+        }
         ok = t == 0 || on(&ms->v_clean, cleans);
       }
       // K(T + 1) has mostly landed too; looked at here, it costs no pause between
@@ -527,6 +599,78 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint8_
   __syncwarp();
 }
 
+// Pairs: issuer t has the key tiles T with T & 1 == t, in buffer t, and its products
+// depend on nothing of the other issuer's: the chain of a tile (load, scores,
+// softmax, values) runs beside the other's.
+__device__ __forceinline__ void run_pair_mma(const PrefillParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int t) {
+  const int k_at = kOffPairK + t * kKPanels * kPanelBytes, v_at = kOffPairV + t * kVPanels * kPanelBytes;
+  const uint64_t q_desc = smem_desc(sbase + kOffQ, 1024, 1024, kLayoutSw128);
+  const uint64_t k_desc = smem_desc(sbase + k_at, 1024, 1024, kLayoutSw128);
+  const uint64_t v_desc = smem_desc(sbase + v_at, kPanelBytes / 2, 1024, kLayoutSw128);
+  constexpr uint32_t kPanel = kPanelBytes >> 4;
+  const uint32_t d_s = tmem + kColS + 128 * t, d_o = tmem + kColO + 128 * t;
+  constexpr int kHeadSteps = 6;
+  auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
+  uint32_t T = 0, mine = 0, jobs = 0, own_jobs = 0;
+  Job job;
+  bool ok = true;
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    const int32_t n = job.tiles(), clean = job.partial(), first = (T ^ t) & 1;
+    if (n == 0) continue;
+    T += n;
+    ok = on(&ms->q_full[0], jobs++);
+    if (!ok) break;
+    if (first >= n) {  // the job's one tile is the other issuer's
+      if (elect_one()) mbar_arrive(smem_u32(&ms->pair_q_empty));
+      __syncwarp();
+      continue;
+    }
+    for (int32_t j = first; j < n; j += 2, ++mine) {
+      const bool last = j + 2 >= n;
+      ok = on(&ms->k_full[t], mine);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < kKPanels; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16(d_s, q_desc + c * kPanel + 2 * kk, k_desc + c * kPanel + 2 * kk, kIdescQK, c != 0 || kk != 0);
+        umma_commit(smem_u32(&ms->s_full[t]));
+        umma_commit(smem_u32(&ms->pair_k_empty[t]));
+        if (last) umma_commit(smem_u32(&ms->pair_q_empty));
+      }
+      __syncwarp();
+      ok = on(&ms->v_full[t], mine);
+      if (!ok) break;
+      if (j == clean) clean_v(block_memory(ms, v_at), block_memory(ms, v_at + kPanelBytes), job.len % kTile);
+      ok = (j != first || on(&ms->o_free[t], own_jobs + 1)) && on(&ms->p_head[t], mine);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kHeadSteps; ++kk)
+          umma_f16_ts(d_o, d_s + 8 * kk, v_desc + (kk >> 2) * kPanel + (kk & 3) * 128, kIdescPV, j != first || kk != 0);
+      }
+      __syncwarp();
+      ok = on(&ms->p_full[t], mine);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = kHeadSteps; kk < 8; ++kk)
+          umma_f16_ts(d_o, d_s + 8 * kk, v_desc + (kk >> 2) * kPanel + (kk & 3) * 128, kIdescPV, 1);
+        if (last) umma_commit(smem_u32(&ms->o_full[t]));
+        umma_commit(smem_u32(&ms->pair_v_empty[t]));
+      }
+      __syncwarp();
+    }
+    ++own_jobs;
+  }
+  if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
+  __syncwarp();
+}
+
 // ------------------------------------------------------------ softmax
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -572,20 +716,24 @@ __device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t* w, in
   }
 }
 
-// One job of query tile t (a warpgroup); `tiles` and `jobs` count what it has done before.
+// One job of softmax t (a warpgroup): its query tile, or of pairs its key tiles.
+// `tiles`, `jobs` and `joins` count what was done before: this warpgroup's tiles,
+// its jobs with tiles, and of pairs the joinings.
+template <bool kPairs>
 __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, uint32_t tmem, const Job& job, int t,
-                                            uint32_t& tiles, uint32_t& jobs) {
+                                            int32_t first, uint32_t& tiles, uint32_t& jobs, uint32_t& joins) {
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
-  const int qi = t * kTile + quad * 32 + lane;       // this thread's query of the job
+  const int row0 = (kPairs ? 0 : t * kTile) + quad * 32, qi = row0 + lane;  // this thread's query of the job
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t s_addr = tmem + lanes + kColS + 128 * t, o_addr = tmem + lanes + kColO + 128 * t;
-  const int32_t n = t ? job.nt1 : job.nt0;
+  constexpr int32_t kStep = kPairs ? 2 : 1;
+  const int32_t n = kPairs ? job.nt0 : t ? job.nt1 : job.nt0;
   const float sl = p.scale * 1.4426950408889634f;    // scores to powers of two
   // keys that this row, and the warp's first row, see
   const int32_t sees = p.causal ? min(job.len, job.see + qi) : job.len;
-  const int32_t warp_sees = p.causal ? min(job.len, job.see + t * kTile + quad * 32) : job.len;
+  const int32_t warp_sees = p.causal ? min(job.len, job.see + row0) : job.len;
   float ref = -INFINITY, sum = 0.0f;
-  for (int32_t j = 0; j < n; ++j, ++tiles) {
+  for (int32_t j = first; j < n; j += kStep, ++tiles) {
     if (!warp_wait_on(&ms->s_full[t], tiles & 1, ms, p.err)) return false;
     tc_fence_after();
     uint32_t raw[4][32];
@@ -615,7 +763,7 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
       const float alpha = moves ? ex2((ref - high) * sl) : 1.0f;
       if (moves) ref = high;
       sum *= alpha;
-      if (j > 0) {  // O_t's last product is complete: S_t(j) was issued after it
+      if (j > first) {  // O_t's last product is complete: S_t(j) was issued after it
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t o[16];
@@ -662,10 +810,34 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
   }
 
   // Epilogue.  A row that saw no key has sum 0.
-  if (n > 0) {
+  if (n > first) {
     if (!warp_wait_on(&ms->o_full[t], jobs & 1, ms, p.err)) return false;
     ++jobs;
     tc_fence_after();
+  }
+  // Pairs: the softmax without the job's first tile hands over its maximum and sum
+  // (written after its O is complete, so after the last ones were read), the other
+  // weights both accumulators by them.
+  const bool join = kPairs && n > 1;
+  float weight = 1.0f, other_weight = 0.0f;
+  if (join) {
+    float2* stats = reinterpret_cast<float2*>(block_memory(ms, kOffStats)) + quad * 32 + lane;
+    if (first != 0) {
+      stats[t * kTile] = make_float2(ref, sum);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->joined[t]));
+      return true;
+    }
+    if (!warp_wait_on(&ms->joined[t ^ 1], joins & 1, ms, p.err)) return false;
+    ++joins;
+    tc_fence_after();
+    const float2 other = stats[(t ^ 1) * kTile];
+    const float high = fmaxf(ref, other.x);
+    weight = ref == high ? 1.0f : ex2((ref - high) * sl);  // (-inf is not apart from -inf)
+    other_weight = other.x == high ? 1.0f : ex2((other.x - high) * sl);
+    sum = weight * sum + other_weight * other.y;
+    ref = high;
   }
   const bool live = qi < job.nq;
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -678,11 +850,23 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
     uint32_t o[32];
     if (n > 0) {
       tmem_ld32(o_addr + 32 * c, o);
-      tmem_wait_ld();
+      if (join) {
+        uint32_t x[32];
+        tmem_ld32(tmem + lanes + kColO + 128 * (t ^ 1) + 32 * c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          o[i] = __float_as_uint(__uint_as_float(o[i]) * weight + __uint_as_float(x[i]) * other_weight);
+      } else {
+        tmem_wait_ld();
+      }
       if (c == 3) {  // the next job's products may overwrite O_t
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ms->o_free[t]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ms->o_free[t]));
+          if (join) mbar_arrive(smem_u32(&ms->o_free[t ^ 1]));
+        }
       }
     } else {
 #pragma unroll
@@ -716,11 +900,16 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
   return true;
 }
 
+template <bool kPairs>
 __device__ __forceinline__ void run_softmax(const PrefillParams& p, Misc* ms, uint32_t tmem, int t) {
-  uint32_t tiles = 0, jobs = 0;
+  uint32_t tiles = 0, jobs = 0, joins = 0;
+  int32_t first = kPairs ? t : 0;  // of pairs, this warpgroup's first key tile of the job
   Job job;
-  for (uint32_t k = 0; next_job(p, ms, k, job); ++k)
-    if (job.nq > t * kTile && !softmax_job(p, ms, tmem, job, t, tiles, jobs)) return;
+  for (uint32_t k = 0; next_job(p, ms, k, job); ++k) {
+    const bool mine = kPairs ? first == 0 || job.nt0 > 1 : job.nq > t * kTile;
+    if (mine && !softmax_job<kPairs>(p, ms, tmem, job, t, first, tiles, jobs, joins)) return;
+    if (kPairs) first ^= job.nt0 & 1;
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -730,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   Misc* ms = reinterpret_cast<Misc*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
   if (tid == kProducerWarp * 32) {
     for (int t = 0; t < 2; ++t) {
@@ -749,6 +938,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ms->job_empty[t]), kJobReaders);
       mbar_init(smem_u32(&ms->turn[t]), 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&ms->pair_k_empty[b]), 1);
+      mbar_init(smem_u32(&ms->pair_v_empty[b]), 1);
+      mbar_init(smem_u32(&ms->joined[b]), 4);
+    }
+    mbar_init(smem_u32(&ms->pair_q_empty), 2);
     mbar_init(smem_u32(&ms->claim), 1);
     mbar_init(smem_u32(&ms->v_clean), 1);
     mbar_init(smem_u32(&ms->mma_done), 2);
@@ -767,26 +962,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ms->tmem_base;
   if (warp >= kFirstSoftmaxWarp) {
     setmaxnreg_inc<kSoftmaxRegs>();
-    run_softmax(p, ms, tmem, (warp - kFirstSoftmaxWarp) >> 2);
+    const int t = (warp - kFirstSoftmaxWarp) >> 2;
+    if (in_pairs(p, ms))
+      run_softmax<true>(p, ms, tmem, t);
+    else
+      run_softmax<false>(p, ms, tmem, t);
   } else {
     setmaxnreg_dec<kOtherRegs>();
     if (warp == kProducerWarp)
       run_producer(p, maps, ms, sbase);
     else if (warp == kSchedulerWarp)
       run_scheduler(p, ms);
+    else if (in_pairs(p, ms))
+      run_pair_mma(p, ms, sbase, tmem, warp - kMmaWarp);
     else
-      run_mma(p, ms, smem, sbase, tmem, warp - kMmaWarp);
+      run_mma(p, ms, sbase, tmem, warp - kMmaWarp);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
-    if (lane == 0) drain(&ms->mma_done, 0);
+  // (What is known above is read anew here.  Kept over the roles it made the issuers
+  // spill a word: 3 % of the ragged batch, and 0.35 us of a launch for its local memory.)
+  if (threadIdx.x >> 5 == kMmaWarp) {
+    const bool one = (threadIdx.x & 31) == 0;
+    if (one) drain(&ms->mma_done, 0);
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(ms->tmem_base, kTmemCols);
     // The last block leaves the counters zero for the workspace's next call.
-    if (lane == 0 && atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
+    if (one && atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
       p.sched[0] = 0;
       p.sched[1] = 0;
     }

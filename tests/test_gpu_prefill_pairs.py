@@ -1,0 +1,117 @@
+"""mla_prefill_fwd on batches whose rows have at most 128 queries: the key tiles alternate
+between the two softmax warpgroups, whose accumulators are joined at a job's end.  Numbers
+of key tiles odd and even, jobs that start with either warpgroup, rows that see keys in one
+of the two only.  Tolerances as derived for the other prompt tests: the joining multiplies
+each float32 accumulator by a power-of-two exponential (2^-22) and adds, far below the
+2^-16 (spread + 1) that they allow beside the two bf16 roundings."""
+import numpy as np
+import pytest
+import torch
+
+from mla_decode_attention_08_gb300 import binding
+from .test_gpu_prefill import TIMEOUT, Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(built_library):
+    binding.load_library(built_library)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,length", [(1, 128), (1, 129), (128, 256), (100, 257), (128, 384), (33, 400), (97, 513),
+                                      (128, 130), (128, 3), (127, 1290)])
+def test_tiles_of_one_row(n, length, causal):
+    c = Case([n], [length], heads=3, causal=causal, seed=n + length, lead=2, tail=3, sms=1)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("sms", [1, 5, 152])
+@pytest.mark.parametrize("causal", [True, False])
+def test_jobs_start_with_either_warpgroup(sms, causal):
+    """Few blocks work through jobs of 0, 1, 2, 3, ... key tiles."""
+    kv = [100, 1, 300, 0, 129, 513, 128, 70, 900, 384, 20, 256, 0, 640, 90]
+    q = [100, 1, 17, 5, 128, 128, 64, 70, 2, 0, 20, 128, 0, 99, 128]
+    c = Case(q, kv, heads=5, causal=causal, seed=sms, lead=1, tail=4, sms=sms)
+    c.run()
+    c.check()
+    out, lse = c.out.clone(), c.lse.clone()
+    c.run()
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q,kv", [([128], [8000]), ([3, 128, 40], [4000, 2500, 1]), ([1], [1152])])
+def test_split_and_paired(q, kv, causal):
+    c = Case(q, kv, heads=2, causal=causal, seed=sum(kv), lead=1, tail=2)
+    assert c.plan.splits > 1
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("batch,sms", [(33, 152), (50, 3), (300, 152), (64, 1)])
+def test_many_short_rows(batch, sms):
+    rng = np.random.default_rng(batch + sms)
+    q = rng.integers(0, 129, batch)
+    kv = q + rng.integers(0, 400, batch) * (rng.random(batch) < 0.5)
+    c = Case(q.tolist(), kv.tolist(), heads=2, seed=batch, tail=1, sms=sms)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("first_large", [True, False])
+def test_maxima_far_apart(first_large):
+    """One warpgroup's scores exceed the other's by hundreds: its weight alone is left."""
+    c = Case([64], [512], heads=2, causal=False, seed=3, sms=1)
+    keys = (torch.arange(512, device="cuda") // 128 % 2 == 0) == first_large
+    c.q[:] = c.q.abs()
+    c.k_nope[keys] = c.k_nope[keys].abs() * 8
+    c.run()
+    c.check()
+
+
+def test_rows_that_see_one_tile_beside_rows_that_see_two():
+    """Causal rows whose second key tile is masked as a whole: its maximum is the lowest."""
+    c = Case([128], [256], heads=2, seed=5, sms=1)
+    c.run()
+    c.check()
+    c = Case([128], [129], heads=2, seed=6, sms=1, tail=4)
+    c.run()
+    c.check()
+
+
+def test_a_row_of_129_queries_beside_short_ones():
+    c = Case([128, 129, 1], [500, 700, 300], heads=3, seed=9, tail=2)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("q,kv", [([300, 5], [700, 40]), ([300, 5], [4000, 3000])])
+def test_replayed_graph_switches_between_the_forms(q, kv):
+    """One captured call over rows that the device finds short, then long, then short."""
+    c = Case(q, kv, heads=2, seed=4)
+    c.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    for qo in ([0, 300, 305], [0, 128, 200], [0, 177, 305], [0, 1, 1], [0, 300, 305]):
+        c.d_qo.copy_(torch.tensor(qo, dtype=torch.int32))
+        c.qo = np.array(qo, dtype=np.int64)
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        graph.replay()
+        c.check()
+
+
+def test_waits_that_run_out_are_reported():
+    c = Case([64, 3], [700, 300], heads=2, seed=1)
+    c.run(fn=binding.mla_prefill_fwd_stall_stream)
+    torch.cuda.synchronize()
+    assert binding.mla_decode_read_error(c.ws) == TIMEOUT
+    c.out.fill_(7.0)
+    c.lse.fill_(7.0)
+    c.run()
+    c.check()
