@@ -29,9 +29,9 @@
 // Bound by the chain of one tile (scores 768 cycles of the tensor pipe, softmax
 // ~1250, values 512, and the looks at barriers between them) against the other
 // tile's: ~3300 cycles for a key tile of both where the pipe alone needs 2560,
-// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 755-765 us,
+// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 753-765 us,
 // 1.8 PFLOP/s, with the SM clock below 1.8 GHz under the power limit (a plain bf16
-// product sustains 1.77 PFLOP/s there); 12 prompts of up to 2047 tokens: 99 us.
+// product sustains 1.77 PFLOP/s there); 12 prompts of up to 2047 tokens: 98 us.
 #include <cstddef>
 
 #include "ops.h"
@@ -742,12 +742,14 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
     tmem_wait_ld();
     const int32_t key0 = (job.j0 + j) * kTile;
     if (warp_sees - key0 < kTile) {
-      const int32_t lim = sees - key0;
+      const int32_t lim = sees - key0, warp_lim = warp_sees - key0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) {
+        if (warp_lim >= 32 * c + 32) continue;  // all of the warp's rows see these keys
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (32 * c + i >= lim) raw[c][i] = 0xFF800000u;  // -inf
+      }
     }
     float top[4];
 #pragma unroll
