@@ -140,6 +140,35 @@ bool encode_shared(CUtensorMap* map, const void* base, int64_t tokens, int64_t t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Parts that a row's keys are cut into, when the (at most) `blocks` of queries leave
+// SMs idle.  By the time that it should take, in tenths of a microsecond: the jobs
+// that an SM works through, each a start and an end (3.5 us) and its key tiles (1.8
+// us, or 1.0 where rows are short and the tiles alternate), then the second kernel
+// (2 us and its float32 parts, written and read at 6 TB/s while all rows' threads fit
+// the GPU, else 3 us and 3 TB/s).  Parts that keep an SM for more than one round are
+// taken only where they promise a twelfth: rows may be shorter than the longest.
+// (16 heads; one part a free SM, at least four key tiles each, before: 64 queries
+// over 1064 keys 13.8 us, now 12.5; a prompt of 1000 tokens 23.5 and 19.2; two rows
+// of up to 500 over up to 8500, whose blocks take half the SMs, 121 and 75.)
+int32_t key_splits(int64_t blocks, int64_t key_tiles, int64_t sms, int64_t rows, bool short_rows) {
+  if (blocks == 0 || blocks >= sms) return 1;
+  const bool few = mla::merges_at_once(rows);
+  auto time = [&](int64_t s, int64_t rounds) {
+    const int64_t job = 35 + (key_tiles + s - 1) / s * (short_rows ? 10 : 18);
+    return rounds * job + (s == 1 ? 0 : few ? 20 + s * rows * 1024 / 600000 : 30 + s * rows * 1024 / 300000);
+  };
+  int64_t best = 1, least = time(1, 1);
+  for (int64_t s = 2; s <= key_tiles && s * blocks <= sms; ++s)
+    if (time(s, 1) <= least) least = time(best = s, 1);
+  int64_t limit = least * 11 / 12;
+  for (int64_t rounds = 2; rounds <= 8; ++rounds) {
+    const int64_t s = rounds * sms / blocks;
+    if (s > key_tiles) break;
+    if (time(s, rounds) < limit) limit = time(best = s, rounds);
+  }
+  return static_cast<int32_t>(best);
+}
+
 bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_heads,
                  int32_t num_sms, mla_prefill_plan_t* out) {
   mla_prefill_plan_t p;
@@ -154,13 +183,9 @@ bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num
   const int64_t tiles = static_cast<int64_t>(total_q) / mla::kPrefillRows +
                         (batch < total_q ? batch : total_q);
   p.tiles = static_cast<int32_t>(tiles);
-  // Blocks of queries alone, and parts of the keys for the SMs they leave idle;
-  // a part is at least four key tiles, below which the second kernel and the
-  // parts' traffic cost more than the shorter walk saves.
-  const int64_t blocks = tiles * num_heads, key_tiles = mla::tiles_of_length(max_kv_len);
-  int64_t splits = blocks > 0 ? num_sms / blocks : 1;
-  if (splits > key_tiles / 4) splits = key_tiles / 4;
-  p.splits = splits < 1 ? 1 : static_cast<int32_t>(splits);
+  const int64_t blocks = tiles * num_heads;
+  p.splits = key_splits(blocks, mla::tiles_of_length(max_kv_len), num_sms, static_cast<int64_t>(total_q) * num_heads,
+                        total_q <= 128 * static_cast<int64_t>(batch));
   if (blocks * p.splits > INT32_MAX) return false;
   uint64_t off = kAlign;  // error word
   p.ws_lse_offset = p.ws_partial_offset = off;

@@ -3,7 +3,7 @@
 //
 // With m = max_s lse_s (0 if every piece is empty) and w_s = exp(lse_s - m):
 // out = sum_s w_s part_s / sum_s w_s and lse = m + log sum_s w_s.  A thread owns
-// eight or 16 values of a row: it reads the row's few lses (the row's threads read
+// four to 16 values of a row: it reads the row's few lses (the row's threads read
 // the same ones) and each piece once.  Bound by the bytes of the pieces.
 #include "ops.h"
 #include "ptx.cuh"
@@ -12,7 +12,6 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroup = 4;  // pieces whose loads are in flight together
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -57,9 +56,9 @@ struct Piece {
 // split has few rows.)
 __device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
   for (int32_t b = 0; b < p.batch; ++b) {
-    const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
+    const int32_t qs = __ldcg(p.qo_indptr + b), qe = __ldcg(p.qo_indptr + b + 1);
     if (token < qs || token >= qe) continue;
-    const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
+    const int32_t ks = __ldcg(p.kv_indptr + b), ke = __ldcg(p.kv_indptr + b + 1);
     if (qs >= 0 && qe <= p.total_q && ks >= 0 && ke >= ks && ke <= p.total_kv &&
         ke - ks <= MLA_PREFILL_MAX_ROW_KEYS)
       return true;
@@ -73,16 +72,25 @@ __device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
 // weights cost (the kernel issues on 8 of 10 cycles with eight).  Four pieces of
 // 16384 x 16 rows of 128: 67 us with eight values and the weights first, 55 with the
 // values beside them, 49.6 us with 16 (6.9 TB/s; a copy reaches 6.7).
-template <bool kF32, int kVec>
+// kGroup pieces' loads are in flight together: 16, with four values a thread, where
+// a prompt's few rows have all their threads on the GPU at once and the trips to L2
+// are what costs (64 queries x 16 heads of nine float32 parts: 19.3 us with the
+// attention before it, 20.7 with eight, 22.6 with eight values and four in flight);
+// four where the SMs' registers turn over (1000 x 16 of two parts: 23.9 us, the
+// other way 34.1).
+template <bool kF32, int kVec, int kGroup>
 __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams p, int32_t chunk_shift) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const uint32_t chunks = static_cast<uint32_t>(p.dim) / kVec;
   const int64_t row = chunk_shift >= 0 ? i >> chunk_shift : i / chunks;
   const int dim0 = kVec * static_cast<int>(i - row * chunks);
+  bool wanted = row < p.rows;
+  // (The rows are an input of the attention before as well, which waited for whoever
+  // wrote them.)
+  if constexpr (kF32) wanted = wanted && in_a_row(p, row / p.heads);
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (row >= p.rows) return;
-  if (p.qo_indptr != nullptr && !in_a_row(p, row / p.heads)) return;
+  if (!wanted) return;
   const float* lses = p.lses + row;
   Piece<kF32, kVec> x[kGroup];
 #pragma unroll
@@ -119,13 +127,18 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
     unpack2(acc[e], lo, hi);
     out[e] = bf16x2(lo * inv, hi * inv);
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.dim + dim0);
+  uint16_t* dst = p.out + row * p.dim + dim0;
+  if constexpr (kVec == 4) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  } else {
 #pragma unroll
-  for (int e = 0; e < kVec / 8; ++e) dst[e] = make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+    for (int e = 0; e < kVec / 8; ++e)
+      reinterpret_cast<uint4*>(dst)[e] = make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+  }
   if (dim0 == 0 && p.lse_out != nullptr) p.lse_out[row] = top + logf(sum);
 }
 
-template <bool kF32, int kVec>
+template <bool kF32, int kVec, int kGroup>
 cudaError_t launch_vec(const MergeParams& p, cudaStream_t stream) {
   const int32_t chunks = p.dim / kVec;
   const int64_t blocks = (p.rows * chunks + kThreads - 1) / kThreads;
@@ -133,14 +146,15 @@ cudaError_t launch_vec(const MergeParams& p, cudaStream_t stream) {
   int32_t shift = -1;  // of `chunks`, where that is a power of two
   for (int32_t k = 0; k < 8; ++k)
     if (chunks == 1 << k) shift = k;
-  return launch_dependent(attn_merge_kernel<kF32, kVec>, static_cast<unsigned>(blocks), kThreads, 0, stream, p, shift);
+  return launch_dependent(attn_merge_kernel<kF32, kVec, kGroup>, static_cast<unsigned>(blocks), kThreads, 0, stream, p, shift);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream) {
-  if (f32_parts) return launch_vec<true, 8>(p, stream);
-  return p.dim % 16 == 0 ? launch_vec<false, 16>(p, stream) : launch_vec<false, 8>(p, stream);
+  // (The parts are rows of 128.)
+  if (f32_parts) return merges_at_once(p.rows) ? launch_vec<true, 4, 16>(p, stream) : launch_vec<true, 8, 4>(p, stream);
+  return p.dim % 16 == 0 ? launch_vec<false, 16, 4>(p, stream) : launch_vec<false, 8, 4>(p, stream);
 }
 
 }  // namespace mla

@@ -83,11 +83,14 @@ struct MergeParams {
   float* lse_out;          // or null
   int64_t rows;
   int32_t pieces, dim;
-  const int32_t* qo_indptr;  // or null: every row
+  const int32_t* qo_indptr;  // of float pieces
   const int32_t* kv_indptr;
   int64_t total_kv;
   int32_t batch, heads, total_q;
 };
+// Whether float parts of `rows` rows of 128 are joined by threads that are all on the
+// GPU at once: four values each, two blocks of 256 an SM.
+inline bool merges_at_once(int64_t rows) { return rows * (128 / 4) <= 152 * 2 * 256; }
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
 
 // mla_prefill_fwd: a persistent block an SM; a job is up to 256 queries of a row

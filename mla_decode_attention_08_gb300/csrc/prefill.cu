@@ -22,7 +22,8 @@
 // each with its own S and O over the same queries, and the second accumulator is
 // joined to the first at the job's end, out of TMEM.  A tile's chain then runs
 // beside the next one's, and the keys stream at nearly the memory's rate.  (64
-// queries over 8256 keys, 16 heads: 22.6 us, one query tile on its own 25.6; 8 rows
+// queries over 8256 keys, 16 heads: 22.6 us, one query tile on its own 25.6, and 19.6
+// since the parts are joined with all their loads in flight; 8 rows
 // of up to 64 queries over up to 4000 keys: 42.1 us and 52.5; 24 rows of up to 128
 // over up to 256: 14.4 and 17.9.)
 //

@@ -115,3 +115,16 @@ def test_waits_that_run_out_are_reported():
     c.lse.fill_(7.0)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q,kv,heads,sms", [([300, 200], [4000, 1500], 2, 10),    # parts over several rounds
+                                            ([400], [3000], 8, 152),              # many rows to join
+                                            ([303], [2000], 8, 152)])             # the last that join at once
+def test_parts_joined(q, kv, heads, sms, causal):
+    c = Case(q, kv, heads=heads, causal=causal, seed=sum(kv) + sms, lead=1, tail=1 if len(q) > 1 else 0, sms=sms)
+    assert c.plan.splits > 1
+    if sms == 10:
+        assert c.plan.tiles * heads * c.plan.splits > sms
+    c.run()
+    c.check()
