@@ -706,14 +706,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // which holds up the other warps' barriers while it lasts: whole 32-byte sectors
 // take half the instructions of 16-byte pieces (which an output that is only
 // 16-byte aligned gets).
-__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t* w, int32_t wide) {
+__device__ __forceinline__ void store_row32(void* dst, const uint32_t* w, int32_t wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
   } else {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    static_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -884,11 +884,11 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
       store_row32(dst, w, p.wide_out);
       store_row32(dst + 16, w + 8, p.wide_out);
     } else if (live) {
-      float4* dst = reinterpret_cast<float4*>(p.part + part_at * kPrefillV + 32 * c);
+      float* dst = p.part + part_at * kPrefillV + 32 * c;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                             __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_row32(dst + 8 * i, o + 8 * i, 1);
     }
     __syncwarp();
   }
