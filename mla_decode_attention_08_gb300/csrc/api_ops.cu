@@ -140,37 +140,40 @@ bool encode_shared(CUtensorMap* map, const void* base, int64_t tokens, int64_t t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Parts that a row's keys are cut into, when the (at most) `blocks` of queries leave
-// SMs idle.  By the time that it should take, in tenths of a microsecond: the jobs
-// that an SM works through, each a start and an end (3.5 us) and its key tiles (1.8
-// us, or 1.0 where rows are short and the tiles alternate), then the second kernel
-// (2 us and its float32 parts, written and read at 6 TB/s while all rows' threads fit
-// the GPU, else 3 us and 3 TB/s).  Parts that keep an SM for more than one round are
-// taken only where they promise a twelfth: rows may be shorter than the longest.
-// (16 heads; one part a free SM, at least four key tiles each, before: 64 queries
-// over 1064 keys 13.8 us, now 12.5; a prompt of 1000 tokens 23.5 and 19.2; two rows
-// of up to 500 over up to 8500, whose blocks take half the SMs, 121 and 75.)
-int32_t key_splits(int64_t blocks, int64_t key_tiles, int64_t sms, int64_t rows, bool short_rows) {
-  if (blocks == 0 || blocks >= sms) return 1;
+// Blocks of 128 queries of any cut of `total_q` into rows, at most: as many rows as
+// there may be end one query into a block.
+int64_t most_blocks(int64_t total_q, int64_t batch) {
+  const int64_t rows = batch < total_q ? batch : total_q;
+  return rows == 0 ? 0 : (total_q - rows) / 128 + rows;
+}
+
+// Parts that a row's keys are cut into, when the (at most) `blocks` of 128 queries
+// leave SMs idle, now or in a second round.  By the time that it should take, in
+// twentieths of a microsecond: a job takes 2 us and 0.95 a key tile; the jobs of one
+// row come in rounds, those of a batch balance over the SMs, its rows' keys on average
+// at 0.7 of the longest; then the second kernel takes 2 us and its float32 parts'
+// bytes, written and read at 6 TB/s while all rows' threads fit the GPU, else at 5.
+// (Fitted to 50 batches of 16 and five heads, each with one to twelve parts: what it
+// takes is 2 % slower than the best of them on average, 14 % at worst.)
+int32_t key_splits(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms, int64_t rows) {
+  if (blocks == 0 || 10 * blocks >= 13 * sms) return 1;
   const bool few = mla::merges_at_once(rows);
-  auto time = [&](int64_t s, int64_t rounds) {
-    const int64_t job = 35 + (key_tiles + s - 1) / s * (short_rows ? 10 : 18);
-    return rounds * job + (s == 1 ? 0 : few ? 20 + s * rows * 1024 / 600000 : 30 + s * rows * 1024 / 300000);
+  auto time = [&](int64_t s) {
+    const int64_t jobs = blocks * s, longest = 40 + 19 * ((key_tiles + s - 1) / s);
+    const int64_t mean = 40 + 19 * ((7 * key_tiles + 10 * s - 1) / (10 * s));
+    const int64_t join = s == 1 ? 0 : 40 + s * rows * 1024 / (few ? 300000 : 250000);
+    if (batch == 1 || jobs <= sms) return (jobs + sms - 1) / sms * longest + join;
+    return (longest > jobs * mean / sms ? longest : jobs * mean / sms) + join;
   };
-  int64_t best = 1, least = time(1, 1);
-  for (int64_t s = 2; s <= key_tiles && s * blocks <= sms; ++s)
-    if (time(s, 1) <= least) least = time(best = s, 1);
-  int64_t limit = least * 11 / 12;
-  for (int64_t rounds = 2; rounds <= 8; ++rounds) {
-    const int64_t s = rounds * sms / blocks;
-    if (s > key_tiles) break;
-    if (time(s, rounds) < limit) limit = time(best = s, rounds);
-  }
+  int64_t best = 1, least = time(1);
+  for (int64_t s = 2; s <= key_tiles && s * blocks <= 8 * sms; ++s)
+    if (time(s) < least) least = time(best = s);
   return static_cast<int32_t>(best);
 }
 
-bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_heads,
-                 int32_t num_sms, mla_prefill_plan_t* out) {
+// The plan's fields for a number of parts; false if it cannot be run.
+bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_heads, int32_t num_sms,
+                 int32_t splits, mla_prefill_plan_t* out) {
   mla_prefill_plan_t p;
   std::memset(&p, 0, sizeof(p));
   p.batch = batch;
@@ -180,13 +183,9 @@ bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num
   p.num_sms = num_sms;
   p.abi_version = MLA_ABI_VERSION;
   // A row of n queries has ceil(n / 256) <= n / 256 + 1 blocks, and none if it is empty.
-  const int64_t tiles = static_cast<int64_t>(total_q) / mla::kPrefillRows +
-                        (batch < total_q ? batch : total_q);
-  p.tiles = static_cast<int32_t>(tiles);
-  const int64_t blocks = tiles * num_heads;
-  p.splits = key_splits(blocks, mla::tiles_of_length(max_kv_len), num_sms, static_cast<int64_t>(total_q) * num_heads,
-                        total_q <= 128 * static_cast<int64_t>(batch));
-  if (blocks * p.splits > INT32_MAX) return false;
+  p.tiles = total_q / mla::kPrefillRows + (batch < total_q ? batch : total_q);
+  p.splits = splits;
+  if (splits < 1 || most_blocks(total_q, batch) * num_heads > INT32_MAX / splits) return false;
   uint64_t off = kAlign;  // error word
   p.ws_lse_offset = p.ws_partial_offset = off;
   if (p.splits > 1) {
@@ -212,7 +211,8 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   if (plan == nullptr || plan->abi_version != MLA_ABI_VERSION || plan->batch < 1 ||
       plan->batch > MLA_PREFILL_MAX_ROWS || plan->total_q < 0 || plan->max_kv_len < 0 || plan->num_heads < 1 ||
       plan->num_heads > 1024 || plan->num_sms < 1 ||
-      !plan_fields(plan->batch, plan->total_q, plan->max_kv_len, plan->num_heads, plan->num_sms, &want) ||
+      !plan_fields(plan->batch, plan->total_q, plan->max_kv_len, plan->num_heads, plan->num_sms, plan->splits,
+                   &want) ||
       std::memcmp(&want, plan, sizeof(want)) != 0)
     return MLA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, kAlign)) return MLA_ERR_INVALID_ARG;
@@ -264,7 +264,7 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   p.batch = plan->batch;
   p.heads = heads;
   p.total_q = plan->total_q;
-  p.tiles = plan->tiles;
+  p.blocks = static_cast<int32_t>(most_blocks(plan->total_q, plan->batch));
   p.num_sms = plan->num_sms;
   p.splits = plan->splits;
   p.causal = causal != 0;
@@ -387,7 +387,9 @@ mla_status_t mla_prefill_plan(int32_t batch, int32_t total_q, int32_t max_kv_len
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
       return MLA_ERR_CUDA;
   }
-  return plan_fields(batch, total_q, max_kv_len, num_heads, num_sms, plan) ? MLA_OK : MLA_ERR_INVALID_ARG;
+  const int32_t splits = key_splits(most_blocks(total_q, batch) * num_heads, batch, mla::tiles_of_length(max_kv_len),
+                                    num_sms, static_cast<int64_t>(total_q) * num_heads);
+  return plan_fields(batch, total_q, max_kv_len, num_heads, num_sms, splits, plan) ? MLA_OK : MLA_ERR_INVALID_ARG;
 }
 
 mla_status_t mla_prefill_fwd(const void* q, int64_t q_token_stride, int64_t q_head_stride,

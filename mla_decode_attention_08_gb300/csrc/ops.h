@@ -105,7 +105,8 @@ struct PrefillParams {
   int32_t* err;
   uint32_t* sched;         // jobs handed out, blocks done: both zero between calls
   float scale;
-  int32_t batch, heads, total_q, tiles, splits, causal, num_sms;
+  int32_t batch, heads, total_q, splits, causal, num_sms;
+  int32_t blocks;          // of 128 queries, at most
   int64_t total_kv;
   int32_t wide_out;        // out is 32-byte aligned
   int32_t stall_stream;    // test hook: no copies are issued, so the waits run out

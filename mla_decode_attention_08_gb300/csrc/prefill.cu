@@ -17,15 +17,17 @@
 // the other tile's softmax runs.  K and V are read from shared memory for both
 // tiles, so a block moves 80 KB for 2 x 128 x 128 x 320 multiply-adds.
 //
-// When no row of the batch has more than one tile of queries, the key tiles
-// themselves alternate ("pairs" below): tile T goes to issuer and softmax T & 1,
+// That takes 2 x 128 queries a job, and a row's last job is its longest.  Where such
+// jobs would leave SMs idle (few of them, or few long ones), a job is one query tile
+// and its key tiles alternate ("pairs" below): tile T goes to issuer and softmax T & 1,
 // each with its own S and O over the same queries, and the second accumulator is
-// joined to the first at the job's end, out of TMEM.  A tile's chain then runs
-// beside the next one's, and the keys stream at nearly the memory's rate.  (64
-// queries over 8256 keys, 16 heads: 22.6 us, one query tile on its own 25.6, and 19.6
-// since the parts are joined with all their loads in flight; 8 rows
-// of up to 64 queries over up to 4000 keys: 42.1 us and 52.5; 24 rows of up to 128
-// over up to 256: 14.4 and 17.9.)
+// joined to the first at the job's end, out of TMEM.  K and V are then read from
+// shared memory for one query tile only, a key tile takes 0.95 us and not 1.75 / 2,
+// but jobs are half as long, and a row's jobs follow each other without a pause.
+// (16 heads, both ways: one prompt of 1000 tokens 14.4 us and 19.2, of 2000 23 and
+// 32, of 4000 62 and 59; 64 queries over 8256 keys 22.6 and 25.6; 8 rows of up to 64
+// queries over up to 4000 keys 42 and 52; 12 prompts of up to 2047 tokens 106 and 98;
+// 16384 tokens in one 10 % longer.)
 //
 // Bound by the chain of one tile (scores 768 cycles of the tensor pipe, softmax
 // ~1250, values 512, and the looks at barriers between them) against the other
@@ -76,7 +78,7 @@ constexpr uint32_t kIdescPV = idesc_bf16(kTile, kPrefillV, false, true);
 // costs bf16 nothing, and most tiles rescale nothing.
 constexpr float kRescaleThreshold = 8.0f;
 
-// One job: up to 256 queries of a row and head over a part of the row's keys.
+// One job: up to 256 queries (pairs: 128) of a row and head over a part of the row's keys.
 struct Job {
   int32_t q0, nq;       // first query token (of the batch) and number of queries
   int32_t k0, len;      // the row's first key and number of keys
@@ -112,7 +114,7 @@ struct Misc {
   uint64_t pair_k_empty[2], pair_v_empty[2], pair_q_empty, joined[2];
   uint64_t mma_done;
   uint32_t tmem_base;
-  int32_t pairs;        // no row of the batch has more than one tile of queries
+  int32_t pairs;        // jobs are of one query tile, and their key tiles alternate
   volatile int32_t abort_flag;
   Job job[2];
 };
@@ -174,22 +176,23 @@ __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
   }
 }
 
-__device__ __forceinline__ int32_t tiles_256(int32_t n) { return n / kPrefillRows + (n % kPrefillRows != 0); }
+__device__ __forceinline__ int32_t parts_of(int32_t n, int32_t size) { return n / size + (n % size != 0); }
 
-// A row, its queries in `blocks` of up to 256.
+// A row of the batch.
 struct Row {
-  int32_t qs, n, ks, len, blocks;
+  int32_t qs, n, ks, len;
   // Key tiles that block i's last query reaches.
   __device__ __forceinline__ int32_t tiles(bool causal, int32_t last) const {
     const int32_t keys = causal ? max(0, min(len, len - n + 1 + last)) : len;
-    return keys / kTile + (keys % kTile != 0);
+    return parts_of(keys, kTile);
   }
-  __device__ __forceinline__ int32_t block_tiles(bool causal, int32_t i) const {
-    return tiles(causal, min(n, (i + 1) * kPrefillRows) - 1);
+  // The same of block i of `size` queries.
+  __device__ __forceinline__ int32_t block_tiles(bool causal, int32_t i, int32_t size) const {
+    return tiles(causal, min(n, (i + 1) * size) - 1);
   }
 };
 __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool report) {
-  Row r = {0, 0, 0, 0, 0};
+  Row r = {0, 0, 0, 0};
   if (b >= p.batch) return r;
   const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
   const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
@@ -197,7 +200,7 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
   const bool bad_k = ks < 0 || ke < ks || ke > p.total_kv || ke - ks > MLA_PREFILL_MAX_ROW_KEYS;
   if (report && (bad_q || bad_k))
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
-  if (!bad_q && !bad_k) r = Row{qs, qe - qs, ks, ke - ks, tiles_256(qe - qs)};
+  if (!bad_q && !bad_k) r = Row{qs, qe - qs, ks, ke - ks};
   return r;
 }
 
@@ -209,10 +212,17 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 // all rows 102 us, with 331 MB read from DRAM for 184 MB of inputs.)  More rows: a
 // run of consecutive rows a lane, and the batch's blocks from the last one on; that
 // many rows even out.
+//
+// Pairs, when no row has more than a tile of queries, when the keys are cut into
+// parts, or when the longest job of two tiles takes longer than nine tenths of an
+// SM's share of all jobs.  (Of 33 batches the wrong way was taken for three, 1 % at
+// worst; with eight tenths 9 %, with 0.95 to 1.1 5 %.)
+constexpr float kTileCost = 1.75f, kJobCost = 3.2f;  // microseconds of two query tiles: a key tile, a job
+constexpr float kFull = 0.9f;
 struct Batch {
   Row row;
   int32_t b0, b1, first, count, total;
-  bool pairs;
+  int32_t size;         // queries of a block: 256, or 128 in pairs
   // More than 32 rows: the row before which the lane's search stands, and the
   // blocks of its run before that row.  A block's jobs come in falling order, so
   // the search only moves back.
@@ -224,15 +234,31 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
   Batch r;
   r.b0 = min(p.batch, lane * run);
   r.b1 = min(p.batch, r.b0 + run);
-  r.count = 0;
-  r.row = Row{0, 0, 0, 0, 0};
+  const bool causal = p.causal != 0;
+  r.row = Row{0, 0, 0, 0};
   bool one = true;
+  int32_t blocks = 0, halves = 0, longest = 0;
+  float work = 0.0f;
   for (int32_t b = r.b0; b < r.b1; ++b) {
     r.row = load_row(p, b, blockIdx.x == 0);
-    r.count += r.row.blocks;
+    const int32_t n = parts_of(r.row.n, kPrefillRows);
+    if (n == 0) continue;
+    const int32_t least = r.row.block_tiles(causal, 0, kPrefillRows), most = r.row.block_tiles(causal, n - 1, kPrefillRows);
+    blocks += n;
+    halves += parts_of(r.row.n, kTile);
     one = one && r.row.n <= kTile;
+    longest = max(longest, most);
+    work += n * (kTileCost * 0.5f * (least + most) + kJobCost);
   }
-  r.pairs = __all_sync(0xffffffffu, one);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    work += __shfl_xor_sync(0xffffffffu, work, d);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, d));
+  }
+  const bool idle = work * p.heads < kFull * p.num_sms * (kTileCost * longest + kJobCost);
+  const bool pairs = __all_sync(0xffffffffu, one) || p.splits > 1 || idle;
+  r.size = pairs ? kTile : kPrefillRows;
+  r.count = pairs ? halves : blocks;
   int32_t incl = r.count;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -241,7 +267,7 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
   }
   r.first = incl - r.count;
   if (p.batch <= 32) {
-    const int32_t size = r.count > 0 ? r.row.block_tiles(p.causal != 0, r.count - 1) : 0;
+    const int32_t size = r.count > 0 ? r.row.block_tiles(causal, r.count - 1, r.size) : 0;
     r.first = 0;
     for (int l = 0; l < 32; ++l) {
       const int32_t other = __shfl_sync(0xffffffffu, size, l), blocks = __shfl_sync(0xffffffffu, r.count, l);
@@ -276,16 +302,16 @@ __device__ __forceinline__ void find_job(const PrefillParams& p, Batch& r, uint3
     if (i >= 0 && i < r.count) {
       while (i < r.before) {
         r.row = load_row(p, --r.at, false);
-        r.before -= r.row.blocks;
+        r.before -= parts_of(r.row.n, r.size);
       }
       row = r.row;
       block = i - r.before;
     }
   }
   if (block >= 0) {
-    const int32_t i0 = block * kPrefillRows, nq = min(kPrefillRows, row.n - i0);
+    const int32_t i0 = block * r.size, nq = min(r.size, row.n - i0);
     const int32_t split = static_cast<int32_t>(rest % p.splits);
-    const int32_t all = row.block_tiles(causal, block), share = (all + p.splits - 1) / p.splits;
+    const int32_t all = row.block_tiles(causal, block, r.size), share = (all + p.splits - 1) / p.splits;
     const int32_t j0 = min(all, split * share), j1 = min(all, j0 + share);
     job->q0 = row.qs + i0;
     job->nq = nq;
@@ -446,7 +472,7 @@ __device__ __forceinline__ void run_producer(const PrefillParams& p, const Prefi
 __device__ __forceinline__ void run_scheduler(const PrefillParams& p, Misc* ms) {
   const int lane = threadIdx.x & 31;
   Batch rows = count_rows(p);
-  if (lane == 0) ms->pairs = rows.pairs;
+  if (lane == 0) ms->pairs = rows.size == kTile;
   uint32_t index = blockIdx.x;
   for (uint32_t k = 0;; ++k) {
     Job* job = &ms->job[k & 1];
@@ -1009,7 +1035,7 @@ cudaError_t prefill_prepare() {
 }
 
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream) {
-  const int64_t jobs = static_cast<int64_t>(p.tiles) * p.heads * p.splits;
+  const int64_t jobs = static_cast<int64_t>(p.blocks) * p.heads * p.splits;
   if (jobs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int64_t grid = jobs < p.num_sms ? jobs : p.num_sms;
   return launch_dependent(prefill_kernel, static_cast<unsigned>(grid), kThreads, kSmemBytes, stream,

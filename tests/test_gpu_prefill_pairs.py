@@ -1,7 +1,8 @@
-"""mla_prefill_fwd on batches whose rows have at most 128 queries: the key tiles alternate
-between the two softmax warpgroups, whose accumulators are joined at a job's end.  Numbers
-of key tiles odd and even, jobs that start with either warpgroup, rows that see keys in one
-of the two only.  Tolerances as derived for the other prompt tests: the joining multiplies
+"""mla_prefill_fwd's two walks.  Batches whose rows have at most 128 queries, or that leave SMs
+idle: the key tiles alternate between the two softmax warpgroups, whose accumulators are
+joined at a job's end.  Numbers of key tiles odd and even, jobs that start with either
+warpgroup, rows that see keys in one of the two only.  And batches planned for one SM, whose
+jobs are of two query tiles.  Tolerances as derived for the other prompt tests: the joining multiplies
 each float32 accumulator by a power-of-two exponential (2^-22) and adds, far below the
 2^-16 (spread + 1) that they allow beside the two bf16 roundings."""
 import numpy as np
@@ -118,13 +119,54 @@ def test_waits_that_run_out_are_reported():
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("q,kv,heads,sms", [([300, 200], [4000, 1500], 2, 10),    # parts over several rounds
+@pytest.mark.parametrize("q,kv,heads,sms", [([300, 200], [4000, 1500], 2, 19),    # parts over several rounds
                                             ([400], [3000], 8, 152),              # many rows to join
                                             ([303], [2000], 8, 152)])             # the last that join at once
 def test_parts_joined(q, kv, heads, sms, causal):
     c = Case(q, kv, heads=heads, causal=causal, seed=sum(kv) + sms, lead=1, tail=1 if len(q) > 1 else 0, sms=sms)
     assert c.plan.splits > 1
-    if sms == 10:
-        assert c.plan.tiles * heads * c.plan.splits > sms
+    if sms == 19:
+        assert (c.q.shape[0] // 128 + len(q)) * heads * c.plan.splits > sms
+    c.run()
+    c.check()
+
+
+# ---- planned for one SM: jobs of two query tiles, which larger GPUs only use for more work
+SIZES = [129, 191, 255, 256, 257, 383, 384, 512, 700]
+
+
+@pytest.mark.parametrize("n", SIZES)
+def test_one_prompt_in_jobs_of_two_tiles(n):
+    c = Case([n], [n], heads=2, seed=n, tail=n % 3, sms=1)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("layout", ["thd", "htd"])
+@pytest.mark.parametrize("q,kv", [([130], [1000]), ([256], [640]), ([300], [300]), ([200], [70]), ([400], [129]),
+                                  ([260], [0]), ([5, 0, 300, 128, 1, 77, 0, 513, 2], [5, 9, 300, 500, 0, 80, 0, 513, 700])])
+def test_rows_in_jobs_of_two_tiles(q, kv, layout, causal):
+    c = Case(q, kv, heads=3, causal=causal, layout=layout, seed=sum(q) + sum(kv), lead=2, tail=3, sms=1)
+    assert c.plan.splits == 1
+    c.run()
+    c.check()
+
+
+def test_both_walks_give_the_same_attention():
+    a, b = (Case([700, 300], [900, 300], heads=2, seed=12, sms=sms) for sms in (1, 152))
+    a.run()
+    b.run()
+    a.check()
+    b.check()
+
+
+def test_waits_of_jobs_of_two_tiles_that_run_out_are_reported():
+    c = Case([300, 10], [300, 40], heads=2, sms=1)
+    c.run(fn=binding.mla_prefill_fwd_stall_stream)
+    torch.cuda.synchronize()
+    assert binding.mla_decode_read_error(c.ws) == TIMEOUT
+    c.out.fill_(7.0)
+    c.lse.fill_(7.0)
     c.run()
     c.check()

@@ -1,5 +1,5 @@
-"""How mla_prefill_plan cuts a row's keys, on the CPU: never without idle SMs, never finer
-than key tiles, rounds bounded, and the workspace sized by the cut."""
+"""How mla_prefill_plan cuts a row's keys, on the CPU: never where the SMs have work, never
+finer than key tiles, rounds bounded, and the workspace sized by the cut."""
 import numpy as np
 import pytest
 
@@ -19,9 +19,10 @@ def test_bounds(seed):
         total, kv = int(2 ** rng.uniform(0, 14)), int(2 ** rng.uniform(0, 17))
         heads = int(rng.integers(1, 40))
         p = binding.mla_prefill_plan(batch, total, kv, heads, sms)
-        blocks, tiles = p.tiles * heads, -(-kv // 128)
+        # as many rows as there may be end one query into a block of 128
+        blocks, tiles = ((total - min(batch, total)) // 128 + min(batch, total)) * heads, -(-kv // 128)
         assert 1 <= p.splits <= max(1, tiles)
-        if blocks >= sms:
+        if 10 * blocks >= 13 * sms:
             assert p.splits == 1
         assert blocks * p.splits <= max(blocks, 8 * sms)
         rows = p.splits * total * heads if p.splits > 1 else 0
@@ -38,6 +39,13 @@ def test_few_queries_take_a_part_for_every_free_sm():
     assert p.splits == 152 // 16
 
 
-def test_blocks_on_half_the_sms_are_cut_over_several_rounds():
+def test_blocks_on_most_of_the_sms_are_cut_over_several_rounds():
     p = binding.mla_prefill_plan(2, 800, 8500, 16, 152)
-    assert p.tiles * 16 < 152 < p.tiles * 16 * p.splits
+    blocks = ((800 - 2) // 128 + 2) * 16
+    assert blocks < 152 < blocks * p.splits
+
+
+def test_a_plan_with_other_parts_is_another_plan():
+    """The parts may be chosen by the caller only together with the workspace's layout."""
+    p = binding.mla_prefill_plan(1, 64, 8256, 16, 152)
+    assert p.ws_bytes == p.ws_partial_offset + -(-p.splits * 64 * 16 * 512 // 256) * 256
