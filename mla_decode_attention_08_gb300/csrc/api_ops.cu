@@ -156,7 +156,8 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
 // (Fitted to 50 batches of 16 and five heads, each with one to twelve parts: what it
 // takes is 2 % slower than the best of them on average, 14 % at worst.)
 int32_t key_splits(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms, int64_t rows) {
-  if (blocks == 0 || 10 * blocks >= 13 * sms) return 1;
+  // (The second kernel looks for its tokens' rows, so thousands of empty ones are not cut.)
+  if (blocks == 0 || 10 * blocks >= 13 * sms || batch > 1024) return 1;
   const bool few = mla::merges_at_once(rows);
   auto time = [&](int64_t s) {
     const int64_t jobs = blocks * s, longest = 40 + 19 * ((key_tiles + s - 1) / s);

@@ -34,6 +34,11 @@ def test_no_keys_and_one_tile_are_not_cut():
         assert binding.mla_prefill_plan(1, 4, kv, 1, 152).splits == 1
 
 
+def test_thousands_of_empty_rows_are_not_cut():
+    assert binding.mla_prefill_plan(1024, 4, 8192, 16, 152).splits > 1
+    assert binding.mla_prefill_plan(1025, 4, 8192, 16, 152).splits == 1
+
+
 def test_few_queries_take_a_part_for_every_free_sm():
     p = binding.mla_prefill_plan(1, 64, 8256, 16, 152)
     assert p.splits == 152 // 16
