@@ -250,33 +250,35 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     longest = max(longest, most);
     work += n * (kTileCost * 0.5f * (least + most) + kJobCost);
   }
+  bool pairs = p.splits > 1 || __all_sync(0xffffffffu, one);
+  if (!pairs) {
+    longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    work += __shfl_xor_sync(0xffffffffu, work, d);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, d));
+    for (int d = 16; d > 0; d >>= 1) work += __shfl_xor_sync(0xffffffffu, work, d);
+    pairs = work * p.heads < kFull * p.num_sms * (kTileCost * longest + kJobCost);
   }
-  const bool idle = work * p.heads < kFull * p.num_sms * (kTileCost * longest + kJobCost);
-  const bool pairs = __all_sync(0xffffffffu, one) || p.splits > 1 || idle;
   r.size = pairs ? kTile : kPrefillRows;
   r.count = pairs ? halves : blocks;
-  int32_t incl = r.count;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  r.first = incl - r.count;
   if (p.batch <= 32) {
-    const int32_t size = r.count > 0 ? r.row.block_tiles(causal, r.count - 1, r.size) : 0;
+    r.total = __reduce_add_sync(0xffffffffu, r.count);
     r.first = 0;
-    for (int l = 0; l < 32; ++l) {
+    const int32_t size = r.count > 0 ? r.row.block_tiles(causal, r.count - 1, r.size) : 0;
+    for (int l = 0; l < p.batch; ++l) {
       const int32_t other = __shfl_sync(0xffffffffu, size, l), blocks = __shfl_sync(0xffffffffu, r.count, l);
       if (other > size || (other == size && l < lane)) r.first += blocks;
     }
+  } else {
+    int32_t incl = r.count;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    r.first = incl - r.count;
+    r.total = __shfl_sync(0xffffffffu, incl, 31);
   }
   r.at = r.b1;
   r.before = r.count;
-  r.total = __shfl_sync(0xffffffffu, incl, 31);
   return r;
 }
 
