@@ -566,11 +566,13 @@ mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const 
  *           overlap on the GPU.
  * Base pointers are 16-byte aligned; strides are in elements, multiples of 8, at
  * least the row's dims, below 2^36 (tokens or heads outermost; the stride of a
- * single token or head is not used).  Values of the rows' own tokens and their scores must be finite; what lies outside
- * the rows (padding, other rows' tokens) may hold anything.  No output may
- * overlap an input.  Rows outside total_q or total_kv, or with more than
- * MLA_PREFILL_MAX_ROW_KEYS keys, set MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and
- * are not written.  Deterministic for a given plan.
+ * single token or head is not used).  Values of the rows' own tokens and their
+ * scores must be finite; what lies outside the rows (padding, other rows' tokens)
+ * may hold anything.  No output may overlap an input.  Rows outside total_q or
+ * total_kv, or with more than MLA_PREFILL_MAX_ROW_KEYS keys, set
+ * MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and are not written; where offsets
+ * decrease, other rows may be left unwritten too.  Deterministic for given rows
+ * and a given plan.
  */
 #define MLA_PREFILL_QK_DIM 192
 #define MLA_PREFILL_NOPE_DIM 128
@@ -585,7 +587,8 @@ typedef struct {
   int32_t num_sms;     /* SMs the split is sized for                                   */
   int32_t splits;      /* parts a row's keys are cut into when the queries alone leave
                         * SMs idle; the parts are joined by a second kernel            */
-  int32_t tiles;       /* blocks of up to 256 queries, at most: total_q / 256 + min(batch, total_q) */
+  int32_t tiles;       /* blocks of up to 256 queries, at most: total_q / 256 + min(batch,
+                        * total_q)                                                     */
   int32_t abi_version; /* MLA_ABI_VERSION                                              */
   uint64_t ws_bytes;   /* workspace bytes mla_prefill_fwd needs                        */
   uint64_t ws_lse_offset;     /* float[splits][total_q][num_heads] when splits > 1     */

@@ -219,6 +219,10 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 // worst; with eight tenths 9 %, with 0.95 to 1.1 5 %.)
 constexpr float kTileCost = 1.75f, kJobCost = 3.2f;  // microseconds of two query tiles: a key tile, a job
 constexpr float kFull = 0.9f;
+// Rows that overlap, which decreasing offsets make (and which are reported), could
+// have any number of blocks.  No more are worked on than rows in order can have;
+// sums stay below this, which is more.
+constexpr int32_t kManyBlocks = 1 << 25;
 struct Batch {
   Row row;
   int32_t b0, b1, first, count, total;
@@ -244,8 +248,8 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     const int32_t n = parts_of(r.row.n, kPrefillRows);
     if (n == 0) continue;
     const int32_t least = r.row.block_tiles(causal, 0, kPrefillRows), most = r.row.block_tiles(causal, n - 1, kPrefillRows);
-    blocks += n;
-    halves += parts_of(r.row.n, kTile);
+    blocks = min(blocks + n, kManyBlocks);
+    halves = min(halves + parts_of(r.row.n, kTile), kManyBlocks);
     one = one && r.row.n <= kTile;
     longest = max(longest, most);
     work += n * (kTileCost * 0.5f * (least + most) + kJobCost);
@@ -277,6 +281,7 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     r.first = incl - r.count;
     r.total = __shfl_sync(0xffffffffu, incl, 31);
   }
+  r.total = min(r.total, p.blocks);
   r.at = r.b1;
   r.before = r.count;
   return r;

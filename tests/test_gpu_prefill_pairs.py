@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from mla_decode_attention_08_gb300 import binding
-from .test_gpu_prefill import TIMEOUT, Case
+from .test_gpu_prefill import QO_INDPTR, TIMEOUT, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,16 @@ def test_waits_of_jobs_of_two_tiles_that_run_out_are_reported():
     c.lse.fill_(7.0)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("batch,sms", [(20, 152), (20, 1), (400, 152), (400, 1)])
+def test_offsets_that_go_back_and_forth_are_reported_and_end(batch, sms):
+    """Every second row is the whole of the tokens: many times the blocks that rows in order have."""
+    c = Case([300] + [0] * (batch - 1), [300] + [0] * (batch - 1), heads=2, seed=1, tail=4, sms=sms)
+    c.d_qo.copy_(torch.tensor([0, 300] * (batch // 2) + [0], dtype=torch.int32))
+    c.run()
+    assert binding.mla_decode_read_error(c.ws) & QO_INDPTR
+    assert (c.out[300:] == 7.0).all() and (c.lse[300:] == 7.0).all()
+    d = Case([300], [300], heads=2, seed=1, sms=sms)
+    d.run()
+    d.check()
