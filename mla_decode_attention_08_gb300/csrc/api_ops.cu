@@ -172,6 +172,29 @@ int32_t key_splits(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms
   return static_cast<int32_t>(best);
 }
 
+// Whether one row of n queries over `keys` keys takes less time in jobs of one query
+// tile than in jobs of two: the longest job, or an SM's share of all, or, as far as
+// they are alike, rounds of them.  (Microseconds of an SM for a job's key tile and for
+// a job: 0.95 and 3.0, of two query tiles 1.75 and 3.2.  16 heads, 2560 queries over
+// 8560 keys, 160 jobs of two tiles for 152 SMs: 156 us, that way 168.)
+bool faster_in_pairs(int64_t n, int64_t keys, bool causal, int64_t heads, int64_t sms) {
+  auto time = [&](int64_t size, double tile, double job) {
+    const int64_t blocks = (n + size - 1) / size;
+    auto tiles = [&](int64_t queries) {  // that the last of a row's first `queries` sees
+      const int64_t seen = causal ? keys - n + queries : keys;
+      return seen > 0 ? (seen + 127) / 128 : 0;
+    };
+    const double last = tile * tiles(n) + job, first = tile * tiles(size < n ? size : n) + job;
+    const double jobs = static_cast<double>(blocks * heads), share = jobs * 0.5 * (first + last) / sms;
+    const double rounds = std::ceil(jobs / sms) * last;
+    double alike = 2.0 * (first + last) / last - 3.0;
+    alike = alike < 0.0 ? 0.0 : alike > 1.0 ? 1.0 : alike;
+    const double all = rounds > share ? share + (rounds - share) * alike : share;
+    return all > last ? all : last;
+  };
+  return time(128, 0.95, 3.0) < time(256, 1.75, 3.2);
+}
+
 // The plan's fields for a number of parts; false if it cannot be run.
 bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_heads, int32_t num_sms,
                  int32_t splits, mla_prefill_plan_t* out) {
@@ -266,6 +289,12 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   p.heads = heads;
   p.total_q = plan->total_q;
   p.blocks = static_cast<int32_t>(most_blocks(plan->total_q, plan->batch));
+  p.walk = mla::kWalkByRows;
+  if (plan->splits > 1)
+    p.walk = mla::kWalkPairs;
+  else if (plan->batch == 1)  // the row that was planned for
+    p.walk = faster_in_pairs(plan->total_q, plan->max_kv_len, causal != 0, heads, plan->num_sms) ? mla::kWalkPairs
+                                                                                               : mla::kWalkTwoTiles;
   p.num_sms = plan->num_sms;
   p.splits = plan->splits;
   p.causal = causal != 0;

@@ -107,6 +107,7 @@ struct PrefillParams {
   float scale;
   int32_t batch, heads, total_q, splits, causal, num_sms;
   int32_t blocks;          // of 128 queries, at most
+  int32_t walk;            // kWalk...
   int64_t total_kv;
   int32_t wide_out;        // out is 32-byte aligned
   int32_t stall_stream;    // test hook: no copies are issued, so the waits run out
@@ -116,6 +117,8 @@ struct PrefillMaps {
 };
 constexpr int kPrefillQk = MLA_PREFILL_QK_DIM, kPrefillNope = MLA_PREFILL_NOPE_DIM;
 constexpr int kPrefillRope = kPrefillQk - kPrefillNope, kPrefillV = MLA_PREFILL_V_DIM;
+// Jobs of two query tiles, of one whose key tiles alternate, or as the rows say.
+constexpr int32_t kWalkByRows = 0, kWalkTwoTiles = 1, kWalkPairs = 2;
 constexpr int kPrefillRows = 256;  // query rows of a job: two tiles of 128
 size_t prefill_smem_bytes();
 cudaError_t prefill_prepare();

@@ -213,10 +213,11 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 // run of consecutive rows a lane, and the batch's blocks from the last one on; that
 // many rows even out.
 //
-// Pairs, when no row has more than a tile of queries, when the keys are cut into
-// parts, or when the longest job of two tiles takes longer than nine tenths of an
-// SM's share of all jobs.  (Of 33 batches the wrong way was taken for three, 1 % at
-// worst; with eight tenths 9 %, with 0.95 to 1.1 5 %.)
+// Pairs, when no row has more than a tile of queries, when the host says so, or, if
+// it leaves that open, when the longest job of two tiles takes longer than nine
+// tenths of an SM's share of all jobs.  (Of 40 batches the slower way is taken for
+// three, by 5, 6 and 14 %; with eight tenths or 0.95 for more.  All that the host
+// weighs for one row, weighed here, would right them, but at 0.3 to 0.9 us a call.)
 constexpr float kTileCost = 1.75f, kJobCost = 3.2f;  // microseconds of two query tiles: a key tile, a job
 constexpr float kFull = 0.9f;
 // Rows that overlap, which decreasing offsets make (and which are reported), could
@@ -254,8 +255,8 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     longest = max(longest, most);
     work += n * (kTileCost * 0.5f * (least + most) + kJobCost);
   }
-  bool pairs = p.splits > 1 || __all_sync(0xffffffffu, one);
-  if (!pairs) {
+  bool pairs = p.walk == kWalkPairs || __all_sync(0xffffffffu, one);
+  if (p.walk == kWalkByRows && !pairs) {
     longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) work += __shfl_xor_sync(0xffffffffu, work, d);
