@@ -108,7 +108,11 @@ struct Misc {
   uint64_t o_full[2];   // the job's last product of tile t complete
   uint64_t o_free[2];   // the job's O_t read out
   uint64_t turn[2];     // the other tile's products are issued
-  uint64_t v_clean;     // V behind the row's end is zeroed
+  // Key tile T's V, T & 1, is zeroed behind the row's end.  One a buffer: issuer 0 can
+  // be a tile ahead of issuer 1, which may not yet have looked at V(T) when V(T + 1) is
+  // zeroed.  Of one buffer it cannot: V(T + 2) is zeroed after K(T + 2) was copied, hence
+  // after both issuers released V(T), which issuer 1 does behind its wait.
+  uint64_t v_clean[2];
   // Pairs: of buffer b, K and V released; the query tile released by both issuers;
   // softmax b's maximum and sum written and O_b complete.
   uint64_t pair_k_empty[2], pair_v_empty[2], pair_q_empty, joined[2];
@@ -534,7 +538,8 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
   constexpr int kHeadSteps = 6;  // k-steps of 16 keys in p_head
   // A wait of this warp; tile 0 starts, so its first turn is the phase before the first.
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity & 1, ms, p.err); };
-  uint32_t turns = t, T = 0, mine = 0, jobs = 0, cleans = 0;
+  // (bit b of clean_phase: the phase of v_clean[b] to wait for next)
+  uint32_t turns = t, T = 0, mine = 0, jobs = 0, clean_phase = 0;
   bool duo = false;  // both tiles have keys: they take turns
   // S_t = Q_t . K(T)^T (one lane)
   auto qk = [&](uint32_t tile, bool last, bool hand_over) {
@@ -577,10 +582,12 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
           const uint32_t f = T * kFillsPerTile + kKPanels;
           clean_v(block_memory(ms, kOffRing + ring_slot(f) * kPanelBytes),
                   block_memory(ms, kOffRing + ring_slot(f + 1) * kPanelBytes), job.len % kTile);
-          if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms->v_clean));
+          if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms->v_clean[T & 1]));
           __syncwarp();
+        } else {
+          ok = on(&ms->v_clean[T & 1], clean_phase >> (T & 1));
+          clean_phase ^= 1u << (T & 1);
         }
-        ok = t == 0 || on(&ms->v_clean, cleans);
       }
       // K(T + 1) has mostly landed too; looked at here, it costs no pause between
       // the products.
@@ -628,7 +635,6 @@ __device__ __forceinline__ void run_mma(const PrefillParams& p, Misc* ms, uint32
       __syncwarp();
     }
     jobs += nt > 0;
-    cleans += clean >= 0;
   }
   if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
   __syncwarp();
@@ -974,6 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ms->job_full[t]), 1);
       mbar_init(smem_u32(&ms->job_empty[t]), kJobReaders);
       mbar_init(smem_u32(&ms->turn[t]), 1);
+      mbar_init(smem_u32(&ms->v_clean[t]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ms->pair_k_empty[b]), 1);
@@ -982,7 +989,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ms->pair_q_empty), 2);
     mbar_init(smem_u32(&ms->claim), 1);
-    mbar_init(smem_u32(&ms->v_clean), 1);
     mbar_init(smem_u32(&ms->mma_done), 2);
     ms->abort_flag = 0;
     fence_mbar_init();
