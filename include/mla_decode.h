@@ -570,9 +570,10 @@ mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const 
  * scores must be finite; what lies outside the rows (padding, other rows' tokens)
  * may hold anything.  No output may overlap an input.  Rows outside total_q or
  * total_kv, or with more than MLA_PREFILL_MAX_ROW_KEYS keys, set
- * MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and are not written; where offsets
- * decrease, other rows may be left unwritten too.  Deterministic for given rows
- * and a given plan.
+ * MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and are not written; where offsets of
+ * queries decrease, other rows may be left unwritten too (all of them when the
+ * keys are split), and so may any row of a call that reports MLA_DERR_TIMEOUT.
+ * Deterministic for given rows and a given plan.
  */
 #define MLA_PREFILL_QK_DIM 192
 #define MLA_PREFILL_NOPE_DIM 128

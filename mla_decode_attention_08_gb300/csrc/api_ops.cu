@@ -312,6 +312,7 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   g.rows = static_cast<int64_t>(plan->total_q) * heads;
   g.pieces = plan->splits;
   g.dim = mla::kPrefillV;
+  g.missing = p.sched + 2;
   g.qo_indptr = qo_indptr;
   g.kv_indptr = kv_indptr;
   g.total_kv = total_kv;
@@ -472,6 +473,7 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
   p.rows = rows;
   p.pieces = num_parts;
   p.dim = dim;
+  p.missing = nullptr;
   p.qo_indptr = p.kv_indptr = nullptr;
   p.total_kv = 0;
   p.batch = p.heads = p.total_q = 0;

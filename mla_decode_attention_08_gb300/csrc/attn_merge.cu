@@ -91,6 +91,9 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
   pdl_wait_primary();
   pdl_launch_dependents();
   if (!wanted) return;
+  // (beside the pieces' loads, looked at before the stores)
+  uint32_t missing = 0;
+  if constexpr (kF32) missing = __ldcg(p.missing);
   const float* lses = p.lses + row;
   Piece<kF32, kVec> x[kGroup];
 #pragma unroll
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
       for (int e = 0; e < kVec / 2; ++e) acc[e] = fma2(w2, x[k].pair(e), acc[e]);
     }
   }
+  if (kF32 && missing != 0) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   uint32_t out[kVec / 2];
 #pragma unroll

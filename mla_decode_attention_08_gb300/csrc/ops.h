@@ -83,6 +83,7 @@ struct MergeParams {
   float* lse_out;          // or null
   int64_t rows;
   int32_t pieces, dim;
+  const uint32_t* missing;   // of float pieces: nonzero if not all were computed, and nothing is to be joined
   const int32_t* qo_indptr;  // of float pieces
   const int32_t* kv_indptr;
   int64_t total_kv;
@@ -103,7 +104,8 @@ struct PrefillParams {
   float* part;             // splits > 1: [splits][total_q][heads][128]
   float* part_lse;         // splits > 1: [splits][total_q][heads]
   int32_t* err;
-  uint32_t* sched;         // jobs handed out, blocks done: both zero between calls
+  uint32_t* sched;         // jobs handed out, blocks done: both zero between calls; then
+                           // whether parts of this call are missing (see MergeParams)
   float scale;
   int32_t batch, heads, total_q, splits, causal, num_sms;
   int32_t blocks;          // of 128 queries, at most

@@ -195,13 +195,15 @@ struct Row {
     return tiles(causal, min(n, (i + 1) * size) - 1);
   }
 };
-__device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool report) {
+// (`back`: set when the row ends before it begins; a bad row is reported by one block.)
+__device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool report, bool& back) {
   Row r = {0, 0, 0, 0};
   if (b >= p.batch) return r;
   const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
   const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
   const bool bad_q = qs < 0 || qe < qs || qe > p.total_q;
   const bool bad_k = ks < 0 || ke < ks || ke > p.total_kv || ke - ks > MLA_PREFILL_MAX_ROW_KEYS;
+  back = back || qe < qs;
   if (report && (bad_q || bad_k))
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
   if (!bad_q && !bad_k) r = Row{qs, qe - qs, ks, ke - ks};
@@ -225,8 +227,10 @@ __device__ __forceinline__ Row load_row(const PrefillParams& p, int32_t b, bool 
 constexpr float kTileCost = 1.75f, kJobCost = 3.2f;  // microseconds of two query tiles: a key tile, a job
 constexpr float kFull = 0.9f;
 // Rows that overlap, which decreasing offsets make (and which are reported), could
-// have any number of blocks.  No more are worked on than rows in order can have;
-// sums stay below this, which is more.
+// have any number of blocks.  No more are worked on than rows in order can have, so
+// some rows may be left out: the joining kernel is told, which would otherwise join
+// what an earlier call left in the workspace for them.  Sums stay below this, which
+// is more.
 constexpr int32_t kManyBlocks = 1 << 25;
 struct Batch {
   Row row;
@@ -245,11 +249,11 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
   r.b1 = min(p.batch, r.b0 + run);
   const bool causal = p.causal != 0;
   r.row = Row{0, 0, 0, 0};
-  bool one = true;
+  bool one = true, back = false;
   int32_t blocks = 0, halves = 0, longest = 0;
   float work = 0.0f;
   for (int32_t b = r.b0; b < r.b1; ++b) {
-    r.row = load_row(p, b, blockIdx.x == 0);
+    r.row = load_row(p, b, blockIdx.x == 0, back);
     const int32_t n = parts_of(r.row.n, kPrefillRows);
     if (n == 0) continue;
     const int32_t least = r.row.block_tiles(causal, 0, kPrefillRows), most = r.row.block_tiles(causal, n - 1, kPrefillRows);
@@ -258,6 +262,10 @@ __device__ __forceinline__ Batch count_rows(const PrefillParams& p) {
     one = one && r.row.n <= kTile;
     longest = max(longest, most);
     work += n * (kTileCost * 0.5f * (least + most) + kJobCost);
+  }
+  if (blockIdx.x == 0) {
+    back = __any_sync(0xffffffffu, back);
+    if (lane == 0) p.sched[2] = back;  // (of every call anew)
   }
   bool pairs = p.walk == kWalkPairs || __all_sync(0xffffffffu, one);
   if (p.walk == kWalkByRows && !pairs) {
@@ -312,8 +320,9 @@ __device__ __forceinline__ void find_job(const PrefillParams& p, Batch& r, uint3
   } else {
     const int32_t i = r.total - 1 - rank - r.first;
     if (i >= 0 && i < r.count) {
+      bool back = false;
       while (i < r.before) {
-        r.row = load_row(p, --r.at, false);
+        r.row = load_row(p, --r.at, false, back);
         r.before -= parts_of(r.row.n, r.size);
       }
       row = r.row;
@@ -1032,6 +1041,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(ms->tmem_base, kTmemCols);
+    // (Abandoned: the parts are not whole.  Block 0 has written the word long before a wait runs out.)
+    if (one && ms->abort_flag) p.sched[2] = 1;
     // The last block leaves the counters zero for the workspace's next call.
     if (one && atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
       p.sched[0] = 0;
