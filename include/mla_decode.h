@@ -567,7 +567,8 @@ mla_status_t mla_kv_append_bf16kv(const void* kv_bf16, int64_t kv_stride, const 
  * Base pointers are 16-byte aligned; strides are in elements, multiples of 8, at
  * least the row's dims, below 2^36 (tokens or heads outermost; the stride of a
  * single token or head is not used).  Values of the rows' own tokens and their
- * scores must be finite; what lies outside the rows (padding, other rows' tokens)
+ * scores must be finite (a query with a score that is NaN gets NaN, as output and
+ * as lse, under any plan); what lies outside the rows (padding, other rows' tokens)
  * may hold anything.  No output may overlap an input.  Rows outside total_q or
  * total_kv, or with more than MLA_PREFILL_MAX_ROW_KEYS keys, set
  * MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and are not written; where offsets of

@@ -861,7 +861,8 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
     sum += (s0 + s1) + (s2 + s3);
   }
 
-  // Epilogue.  A row that saw no key has sum 0.
+  // Epilogue.  A row that saw no key has sum 0; a NaN score makes it NaN, which reaches
+  // the output and the log-sum-exp (and through them the joined parts).
   if (n > first) {
     if (!warp_wait_on(&ms->o_full[t], jobs & 1, ms, p.err)) return false;
     ++jobs;
@@ -892,7 +893,7 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
     ref = high;
   }
   const bool live = qi < job.nq;
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   const int64_t at = static_cast<int64_t>(job.q0 + qi) * p.heads + job.head;
   const int64_t part_at = static_cast<int64_t>(job.split) * p.total_q * p.heads + at;
   // (one copy of a chunk's code: it runs once a job, and unrolled it is fetched
@@ -942,7 +943,7 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
     __syncwarp();
   }
   if (live) {
-    const float lse = sum > 0.0f ? ref * p.scale + logf(sum) : -INFINITY;
+    const float lse = sum != 0.0f ? ref * p.scale + logf(sum) : -INFINITY;
     if (p.splits > 1)
       p.part_lse[part_at] = lse;
     else if (p.lse != nullptr)
