@@ -139,7 +139,22 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const KvAppendPa
     for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    const float r = rsqrtf(sum * (1.0f / kVDim) + p.eps);
+    float r = rsqrtf(sum * (1.0f / kVDim) + p.eps);
+    // Squares below 2^-126 lose their bits.  Where they may count (no term above
+    // 2^-100, and no eps beside which they vanish: one of 2^-80 is 2^29 times their
+    // mean) the row is scaled by 2^100 first, and eps by its square.
+    if (sum < 0x1p-100f && p.eps < 0x1p-80f) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] *= 0x1p100f;
+        b[i] *= 0x1p100f;
+        sum += a[i] * a[i] + b[i] * b[i];
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      r = rsqrtf(sum * (1.0f / kVDim) + p.eps * 0x1p100f * 0x1p100f);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       a[i] = a[i] * r * wa[i];
