@@ -463,7 +463,7 @@ def _append(fn, kv, norm_weight, rope_table, positions, slots, cache, kv_scale, 
             eps, interleaved, q_pe, q_out, latent_out):
     dev = _device_of(kv, "kv")
     rows = cache.shape
-    if rows[-1] != QK_HEAD_DIM or len(rows) != 2 and (len(rows) != 3 or rows[1] != 1):
+    if len(rows) not in (2, 3) or rows[-1] != QK_HEAD_DIM or len(rows) == 3 and rows[1] != 1:
         raise ValueError(f"the cache must be [rows, 576] or [rows, 1, 576], got {list(rows)}")
     p_kv = _view_ptr(kv, "kv", _BF16, dev)
     p_weight = _ptr(norm_weight, "norm_weight", _BF16, dev)
@@ -511,6 +511,8 @@ def mla_kv_append(kv, norm_weight, rope_table, positions, slots, kv_fp8, kv_scal
     (a negative slot skips the token), ``kv_fp8`` [rows, 576], ``kv_scale`` float32 [1];
     ``q_pe`` -> ``q_out`` bf16 [T, H, 64] (strided; may be one tensor), ``latent_out``
     bf16 [T, 576].  ``workspace``: STEP_WORKSPACE_BYTES, zeroed once."""
+    if kv_scale is not None and not isinstance(kv_scale, _Tensor):
+        _refuse(kv_scale, "kv_scale", _F32T, None)
     if kv_scale is None or kv_scale.numel() != 1:
         raise ValueError("kv_scale must be one float32")
     if not isinstance(kv_fp8, _Tensor) or kv_fp8.dtype not in _E4M3_CODES:
@@ -549,7 +551,7 @@ def _prefill(fn, q, k_nope, k_rope, v, qo_indptr, kv_indptr, out, stream, plan, 
     p_lse = None if lse is None else _ptr(lse, "lse", _F32T, dev)
     p_ws = _workspace(workspace, dev)
     t, h, b = plan.total_q, plan.num_heads, plan.batch
-    n = k_nope.shape[0]
+    n = k_nope.shape[0] if k_nope.shape else 0
     _expect("q", q, (t, h, PREFILL_QK_DIM))
     _expect("k_nope", k_nope, (n, h, PREFILL_NOPE_DIM))
     _expect("k_rope", k_rope, (n, PREFILL_QK_DIM - PREFILL_NOPE_DIM))
