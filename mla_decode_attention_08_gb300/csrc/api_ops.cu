@@ -300,6 +300,7 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   p.splits = plan->splits;
   p.causal = causal != 0;
   p.total_kv = total_kv;
+  p.part_rows = static_cast<int64_t>((workspace_bytes - plan->ws_partial_offset) / (mla::kPrefillV * sizeof(float)));
   p.wide_out = aligned(out, 32) ? 1 : 0;
   p.stall_stream = stall_stream ? 1 : 0;
   st = launched(mla::launch_prefill(p, m, stream));
@@ -319,6 +320,8 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   g.batch = plan->batch;
   g.heads = heads;
   g.total_q = plan->total_q;
+  g.part_rows = p.part_rows;
+  g.err = p.err;
   return launched(mla::launch_attn_merge(g, true, stream));
 }
 
@@ -477,6 +480,8 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
   p.qo_indptr = p.kv_indptr = nullptr;
   p.total_kv = 0;
   p.batch = p.heads = p.total_q = 0;
+  p.part_rows = 0;
+  p.err = nullptr;
   return launched(mla::launch_attn_merge(p, false, stream));
 }
 

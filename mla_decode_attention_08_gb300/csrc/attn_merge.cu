@@ -5,6 +5,7 @@
 // out = sum_s w_s part_s / sum_s w_s and lse = m + log sum_s w_s.  A thread owns
 // four to 16 values of a row: it reads the row's few lses (the row's threads read
 // the same ones) and each piece once.  Bound by the bytes of the pieces.
+#include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -93,7 +94,12 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
   if (!wanted) return;
   // (beside the pieces' loads, looked at before the stores)
   uint32_t missing = 0;
-  if constexpr (kF32) missing = __ldcg(p.missing);
+  if constexpr (kF32) {
+    missing = __ldcg(p.missing);
+    if (!MLA_DCHECK(dim0 + kVec <= p.dim && p.dim == 128 && p.rows == static_cast<int64_t>(p.total_q) * p.heads &&
+                        p.pieces * p.rows <= p.part_rows, p.err))
+      return;
+  }
   const float* lses = p.lses + row;
   Piece<kF32, kVec> x[kGroup];
 #pragma unroll

@@ -8,6 +8,7 @@
 // goes through shared memory.  Bound by bytes for many tokens (8192 of them with
 // 16 heads into a bf16 cache with the dense copy: 64 MB in 9.4 us, part of it out
 // of L2), by one trip to memory and the launch for few (256 tokens: 2.6 us).
+#include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
 #include "schedule.h"
@@ -58,6 +59,7 @@ template <bool kE4m3>
 __device__ __forceinline__ void store_cache8(const KvAppendParams& p, int32_t slot, int dim,
                                              const float (&x)[8], float scale) {
   const int64_t at = static_cast<int64_t>(slot) * kQkDim + dim;
+  if (!MLA_DCHECK(at >= 0 && dim + 8 <= kQkDim && at + 8 <= p.kv_rows * kQkDim, p.err)) return;
   if constexpr (kE4m3)
     *reinterpret_cast<uint2*>(p.cache + at) = codes8(x, scale);
   else
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const KvAppendPa
     store_cache8<kE4m3>(p, slot, 8 * lane, a, scale);
     store_cache8<kE4m3>(p, slot, kVDim / 2 + 8 * lane, b, scale);
     uint16_t* dense = p.latent_out == nullptr ? nullptr : p.latent_out + t * kQkDim;
+    if (!MLA_DCHECK(!turns || (first >= kVDim && second + 8 <= kQkDim), p.err)) return;
     if (dense != nullptr) {
       *reinterpret_cast<uint4*>(dense + 8 * lane) = pack8(a);
       *reinterpret_cast<uint4*>(dense + kVDim / 2 + 8 * lane) = pack8(b);
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const KvAppendPa
   const int first = first_piece<kInterleaved>(lane & 3), second = first + second_piece<kInterleaved>();
   const uint16_t* src = p.q_pe + t * p.q_token_stride + h * p.q_head_stride;
   uint16_t* dst = p.q_out + t * p.qo_token_stride + h * p.qo_head_stride;
+  if (!MLA_DCHECK(t < p.num_tokens && h >= 0 && max(first, second) + 8 <= kRopeDim, p.err)) return;
   const uint4 r0 = load16(src + first), r1 = load16(src + second);
   if (slot < 0 || slot >= p.kv_rows || pos < 0 || pos >= p.max_positions) return;  // reported by the token's first warp
   float c[8], s[8], u[8], v[8];

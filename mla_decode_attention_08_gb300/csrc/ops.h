@@ -88,6 +88,9 @@ struct MergeParams {
   const int32_t* kv_indptr;
   int64_t total_kv;
   int32_t batch, heads, total_q;
+  // of float pieces, for the debug build's checks: rows that the workspace has room for, and the error word
+  int64_t part_rows;
+  int32_t* err;
 };
 // Whether float parts of `rows` rows of 128 are joined by threads that are all on the
 // GPU at once: four values each, two blocks of 256 an SM.
@@ -111,6 +114,7 @@ struct PrefillParams {
   int32_t blocks;          // of 128 queries, at most
   int32_t walk;            // kWalk...
   int64_t total_kv;
+  int64_t part_rows;       // rows of parts that the workspace has room for (for the debug build's checks)
   int32_t wide_out;        // out is 32-byte aligned
   int32_t stall_stream;    // test hook: no copies are issued, so the waits run out
 };

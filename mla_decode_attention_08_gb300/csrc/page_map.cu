@@ -12,6 +12,7 @@
 // entry.  A page the step itself hands out is read from free_pages at its
 // prefix, not from the table, so that no entry depends on another block's
 // table writes.
+#include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -91,6 +92,9 @@ __device__ __forceinline__ RowView view_row(const PageMapParams& p, const uint32
 
 // Page pg of the row; -1 (with the error bit) when its id is not a page of the pool.
 __device__ __forceinline__ int32_t page_id(const PageMapParams& p, const RowView& r, uint32_t pg) {
+  if (!MLA_DCHECK(pg < r.pages_before ? pg < static_cast<uint32_t>(p.max_pages)
+                                      : r.need0 + (pg - r.pages_before) < static_cast<uint32_t>(p.num_free), p.err))
+    return -1;
   const int32_t id = pg < r.pages_before ? r.table[pg] : __ldg(p.free_pages + r.need0 + (pg - r.pages_before));
   if (id < 0 || id >= p.num_pages) {
     atomicOr(p.err, MLA_DERR_KV_INDEX);
@@ -211,8 +215,9 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapParams 
   for (uint32_t i = gtid; i < total.pages; i += gthreads) {
     const int32_t b = row_of(pages, 0, n, i);
     const RowView r = view_row(p, kv, fresh, pages, b);
-    p.block_table[static_cast<int64_t>(b) * p.table_stride + r.pages_before + (i - r.need0)] =
-        __ldg(p.free_pages + i);
+    const uint32_t column = r.pages_before + (i - r.need0);
+    if (MLA_DCHECK(b < n && column < static_cast<uint32_t>(p.max_pages) && i < static_cast<uint32_t>(p.num_free), p.err))
+      p.block_table[static_cast<int64_t>(b) * p.table_stride + column] = __ldg(p.free_pages + i);
   }
   // The index of every cached token, four at a time: each block a contiguous
   // share, whose rows are found first, so that a thread searches among those.
@@ -251,6 +256,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const PageMapParams 
         if (k < 3) id = page_id(p, r, pg);
       }
     }
+    if (!MLA_DCHECK(min(4 * u + 4, total.kv) <= static_cast<uint32_t>(p.kv_indices_len) && b <= n, p.err)) continue;
     if (4 * u + 4 <= total.kv) {
       *reinterpret_cast<int4*>(p.kv_indices + 4 * u) = make_int4(v[0], v[1], v[2], v[3]);
     } else {

@@ -381,6 +381,14 @@ struct Loads {
 // and 105 with the next job taken as a job starts.)
 constexpr int32_t kClaimTiles = 1;
 
+// Whether a copy that starts at this token does so inside its tensor (debug build; a
+// failed check ends the call through the abort flag).
+__device__ __forceinline__ bool copy_ok(const PrefillParams& p, Misc* ms, const Job& job, int32_t token, int64_t tokens) {
+  if (MLA_DCHECK(token >= 0 && token < tokens && job.head >= 0 && job.head < p.heads, p.err)) return true;
+  ms->abort_flag = 1;
+  return false;
+}
+
 // The copies of one job (lane 0).
 __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMaps& m, Misc* ms, uint32_t sbase,
                                          const Job& job, Loads& l, uint64_t keep, uint64_t once) {
@@ -389,6 +397,7 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
   if (n == 0) mbar_arrive(smem_u32(&ms->claim));
   auto load_q = [&](int t, uint32_t& count) {
     if (!wait_on(&ms->q_empty[t], (count + 1) & 1, ms, p.err)) return false;  // (the first passes)
+    if (!copy_ok(p, ms, job, job.q0 + t * kTile, p.total_q)) return false;
     ++count;
     const uint32_t bar = smem_u32(&ms->q_full[t]);
     mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
@@ -402,6 +411,7 @@ __device__ __forceinline__ bool load_job(const PrefillParams& p, const PrefillMa
     const int32_t key = job.k0 + (job.j0 + j) * kTile;
     if (j == claim) mbar_arrive(smem_u32(&ms->claim));
     if (T > 1 && !wait_on(&ms->v_empty[T & 1], ((T >> 1) + 1) & 1, ms, p.err)) return false;
+    if (!copy_ok(p, ms, job, key, p.total_kv)) return false;
     uint32_t bar = smem_u32(&ms->k_full[T & 1]);
     mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
     tma_load_3d(ring + ring_slot(f) * kPanelBytes, &m.k_nope, 0, job.head, key, bar, keep);
@@ -434,6 +444,7 @@ __device__ __forceinline__ bool load_pair_job(const PrefillParams& p, const Pref
     const int32_t key = job.k0 + (job.j0 + j) * kTile;
     if (j == claim) mbar_arrive(smem_u32(&ms->claim));
     if (!wait_on(&ms->pair_k_empty[b], before, ms, p.err)) return false;
+    if (!copy_ok(p, ms, job, key, p.total_kv)) return false;
     uint32_t bar = smem_u32(&ms->k_full[b]), dst = sbase + kOffPairK + b * kKPanels * kPanelBytes;
     mbar_arrive_expect_tx(bar, kKPanels * kPanelBytes);
     tma_load_3d(dst, &m.k_nope, 0, job.head, key, bar, keep);
@@ -442,6 +453,7 @@ __device__ __forceinline__ bool load_pair_job(const PrefillParams& p, const Pref
     ++l.k;
     if (j == 0) {
       if (!wait_on(&ms->pair_q_empty, (l.q0 + 1) & 1, ms, p.err)) return false;
+      if (!copy_ok(p, ms, job, job.q0, p.total_q)) return false;
       ++l.q0;
       bar = smem_u32(&ms->q_full[0]);
       mbar_arrive_expect_tx(bar, kQPanels * kPanelBytes);
@@ -892,7 +904,11 @@ __device__ __forceinline__ bool softmax_job(const PrefillParams& p, Misc* ms, ui
     sum = weight * sum + other_weight * other.y;
     ref = high;
   }
-  const bool live = qi < job.nq;
+  bool live = qi < job.nq;
+  if (live)
+    live = MLA_DCHECK(job.q0 >= 0 && job.q0 + qi < p.total_q && job.head >= 0 && job.head < p.heads && job.split >= 0 &&
+                          job.split < p.splits &&
+                          (p.splits == 1 || static_cast<int64_t>(p.splits) * p.total_q * p.heads <= p.part_rows), p.err);
   const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
   const int64_t at = static_cast<int64_t>(job.q0 + qi) * p.heads + job.head;
   const int64_t part_at = static_cast<int64_t>(job.split) * p.total_q * p.heads + at;
