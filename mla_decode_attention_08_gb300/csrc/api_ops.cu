@@ -159,7 +159,7 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
 int32_t key_splits(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms, int64_t rows) {
   // (The second kernel looks for its tokens' rows, so thousands of empty ones are not cut.)
   if (blocks == 0 || 10 * blocks >= 13 * sms || batch > 1024) return 1;
-  const bool few = mla::merges_at_once(rows);
+  const bool few = mla::merges_at_once(rows, static_cast<int32_t>(sms));
   auto time = [&](int64_t s) {
     const int64_t jobs = blocks * s, longest = 40 + 19 * ((key_tiles + s - 1) / s);
     const int64_t mean = 40 + 19 * ((7 * key_tiles + 10 * s - 1) / (10 * s));
@@ -320,6 +320,7 @@ mla_status_t run_prefill(const void* q, int64_t q_token_stride, int64_t q_head_s
   g.batch = plan->batch;
   g.heads = heads;
   g.total_q = plan->total_q;
+  g.num_sms = plan->num_sms;
   g.part_rows = p.part_rows;
   g.err = p.err;
   return launched(mla::launch_attn_merge(g, true, stream));
@@ -479,7 +480,7 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
   p.missing = nullptr;
   p.qo_indptr = p.kv_indptr = nullptr;
   p.total_kv = 0;
-  p.batch = p.heads = p.total_q = 0;
+  p.batch = p.heads = p.total_q = p.num_sms = 0;
   p.part_rows = 0;
   p.err = nullptr;
   return launched(mla::launch_attn_merge(p, false, stream));

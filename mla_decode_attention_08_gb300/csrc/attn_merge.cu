@@ -163,7 +163,7 @@ cudaError_t launch_vec(const MergeParams& p, cudaStream_t stream) {
 
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream) {
   // (The parts are rows of 128.)
-  if (f32_parts) return merges_at_once(p.rows) ? launch_vec<true, 4, 16>(p, stream) : launch_vec<true, 8, 4>(p, stream);
+  if (f32_parts) return merges_at_once(p.rows, p.num_sms) ? launch_vec<true, 4, 16>(p, stream) : launch_vec<true, 8, 4>(p, stream);
   return p.dim % 16 == 0 ? launch_vec<false, 16, 4>(p, stream) : launch_vec<false, 8, 4>(p, stream);
 }
 

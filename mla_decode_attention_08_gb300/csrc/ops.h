@@ -87,14 +87,14 @@ struct MergeParams {
   const int32_t* qo_indptr;  // of float pieces
   const int32_t* kv_indptr;
   int64_t total_kv;
-  int32_t batch, heads, total_q;
+  int32_t batch, heads, total_q, num_sms;
   // of float pieces, for the debug build's checks: rows that the workspace has room for, and the error word
   int64_t part_rows;
   int32_t* err;
 };
 // Whether float parts of `rows` rows of 128 are joined by threads that are all on the
 // GPU at once: four values each, two blocks of 256 an SM.
-inline bool merges_at_once(int64_t rows) { return rows * (128 / 4) <= 152 * 2 * 256; }
+inline bool merges_at_once(int64_t rows, int32_t sms) { return rows * (128 / 4) <= static_cast<int64_t>(sms) * 2 * 256; }
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
 
 // mla_prefill_fwd: a persistent block an SM; a job is up to 256 queries of a row
