@@ -428,7 +428,10 @@ mla_status_t mla_mxfp4_quantize(const void* src_bf16, int64_t rows, void* dst_fp
  * step: mla_page_map (lengths -> tables and maps), mla_kv_append (new tokens ->
  * cache), then mla_decode_fwd over kv_indptr / kv_indices, or mla_prefill_fwd
  * over the prompt's expanded keys and values (in pieces joined by
- * mla_attn_merge when the keys are attended a part at a time).
+ * mla_attn_merge when the keys are attended a part at a time).  Of the decode calls
+ * mla_decode_fwd alone takes kv_indices, so that order is the e4m3 cache's;
+ * mla_decode_fwd_bf16kv reads rows that lie one behind the other, as
+ * mla_kv_append_bf16kv leaves them only where a row's pages do.
  *
  * As on the forward path nothing is allocated and nothing synchronises, work is
  * ordered on `stream`, the device of the pointers must be current, and every
@@ -453,7 +456,8 @@ mla_status_t mla_mxfp4_quantize(const void* src_bf16, int64_t rows, void* dst_fp
  *               the page-size-1 table of mla_decode_fwd
  *   positions[qo_indptr[b] + i]  = L_b + i                            for i < n_b
  *   slots[qo_indptr[b] + i]      = the cache row of that token, as in kv_indices
- *   pages_used[0] = pages taken from free_pages
+ *   pages_used[0] = pages taken from free_pages (a caller that has the lengths on
+ *               the host as well need not read it back before its next step)
  * slots past the last new token are set to -1 and positions there to 0 up to
  * slots_len, so that an append launched for slots_len tokens skips them;
  * kv_indices past the last token keeps its values.  Table entries other than the
@@ -590,7 +594,7 @@ typedef struct {
   int32_t splits;      /* parts a row's keys are cut into when the queries alone leave
                         * SMs idle; the parts are joined by a second kernel            */
   int32_t tiles;       /* blocks of up to 256 queries, at most: total_q / 256 + min(batch,
-                        * total_q)                                                     */
+                        * total_q) (for the caller; launches count blocks of 128)      */
   int32_t abi_version; /* MLA_ABI_VERSION                                              */
   uint64_t ws_bytes;   /* workspace bytes mla_prefill_fwd needs                        */
   uint64_t ws_lse_offset;     /* float[splits][total_q][num_heads] when splits > 1     */

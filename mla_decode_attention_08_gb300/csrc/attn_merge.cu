@@ -54,7 +54,7 @@ struct Piece {
 
 // Whether `token` is one that mla_prefill_fwd has computed: it belongs to a row,
 // and the row's tokens and keys lie in their tensors.  (A batch whose keys are
-// split has few rows.)
+// split has at most 1024 rows; the plan does not cut more.)
 __device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
   for (int32_t b = 0; b < p.batch; ++b) {
     const int32_t qs = __ldcg(p.qo_indptr + b), qe = __ldcg(p.qo_indptr + b + 1);
@@ -72,7 +72,7 @@ __device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
 // multiple of 16 long a thread takes 16 of its values, which halves what the
 // weights cost (the kernel issues on 8 of 10 cycles with eight).  Four pieces of
 // 16384 x 16 rows of 128: 67 us with eight values and the weights first, 55 with the
-// values beside them, 49.6 us with 16 (6.9 TB/s; a copy reaches 6.7).
+// values beside them, 49.5 us with 16 (6.9 TB/s; a copy reaches 6.7).
 // kGroup pieces' loads are in flight together: 16, with four values a thread, where
 // a prompt's few rows have all their threads on the GPU at once and the trips to L2
 // are what costs (64 queries x 16 heads of nine float32 parts: 19.3 us with the

@@ -5,9 +5,11 @@
 // the 512 latent values (16 a lane, sum of squares by shuffles), rotates the
 // key and writes the cache row, the others rotate eight heads of the query
 // each (four lanes a head).  Every value is read once and written once; nothing
-// goes through shared memory.  Bound by bytes for many tokens (8192 of them with
-// 16 heads into a bf16 cache with the dense copy: 64 MB in 9.4 us, part of it out
-// of L2), by one trip to memory and the launch for few (256 tokens: 2.6 us).
+// goes through shared memory.  Bound by the way to memory: a warp loads once and is
+// done, so few bytes are in flight.  8192 tokens with 16 heads into a bf16 cache with the
+// dense copy, 64 MB: 9 us where the inputs are in L2, 14.7 us out of DRAM (a quarter of
+// its rate, warps waiting for loads); into an e4m3 cache 13.3 and 19.0 us, as the codes'
+// float32 divisions add to the chain.  256 tokens, a launch and one trip: 2.7 us.
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"

@@ -32,9 +32,15 @@
 // Bound by the chain of one tile (scores 768 cycles of the tensor pipe, softmax
 // ~1250, values 512, and the looks at barriers between them) against the other
 // tile's: ~3300 cycles for a key tile of both where the pipe alone needs 2560,
-// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 753-765 us,
-// 1.8 PFLOP/s, with the SM clock below 1.8 GHz under the power limit (a plain bf16
-// product sustains 1.77 PFLOP/s there); 12 prompts of up to 2047 tokens: 98 us.
+// and ~6700 more a job.  One prompt of 16384 tokens, 16 heads, causal: 753-770 us,
+// 1.8 PFLOP/s, in a burst of five (a plain bf16 product reaches 1.97 in one); over
+// thousands of calls 858 us, 1.6 PFLOP/s, with the SM clock at 1.65 GHz under the power
+// limit (a plain product sustains 1.77).  12 prompts of up to 2047 tokens: 96-98 us.
+//
+// P is rounded to bf16 because the second product's operands have one type and V is
+// bf16; its sum is taken before the rounding, whose errors have independent signs.  Both
+// roundings together leave the output 0.0018 to 0.0022 off in the 2-norm, where rounding
+// the output alone leaves 0.0016.  The exponential's approximation (2^-22) is far below.
 #include <cstddef>
 
 #include "ops.h"
