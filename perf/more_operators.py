@@ -129,7 +129,7 @@ def work(case):
         pages = sum(-(-t // page) - f for t, f in zip(total, first))
         tokens = sum(t - f * page for t, f in zip(total, first))
         elem = 1 if case["cache"] == "e4m3" else 2
-        return {"bytes": tokens * DIM * elem + pages * DIM * 2 + 8 * sum(new), "flops": tokens * DIM}
+        return {"bytes": tokens * DIM * elem + pages * DIM * 2 + 4 * sum(new), "flops": tokens * DIM}
     if op == "scores":
         q, blocks = _rows(case)[0], sum(_blocks(case))
         pairs = sum(n * b for n, b in zip(q, _blocks(case)))
@@ -187,7 +187,6 @@ def prepare(case, seed):
         i = torch.arange(sum(new), device="cuda")
         row = torch.searchsorted(at[1:], i, right=True)
         pos = (_ints(total) - _ints(new))[row] + i - at[row]
-        s["positions"] = pos.int()
         s["slots"] = (table[row, pos // page] * page + pos % page).int()
         if case["cache"] == "e4m3":
             s["pool"], s["scale"] = _e4m3(g, pool * page), torch.full((1,), 1.0 / 60.0, device="cuda")
@@ -240,9 +239,9 @@ def _own_attention(s):
 def _own_means(s):
     more = dict(page_size=s["page"], workspace=s["ws"])
     if s["cache"] == "e4m3":
-        s["lib"].mla_block_means(s["pool"], s["scale"], s["positions"], s["slots"], s["means"], **more)
+        s["lib"].mla_block_means(s["pool"], s["scale"], s["slots"], s["means"], **more)
     else:
-        s["lib"].mla_block_means_bf16kv(s["pool"], s["positions"], s["slots"], s["means"], **more)
+        s["lib"].mla_block_means_bf16kv(s["pool"], s["slots"], s["means"], **more)
     return [s["means"]]
 
 
@@ -287,12 +286,12 @@ def _plain_attention(s):
 
 
 def _plain_means(s):
-    page, pos, slots = s["page"], s["positions"].long(), s["slots"].long()
+    page, slots = s["page"], s["slots"].long()
     # tokens that end their page, or with which their row ends
-    goes_on = torch.cat([pos[1:] == pos[:-1] + 1, pos.new_zeros(1, dtype=torch.bool)])
-    ends = (pos % page == page - 1) | ~goes_on
-    ends = torch.sort(ends.int(), descending=True, stable=True).indices[:s["num_pages"]]
-    pages, count = slots[ends] // page, (pos[ends] % page + 1)[:, None]
+    goes_on = torch.cat([slots[1:] == slots[:-1] + 1, slots.new_zeros(1, dtype=torch.bool)])
+    ends = (slots % page == page - 1) | ~goes_on
+    ends = slots[torch.sort(ends.int(), descending=True, stable=True).indices[:s["num_pages"]]]
+    pages, count = ends // page, (ends % page + 1)[:, None]
     x = s["pool"].view(torch.float8_e4m3fn) if s["cache"] == "e4m3" else s["pool"]
     x = x.unflatten(0, (-1, page))[pages].float()
     inside = torch.arange(page, device=slots.device) < count
