@@ -205,7 +205,7 @@ def prepare(case, seed):
         else:
             # kept to few bits, so that some are alike
             s["scores"] = torch.randn(s["table"].shape, generator=g, device="cuda").bfloat16().float()
-            s["total"] = sum(_chosen_tokens(case))
+            s["total"], s["num_pages"] = sum(_chosen_tokens(case)), pool
             s["out"] = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (case["batch"] + 1, s["total"])]
             s["chosen"] = torch.empty(case["batch"], case["blocks"], dtype=torch.int32, device="cuda")
     if own:
@@ -254,7 +254,8 @@ def _own_scores(s):
 def _own_select(s):
     indptr, indices = s["out"]
     s["lib"].mla_block_select(s["scores"], s["table"], s["kv_indptr"], indptr, indices, page_size=s["page"],
-                              blocks=s["blocks"], sink=1, recent=2, chosen=s["chosen"], workspace=s["ws"])
+                              num_pages=s["num_pages"], blocks=s["blocks"], sink=1, recent=2, chosen=s["chosen"],
+                              workspace=s["ws"])
     return [indptr, indices, s["chosen"]]
 
 
