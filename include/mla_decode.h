@@ -266,6 +266,32 @@ mla_status_t mla_decode_fwd_mxfp4(const void* q_bf16, const void* kv_fp4, const 
                                   const mla_plan_t* plan, int64_t kv_rows, void* workspace,
                                   size_t workspace_bytes);
 
+/*
+ * mla_decode_fwd_lse, mla_decode_fwd_bf16kv_lse, mla_decode_fwd_mxfp4_lse - the same three
+ * steps, which also report each query token's and head's log-sum-exp over the tokens that it
+ * sees, lse_out[t][h] = log sum_j exp(q[t][h] . K[j] / 24), natural, -inf where it sees none:
+ * what mla_attn_merge needs to join the step's output with attention over other keys (see
+ * mla_shared_fwd).
+ *   lse_out  device float [B * qo_len][16], 4-byte aligned.  Written wherever out is.
+ * Every other argument is that of the step without it.
+ */
+mla_status_t mla_decode_fwd_lse(const void* q_bf16, const void* kv_fp8, const float* kv_scale,
+                                const int32_t* qo_indptr, const int32_t* kv_indptr, void* out_bf16,
+                                float* lse_out, cudaStream_t stream, const mla_plan_t* plan,
+                                const int32_t* kv_indices, int64_t kv_indices_len, int64_t kv_rows,
+                                void* workspace, size_t workspace_bytes);
+mla_status_t mla_decode_fwd_bf16kv_lse(const void* q_bf16, const void* kv_bf16,
+                                       const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                       void* out_bf16, float* lse_out, cudaStream_t stream,
+                                       const mla_plan_t* plan, const int32_t* kv_indices,
+                                       int64_t kv_indices_len, int64_t kv_rows, void* workspace,
+                                       size_t workspace_bytes);
+mla_status_t mla_decode_fwd_mxfp4_lse(const void* q_bf16, const void* kv_fp4, const void* kv_scales,
+                                      int32_t scale_bias, const int32_t* qo_indptr,
+                                      const int32_t* kv_indptr, void* out_bf16, float* lse_out,
+                                      cudaStream_t stream, const mla_plan_t* plan, int64_t kv_rows,
+                                      void* workspace, size_t workspace_bytes);
+
 /* The two stages of mla_decode_fwd launched separately (same arguments); the
  * pair is equivalent to one mla_decode_fwd call.  Used to time stage 1 alone.
  * mla_decode_stage1_bf16kv is stage 1 of mla_decode_fwd_bf16kv; stage 2 is
@@ -643,6 +669,159 @@ mla_status_t mla_prefill_fwd_stall_stream(const void* q, int64_t q_token_stride,
 mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t num_parts,
                             int64_t rows, int32_t dim, void* out_bf16, float* lse_out,
                             cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Decode steps over long contexts: a prefix that the rows of a batch share is attended
+ * once for all of them, or a row attends only the pages that a cheap score chooses.
+ *
+ * A shared prefix: mla_shared_fwd over the prefix (its tokens' rows of the cache) and
+ * mla_decode_fwd_lse over each row's own tokens, both with log-sum-exps, are two pieces
+ * that mla_attn_merge joins.  The row's own tokens hold its query tokens', which the
+ * decode step masks; the prefix is seen whole.
+ * Chosen pages: mla_page_map and mla_kv_append as before, mla_block_means (the pages that
+ * the step wrote to), mla_block_scores, mla_block_select, and mla_decode_fwd over
+ * sel_indptr / sel_indices.
+ *
+ * Nothing is allocated and nothing synchronises, work is ordered on `stream`, the device
+ * of the pointers must be current, and every call can be captured into a CUDA graph after
+ * one call outside capture.  The mla_block_* calls take the small workspace of
+ * mla_page_map (only the error word; calls may share it).
+ */
+
+/*
+ * mla_shared_fwd - attention of groups of decode queries over keys that the whole group
+ * sees.  Group g owns query tokens [qo_indptr[g], qo_indptr[g+1]) and keys [kv_indptr[g],
+ * kv_indptr[g+1]); for each of its query tokens t and heads h
+ *   s_j = q[t][h] . K[j] / 24,   out[t][h] = softmax_j(s) . K[j][0:512],
+ *   lse[t][h] = log sum_j exp(s_j)                       (natural)
+ * over all of the group's keys, with K the e4m3 cache's values code * *kv_scale.  A group
+ * without keys gives zeros and lse -inf.  The query enters the products as two e4m3 terms
+ * (exact down to 2^-14 of its token's largest magnitude), a probability as two e4m3 terms
+ * (to 2^-8 of itself, or 2^-16 of the row's largest); accumulation and softmax statistics
+ * are float32; out is rounded once.
+ *   q_bf16     device, bf16 [total_q][16][576], 16-byte aligned.  A token with a value that
+ *              is not finite gets NaN, as output and as lse.
+ *   kv_fp8     device, e4m3fn codes [kv_rows][576], 16-byte aligned.  Codes of the groups'
+ *              keys must be finite; other rows may hold anything.
+ *   kv_scale   device, float[1], positive and finite.
+ *   qo_indptr, kv_indptr  device int32 [batch + 1], non-decreasing.  Empty groups are
+ *              allowed on either side.
+ *   kv_indices device int32 page table (page size 1), as mla_decode_fwd's, or NULL: key j is
+ *              cache row j.  An entry outside [0, kv_rows) sets MLA_DERR_KV_INDEX; row 0 is
+ *              read in its place.
+ *   out_bf16   device, bf16 [total_q][16][512], 16-byte aligned; lse device float
+ *              [total_q][16], or NULL.  Tokens of no group are left alone.
+ *   plan, workspace  from mla_shared_plan; workspace 256-byte aligned, zeroed once (it holds
+ *              the error word, counters that each call leaves zero, and the parts of split
+ *              keys).  Calls sharing a workspace must not overlap on the GPU.
+ * No output may overlap an input.  Groups outside total_q or the keys (kv_indices_len, or
+ * kv_rows), or with more than MLA_SHARED_MAX_KEYS keys, set MLA_DERR_QO_INDPTR /
+ * MLA_DERR_KV_INDPTR and are not written; where offsets of queries decrease, other groups
+ * may be left unwritten too, and so may any group of a call that reports MLA_DERR_TIMEOUT.
+ * Deterministic for given groups and a given plan.
+ */
+#define MLA_SHARED_MAX_GROUPS 65536
+#define MLA_SHARED_MAX_KEYS (1 << 25) /* half a second of one block's work: the waits are bounded */
+typedef struct {
+  int32_t batch;       /* groups                                                      */
+  int32_t total_q;     /* query tokens that q and out have room for (0 allowed)        */
+  int32_t max_kv_len;  /* upper bound on a group's keys (sizes the split only)         */
+  int32_t num_sms;     /* SMs the split is sized for                                   */
+  int32_t splits;      /* parts a group's keys are cut into when the queries alone leave
+                        * SMs idle; the parts are joined by a second kernel            */
+  int32_t abi_version; /* MLA_ABI_VERSION                                              */
+  uint64_t ws_bytes;   /* workspace bytes mla_shared_fwd needs                         */
+  uint64_t ws_lse_offset;     /* float[splits][total_q][16] when splits > 1            */
+  uint64_t ws_partial_offset; /* float[splits][total_q][16][512] when splits > 1       */
+} mla_shared_plan_t;
+
+/* Pure host.  batch 1 .. MLA_SHARED_MAX_GROUPS, total_q and max_kv_len >= 0; num_sms <= 0 asks the device. */
+mla_status_t mla_shared_plan(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_sms,
+                             mla_shared_plan_t* plan);
+
+mla_status_t mla_shared_fwd(const void* q_bf16, const void* kv_fp8, const float* kv_scale,
+                            const int32_t* qo_indptr, const int32_t* kv_indptr, void* out_bf16, float* lse,
+                            cudaStream_t stream, const mla_shared_plan_t* plan, const int32_t* kv_indices,
+                            int64_t kv_indices_len, int64_t kv_rows, void* workspace, size_t workspace_bytes);
+
+/* Test hook for the bounded waits, as mla_decode_fwd_stall_stream: no copy is
+ * issued, every wait runs out, the call reports MLA_DERR_TIMEOUT and returns. */
+mla_status_t mla_shared_fwd_stall_stream(const void* q_bf16, const void* kv_fp8, const float* kv_scale,
+                                         const int32_t* qo_indptr, const int32_t* kv_indptr, void* out_bf16,
+                                         float* lse, cudaStream_t stream, const mla_shared_plan_t* plan,
+                                         const int32_t* kv_indices, int64_t kv_indices_len, int64_t kv_rows,
+                                         void* workspace, size_t workspace_bytes);
+
+/*
+ * mla_block_means - the mean cache row of every page that a step has written to, after
+ * mla_kv_append with the same slots.  A slot s = slots[t] >= 0 ends its page where slots[t+1]
+ * is not s + 1 or lies on the next page; then with P = page_size and page = s / P
+ *   means[page] = bf16(mean of cache rows page P .. s)        (float32 sums, rounded once)
+ * The means of other pages are left alone.  That is the mean of what the page holds when a
+ * row's new tokens stand one behind the other in `slots` and the row's tokens fill the page
+ * from its first row on, as mla_page_map lays them out; negative slots are padding.
+ *   kv_fp8     device e4m3fn codes [kv_rows][576] with kv_scale device float[1] (values code *
+ *              *kv_scale), or kv_bf16 device bf16 [kv_rows][576]; 16-byte aligned.
+ *   slots      device int32 [num_tokens] (num_tokens 0 launches nothing).
+ *   means      device bf16 [num_pages][576], 16-byte aligned.
+ * A slot outside the cache or on a page without a mean sets MLA_DERR_KV_INDEX and is skipped.
+ */
+mla_status_t mla_block_means(const void* kv_fp8, const float* kv_scale, int64_t kv_rows, const int32_t* slots,
+                             int64_t num_tokens, void* means, int32_t num_pages, int32_t page_size,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+mla_status_t mla_block_means_bf16kv(const void* kv_bf16, int64_t kv_rows, const int32_t* slots,
+                                    int64_t num_tokens, void* means, int32_t num_pages, int32_t page_size,
+                                    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * mla_block_scores - what each row's queries score against the means of its pages.  Row b has
+ * query tokens [qo_indptr[b], qo_indptr[b+1]) and kv_indptr[b+1] - kv_indptr[b] cached tokens
+ * on n_b = ceil(tokens / page_size) pages, block_table[b][0 .. n_b):
+ *   scores[b][j] = max over its query tokens t and heads h of q[t][h] . means[block_table[b][j]] / 24
+ * for j < n_b and -inf for n_b <= j < max_pages.  bf16 products, float32 sums; a NaN score
+ * stays NaN.  A row without query tokens scores -inf.
+ *   q_bf16      device bf16 [total_q][16][576], 16-byte aligned.
+ *   means       device bf16 [num_pages][576], 16-byte aligned.
+ *   block_table device int32, row b at block_table + b * table_stride, max_pages entries.
+ *   qo_indptr, kv_indptr  device int32 [batch + 1]; batch 1 .. MLA_MAX_MAP_ROWS.
+ *   scores      device float, row b at scores + b * scores_stride, max_pages entries.
+ * Strides are in elements and at least max_pages.  A page id outside [0, num_pages) sets
+ * MLA_DERR_KV_INDEX and scores -inf; a row outside total_q, or with a negative length or more
+ * than max_pages pages, sets MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and scores -inf throughout.
+ */
+mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* means, int32_t num_pages,
+                              const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                              const int32_t* qo_indptr, const int32_t* kv_indptr, int32_t batch,
+                              int32_t page_size, float* scores, int64_t scores_stride, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * mla_block_select - the pages that each row attends, as the page table of mla_decode_fwd.
+ * Row b (lengths and pages as in mla_block_scores) takes all of its n_b pages if n_b <= blocks;
+ * else `blocks` of them: the first `sink`, the last `recent`, and of the others those with the
+ * highest scores, the lower page where scores are alike (both zeros are; a NaN is above all).
+ *   chosen[b][i]  = the i-th page taken, in rising order, -1 behind the last (or chosen is NULL)
+ *   sel_indptr    = prefix sums of the rows' tokens on the pages taken
+ *   sel_indices   = those tokens' cache rows, block_table[b][page] * page_size + place, in order
+ * The row's tokens keep their order, so its last ones stay last: where `recent` pages hold the
+ * row's query tokens ((recent - 1) * page_size + 1 >= tokens), the decode step masks as it does
+ * over the whole row.
+ *   blocks        1 .. MLA_SELECT_MAX_BLOCKS;  sink >= 0, recent >= 1, sink + recent <= blocks.
+ *   scores        device float, row b at scores + b * scores_stride; those of the first `sink` and
+ *                 last `recent` pages and of rows of up to `blocks` pages are not read.
+ *   sel_indptr    device int32 [batch + 1];  sel_indices device int32 [sel_indices_len];
+ *   chosen        device int32 [batch][blocks], or NULL.
+ * sel_indices past the last token keeps its values.  No output may overlap another array.  A
+ * step that cannot be laid out (MLA_DERR_KV_INDPTR, or MLA_DERR_CAPACITY where sel_indices is
+ * too short) is emptied: sel_indptr is 0, chosen -1.  A page id outside [0, num_pages) sets
+ * MLA_DERR_KV_INDEX; tokens on that page get -1.
+ */
+#define MLA_SELECT_MAX_BLOCKS 8192
+mla_status_t mla_block_select(const float* scores, int64_t scores_stride, const int32_t* block_table,
+                              int64_t table_stride, int32_t max_pages, const int32_t* kv_indptr, int32_t batch,
+                              int32_t page_size, int32_t num_pages, int32_t blocks, int32_t sink, int32_t recent,
+                              int32_t* sel_indptr, int32_t* sel_indices, int64_t sel_indices_len,
+                              int32_t* chosen, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Zero a workspace (cudaMemsetAsync of ws_bytes on `stream`). */
 mla_status_t mla_decode_workspace_init(void* workspace, size_t workspace_bytes, cudaStream_t stream);

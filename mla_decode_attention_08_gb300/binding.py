@@ -50,6 +50,14 @@ class mla_prefill_plan_t(ctypes.Structure):
                 ("ws_partial_offset", ctypes.c_uint64)]
 
 
+class mla_shared_plan_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("max_kv_len", ctypes.c_int32), ("num_sms", ctypes.c_int32),
+                ("splits", ctypes.c_int32), ("abi_version", ctypes.c_int32),
+                ("ws_bytes", ctypes.c_uint64), ("ws_lse_offset", ctypes.c_uint64),
+                ("ws_partial_offset", ctypes.c_uint64)]
+
+
 _VP, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _PLANP = ctypes.POINTER(mla_plan_t)
 _FWD_ARGS = [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _PLANP, _VP, _I64, _I64, _VP, _SZ]
@@ -57,6 +65,11 @@ _FWD_BF16KV_ARGS = _FWD_ARGS[:2] + _FWD_ARGS[3:]  # no kv_scale
 # q, kv_fp4, kv_scales, scale_bias, qo_indptr, kv_indptr, out, stream, plan, kv_rows, ws, ws_bytes
 _FWD_MXFP4_ARGS = [_VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _PLANP, _I64, _VP, _SZ]
 _F32 = ctypes.c_float
+_SHARED_PLANP = ctypes.POINTER(mla_shared_plan_t)
+# q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, lse, stream, plan, kv_indices + len, kv_rows, ws, ws_bytes
+_SHARED_ARGS = [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SHARED_PLANP, _VP, _I64, _I64, _VP, _SZ]
+# kv, kv_scale, kv_rows, slots, num_tokens, means, num_pages, page_size, ws, ws_bytes, stream
+_MEANS_ARGS = [_VP, _VP, _I64, _VP, _I64, _VP, _I32, _I32, _VP, _SZ, _VP]
 _PREFILL_PLANP = ctypes.POINTER(mla_prefill_plan_t)
 # kv, kv_stride, weight, eps, rope_table, max_positions, interleaved, positions, slots, num_tokens,
 # cache, kv_scale, kv_rows, latent_out, q_pe + strides, q_out + strides, heads, ws, ws_bytes, stream
@@ -74,6 +87,18 @@ SIGNATURES = {
     "mla_prefill_fwd": (ctypes.c_int, _PREFILL_ARGS),
     "mla_prefill_fwd_stall_stream": (ctypes.c_int, _PREFILL_ARGS),
     "mla_attn_merge": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _VP, _VP, _VP]),
+    "mla_shared_plan": (ctypes.c_int, [_I32, _I32, _I32, _I32, _SHARED_PLANP]),
+    "mla_shared_fwd": (ctypes.c_int, _SHARED_ARGS),
+    "mla_shared_fwd_stall_stream": (ctypes.c_int, _SHARED_ARGS),
+    "mla_block_means": (ctypes.c_int, _MEANS_ARGS),
+    "mla_block_means_bf16kv": (ctypes.c_int, _MEANS_ARGS[:1] + _MEANS_ARGS[2:]),  # no kv_scale
+    "mla_block_scores": (ctypes.c_int, [_VP, _I32, _VP, _I32, _VP, _I64, _I32, _VP, _VP, _I32, _I32, _VP, _I64,
+                                        _VP, _SZ, _VP]),
+    "mla_block_select": (ctypes.c_int, [_VP, _I64, _VP, _I64, _I32, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _VP,
+                                        _VP, _I64, _VP, _VP, _SZ, _VP]),
+    "mla_decode_fwd_lse": (ctypes.c_int, _FWD_ARGS[:6] + [_VP] + _FWD_ARGS[6:]),
+    "mla_decode_fwd_bf16kv_lse": (ctypes.c_int, _FWD_BF16KV_ARGS[:5] + [_VP] + _FWD_BF16KV_ARGS[5:]),
+    "mla_decode_fwd_mxfp4_lse": (ctypes.c_int, _FWD_MXFP4_ARGS[:7] + [_VP] + _FWD_MXFP4_ARGS[7:]),
     "mla_decode_plan": (ctypes.c_int, [_I32, _I32, _I32, _PLANP]),
     "mla_decode_plan_mtp": (ctypes.c_int, [_I32, _I32, _I32, _I32, _PLANP]),
     "mla_decode_fwd": (ctypes.c_int, _FWD_ARGS),
@@ -209,12 +234,24 @@ def _fwd_mxfp4_args(q, kv_fp4, kv_scales, qo_indptr, kv_indptr, out, stream, pla
             _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
 
 
+def _fwd(fn: str, args: tuple, q, lse, at: int) -> None:
+    """Call decode step ``fn``, or where a tensor for the log-sum-exps is given the form of
+    it that reports them, whose argument it is in place ``at``."""
+    if lse is not None:
+        p_lse = _dev_ptr(lse, "lse", torch.float32)
+        if lse.shape != q.shape[:2]:
+            raise ValueError(f"lse must be {list(q.shape[:2])}, got {list(lse.shape)}")
+        fn, args = fn + "_lse", (*args[:at], p_lse, *args[at:])
+    _check(fn, getattr(load_library(), fn)(*args))
+
+
 def mla_decode_fwd_mxfp4(q, kv_fp4, kv_scales, qo_indptr, kv_indptr, out, stream=None, *, plan,
-                         workspace, scale_bias: int = 0) -> torch.Tensor:
-    """Decode step over an MXFP4 cache (elements ``[N, 288]``, scales ``[N, 18]``); returns ``out``."""
-    _check("mla_decode_fwd_mxfp4", load_library().mla_decode_fwd_mxfp4(
-        *_fwd_mxfp4_args(q, kv_fp4, kv_scales, qo_indptr, kv_indptr, out, stream, plan, workspace,
-                         scale_bias)))
+                         workspace, scale_bias: int = 0, lse=None) -> torch.Tensor:
+    """Decode step over an MXFP4 cache (elements ``[N, 288]``, scales ``[N, 18]``); returns ``out``.
+
+    ``lse`` float32 [T, 16] or None, as in mla_decode_fwd."""
+    _fwd("mla_decode_fwd_mxfp4", _fwd_mxfp4_args(q, kv_fp4, kv_scales, qo_indptr, kv_indptr, out, stream,
+                                                 plan, workspace, scale_bias), q, lse, 7)
     return out
 
 
@@ -245,11 +282,12 @@ def mla_mxfp4_quantize(src_bf16, dst_fp4, dst_scales, stream=None) -> None:
 
 
 def mla_decode_fwd_bf16kv(q, kv_bf16, qo_indptr, kv_indptr, out, stream=None, *, plan,
-                          workspace, kv_indices=None) -> torch.Tensor:
-    """Decode step over a bf16 cache ``[N, 576]`` (no scale); writes and returns ``out``."""
-    _check("mla_decode_fwd_bf16kv", load_library().mla_decode_fwd_bf16kv(
-        *_fwd_bf16kv_args(q, kv_bf16, qo_indptr, kv_indptr, out, stream, plan, kv_indices,
-                          workspace)))
+                          workspace, kv_indices=None, lse=None) -> torch.Tensor:
+    """Decode step over a bf16 cache ``[N, 576]`` (no scale); writes and returns ``out``.
+
+    ``lse`` float32 [T, 16] or None, as in mla_decode_fwd."""
+    _fwd("mla_decode_fwd_bf16kv", _fwd_bf16kv_args(q, kv_bf16, qo_indptr, kv_indptr, out, stream, plan,
+                                                   kv_indices, workspace), q, lse, 5)
     return out
 
 
@@ -261,11 +299,13 @@ def mla_decode_stage1_bf16kv(q, kv_bf16, qo_indptr, kv_indptr, out, stream=None,
 
 
 def mla_decode_fwd(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream=None, *, plan,
-                   workspace, kv_indices=None) -> torch.Tensor:
-    """Decode step; writes ``out`` (bf16 [B, 16, 512]) and returns it."""
-    _check("mla_decode_fwd", load_library().mla_decode_fwd(
-        *_fwd_args(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream, plan, kv_indices,
-                   workspace)))
+                   workspace, kv_indices=None, lse=None) -> torch.Tensor:
+    """Decode step; writes ``out`` (bf16 [B, 16, 512]) and returns it.
+
+    ``lse`` float32 [T, 16] takes each token's and head's natural log-sum-exp
+    (mla_decode_fwd_lse), with which mla_attn_merge joins ``out`` to attention over other keys."""
+    _fwd("mla_decode_fwd", _fwd_args(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream, plan, kv_indices,
+                                     workspace), q, lse, 6)
     return out
 
 
@@ -604,6 +644,171 @@ def mla_attn_merge(parts, lses, out, stream=None, *, lse_out=None) -> torch.Tens
     _call("mla_attn_merge", dev, p_parts, p_lses, shape[0], shape[1:-1].numel(), shape[-1], p_out, p_lse,
           _on("mla_attn_merge", stream, dev))
     return out
+
+
+# ---------------------------------------------------------------- decode steps over long contexts
+def mla_shared_plan(batch: int, total_q: int, max_kv_len: int, num_sms: int = 0) -> mla_shared_plan_t:
+    """Plan of mla_shared_fwd for ``batch`` groups with ``total_q`` query tokens in all."""
+    plan = mla_shared_plan_t()
+    _check("mla_shared_plan", load_library().mla_shared_plan(batch, total_q, max_kv_len, num_sms,
+                                                            ctypes.byref(plan)))
+    return plan
+
+
+def _cache_rows(cache, name: str, dtypes) -> int:
+    """Rows of a cache [rows, 576] or [rows, 1, 576] of one of ``dtypes``."""
+    if not isinstance(cache, _Tensor) or cache.dtype not in dtypes:
+        raise TypeError(f"{name} must be a CUDA tensor of {' or '.join(map(str, dtypes))}")
+    shape = cache.shape
+    if len(shape) not in (2, 3) or shape[-1] != QK_HEAD_DIM or len(shape) == 3 and shape[1] != 1:
+        raise ValueError(f"{name} must be [rows, 576] or [rows, 1, 576], got {list(shape)}")
+    return shape[0]
+
+
+def _scale_ptr(kv_scale, dev: int) -> int:
+    p = _ptr(kv_scale, "kv_scale", _F32T, dev)
+    if kv_scale.numel() != 1:
+        raise ValueError("kv_scale must be one float32")
+    return p
+
+
+def _shared(fn, q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream, plan, workspace, kv_indices, lse):
+    dev = _device_of(q, "q")
+    rows = _cache_rows(kv_fp8, "kv_fp8", _E4M3_CODES)
+    p_q, p_kv = _ptr(q, "q", _BF16, dev), _ptr(kv_fp8, "kv_fp8", kv_fp8.dtype, dev)
+    p_scale = _scale_ptr(kv_scale, dev)
+    p_qo, p_ki = _ptr(qo_indptr, "qo_indptr", _I32T, dev), _ptr(kv_indptr, "kv_indptr", _I32T, dev)
+    p_out = _ptr(out, "out", _BF16, dev)
+    p_idx = None if kv_indices is None else _ptr(kv_indices, "kv_indices", _I32T, dev)
+    p_lse = None if lse is None else _ptr(lse, "lse", _F32T, dev)
+    p_ws = _workspace(workspace, dev)
+    t, b = plan.total_q, plan.batch
+    _expect("q", q, (t, NUM_HEADS, QK_HEAD_DIM))
+    _expect("out", out, (t, NUM_HEADS, V_HEAD_DIM))
+    if lse is not None:
+        _expect("lse", lse, (t, NUM_HEADS))
+    if qo_indptr.numel() != b + 1 or kv_indptr.numel() != b + 1:
+        raise ValueError("qo_indptr and kv_indptr must hold plan.batch + 1 entries")
+    _call(fn, dev, p_q, p_kv, p_scale, p_qo, p_ki, p_out, p_lse, _on(fn, stream, dev), ctypes.byref(plan),
+          p_idx, 0 if kv_indices is None else kv_indices.numel(), rows, p_ws, workspace.nbytes)
+
+
+def mla_shared_fwd(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream=None, *, plan, workspace,
+                   kv_indices=None, lse=None) -> torch.Tensor:
+    """Attention of groups of decode queries over keys that their whole group sees, for
+    instance a prefix that a batch shares (see the C header); writes and returns ``out``.
+
+    ``q`` bf16 [total_q, 16, 576], ``kv_fp8`` [rows, 576], ``qo_indptr``/``kv_indptr`` int32
+    [groups + 1], ``out`` bf16 [total_q, 16, 512], ``lse`` float32 [total_q, 16] or None,
+    ``kv_indices`` int32 cache rows of the groups' keys, or None where they are the rows
+    themselves."""
+    _shared("mla_shared_fwd", q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream, plan, workspace,
+            kv_indices, lse)
+    return out
+
+
+def mla_shared_fwd_stall_stream(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream=None, *, plan,
+                                workspace, kv_indices=None, lse=None) -> None:
+    """Test hook: the launch of mla_shared_fwd with copies that never arrive, so that the
+    bounded waits run out and the call reports MLA_DERR_TIMEOUT."""
+    _shared("mla_shared_fwd_stall_stream", q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, stream, plan,
+            workspace, kv_indices, lse)
+
+
+def _pages_of(means, dev: int):
+    p = _ptr(means, "means", _BF16, dev)
+    if means.dim() != 2 or means.shape[1] != QK_HEAD_DIM:
+        raise ValueError(f"means must be [pages, {QK_HEAD_DIM}], got {list(means.shape)}")
+    return p, means.shape[0]
+
+
+def _means(fn, cache, rows, scale, slots, means, stream, page_size, workspace, dev):
+    p_cache = _ptr(cache, "the cache", cache.dtype, dev)
+    p_slots, p_ws = _ptr(slots, "slots", _I32T, dev), _workspace(workspace, dev)
+    p_means, pages = _pages_of(means, dev)
+    _call(fn, dev, p_cache, *scale, rows, p_slots, slots.numel(), p_means, pages, page_size, p_ws,
+          workspace.nbytes, _on(fn, stream, dev))
+
+
+def mla_block_means(kv_fp8, kv_scale, slots, means, stream=None, *, page_size: int, workspace) -> None:
+    """The mean cache row of every page that ``slots`` (int32 [T], as mla_kv_append took them)
+    wrote to, into ``means`` bf16 [pages, 576]; other pages' means are left alone (see the C
+    header).  ``workspace``: STEP_WORKSPACE_BYTES, zeroed once."""
+    rows = _cache_rows(kv_fp8, "kv_fp8", _E4M3_CODES)
+    dev = _device_of(kv_fp8, "kv_fp8")
+    _means("mla_block_means", kv_fp8, rows, (_scale_ptr(kv_scale, dev),), slots, means, stream, page_size,
+           workspace, dev)
+
+
+def mla_block_means_bf16kv(kv_bf16, slots, means, stream=None, *, page_size: int, workspace) -> None:
+    """mla_block_means of a bf16 cache ``[rows, 576]`` (no scale)."""
+    rows = _cache_rows(kv_bf16, "kv_bf16", (_BF16,))
+    _means("mla_block_means_bf16kv", kv_bf16, rows, (), slots, means, stream, page_size, workspace,
+           _device_of(kv_bf16, "kv_bf16"))
+
+
+def _rows_of(name: str, t, dtype, dev: int, batch: int):
+    """Address, row stride and width of a [batch, width] operand with dense rows."""
+    p = _view_ptr(t, name, dtype, dev)
+    if t.dim() != 2 or t.shape[0] != batch:
+        raise ValueError(f"{name} must be [{batch}, max_pages], got {list(t.shape)}")
+    row = _stride1(name, t)
+    if row < t.shape[1]:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return p, row, t.shape[1]
+
+
+def mla_block_scores(q, means, block_table, qo_indptr, kv_indptr, scores, stream=None, *, page_size: int,
+                     workspace) -> torch.Tensor:
+    """The highest product of a row's queries with each of its pages' means, over 24 (see the
+    C header); writes and returns ``scores``.
+
+    ``q`` bf16 [T, 16, 576], ``means`` bf16 [pages, 576], ``block_table`` int32 [B, max_pages] and
+    ``scores`` float32 [B, max_pages] (rows may be strided), ``qo_indptr``/``kv_indptr`` int32
+    [B + 1]; scores behind a row's pages are -inf."""
+    dev = _device_of(q, "q")
+    p_q, (p_means, pages) = _ptr(q, "q", _BF16, dev), _pages_of(means, dev)
+    if q.dim() != 3 or q.shape[1] != NUM_HEADS or q.shape[2] != QK_HEAD_DIM:
+        raise ValueError(f"q must be [tokens, {NUM_HEADS}, {QK_HEAD_DIM}], got {list(q.shape)}")
+    p_qo, p_kv = _ptr(qo_indptr, "qo_indptr", _I32T, dev), _ptr(kv_indptr, "kv_indptr", _I32T, dev)
+    b = kv_indptr.numel() - 1
+    if qo_indptr.numel() != b + 1:
+        raise ValueError("qo_indptr and kv_indptr must have one length")
+    p_table, table_row, width = _rows_of("block_table", block_table, _I32T, dev, b)
+    p_scores, scores_row, scores_width = _rows_of("scores", scores, _F32T, dev, b)
+    if scores_width != width:
+        raise ValueError("block_table and scores must have one width")
+    p_ws = _workspace(workspace, dev)
+    _call("mla_block_scores", dev, p_q, q.shape[0], p_means, pages, p_table, table_row, width, p_qo, p_kv, b,
+          page_size, p_scores, scores_row, p_ws, workspace.nbytes, _on("mla_block_scores", stream, dev))
+    return scores
+
+
+def mla_block_select(scores, block_table, kv_indptr, sel_indptr, sel_indices, stream=None, *, page_size: int,
+                     num_pages: int, blocks: int, sink: int, recent: int, workspace, chosen=None) -> None:
+    """The pages that each row attends, as mla_decode_fwd's page table (see the C header): all of
+    up to ``blocks`` pages, else the first ``sink``, the last ``recent`` and the highest scores.
+
+    ``scores`` float32 and ``block_table`` int32 [B, max_pages] (rows may be strided), ``kv_indptr``
+    int32 [B + 1] of the whole rows, then the outputs: ``sel_indptr`` int32 [B + 1],
+    ``sel_indices`` int32, ``chosen`` int32 [B, blocks] or None."""
+    dev = _device_of(scores, "scores")
+    p_kv = _ptr(kv_indptr, "kv_indptr", _I32T, dev)
+    b = kv_indptr.numel() - 1
+    p_scores, scores_row, scores_width = _rows_of("scores", scores, _F32T, dev, b)
+    p_table, table_row, width = _rows_of("block_table", block_table, _I32T, dev, b)
+    if scores_width != width:
+        raise ValueError("block_table and scores must have one width")
+    p_ptr, p_idx = _ptr(sel_indptr, "sel_indptr", _I32T, dev), _ptr(sel_indices, "sel_indices", _I32T, dev)
+    if sel_indptr.numel() != b + 1:
+        raise ValueError("sel_indptr must hold one entry a row and one more")
+    p_chosen = None if chosen is None else _ptr(chosen, "chosen", _I32T, dev)
+    if chosen is not None:
+        _expect("chosen", chosen, (b, blocks))
+    p_ws = _workspace(workspace, dev)
+    _call("mla_block_select", dev, p_scores, scores_row, p_table, table_row, width, p_kv, b, page_size, num_pages,
+          blocks, sink, recent, p_ptr, p_idx, sel_indices.numel(), p_chosen, p_ws, workspace.nbytes,
+          _on("mla_block_select", stream, dev))
 
 
 def mla_debug_q_operand(q, kv_scale, tokens_per_cta: int = 1, stream=None):

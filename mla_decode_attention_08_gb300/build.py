@@ -25,7 +25,8 @@ LIB_DEBUG = os.path.join(PKG, "libmla_decode_debug.so")
 BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(PKG, "libmla_decode_trace.so")
 SOURCES = ["stage1.cu", "stage2.cu", "fp8_quant.cu", "mxfp4_quant.cu", "api.cu", "static_scratch.cu",
-           "page_map.cu", "kv_append.cu", "attn_merge.cu", "prefill.cu", "api_ops.cu"]
+           "page_map.cu", "kv_append.cu", "attn_merge.cu", "prefill.cu", "api_ops.cu",
+           "shared.cu", "block_means.cu", "block_scores.cu", "block_select.cu", "api_long.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -181,9 +181,12 @@ mla_status_t prepare_device(int* device_out) {
     return MLA_ERR_CUDA;
   if (major != 10 || minor != 3) return MLA_ERR_UNSUPPORTED;
   if (static_cast<size_t>(smem) < mla::stage1_smem_bytes()) return MLA_ERR_UNSUPPORTED;
-  if (static_cast<size_t>(smem) < mla::prefill_smem_bytes()) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<size_t>(smem) < mla::prefill_smem_bytes() ||
+      static_cast<size_t>(smem) < mla::shared_smem_bytes())
+    return MLA_ERR_UNSUPPORTED;
   if (mla::stage1_prepare(device) != cudaSuccess || mla::page_map_prepare() != cudaSuccess ||
-      mla::prefill_prepare() != cudaSuccess)
+      mla::prefill_prepare() != cudaSuccess || mla::shared_prepare() != cudaSuccess ||
+      mla::block_scores_prepare() != cudaSuccess || mla::block_select_prepare() != cudaSuccess)
     return MLA_ERR_CUDA;
   ready[device].store(1, std::memory_order_release);
   return MLA_OK;
@@ -219,7 +222,7 @@ constexpr int32_t kCtaTokens = 2;
 int32_t siblings_of(const mla_plan_t* plan) { return plan->qo_len > kCtaTokens ? 2 : 1; }
 
 mla::Stage2Params stage2_params(const int32_t* qo_indptr, void* out, const mla_plan_t* plan,
-                                void* workspace) {
+                                void* workspace, float* lse_out) {
   auto* ws = static_cast<uint8_t*>(workspace);
   mla::Stage2Params s;
   s.qo_indptr = qo_indptr;
@@ -228,6 +231,7 @@ mla::Stage2Params stage2_params(const int32_t* qo_indptr, void* out, const mla_p
   s.prefix = reinterpret_cast<const int32_t*>(ws + plan->ws_prefix_offset);
   s.workers = reinterpret_cast<const int32_t*>(ws + plan->ws_workers_offset);
   s.lse = reinterpret_cast<const float*>(ws + plan->ws_lse_offset);
+  s.lse_out = lse_out;
   s.partial = reinterpret_cast<const uint16_t*>(ws + plan->ws_partial_offset);
   s.batch = plan->batch;
   s.grid = plan->grid;
@@ -246,7 +250,8 @@ mla_status_t run_stage1(const void* q, const void* kv, const float* kv_scale,
                         cudaStream_t stream, const mla_plan_t* plan, const int32_t* kv_indices,
                         int64_t kv_indices_len, int64_t kv_rows, void* workspace,
                         size_t workspace_bytes, mla::CacheFormat fmt, bool stall_stream = false,
-                        const void* mx_scales = nullptr, int32_t mx_bias = 0) {
+                        const void* mx_scales = nullptr, int32_t mx_bias = 0,
+                        float* lse_out = nullptr) {
   using mla::CacheFormat;
   mla_status_t st = check_plan(plan);
   if (st != MLA_OK) return st;
@@ -254,7 +259,8 @@ mla_status_t run_stage1(const void* q, const void* kv, const float* kv_scale,
       (mx_scales == nullptr && fmt == CacheFormat::kMxfp4) || qo_indptr == nullptr ||
       kv_indptr == nullptr || out == nullptr)
     return MLA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) || !aligned(lse_out, 4))
+    return MLA_ERR_INVALID_ARG;
   if (kv_rows < 1 || kv_rows > INT32_MAX) return MLA_ERR_INVALID_ARG;
   if (kv_indices != nullptr && (kv_indices_len < 0 || kv_indices_len > INT32_MAX))
     return MLA_ERR_INVALID_ARG;
@@ -292,6 +298,7 @@ mla_status_t run_stage1(const void* q, const void* kv, const float* kv_scale,
   p.prefix = reinterpret_cast<int32_t*>(ws + plan->ws_prefix_offset);
   p.workers = reinterpret_cast<int32_t*>(ws + plan->ws_workers_offset);
   p.lse = reinterpret_cast<float*>(ws + plan->ws_lse_offset);
+  p.lse_out = lse_out;
   p.partial = reinterpret_cast<uint16_t*>(ws + plan->ws_partial_offset);
   p.kv_rows = kv_rows;
   p.kv_indices_len = gather ? kv_indices_len : 0;
@@ -312,8 +319,9 @@ mla_status_t run_stage1(const void* q, const void* kv, const float* kv_scale,
 }
 
 mla_status_t run_stage2(const int32_t* qo_indptr, void* out, cudaStream_t stream,
-                        const mla_plan_t* plan, void* workspace, bool programmatic) {
-  return mla::launch_stage2(stage2_params(qo_indptr, out, plan, workspace), programmatic,
+                        const mla_plan_t* plan, void* workspace, bool programmatic,
+                        float* lse_out = nullptr) {
+  return mla::launch_stage2(stage2_params(qo_indptr, out, plan, workspace, lse_out), programmatic,
                             stream) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;
@@ -325,19 +333,25 @@ mla_status_t run_decode(const void* q, const void* kv, const float* kv_scale,
                         cudaStream_t stream, const mla_plan_t* plan, const int32_t* kv_indices,
                         int64_t kv_indices_len, int64_t kv_rows, void* workspace,
                         size_t workspace_bytes, mla::CacheFormat fmt, bool stall_stream = false,
-                        const void* mx_scales = nullptr, int32_t mx_bias = 0) {
+                        const void* mx_scales = nullptr, int32_t mx_bias = 0,
+                        float* lse_out = nullptr) {
   mla_status_t st = run_stage1(q, kv, kv_scale, qo_indptr, kv_indptr, out, stream, plan,
                                kv_indices, kv_indices_len, kv_rows, workspace, workspace_bytes,
-                               fmt, stall_stream, mx_scales, mx_bias);
+                               fmt, stall_stream, mx_scales, mx_bias, lse_out);
   // The cluster split combines inside stage 1: no second kernel.
   if (st == MLA_OK && cluster_of(plan, fmt, kv_indices) == 0)
-    st = run_stage2(qo_indptr, out, stream, plan, workspace, true);
+    st = run_stage2(qo_indptr, out, stream, plan, workspace, true, lse_out);
   return st;
 }
 
 }  // namespace
 
 mla_status_t mla::device_ready(int* device) { return prepare_device(device); }
+
+bool mla::cache_maps(const void* kv_fp8, int64_t rows, bool gather, int device, CUtensorMap* latent,
+                     CUtensorMap* rope) {
+  return kv_maps(kv_fp8, rows, gather, false, device, latent, rope);
+}
 
 extern "C" {
 
@@ -449,6 +463,29 @@ mla_status_t mla_decode_fwd_bf16kv(const void* q_bf16, const void* kv_bf16,
                     mla::CacheFormat::kBf16);
 }
 
+mla_status_t mla_decode_fwd_lse(const void* q_bf16, const void* kv_fp8, const float* kv_scale,
+                                const int32_t* qo_indptr, const int32_t* kv_indptr, void* out_bf16,
+                                float* lse_out, cudaStream_t stream, const mla_plan_t* plan,
+                                const int32_t* kv_indices, int64_t kv_indices_len, int64_t kv_rows,
+                                void* workspace, size_t workspace_bytes) {
+  if (lse_out == nullptr) return MLA_ERR_INVALID_ARG;
+  return run_decode(q_bf16, kv_fp8, kv_scale, qo_indptr, kv_indptr, out_bf16, stream, plan,
+                    kv_indices, kv_indices_len, kv_rows, workspace, workspace_bytes,
+                    mla::CacheFormat::kE4m3, false, nullptr, 0, lse_out);
+}
+
+mla_status_t mla_decode_fwd_bf16kv_lse(const void* q_bf16, const void* kv_bf16,
+                                       const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                       void* out_bf16, float* lse_out, cudaStream_t stream,
+                                       const mla_plan_t* plan, const int32_t* kv_indices,
+                                       int64_t kv_indices_len, int64_t kv_rows, void* workspace,
+                                       size_t workspace_bytes) {
+  if (lse_out == nullptr) return MLA_ERR_INVALID_ARG;
+  return run_decode(q_bf16, kv_bf16, nullptr, qo_indptr, kv_indptr, out_bf16, stream, plan,
+                    kv_indices, kv_indices_len, kv_rows, workspace, workspace_bytes,
+                    mla::CacheFormat::kBf16, false, nullptr, 0, lse_out);
+}
+
 mla_status_t mla_decode_fwd_stall_stream(const void* q_bf16, const void* kv_fp8,
                                          const float* kv_scale, const int32_t* qo_indptr,
                                          const int32_t* kv_indptr, void* out_bf16,
@@ -468,6 +505,17 @@ mla_status_t mla_decode_fwd_mxfp4(const void* q_bf16, const void* kv_fp4, const 
   return run_decode(q_bf16, kv_fp4, nullptr, qo_indptr, kv_indptr, out_bf16, stream, plan, nullptr,
                     0, kv_rows, workspace, workspace_bytes, mla::CacheFormat::kMxfp4, false,
                     kv_scales, scale_bias);
+}
+
+mla_status_t mla_decode_fwd_mxfp4_lse(const void* q_bf16, const void* kv_fp4, const void* kv_scales,
+                                      int32_t scale_bias, const int32_t* qo_indptr,
+                                      const int32_t* kv_indptr, void* out_bf16, float* lse_out,
+                                      cudaStream_t stream, const mla_plan_t* plan, int64_t kv_rows,
+                                      void* workspace, size_t workspace_bytes) {
+  if (lse_out == nullptr) return MLA_ERR_INVALID_ARG;
+  return run_decode(q_bf16, kv_fp4, nullptr, qo_indptr, kv_indptr, out_bf16, stream, plan, nullptr,
+                    0, kv_rows, workspace, workspace_bytes, mla::CacheFormat::kMxfp4, false,
+                    kv_scales, scale_bias, lse_out);
 }
 
 mla_status_t mla_decode_fwd_mxfp4_stall_stream(const void* q_bf16, const void* kv_fp4,

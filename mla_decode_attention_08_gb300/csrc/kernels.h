@@ -32,6 +32,7 @@ constexpr int kNumRSlots = 2;
 constexpr int kStage1Threads = 256;
 constexpr int kStage1ThreadsGather = 384;
 constexpr int kStage1ThreadsMx = 512;  // MXFP4 cache: warps 8-15 convert its panels
+constexpr float kLn2 = 0.693147180559945309f;  // base-2 log-sum-exps to natural ones
 constexpr long long kWaitLimitCycles = 2000000000LL;  // ~1 s per pipeline wait at 2 GHz
 
 // Start-up trace of trace builds (-DMLA_TRACE, `build(trace=True)`): per stage-1
@@ -98,6 +99,7 @@ struct Stage1Params {
   int32_t* prefix;            // [B+1]
   int32_t* workers;           // [grid*8]: worker record + combine job
   float* lse;                 // [2*grid*kQ*16] (kQ: this launch's tokens per row)
+  float* lse_out;             // natural log-sum-exps [B * row_tokens][16], or null
   uint16_t* partial;          // bf16 bits [2*grid*kQ*16*512]
   int64_t kv_rows;
   int64_t kv_indices_len;
@@ -135,6 +137,7 @@ struct Stage2Params {
   const int32_t* workers;  // [grid*8] (t0, t1, first_row, last_row, job tq, job first
                            // worker, job last worker, job first slot), written by stage 1
   const float* lse;
+  float* lse_out;           // natural log-sum-exps [B * qo_len][16], or null
   const uint16_t* partial;  // bf16 bits
   int32_t batch;
   int32_t grid;

@@ -1,5 +1,5 @@
-// Parameter blocks and launchers of the operators around the decode step
-// (internal to libmla_decode).
+// Parameter blocks and launchers of the operators around the decode step and over long
+// contexts (internal to libmla_decode).
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -11,6 +11,9 @@ namespace mla {
 
 // api.cu: MLA_OK when the current device is an sm_103 part whose kernels are set up.
 mla_status_t device_ready(int* device);
+// api.cu: the descriptors of an e4m3 cache's latent and rope boxes (tiles of 128 rows, or
+// single rows for gathers of four).
+bool cache_maps(const void* kv_fp8, int64_t rows, bool gather, int device, CUtensorMap* latent, CUtensorMap* rope);
 
 // A launch as a programmatic dependent of the previous kernel of the stream:
 // the kernel may be scheduled while that one finishes and waits for it
@@ -73,9 +76,9 @@ cudaError_t launch_kv_append(const KvAppendParams& p, bool e4m3, bool interleave
                              cudaStream_t stream);
 
 // Joins `pieces` outputs [pieces][rows][dim] by their log-sum-exps
-// [pieces][rows].  bf16 pieces (the public operator) or float ones (the split
-// of mla_prefill_fwd, a row for each token and head; tokens that it has not
-// computed are left alone).
+// [pieces][rows].  bf16 pieces (the public operator) or float ones (the splits
+// of mla_prefill_fwd and mla_shared_fwd, a row for each token and head; tokens that
+// they have not computed are left alone).
 struct MergeParams {
   const void* parts;
   const float* lses;
@@ -92,9 +95,11 @@ struct MergeParams {
   int64_t part_rows;
   int32_t* err;
 };
-// Whether float parts of `rows` rows of 128 are joined by threads that are all on the
+// Whether float parts of `rows` rows of `dim` are joined by threads that are all on the
 // GPU at once: four values each, two blocks of 256 an SM.
-inline bool merges_at_once(int64_t rows, int32_t sms) { return rows * (128 / 4) <= static_cast<int64_t>(sms) * 2 * 256; }
+inline bool merges_at_once(int64_t rows, int32_t dim, int32_t sms) {
+  return rows * (dim / 4) <= static_cast<int64_t>(sms) * 2 * 256;
+}
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
 
 // mla_prefill_fwd: a persistent block an SM; a job is up to 256 queries of a row
@@ -129,5 +134,75 @@ constexpr int kPrefillRows = 256;  // query rows of a job: two tiles of 128
 size_t prefill_smem_bytes();
 cudaError_t prefill_prepare();
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream);
+
+// mla_shared_fwd: a persistent block an SM; a job is up to four query tokens of a group
+// over one split of its keys.
+struct SharedParams {
+  const uint16_t* q;         // bf16 [total_q][16][576]
+  const float* kv_scale;
+  const int32_t* qo_indptr;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices; // or null: keys are rows of the cache
+  uint16_t* out;             // bf16 [total_q][16][512]
+  float* lse;                // [total_q][16] or null
+  float* part;               // splits > 1: [splits][total_q][16][512]
+  float* part_lse;           // splits > 1: [splits][total_q][16]
+  int32_t* err;
+  uint32_t* sched;           // as PrefillParams::sched
+  int64_t kv_rows;
+  int64_t kv_limit;          // keys that kv_indptr may count: kv_indices' entries, or kv_rows
+  int64_t part_rows;         // rows of parts that the workspace has room for (for the debug build's checks)
+  int32_t batch, total_q, blocks, splits, num_sms;
+  int32_t stall_stream;      // test hook: no copies are issued, so the waits run out
+};
+struct SharedMaps {
+  CUtensorMap latent, rope;
+};
+constexpr int kSharedTokens = 4;  // query tokens of a job
+size_t shared_smem_bytes();
+cudaError_t shared_prepare();
+cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream);
+
+struct BlockMeansParams {
+  const uint8_t* cache;      // e4m3 codes or bf16 rows
+  const float* kv_scale;     // e4m3 only
+  const int32_t* slots;
+  uint16_t* means;           // bf16 [num_pages][576]
+  int32_t* err;
+  int64_t kv_rows;
+  int64_t limit;             // slots below it lie in the cache and on a page with a mean
+  int64_t num_tokens;
+  int32_t page_size;
+};
+cudaError_t launch_block_means(const BlockMeansParams& p, bool e4m3, int32_t num_sms, cudaStream_t stream);
+
+struct BlockScoresParams {
+  const uint16_t* q;         // bf16 [total_q][16][576]
+  const uint16_t* means;     // bf16 [num_pages][576]
+  const int32_t* block_table;
+  const int32_t* qo_indptr;
+  const int32_t* kv_indptr;
+  float* scores;
+  int32_t* err;
+  int64_t table_stride, scores_stride;
+  int32_t batch, total_q, max_pages, num_pages, page_size;
+};
+cudaError_t block_scores_prepare();
+cudaError_t launch_block_scores(const BlockScoresParams& p, cudaStream_t stream);
+
+struct BlockSelectParams {
+  const float* scores;
+  const int32_t* block_table;
+  const int32_t* kv_indptr;
+  int32_t* sel_indptr;
+  int32_t* sel_indices;
+  int32_t* chosen;           // [batch][blocks] or null
+  int32_t* err;
+  int64_t table_stride, scores_stride, indices_len;
+  int32_t batch, max_pages, num_pages, page_size;
+  int32_t blocks, sink, recent;
+};
+cudaError_t block_select_prepare();
+cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream);
 
 }  // namespace mla

@@ -1,0 +1,860 @@
+// mla_shared_fwd: decode queries of many rows over keys that all of them see (a prefix
+// that the rows of a group share), e4m3 cache, with the log-sum-exp that joins the
+// result to each row's own keys.
+//
+// The decode step reads a row's keys once for its 16 heads, and is bound by those
+// bytes.  Here a block takes four query tokens, 64 rows of 16 heads each, over the same
+// keys, so that the tensor cores bound it.  For a tile of 128 keys (T):
+//   S^T[key][row]  = K(T) . Q^T      128 x 128 x 576: 64 rows of high terms, 64 of low
+//   O^T[dim][row] += V(T)^T . P^T    4 x 128 x 64 x 128, once for P's high terms and
+//                                    once for its low ones
+// K(T) and V(T) are the same e4m3 codes in shared memory (V the first 512 dims), read
+// by key for the first product and by dim for the second, so nothing is converted.  A
+// bf16 query is two e4m3 terms, q 2^k = hi + lo / 16, exact down to 2^-14 of the token's
+// largest magnitude; a probability p in [0, 2^8] is hi + lo, exact to 2^-8 of itself and
+// 2^-10, which is 2^-16 of the row's reference (2^6).  TMEM is full: two S of 128 columns, O in four
+// chunks of 64.
+//
+// Persistent blocks, one an SM, 12 warps, take jobs (four query tokens of a group over
+// a part of its keys) from a counter:
+//   * warp 3 finds the jobs,
+//   * warp 2 streams the keys by TMA (boxes of 128 rows, or gathers of four rows by a
+//     page table): four 128-dim panels a tile into two buffers, the 64 rotated dims
+//     into one,
+//   * warp 0 issues the products, S of tile T + 1 before O of tile T,
+//   * warps 4-7 and 8-11 run the softmax of two query tokens each, a thread a key: the
+//     maximum over keys is over lanes, so it is only looked for when a score passes the
+//     running reference by two powers of two, which few tiles' do.
+// Parts of keys leave float32 results, which attn_merge.cu joins.
+#include <cstddef>
+
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+#include "ops.h"
+#include "ptx.cuh"
+#include "schedule.h"
+
+namespace mla {
+namespace {
+
+constexpr int kTokens = kSharedTokens;             // query tokens of a block
+constexpr int kRows = kTokens * kNumHeads;         // 64
+constexpr int kPanelBytes = kTileTokens * 128;     // 128 keys (or operand rows) x 128 dims
+constexpr int kPanels = kVDim / 128;               // latent panels of a tile
+constexpr int kRopeBytes = kTileTokens * 64;
+constexpr int kPBytes = kTileTokens * kRows;       // one term of P: a key's 64 rows are contiguous
+constexpr int kOffKeys = 0;                        // [2][kPanels]
+constexpr int kOffRope = kOffKeys + 2 * kPanels * kPanelBytes;
+constexpr int kOffQ = kOffRope + kRopeBytes;       // [kPanels], 64 rows of high terms, then 64 of low
+constexpr int kOffQRope = kOffQ + kPanels * kPanelBytes;
+constexpr int kOffP = kOffQRope + kRopeBytes;      // high terms, low terms
+constexpr int kOffMisc = kOffP + 2 * kPBytes;
+
+constexpr int kThreads = 384;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
+              "register split exceeds the launch allocation");
+constexpr int kMmaWarp = 0, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;
+constexpr uint32_t kSoftmaxWarps = 8;
+constexpr uint32_t kJobReaders = 2 + kSoftmaxWarps;
+constexpr uint32_t kBarSoftmax = 1;                // + g: named barrier of a softmax warpgroup
+constexpr uint32_t kLayoutSw128 = 2, kLayoutSw64 = 4;
+constexpr uint32_t kColS = 0, kColO = 256;         // S of tile T at 128 (T & 1); chunk c of O at + 64 c
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kIdescQK = idesc_e4m3(128, 128, false, false);
+constexpr uint32_t kIdescPV = idesc_e4m3(128, kRows, true, true);
+constexpr float kSmScaleLog2 = 1.4426950408889634f / 24.0f;  // dot products to powers of two
+// P = 2^(s - reference + kTop); the reference follows a maximum that passes it by
+// kAhead, so P stays below 2^8, which e4m3 holds.  The farther apart the two, the
+// rarer the maximum is looked for and the coarser the small probabilities: with these a
+// probability of 2^-15 of the reference's is still a step of the low term.
+constexpr float kTop = 6.0f, kAhead = 2.0f;
+
+struct Job {
+  int32_t q0, nq;    // first query token, number of them (up to four)
+  int32_t k0, keys;  // first key of the part (of all groups' keys), and keys
+  int32_t split;
+  int32_t live;      // 0: no more jobs
+  __device__ __forceinline__ int32_t tiles() const { return (keys + kTileTokens - 1) / kTileTokens; }
+};
+
+// Key tiles are numbered through all of a block's jobs (T), and so are the jobs that
+// have any; the numbers give the barriers' phases.  The waits of each barrier come in
+// order, and none can be two phases behind: what completes a phase needs, through the
+// other roles, that its waiters have passed the one before (said at each).
+struct Misc {
+  uint64_t job_full[2], job_empty[2];
+  uint64_t claim;        // the copies of a job's last tile are due: take the next job
+  uint64_t key_full[2 * kPanels], key_empty[2 * kPanels];  // panel c of tile T: kPanels (T & 1) + c
+  uint64_t rope_full, rope_empty;
+  uint64_t q_full;       // a job's query operand written ...
+  uint64_t q_empty;      // ... and read by its last scores
+  uint64_t s_full[2];    // S(T) complete, T & 1; S(T + 2) is issued behind O(T), that is behind p_full(T)
+  uint64_t p_full;       // P(T) written, O rescaled; P(T + 1) is written behind pv_done(T)
+  uint64_t pv_done;      // O(T) complete
+  uint64_t o_free;       // a job's O read out
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  volatile int32_t abort_flag;
+  Job job[2];
+  alignas(16) float red[2][4][32];  // [warpgroup][warp][row]: maxima, sums
+  alignas(16) float factor[2][32];  // of O's rows: rescaling, at the end the division
+  uint32_t amax[2][2][4];           // [warpgroup][token][warp]
+};
+constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of one block");
+
+// Bounded waits on an mbarrier phase by a whole warp, which polls and gives up
+// together; false when the call is being abandoned.
+__device__ __forceinline__ bool warp_wait_on(const uint64_t* bar, uint32_t parity, Misc* ms, int32_t* err) {
+  const uint32_t b = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(b, parity & 1))) return true;
+  const long long start = clock64();
+  for (uint32_t n = 1;; ++n) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity & 1))) return true;
+    if ((n & 15) == 0) {
+      const bool late = clock64() - start > kWaitLimitCycles;
+      if (__any_sync(0xffffffffu, late || ms->abort_flag)) {
+        if (late && !ms->abort_flag) atomicOr(err, MLA_DERR_TIMEOUT);
+        ms->abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+// Bounded wait while draining at the end of a call.
+__device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
+  const long long start = clock64();
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(smem_u32(bar), parity & 1)) return;
+    if ((n & 15) == 15 && clock64() - start > kWaitLimitCycles) return;
+  }
+}
+
+// ------------------------------------------------------------ scheduler (one warp)
+struct Group {
+  int32_t qs, n, ks, len;
+};
+// (`back`: set when the group ends before it begins; a bad group has no tokens.)
+__device__ __forceinline__ Group load_group(const SharedParams& p, int32_t g, bool report, bool& back) {
+  const int32_t qs = __ldg(p.qo_indptr + g), qe = __ldg(p.qo_indptr + g + 1);
+  const int32_t ks = __ldg(p.kv_indptr + g), ke = __ldg(p.kv_indptr + g + 1);
+  const bool bad_q = qs < 0 || qe < qs || qe > p.total_q;
+  const bool bad_k = ks < 0 || ke < ks || ke > p.kv_limit || ke - ks > MLA_SHARED_MAX_KEYS;
+  back = back || qe < qs;
+  if (report && (bad_q || bad_k))
+    atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
+  return bad_q || bad_k ? Group{0, 0, 0, 0} : Group{qs, qe - qs, ks, ke - ks};
+}
+__device__ __forceinline__ int32_t blocks_of(int32_t n) { return (n + kTokens - 1) / kTokens; }
+
+// The groups as the warp holds them: a run of consecutive groups a lane.
+struct Batch {
+  int32_t g0, first, count, total;  // the lane's first group, blocks before and in its run; all blocks
+};
+// Groups that overlap, which decreasing offsets make (and which are reported), could have
+// any number of blocks.  No more are worked on than groups in order can have, so some may
+// be left out, and the joining kernel is told so.
+constexpr int32_t kManyBlocks = 1 << 25;
+__device__ __forceinline__ Batch count_groups(const SharedParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int32_t run = (p.batch + 31) / 32;
+  Batch r;
+  r.g0 = min(p.batch, lane * run);
+  const int32_t g1 = min(p.batch, r.g0 + run);
+  bool back = false;
+  r.count = 0;
+  for (int32_t g = r.g0; g < g1; ++g)
+    r.count = min(r.count + blocks_of(load_group(p, g, blockIdx.x == 0, back).n), kManyBlocks);
+  if (blockIdx.x == 0) {
+    back = __any_sync(0xffffffffu, back);
+    if (lane == 0) p.sched[2] = back;  // (of every call anew)
+  }
+  int32_t incl = r.count;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  r.first = incl - r.count;
+  r.total = min(__shfl_sync(0xffffffffu, incl, 31), p.blocks);
+  return r;
+}
+
+// Job `index` into `job`: blocks run fastest, so that the SMs at work read the same keys.
+__device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, uint32_t index, Job* job) {
+  const uint32_t total = static_cast<uint32_t>(r.total);
+  if (total == 0 || index >= total * static_cast<uint32_t>(p.splits)) {
+    if ((threadIdx.x & 31) == 0) job->live = job->nq = job->keys = 0;
+    __syncwarp();
+    return;
+  }
+  const int32_t split = static_cast<int32_t>(index / total);
+  int32_t block = static_cast<int32_t>(index % total) - r.first;
+  if (block >= 0 && block < r.count) {
+    bool back = false;
+    Group g = load_group(p, r.g0, false, back);
+    for (int32_t at = r.g0; block >= blocks_of(g.n);) {  // (ends within the lane's run)
+      block -= blocks_of(g.n);
+      g = load_group(p, ++at, false, back);
+    }
+    const int32_t tiles = tiles_of_length(g.len), share = (tiles + p.splits - 1) / p.splits;
+    const int32_t a = min(g.len, split * share * kTileTokens), b = min(g.len, (split + 1) * share * kTileTokens);
+    job->q0 = g.qs + block * kTokens;
+    job->nq = min(kTokens, g.n - block * kTokens);
+    job->k0 = g.ks + a;
+    job->keys = b - a;
+    job->split = split;
+    job->live = 1;
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void run_scheduler(const SharedParams& p, Misc* ms) {
+  const int lane = threadIdx.x & 31;
+  const Batch groups = count_groups(p);
+  uint32_t index = blockIdx.x;  // the first job is the block's own, the others come from a counter
+  for (uint32_t k = 0;; ++k) {
+    Job* job = &ms->job[k & 1];
+    if (!warp_wait_on(&ms->job_empty[k & 1], (k >> 1) + 1, ms, p.err)) return;  // (the first two pass)
+    find_job(p, groups, index, job);
+    const int32_t live = job->live;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
+    if (live == 0 || !warp_wait_on(&ms->claim, k, ms, p.err)) return;
+    if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
+    index = __shfl_sync(0xffffffffu, index, 0);
+  }
+}
+
+// Job number `k` of this block, for one of its readers (a whole warp).
+__device__ __forceinline__ bool next_job(const SharedParams& p, Misc* ms, uint32_t k, Job& job) {
+  if (!warp_wait_on(&ms->job_full[k & 1], k >> 1, ms, p.err)) return false;
+  job = ms->job[k & 1];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms->job_empty[k & 1]));
+  return job.live != 0;
+}
+
+// ------------------------------------------------------------ producer (one warp)
+// A page table's four cache rows of this lane, keys 4 lane .. 4 lane + 3 of a tile; keys
+// behind the part's end repeat its last one.
+template <bool kPaged>
+__device__ __forceinline__ void load_rows(const SharedParams& p, const Job& job, int32_t j, int32_t (&rows)[4]) {
+  if constexpr (kPaged) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      rows[i] = __ldg(p.kv_indices + job.k0 + min(job.keys - 1, j * kTileTokens + 4 * static_cast<int>(threadIdx.x & 31) + i));
+  }
+}
+__device__ __forceinline__ void check_rows(const SharedParams& p, int32_t (&rows)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (rows[i] >= 0 && rows[i] < p.kv_rows) continue;
+    atomicOr(p.err, MLA_DERR_KV_INDEX);
+    rows[i] = 0;
+  }
+}
+
+// A panel of `kWidth` bytes a key, by boxes or by gathers.
+template <bool kPaged, int kWidth>
+__device__ __forceinline__ void copy_panel(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t key,
+                                           const int32_t (&rows)[4], const uint64_t* full, uint64_t policy) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t bar = smem_u32(full);
+  if (lane == 0) mbar_arrive_expect_tx(bar, kTileTokens * kWidth);
+  if constexpr (kPaged) {
+    __syncwarp();
+    tma_gather4(dst + lane * 4 * kWidth, map, x, rows[0], rows[1], rows[2], rows[3], bar, policy);
+  } else if (lane == 0) {
+    tma_load_2d(dst, map, x, key, bar, policy);
+  }
+  __syncwarp();
+}
+
+template <bool kPaged>
+__device__ __forceinline__ void run_producer(const SharedParams& p, const SharedMaps& m, Misc* ms, uint32_t sbase) {
+  const int lane = threadIdx.x & 31;
+  // (several blocks read a key at about the same time)
+  const uint64_t keep = l2_policy_evict_normal();
+  uint32_t T = 0, ropes = 0, panels = 0;  // tiles done; copies of rope panels and of latent ones
+  Job job;
+  bool ok = true;
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    const int32_t n = p.stall_stream ? 0 : job.tiles();
+    if (n == 0 && lane == 0) mbar_arrive(smem_u32(&ms->claim));
+    int32_t rows[4], next[4] = {0, 0, 0, 0};
+    if (n > 0) load_rows<kPaged>(p, job, 0, next);
+    for (int32_t j = 0; j < n && ok; ++j, ++T) {
+      const int32_t key = job.k0 + j * kTileTokens;
+      if (j == n - 1 && lane == 0) mbar_arrive(smem_u32(&ms->claim));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows[i] = next[i];
+      if constexpr (kPaged) check_rows(p, rows);
+      if (j + 1 < n) load_rows<kPaged>(p, job, j + 1, next);
+      if (!MLA_DCHECK(kPaged || (key >= 0 && key < p.kv_rows), p.err)) {
+        ms->abort_flag = 1;
+        ok = false;
+        break;
+      }
+      if (T > 0) ok = warp_wait_on(&ms->rope_empty, T - 1, ms, p.err);
+      if (!ok) break;
+      copy_panel<kPaged, 64>(sbase + kOffRope, &m.rope, kVDim, key, rows, &ms->rope_full, keep);
+      ++ropes;
+#pragma unroll 1
+      for (int c = 0; c < kPanels; ++c) {
+        const uint32_t at = kPanels * (T & 1) + c;
+        if (T > 1) ok = warp_wait_on(&ms->key_empty[at], (T >> 1) - 1, ms, p.err);
+        if (!ok) break;
+        copy_panel<kPaged, 128>(sbase + kOffKeys + at * kPanelBytes, &m.latent, 128 * c, key, rows, &ms->key_full[at], keep);
+        ++panels;
+      }
+    }
+  }
+  if (!ms->abort_flag) return;  // the issuer waits for every copy
+  // Abandoned: the copies in flight land before the block's memory is given up.
+  if (lane == 0) {
+    if (ropes > 0) drain(&ms->rope_full, ropes - 1);
+    for (uint32_t f = panels > 2 * kPanels ? panels - 2 * kPanels : 0; f < panels; ++f)
+      drain(&ms->key_full[f % (2 * kPanels)], f / (2 * kPanels));
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------ MMA issuer (one warp, an elected lane issues)
+// Keys behind the part's end lie in the tile's boxes too (another row's, or never
+// written): their probabilities are zero, but zero times NaN is NaN, so they are zeroed
+// in shared memory before either product reads them.
+__device__ __forceinline__ void clean_keys(uint8_t* panels, int32_t keys) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int c = 0; c < kPanels; ++c)
+#pragma unroll 1
+    for (int32_t i = keys * 8 + lane; i < kTileTokens * 8; i += 32)
+      *reinterpret_cast<uint4*>(panels + c * kPanelBytes + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <bool kPaged>
+__device__ __forceinline__ void run_mma(const SharedParams& p, Misc* ms, uint8_t* smem, uint32_t sbase, uint32_t tmem) {
+  constexpr uint32_t kPanel = kPanelBytes >> 4;  // in descriptor address units
+  const uint64_t key_k = smem_desc(sbase + kOffKeys, 1024, 1024, kLayoutSw128);
+  const uint64_t rope_k = smem_desc(sbase + kOffRope, 512, 512, kLayoutSw64);
+  const uint64_t q_k = smem_desc(sbase + kOffQ, 1024, 1024, kLayoutSw128);
+  const uint64_t q_rope = smem_desc(sbase + kOffQRope, 512, 512, kLayoutSw64);
+  const uint64_t p_mn = smem_desc(sbase + kOffP, 512, 512, kLayoutSw64);
+  auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity, ms, p.err); };
+  // S(T) = K(T) . Q^T, panel by panel as they land
+  auto scores = [&](uint32_t T, int32_t keys, bool last) {
+    const uint32_t d = tmem + kColS + 128 * (T & 1);
+    const bool clean = !kPaged && keys < kTileTokens;
+    if (clean) {
+      for (int c = 0; c < kPanels; ++c)
+        if (!on(&ms->key_full[kPanels * (T & 1) + c], T >> 1)) return false;
+      clean_keys(smem + kOffKeys + kPanels * (T & 1) * kPanelBytes, keys);
+    }
+    if (!on(&ms->rope_full, T)) return false;
+    tc_fence_after();
+    if (elect_one()) {
+      umma_f8(d, rope_k, q_rope, kIdescQK, 0);
+      umma_f8(d, rope_k + 2, q_rope + 2, kIdescQK, 1);
+      umma_commit(smem_u32(&ms->rope_empty));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kPanels; ++c) {
+      if (!on(&ms->key_full[kPanels * (T & 1) + c], T >> 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t a = key_k + (kPanels * (T & 1) + c) * kPanel, b = q_k + c * kPanel;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_f8(d, a + 2 * kk, b + 2 * kk, kIdescQK, 1);
+        if (c == kPanels - 1) {
+          umma_commit(smem_u32(&ms->s_full[T & 1]));
+          if (last) umma_commit(smem_u32(&ms->q_empty));
+        }
+      }
+      __syncwarp();
+    }
+    return true;
+  };
+  uint32_t T = 0, jobs = 0;
+  Job job;
+  bool ok = true;
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    const int32_t n = job.tiles();
+    if (n == 0) continue;
+    ok = on(&ms->q_full, jobs) && scores(T, job.keys, n == 1);
+    for (int32_t j = 0; j < n && ok; ++j, ++T) {
+      if (j + 1 < n) ok = scores(T + 1, job.keys - (j + 1) * kTileTokens, j + 2 == n);
+      ok = ok && (j > 0 || jobs == 0 || on(&ms->o_free, jobs - 1)) && on(&ms->p_full, T);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < kPanels; ++c) {
+          const uint64_t a = key_k + (kPanels * (T & 1) + c) * kPanel;
+          const uint32_t d = tmem + kColO + kRows * c;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {  // 32 keys each: 4 KB of a panel, 2 KB of a term of P
+            umma_f8(d, a + 256 * kk, p_mn + 128 * kk, kIdescPV, j != 0 || kk != 0);
+            umma_f8(d, a + 256 * kk, p_mn + (kPBytes >> 4) + 128 * kk, kIdescPV, 1);
+          }
+          umma_commit(smem_u32(&ms->key_empty[kPanels * (T & 1) + c]));
+        }
+        umma_commit(smem_u32(&ms->pv_done));
+      }
+      __syncwarp();
+    }
+    ++jobs;
+  }
+  if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
+  __syncwarp();
+}
+
+// ------------------------------------------------------------ softmax (two warpgroups)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+// Sum of v[h] over the warp's lanes, for h = (lane >> 1) & 15: four exchanges that move
+// half of what is left to the partner.
+__device__ __forceinline__ float transposed_sum16(float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int half = 8, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int k = 0; k < half; ++k) {
+      const float send = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+      v[k] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+// Whether any thread of warpgroup g says so (and a barrier of its threads).
+__device__ __forceinline__ bool any_of_group(bool v, int g) {
+  uint32_t r;
+  asm volatile("{ .reg .pred a, b; setp.ne.u32 a, %1, 0; bar.red.or.pred b, %2, 128, a; selp.u32 %0, 1, 0, b; }"
+               : "=r"(r) : "r"(static_cast<uint32_t>(v)), "r"(kBarSoftmax + g) : "memory");
+  return r != 0;
+}
+// 16 probabilities (0 .. 2^8) as two e4m3 terms, hi = e4m3(p), lo = e4m3(p - hi), each
+// packed four to a word.  By way of half precision, whose 11 bits both terms fit in.
+__device__ __forceinline__ void split_p(const float (&x)[16], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const __half2 v = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
+    const uint16_t h = cvt_f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
+    const uint32_t back = cvt_e4m3x2_to_f16x2(h);
+    const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
+    const uint16_t l = cvt_f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+    if (k & 1) {
+      hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
+      lo[k >> 1] |= static_cast<uint32_t>(l) << 16;
+    } else {
+      hi[k >> 1] = h;
+      lo[k >> 1] = l;
+    }
+  }
+}
+// 16 query values, scaled, as hi = e4m3(x), lo = e4m3(16 (x - hi)).
+__device__ __forceinline__ void split_q(const uint4& a, const uint4& b, float up, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float x = __uint_as_float(w[k] << 16) * up, y = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+    const uint16_t h = cvt_e4m3x2(x, y);
+    const uint32_t back = cvt_e4m3x2_to_f16x2(h);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    const uint16_t l = cvt_e4m3x2((x - f.x) * 16.0f, (y - f.y) * 16.0f);
+    if (k & 1) {
+      hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
+      lo[k >> 1] |= static_cast<uint32_t>(l) << 16;
+    } else {
+      hi[k >> 1] = h;
+      lo[k >> 1] = l;
+    }
+  }
+}
+// Byte address of 16-dim piece `ch` of operand row `row` of the query.
+__device__ __forceinline__ uint32_t q_piece(uint32_t sbase, int row, int ch) {
+  if (ch < 32) return sbase + kOffQ + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+  return sbase + kOffQRope + row * 64 + (((ch - 32) ^ ((row >> 1) & 3)) << 4);
+}
+
+// The query operand's rows of warpgroup g's two tokens, each scaled by a power of two so
+// that its largest magnitude lies in (224, 448].  scale[i]: what turns token i's products
+// into powers of two (NaN for a query that is not finite, whose outputs become NaN).
+__device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_t sbase, const Job& job, int g,
+                                        float kv_scale, float (&scale)[2]) {
+  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31;
+  constexpr int kRounds = 2 * kNumHeads * (kQkDim / 16) / 128;  // pieces a thread
+  static_assert(kRounds * 128 == 2 * kNumHeads * (kQkDim / 16), "whole rounds");
+  uint4 raw[kRounds][2];
+  uint32_t amax[2] = {0, 0};
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int piece = t + 128 * r, row = piece / (kQkDim / 16), ch = piece % (kQkDim / 16);
+    raw[r][0] = raw[r][1] = make_uint4(0, 0, 0, 0);
+    const int token = 2 * g + (row >> 4);
+    if (token < job.nq && MLA_DCHECK(job.q0 >= 0 && job.q0 + token < p.total_q, p.err)) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (static_cast<int64_t>(job.q0 + 2 * g) * kNumHeads + row) * kQkDim + 16 * ch);
+      raw[r][0] = __ldg(src);
+      raw[r][1] = __ldg(src + 1);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const uint32_t w[8] = {raw[r][0].x, raw[r][0].y, raw[r][0].z, raw[r][0].w, raw[r][1].x, raw[r][1].y, raw[r][1].z, raw[r][1].w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    const int which = (t + 128 * r) / (kQkDim / 16) >> 4;
+    amax[0] = which == 0 ? max(amax[0], top) : amax[0];
+    amax[1] = which == 1 ? max(amax[1], top) : amax[1];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    amax[i] = __reduce_max_sync(0xffffffffu, amax[i]);
+    if (lane == 0) ms->amax[g][i][warp] = amax[i];
+  }
+  named_bar_sync(kBarSoftmax + g, 128);
+  float up[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t top = max(max(ms->amax[g][i][0], ms->amax[g][i][1]), max(ms->amax[g][i][2], ms->amax[g][i][3]));
+    // The exponent e of the largest magnitude m 2^e, 1 <= m < 2, of bf16 bits: scaled to
+    // 2^8 m where m <= 1.75, else to 2^7 m.  (Zeros and denormals: clamped.)
+    const int e = static_cast<int>(top >> 7) - 127;
+    int k2 = (top & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
+    k2 = top == 0 ? 0 : min(max(k2, -126), 126);
+    up[i] = __int_as_float((k2 + 127) << 23);
+    scale[i] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((127 - k2) << 23) * kv_scale * kSmScaleLog2;
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int piece = t + 128 * r, row = piece / (kQkDim / 16), ch = piece % (kQkDim / 16);
+    uint32_t hi[4], lo[4];
+    split_q(raw[r][0], raw[r][1], row < kNumHeads ? up[0] : up[1], hi, lo);
+    st_shared_v4(q_piece(sbase, 2 * kNumHeads * g + row, ch), hi);
+    st_shared_v4(q_piece(sbase, kRows + 2 * kNumHeads * g + row, ch), lo);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+}
+
+// A warpgroup's warps meet at named barriers, so none may leave alone: a wait that ran
+// out is passed over (the others then return at once, and what is computed is not
+// written), and a job is taken by all four warps or by none.
+__device__ __forceinline__ bool next_job_of_group(const SharedParams& p, Misc* ms, uint32_t k, Job& job, int g) {
+  const bool live = next_job(p, ms, k, job);
+  return !any_of_group(!live, g);
+}
+
+__device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int g) {
+  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31;
+  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t bar = kBarSoftmax + g;
+  const float kv_scale = __ldg(p.kv_scale);
+  const uint32_t s_hi = tmem + lanes + kColS + 32 * g, s_lo = s_hi + kRows;
+  const uint32_t o_addr = tmem + lanes + kColO + 32 * g;
+  // this thread's key of a tile: its row of either term of P, two 16-byte pieces a warpgroup
+  const uint32_t p_row = sbase + kOffP + t * kRows;
+  const uint32_t swizzle = (t >> 1) & 3;
+  uint32_t T = 0, jobs = 0;
+  float scale[2], next_scale[2];
+  Job job, next;
+  bool live = next_job_of_group(p, ms, 0, job, g);
+  if (live && job.tiles() > 0) write_q(p, ms, sbase, job, g, kv_scale, scale);
+  for (uint32_t k = 0; live; ++k) {
+    const int32_t n = job.tiles();
+    // off: kTop less the reference; sum: of this thread's keys
+    float off[2][16], sum[2][16];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 16; ++h) {
+        off[i][h] = INFINITY;
+        sum[i][h] = 0.0f;
+      }
+    for (int32_t j = 0; j < n; ++j, ++T) {
+      warp_wait_on(&ms->s_full[T & 1], T >> 1, ms, p.err);
+      tc_fence_after();
+      const bool seen = j * kTileTokens + t < job.keys;
+      float x[2][16], high = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t hi[16], lo[16];
+        tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi);
+        tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo);
+        tmem_wait_ld();
+        const float a = scale[i], b = scale[i] * 0.0625f;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          x[i][h] = fmaf(__uint_as_float(lo[h]), b, fmaf(__uint_as_float(hi[h]), a, off[i][h]));
+          high = fmaxf(high, x[i][h]);
+        }
+      }
+      // (a job's first tile: off is infinite)
+      bool moved = false;
+      if (any_of_group(seen && high > kTop + kAhead, g)) {
+        moved = j > 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t hi[16], lo[16];
+          tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi);
+          tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo);
+          tmem_wait_ld();
+          const float a = scale[i], b = scale[i] * 0.0625f;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) {
+            x[i][h] = fmaf(__uint_as_float(lo[h]), b, __uint_as_float(hi[h]) * a);
+            const float m = warp_max(seen ? x[i][h] : -INFINITY);
+            if (lane == 0) ms->red[g][warp][16 * i + h] = m;
+          }
+        }
+        named_bar_sync(bar, 128);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int h = 0; h < 16; ++h) {
+            const float m = fmaxf(fmaxf(ms->red[g][0][16 * i + h], ms->red[g][1][16 * i + h]),
+                                  fmaxf(ms->red[g][2][16 * i + h], ms->red[g][3][16 * i + h]));
+            float factor = 1.0f;
+            if (m + off[i][h] > kTop + kAhead) {
+              const float to = kTop - m;
+              factor = ex2(to - off[i][h]);  // 0 on a job's first tile
+              off[i][h] = to;
+              sum[i][h] *= factor;
+            }
+            if (t == 0) ms->factor[g][16 * i + h] = factor;
+            x[i][h] += off[i][h];
+          }
+        }
+      }
+      uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          x[i][h] = seen ? ex2(x[i][h]) : 0.0f;
+          sum[i][h] += x[i][h];
+        }
+        split_p(x[i], hi[i], lo[i]);
+      }
+      if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);  // P(T - 1) is read
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t at = p_row + (((2 * g + i) ^ swizzle) << 4);
+        st_shared_v4(at, hi[i]);
+        st_shared_v4(at + kPBytes, lo[i]);
+      }
+      fence_proxy_async_smem();
+      if (moved) {
+        named_bar_sync(bar, 128);  // thread 0's factors are written
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < kPanels; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + kRows * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ms->factor[g][i]);
+          tmem_st32(o_addr + kRows * c, o);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
+    }
+
+    // ------------------------------------------------ sums over the keys
+    float inv[2][16];  // what divides this job's rows
+    float lse = -INFINITY;
+    named_bar_sync(bar, 128);  // (red and factor are read)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s = transposed_sum16(sum[i]);
+      if ((lane & 1) == 0) ms->red[g][warp][16 * i + (lane >> 1)] = s;
+    }
+    named_bar_sync(bar, 128);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int h = 0; h < 16; ++h) {
+        const float s = (ms->red[g][0][16 * i + h] + ms->red[g][1][16 * i + h]) +
+                        (ms->red[g][2][16 * i + h] + ms->red[g][3][16 * i + h]);
+        inv[i][h] = s != 0.0f ? kv_scale / s : 0.0f;
+        if (t == 16 * i + h) lse = n > 0 ? kLn2 * (log2f(s) - off[i][h]) : -INFINITY;
+      }
+    }
+
+    // ------------------------------------------------ the next job's query, while the last products run
+    const bool more = next_job_of_group(p, ms, k + 1, next, g);
+    if (more && next.tiles() > 0) {
+      if (jobs > 0 || n > 0) warp_wait_on(&ms->q_empty, jobs + (n > 0) - 1, ms, p.err);
+      write_q(p, ms, sbase, next, g, kv_scale, next_scale);
+    }
+    if (n > 0) {
+      warp_wait_on(&ms->pv_done, T - 1, ms, p.err);
+      tc_fence_after();
+    }
+
+    // ------------------------------------------------ output
+    // A thread has one dim of a chunk; a warp's lanes write 32 neighbouring ones.
+    const int tokens = min(2, job.nq - 2 * g);  // of this warpgroup
+    const int64_t row0 = (static_cast<int64_t>(p.splits > 1 ? job.split : 0) * p.total_q + job.q0 + 2 * g) * kNumHeads;
+    const bool fits = !ms->abort_flag && MLA_DCHECK(tokens <= 0 || (job.q0 >= 0 && job.q0 + 2 * g + tokens <= p.total_q && job.split >= 0 &&
+                                 job.split < p.splits && (p.splits == 1 || row0 + tokens * kNumHeads <= p.part_rows)), p.err);
+#pragma unroll 1
+    for (int c = 0; c < kPanels; ++c) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i >= tokens || !fits) break;
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld16(o_addr + kRows * c + 16 * i, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int h = 0; h < 16; ++h) o[h] = 0;
+        }
+        const int64_t at = (row0 + 16 * i) * kVDim + 128 * c + t;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          const float v = __uint_as_float(o[h]) * inv[i][h];
+          if (p.splits > 1) {
+            p.part[at + h * kVDim] = v;
+          } else {
+            uint16_t b;
+            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v));
+            p.out[at + h * kVDim] = b;
+          }
+        }
+      }
+    }
+    if (t < 16 * tokens && fits) {
+      if (p.splits > 1)
+        p.part_lse[row0 + t] = lse;
+      else if (p.lse != nullptr)
+        p.lse[row0 + t] = lse;
+    }
+    __syncwarp();
+    if (n > 0) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->o_free));
+      ++jobs;
+    }
+    job = next;
+    live = more;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) scale[i] = next_scale[i];
+  }
+}
+
+template <bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_kernel(const __grid_constant__ SharedMaps maps, const SharedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Misc* ms = reinterpret_cast<Misc*>(smem + kOffMisc);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
+  if (tid == kProducerWarp * 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ms->job_full[i]), 1);
+      mbar_init(smem_u32(&ms->job_empty[i]), kJobReaders);
+      mbar_init(smem_u32(&ms->s_full[i]), 1);
+    }
+    for (int i = 0; i < 2 * kPanels; ++i) {
+      mbar_init(smem_u32(&ms->key_full[i]), 1);
+      mbar_init(smem_u32(&ms->key_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ms->claim), 1);
+    mbar_init(smem_u32(&ms->rope_full), 1);
+    mbar_init(smem_u32(&ms->rope_empty), 1);
+    mbar_init(smem_u32(&ms->q_full), kSoftmaxWarps);
+    mbar_init(smem_u32(&ms->q_empty), 1);
+    mbar_init(smem_u32(&ms->p_full), kSoftmaxWarps);
+    mbar_init(smem_u32(&ms->pv_done), 1);
+    mbar_init(smem_u32(&ms->o_free), kSoftmaxWarps);
+    mbar_init(smem_u32(&ms->mma_done), 1);
+    ms->abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&maps.latent);
+    prefetch_tensormap(&maps.rope);
+  }
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem_base;
+  if (warp >= kFirstSoftmaxWarp) {
+    setmaxnreg_inc<kSoftmaxRegs>();
+    run_softmax(p, ms, sbase, tmem, (warp - kFirstSoftmaxWarp) >> 2);
+  } else {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp == kProducerWarp)
+      run_producer<kPaged>(p, maps, ms, sbase);
+    else if (warp == kSchedulerWarp)
+      run_scheduler(p, ms);
+    else if (warp == kMmaWarp)
+      run_mma<kPaged>(p, ms, smem, sbase, tmem);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    const bool one = (threadIdx.x & 31) == 0;
+    if (one) drain(&ms->mma_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+    // (Abandoned: the parts are not whole.  Block 0 has written the word long before a wait runs out.)
+    if (one && ms->abort_flag) p.sched[2] = 1;
+    // The last block leaves the counters zero for the workspace's next call.
+    if (one && atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
+      p.sched[0] = 0;
+      p.sched[1] = 0;
+    }
+  }
+}
+
+}  // namespace
+
+size_t shared_smem_bytes() { return kSmemBytes; }
+
+cudaError_t shared_prepare() {
+  const cudaError_t e = cudaFuncSetAttribute(shared_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(shared_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+}
+
+cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream) {
+  const int64_t jobs = static_cast<int64_t>(p.blocks) * p.splits;
+  if (jobs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(jobs < p.num_sms ? jobs : p.num_sms);
+  return p.kv_indices != nullptr ? launch_dependent(shared_kernel<true>, grid, kThreads, kSmemBytes, stream, maps, p)
+                                 : launch_dependent(shared_kernel<false>, grid, kThreads, kSmemBytes, stream, maps, p);
+}
+
+}  // namespace mla

@@ -491,6 +491,9 @@ __device__ __forceinline__ void zero_row(const Stage1Params& p, int32_t b) {
   uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(tq) * kNumHeads * kVDim);
   const int n = cta_tokens<kQ>(p) * kNumHeads * kVDim * 2 / 16;
   for (int i = 0; i < n; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+  if (p.lse_out != nullptr)
+    for (int i = 0; i < cta_tokens<kQ>(p) * kNumHeads; ++i)
+      p.lse_out[static_cast<size_t>(tq) * kNumHeads + i] = -INFINITY;
 }
 
 // Contiguous rows: the worker's first tile, issued by the prologue thread that
@@ -822,6 +825,8 @@ __device__ __forceinline__ void cluster_combine(const Stage1Params& p, Misc* ms,
       mine = j == i ? e : mine;
     }
     ms->cl_w[i][h] = sum > 0.0f ? mine / sum : 0.0f;
+    if (p.lse_out != nullptr && i == 0 && rank == 0 && MLA_DCHECK(tq < total_tokens(p), p.err))
+      p.lse_out[static_cast<size_t>(tq) * kNumHeads + h] = kLn2 * (m + log2f(sum));
     if (tid == 0) MLA_TRACE_CLK(kTrCombineW);
   }
   __syncthreads();
@@ -2186,6 +2191,17 @@ __device__ void run_softmax(const Stage1Params& p, Misc* ms, uint32_t sbase, uin
         bulk_store(p.out + static_cast<size_t>(tq + q0) * kNumHeads * kVDim,
                    stage_q + q0 * kNumHeads * kVDim * 2, gn * kNumHeads * kVDim * 2);
         bulk_commit();
+      }
+      if (p.lse_out != nullptr && write && t < 16 * gn) {
+        // (selected, not indexed: an index known only here would put both arrays in local memory)
+        float mm = m_ref[0][0], ll = l_tot[0][0];
+#pragma unroll
+        for (int e = 1; e < 16 * kQt; ++e) {
+          mm = t == e ? m_ref[e >> 4][e & 15] : mm;
+          ll = t == e ? l_tot[e >> 4][e & 15] : ll;
+        }
+        if (MLA_DCHECK(tq + q0 + gn <= total_tokens(p), p.err))
+          p.lse_out[static_cast<size_t>(tq + q0) * kNumHeads + t] = kLn2 * (mm + log2f(ll));
       }
     } else {
       // bf16 partial of query token qi (as the pages keep their split

@@ -114,6 +114,11 @@ __global__ void __launch_bounds__(kStage2Threads) mla_decode_stage2_kernel(const
     const __nv_bfloat16 y = __float2bfloat16_rn(wsum[h] > 0.0f ? acc[h] / wsum[h] : 0.0f);
     blk[h * kStage2Threads + dd] = *reinterpret_cast<const uint16_t*>(&y);
   }
+  if (p.lse_out != nullptr && cc == 0 && dd == 0) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      p.lse_out[static_cast<size_t>(tq) * kNumHeads + 4 * j + h] = kLn2 * (m[h] + log2f(wsum[h]));
+  }
   __syncthreads();
   // 4 heads x 16 vectors of 8 dims.
   if (dd < 64) {
@@ -226,6 +231,11 @@ __global__ void __launch_bounds__(kStage2Threads, 8) mla_decode_stage2_wide_kern
   for (int h = 0; h < kHeads; ++h) {
     const __nv_bfloat16 y = __float2bfloat16_rn(wsum[h] > 0.0f ? acc[h] / wsum[h] : 0.0f);
     blk[h * kStage2Threads + dd] = *reinterpret_cast<const uint16_t*>(&y);
+  }
+  if (p.lse_out != nullptr && cc == 0 && dd == 0) {
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+      p.lse_out[static_cast<size_t>(tq) * kNumHeads + kHeads * hh + h] = kLn2 * (m[h] + log2f(wsum[h]));
   }
   __syncthreads();
   // 8 heads x 16 vectors of 8 dims: one 16-byte store a thread.
