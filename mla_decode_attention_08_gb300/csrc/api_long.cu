@@ -96,6 +96,7 @@ mla_status_t run_shared(const void* q, const void* kv, const float* kv_scale, co
   auto* ws = static_cast<uint8_t*>(workspace);
   mla::SharedParams p;
   p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint8_t*>(kv);
   p.kv_scale = kv_scale;
   p.qo_indptr = qo_indptr;
   p.kv_indptr = kv_indptr;

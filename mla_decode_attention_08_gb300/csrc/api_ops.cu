@@ -159,7 +159,7 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
 int32_t key_splits(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms, int64_t rows) {
   // (The second kernel looks for its tokens' rows, so thousands of empty ones are not cut.)
   if (blocks == 0 || 10 * blocks >= 13 * sms || batch > 1024) return 1;
-  const bool few = mla::merges_at_once(rows, mla::kPrefillV, static_cast<int32_t>(sms));
+  const bool few = mla::merges_at_once(rows, static_cast<int32_t>(sms));
   auto time = [&](int64_t s) {
     const int64_t jobs = blocks * s, longest = 40 + 19 * ((key_tiles + s - 1) / s);
     const int64_t mean = 40 + 19 * ((7 * key_tiles + 10 * s - 1) / (10 * s));

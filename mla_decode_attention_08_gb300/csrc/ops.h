@@ -97,7 +97,7 @@ struct MergeParams {
 };
 // Whether float parts of `rows` rows of `dim` are joined by threads that are all on the
 // GPU at once: four values each, two blocks of 256 an SM.
-inline bool merges_at_once(int64_t rows, int32_t dim, int32_t sms) {
+inline bool merges_at_once(int64_t rows, int32_t sms, int32_t dim = 128) {
   return rows * (dim / 4) <= static_cast<int64_t>(sms) * 2 * 256;
 }
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
@@ -139,6 +139,7 @@ cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cuda
 // over one split of its keys.
 struct SharedParams {
   const uint16_t* q;         // bf16 [total_q][16][576]
+  const uint8_t* kv;         // e4m3 codes [kv_rows][576]
   const float* kv_scale;
   const int32_t* qo_indptr;
   const int32_t* kv_indptr;

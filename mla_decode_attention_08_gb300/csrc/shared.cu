@@ -10,21 +10,23 @@
 //                                    once for its low ones
 // K(T) and V(T) are the same e4m3 codes in shared memory (V the first 512 dims), read
 // by key for the first product and by dim for the second, so nothing is converted.  A
-// bf16 query is two e4m3 terms, q 2^k = hi + lo / 16, exact down to 2^-14 of the token's
-// largest magnitude; a probability p in [0, 2^8] is hi + lo, exact to 2^-8 of itself and
-// 2^-10, which is 2^-16 of the row's reference (2^6).  TMEM is full: two S of 128 columns, O in four
-// chunks of 64.
+// bf16 query is two e4m3 terms, q 2^k = hi + lo / 8, exact down to 2^-13 of the token's
+// largest magnitude; a probability p in [0, 2^8] is hi + lo, to 2^-8 of itself and 2^-10,
+// which is 2^-14 of the row's reference (2^4).  TMEM is full: two S of 128 columns, O in
+// four chunks of 64.
 //
-// Persistent blocks, one an SM, 12 warps, take jobs (four query tokens of a group over
-// a part of its keys) from a counter:
+// Persistent blocks, one an SM, take jobs (four query tokens of a group over a part of its
+// keys) from a counter:
 //   * warp 3 finds the jobs,
-//   * warp 2 streams the keys by TMA (boxes of 128 rows, or gathers of four rows by a
-//     page table): four 128-dim panels a tile into two buffers, the 64 rotated dims
-//     into one,
-//   * warp 0 issues the products, S of tile T + 1 before O of tile T,
+//   * the keys come as four panels of 128 dims a tile into two buffers, and the 64 rotated
+//     dims into one: by warp 2 through TMA in boxes of 128 rows, or, by a page table, by
+//     warps 12-15 in 16-byte copies (TMA's gathers of four rows take 74 cycles each to
+//     issue from one warp, 160 a tile, and 20 from four; the copies of four warps bring a
+//     panel in 500 cycles),
+//   * warps 0 and 1 issue the products S and O, each as soon as it can,
 //   * warps 4-7 and 8-11 run the softmax of two query tokens each, a thread a key: the
 //     maximum over keys is over lanes, so it is only looked for when a score passes the
-//     running reference by two powers of two, which few tiles' do.
+//     running reference by four powers of two, which few tiles' do.
 // Parts of keys leave float32 results, which attn_merge.cu joins.
 #include <cstddef>
 
@@ -51,13 +53,23 @@ constexpr int kOffQRope = kOffQ + kPanels * kPanelBytes;
 constexpr int kOffP = kOffQRope + kRopeBytes;      // high terms, low terms
 constexpr int kOffMisc = kOffP + 2 * kPBytes;
 
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168,
+constexpr int kScoreWarp = 0, kValueWarp = 1, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;
+constexpr int kFirstCopyWarp = 12;
+constexpr uint32_t kSoftmaxWarps = 8, kCopyWarps = 4;
+// Threads of a block, and registers: launched with 168 a thread (128 with a page table),
+// of which the softmax warpgroups take the others' share.
+template <bool kPaged>
+__host__ __device__ constexpr int threads() { return kPaged ? 512 : 384; }
+template <bool kPaged>
+__host__ __device__ constexpr int softmax_regs() { return kPaged ? 192 : 200; }
+template <bool kPaged>
+__host__ __device__ constexpr int other_regs() { return kPaged ? 64 : 104; }
+static_assert(2 * 128 * softmax_regs<false>() + 128 * other_regs<false>() <= threads<false>() * 168 &&
+                  2 * 128 * softmax_regs<true>() + 256 * other_regs<true>() <= threads<true>() * 128,
               "register split exceeds the launch allocation");
-constexpr int kMmaWarp = 0, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;
-constexpr uint32_t kSoftmaxWarps = 8;
-constexpr uint32_t kJobReaders = 2 + kSoftmaxWarps;
+// What reads a job: two issuers, the softmax, and the producer or the copying warps.
+template <bool kPaged>
+__host__ __device__ constexpr uint32_t job_readers() { return 2 + kSoftmaxWarps + (kPaged ? kCopyWarps : 1); }
 constexpr uint32_t kBarSoftmax = 1;                // + g: named barrier of a softmax warpgroup
 constexpr uint32_t kLayoutSw128 = 2, kLayoutSw64 = 4;
 constexpr uint32_t kColS = 0, kColO = 256;         // S of tile T at 128 (T & 1); chunk c of O at + 64 c
@@ -65,11 +77,13 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kIdescQK = idesc_e4m3(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_e4m3(128, kRows, true, true);
 constexpr float kSmScaleLog2 = 1.4426950408889634f / 24.0f;  // dot products to powers of two
-// P = 2^(s - reference + kTop); the reference follows a maximum that passes it by
-// kAhead, so P stays below 2^8, which e4m3 holds.  The farther apart the two, the
-// rarer the maximum is looked for and the coarser the small probabilities: with these a
-// probability of 2^-15 of the reference's is still a step of the low term.
-constexpr float kTop = 6.0f, kAhead = 2.0f;
+// A probability is 2^(s - reference + 4), computed 2^8 smaller (split_p): the reference
+// stands at kTop.  It follows a maximum that passes it by four powers of two, so none is
+// above 2^8, which e4m3 holds.  The farther apart the two, the rarer the maximum is looked
+// for (normal scores of two powers of two: in half of 64 tiles with a distance of two, in
+// three with four; 308 and 252 us for 256 queries over 32768 keys) and the coarser the small
+// probabilities: with these one of 2^-13 of the reference's is still a step of the low term.
+constexpr float kTop = -4.0f;
 
 struct Job {
   int32_t q0, nq;    // first query token, number of them (up to four)
@@ -90,17 +104,18 @@ struct Misc {
   uint64_t rope_full, rope_empty;
   uint64_t q_full;       // a job's query operand written ...
   uint64_t q_empty;      // ... and read by its last scores
-  uint64_t s_full[2];    // S(T) complete, T & 1; S(T + 2) is issued behind O(T), that is behind p_full(T)
+  uint64_t s_full[2];    // S(T) complete, T & 1 ...
+  uint64_t s_free[2];    // ... and read; S(T + 2) is issued behind that
   uint64_t p_full;       // P(T) written, O rescaled; P(T + 1) is written behind pv_done(T)
   uint64_t pv_done;      // O(T) complete
   uint64_t o_free;       // a job's O read out
-  uint64_t mma_done;
+  uint64_t mma_done;     // both issuers' last products
   uint32_t tmem_base;
   volatile int32_t abort_flag;
   Job job[2];
   alignas(16) float red[2][4][32];  // [warpgroup][warp][row]: maxima, sums
   alignas(16) float factor[2][32];  // of O's rows: rescaling, at the end the division
-  uint32_t amax[2][2][4];           // [warpgroup][token][warp]
+  uint32_t amax[2][4];              // [warpgroup][warp]: of |q|
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one block");
@@ -211,20 +226,23 @@ __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, 
   __syncwarp();
 }
 
-__device__ __forceinline__ void run_scheduler(const SharedParams& p, Misc* ms) {
+// The first job is the block's own and found before the roles start; the others come from
+// a counter.
+__device__ __forceinline__ void run_scheduler(const SharedParams& p, const Batch& groups, Misc* ms) {
   const int lane = threadIdx.x & 31;
-  const Batch groups = count_groups(p);
-  uint32_t index = blockIdx.x;  // the first job is the block's own, the others come from a counter
   for (uint32_t k = 0;; ++k) {
     Job* job = &ms->job[k & 1];
-    if (!warp_wait_on(&ms->job_empty[k & 1], (k >> 1) + 1, ms, p.err)) return;  // (the first two pass)
-    find_job(p, groups, index, job);
+    if (k > 0) {
+      uint32_t index = 0;
+      if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
+      index = __shfl_sync(0xffffffffu, index, 0);
+      if (k > 1 && !warp_wait_on(&ms->job_empty[k & 1], (k >> 1) - 1, ms, p.err)) return;
+      find_job(p, groups, index, job);
+    }
     const int32_t live = job->live;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
     if (live == 0 || !warp_wait_on(&ms->claim, k, ms, p.err)) return;
-    if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
-    index = __shfl_sync(0xffffffffu, index, 0);
   }
 }
 
@@ -237,43 +255,7 @@ __device__ __forceinline__ bool next_job(const SharedParams& p, Misc* ms, uint32
   return job.live != 0;
 }
 
-// ------------------------------------------------------------ producer (one warp)
-// A page table's four cache rows of this lane, keys 4 lane .. 4 lane + 3 of a tile; keys
-// behind the part's end repeat its last one.
-template <bool kPaged>
-__device__ __forceinline__ void load_rows(const SharedParams& p, const Job& job, int32_t j, int32_t (&rows)[4]) {
-  if constexpr (kPaged) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      rows[i] = __ldg(p.kv_indices + job.k0 + min(job.keys - 1, j * kTileTokens + 4 * static_cast<int>(threadIdx.x & 31) + i));
-  }
-}
-__device__ __forceinline__ void check_rows(const SharedParams& p, int32_t (&rows)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (rows[i] >= 0 && rows[i] < p.kv_rows) continue;
-    atomicOr(p.err, MLA_DERR_KV_INDEX);
-    rows[i] = 0;
-  }
-}
-
-// A panel of `kWidth` bytes a key, by boxes or by gathers.
-template <bool kPaged, int kWidth>
-__device__ __forceinline__ void copy_panel(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t key,
-                                           const int32_t (&rows)[4], const uint64_t* full, uint64_t policy) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t bar = smem_u32(full);
-  if (lane == 0) mbar_arrive_expect_tx(bar, kTileTokens * kWidth);
-  if constexpr (kPaged) {
-    __syncwarp();
-    tma_gather4(dst + lane * 4 * kWidth, map, x, rows[0], rows[1], rows[2], rows[3], bar, policy);
-  } else if (lane == 0) {
-    tma_load_2d(dst, map, x, key, bar, policy);
-  }
-  __syncwarp();
-}
-
-template <bool kPaged>
+// ------------------------------------------------------------ keys by TMA (one warp)
 __device__ __forceinline__ void run_producer(const SharedParams& p, const SharedMaps& m, Misc* ms, uint32_t sbase) {
   const int lane = threadIdx.x & 31;
   // (several blocks read a key at about the same time)
@@ -284,35 +266,36 @@ __device__ __forceinline__ void run_producer(const SharedParams& p, const Shared
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t n = p.stall_stream ? 0 : job.tiles();
     if (n == 0 && lane == 0) mbar_arrive(smem_u32(&ms->claim));
-    int32_t rows[4], next[4] = {0, 0, 0, 0};
-    if (n > 0) load_rows<kPaged>(p, job, 0, next);
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
       const int32_t key = job.k0 + j * kTileTokens;
       if (j == n - 1 && lane == 0) mbar_arrive(smem_u32(&ms->claim));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) rows[i] = next[i];
-      if constexpr (kPaged) check_rows(p, rows);
-      if (j + 1 < n) load_rows<kPaged>(p, job, j + 1, next);
-      if (!MLA_DCHECK(kPaged || (key >= 0 && key < p.kv_rows), p.err)) {
+      if (!MLA_DCHECK(key >= 0 && key < p.kv_rows, p.err)) {
         ms->abort_flag = 1;
         ok = false;
         break;
       }
       if (T > 0) ok = warp_wait_on(&ms->rope_empty, T - 1, ms, p.err);
       if (!ok) break;
-      copy_panel<kPaged, 64>(sbase + kOffRope, &m.rope, kVDim, key, rows, &ms->rope_full, keep);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(smem_u32(&ms->rope_full), kRopeBytes);
+        tma_load_2d(sbase + kOffRope, &m.rope, kVDim, key, smem_u32(&ms->rope_full), keep);
+      }
       ++ropes;
 #pragma unroll 1
       for (int c = 0; c < kPanels; ++c) {
         const uint32_t at = kPanels * (T & 1) + c;
         if (T > 1) ok = warp_wait_on(&ms->key_empty[at], (T >> 1) - 1, ms, p.err);
         if (!ok) break;
-        copy_panel<kPaged, 128>(sbase + kOffKeys + at * kPanelBytes, &m.latent, 128 * c, key, rows, &ms->key_full[at], keep);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(smem_u32(&ms->key_full[at]), kPanelBytes);
+          tma_load_2d(sbase + kOffKeys + at * kPanelBytes, &m.latent, 128 * c, key, smem_u32(&ms->key_full[at]), keep);
+        }
         ++panels;
       }
+      __syncwarp();
     }
   }
-  if (!ms->abort_flag) return;  // the issuer waits for every copy
+  if (!ms->abort_flag) return;  // the issuers wait for every copy
   // Abandoned: the copies in flight land before the block's memory is given up.
   if (lane == 0) {
     if (ropes > 0) drain(&ms->rope_full, ropes - 1);
@@ -322,7 +305,114 @@ __device__ __forceinline__ void run_producer(const SharedParams& p, const Shared
   __syncwarp();
 }
 
-// ------------------------------------------------------------ MMA issuer (one warp, an elected lane issues)
+// ------------------------------------------------------------ keys by a page table (four warps)
+// Panel f of a block: five a tile, the rotated dims, then the latent ones.  A thread's copies
+// complete in order, so it can hand over a panel once at most the later ones are in flight;
+// before it waits for a buffer it hands over everything, since the buffer may wait for that.
+struct Copies {
+  uint32_t done = 0;    // panels handed over
+  uint32_t issued = 0;
+  __device__ __forceinline__ void hand_over(Misc* ms) {
+    const uint32_t T = done / (kPanels + 1), c = done % (kPanels + 1);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+      mbar_arrive(smem_u32(c == 0 ? &ms->rope_full : &ms->key_full[kPanels * (T & 1) + c - 1]));
+    ++done;
+  }
+  __device__ __forceinline__ void finish(Misc* ms) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    while (done < issued) hand_over(ms);
+  }
+};
+constexpr int kCopyThreads = 32 * kCopyWarps;
+
+// A thread's rows of a tile: it copies piece t & 7 of latent row 16 i + t / 8 and piece t & 3 of
+// the rotated dims of row 32 i + t / 4.
+constexpr int kLatentRows = kTileTokens * 8 / kCopyThreads, kRopeRows = kTileTokens * 4 / kCopyThreads;
+static_assert(kLatentRows * kCopyThreads == kTileTokens * 8 && kCopyThreads % 8 == 0, "whole panels");
+struct CopyRows {
+  int32_t latent[kLatentRows], rope[kRopeRows];
+  // (keys behind the part's end repeat its last one)
+  __device__ __forceinline__ void load(const SharedParams& p, const Job& job, int32_t j) {
+    const int t = threadIdx.x - 32 * kFirstCopyWarp;
+    const int32_t* at = p.kv_indices + job.k0;
+    const int32_t last = job.keys - 1, key = j * kTileTokens;
+#pragma unroll
+    for (int i = 0; i < kLatentRows; ++i) latent[i] = __ldg(at + min(last, key + (t >> 3) + i * (kCopyThreads / 8)));
+#pragma unroll
+    for (int i = 0; i < kRopeRows; ++i) rope[i] = __ldg(at + min(last, key + (t >> 2) + i * (kCopyThreads / 4)));
+  }
+  __device__ __forceinline__ void check(const SharedParams& p) {
+    bool bad = false;
+    auto one = [&](int32_t& row) {
+      const bool out = row < 0 || row >= p.kv_rows;
+      bad = bad || out;
+      row = out ? 0 : row;
+    };
+#pragma unroll
+    for (int i = 0; i < kLatentRows; ++i) one(latent[i]);
+#pragma unroll
+    for (int i = 0; i < kRopeRows; ++i) one(rope[i]);
+    if (bad) atomicOr(p.err, MLA_DERR_KV_INDEX);
+  }
+};
+
+__device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint32_t sbase) {
+  const int t = threadIdx.x - 32 * kFirstCopyWarp;
+  const int piece = t & 7, row0 = t >> 3, rope_piece = t & 3, rope_row0 = t >> 2;
+  const uint8_t* latent = p.kv + 16 * piece;
+  const uint8_t* rope = p.kv + kVDim + 16 * rope_piece;
+  // (of the rows that a thread copies all have the same place in a swizzle's pattern)
+  const uint32_t latent_at = sbase + kOffKeys + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
+  const uint32_t rope_at = sbase + kOffRope + rope_row0 * 64 + ((rope_piece ^ ((rope_row0 >> 1) & 3)) << 4);
+  Copies copies;
+  CopyRows rows, next;
+  uint32_t T = 0;
+  Job job;
+  bool ok = true;
+  // A buffer is free, or everything before is handed over and it is waited for.
+  auto buffer = [&](const uint64_t* empty, uint32_t phase) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(empty), phase & 1))) return true;
+    copies.finish(ms);
+    return warp_wait_on(empty, phase, ms, p.err);
+  };
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    const int32_t n = p.stall_stream ? 0 : job.tiles();
+    if (n == 0 && t == 0) mbar_arrive(smem_u32(&ms->claim));
+    if (n > 0) next.load(p, job, 0);
+    for (int32_t j = 0; j < n && ok; ++j, ++T) {
+      if (j == n - 1 && t == 0) mbar_arrive(smem_u32(&ms->claim));
+      rows = next;
+      rows.check(p);
+      if (j + 1 < n) next.load(p, job, j + 1);
+      if (T > 0) ok = buffer(&ms->rope_empty, T - 1);
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < kRopeRows; ++i)
+        cp_async_16(rope_at + i * (kCopyThreads / 4) * 64, rope + static_cast<int64_t>(rows.rope[i]) * kQkDim);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++copies.issued;
+#pragma unroll 1
+      for (int c = 0; c < kPanels; ++c) {
+        const uint32_t at = kPanels * (T & 1) + c;
+        if (T > 1) ok = buffer(&ms->key_empty[at], (T >> 1) - 1);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kLatentRows; ++i)
+          cp_async_16(latent_at + at * kPanelBytes + i * (kCopyThreads / 8) * 128,
+                      latent + static_cast<int64_t>(rows.latent[i]) * kQkDim + 128 * c);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++copies.issued;
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        while (copies.done + 2 < copies.issued) copies.hand_over(ms);
+      }
+    }
+    copies.finish(ms);  // (the next job may be far off)
+  }
+}
+
+// ------------------------------------------------------------ MMA issuers (a warp each, an elected lane issues)
 // Keys behind the part's end lie in the tile's boxes too (another row's, or never
 // written): their probabilities are zero, but zero times NaN is NaN, so they are zeroed
 // in shared memory before either product reads them.
@@ -337,65 +427,83 @@ __device__ __forceinline__ void clean_keys(uint8_t* panels, int32_t keys) {
   __syncwarp();
 }
 
+// S(T) = K(T) . Q^T, panel by panel as they land.
 template <bool kPaged>
-__device__ __forceinline__ void run_mma(const SharedParams& p, Misc* ms, uint8_t* smem, uint32_t sbase, uint32_t tmem) {
+__device__ __forceinline__ void run_scores(const SharedParams& p, Misc* ms, uint8_t* smem, uint32_t sbase, uint32_t tmem) {
   constexpr uint32_t kPanel = kPanelBytes >> 4;  // in descriptor address units
   const uint64_t key_k = smem_desc(sbase + kOffKeys, 1024, 1024, kLayoutSw128);
   const uint64_t rope_k = smem_desc(sbase + kOffRope, 512, 512, kLayoutSw64);
   const uint64_t q_k = smem_desc(sbase + kOffQ, 1024, 1024, kLayoutSw128);
   const uint64_t q_rope = smem_desc(sbase + kOffQRope, 512, 512, kLayoutSw64);
-  const uint64_t p_mn = smem_desc(sbase + kOffP, 512, 512, kLayoutSw64);
   auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity, ms, p.err); };
-  // S(T) = K(T) . Q^T, panel by panel as they land
-  auto scores = [&](uint32_t T, int32_t keys, bool last) {
-    const uint32_t d = tmem + kColS + 128 * (T & 1);
-    const bool clean = !kPaged && keys < kTileTokens;
-    if (clean) {
-      for (int c = 0; c < kPanels; ++c)
-        if (!on(&ms->key_full[kPanels * (T & 1) + c], T >> 1)) return false;
-      clean_keys(smem + kOffKeys + kPanels * (T & 1) * kPanelBytes, keys);
-    }
-    if (!on(&ms->rope_full, T)) return false;
-    tc_fence_after();
-    if (elect_one()) {
-      umma_f8(d, rope_k, q_rope, kIdescQK, 0);
-      umma_f8(d, rope_k + 2, q_rope + 2, kIdescQK, 1);
-      umma_commit(smem_u32(&ms->rope_empty));
-    }
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < kPanels; ++c) {
-      if (!on(&ms->key_full[kPanels * (T & 1) + c], T >> 1)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t a = key_k + (kPanels * (T & 1) + c) * kPanel, b = q_k + c * kPanel;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_f8(d, a + 2 * kk, b + 2 * kk, kIdescQK, 1);
-        if (c == kPanels - 1) {
-          umma_commit(smem_u32(&ms->s_full[T & 1]));
-          if (last) umma_commit(smem_u32(&ms->q_empty));
-        }
-      }
-      __syncwarp();
-    }
-    return true;
-  };
   uint32_t T = 0, jobs = 0;
   Job job;
   bool ok = true;
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t n = job.tiles();
     if (n == 0) continue;
-    ok = on(&ms->q_full, jobs) && scores(T, job.keys, n == 1);
+    ok = on(&ms->q_full, jobs++);
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
-      if (j + 1 < n) ok = scores(T + 1, job.keys - (j + 1) * kTileTokens, j + 2 == n);
-      ok = ok && (j > 0 || jobs == 0 || on(&ms->o_free, jobs - 1)) && on(&ms->p_full, T);
+      const uint32_t d = tmem + kColS + 128 * (T & 1), first = kPanels * (T & 1);
+      const int32_t keys = job.keys - j * kTileTokens;
+      if (!kPaged && keys < kTileTokens) {
+        for (int c = 0; c < kPanels && ok; ++c) ok = on(&ms->key_full[first + c], T >> 1);
+        if (!ok) break;
+        clean_keys(smem + kOffKeys + first * kPanelBytes, keys);
+      }
+      ok = (T < 2 || on(&ms->s_free[T & 1], (T >> 1) - 1)) && on(&ms->rope_full, T);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        umma_f8(d, rope_k, q_rope, kIdescQK, 0);
+        umma_f8(d, rope_k + 2, q_rope + 2, kIdescQK, 1);
+        umma_commit(smem_u32(&ms->rope_empty));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < kPanels; ++c) {
+        ok = ok && on(&ms->key_full[first + c], T >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = key_k + (first + c) * kPanel, b = q_k + c * kPanel;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) umma_f8(d, a + 2 * kk, b + 2 * kk, kIdescQK, 1);
+          if (c == kPanels - 1) {
+            umma_commit(smem_u32(&ms->s_full[T & 1]));
+            if (j == n - 1) umma_commit(smem_u32(&ms->q_empty));
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
+  __syncwarp();
+}
+
+// O(T) += V(T)^T . P(T)^T.  (The panels have landed: S(T), which P(T) comes from, read them.)
+__device__ __forceinline__ void run_values(const SharedParams& p, Misc* ms, uint32_t sbase, uint32_t tmem) {
+  constexpr uint32_t kPanel = kPanelBytes >> 4;
+  const uint64_t key_mn = smem_desc(sbase + kOffKeys, 1024, 1024, kLayoutSw128);
+  const uint64_t p_mn = smem_desc(sbase + kOffP, 512, 512, kLayoutSw64);
+  auto on = [&](const uint64_t* bar, uint32_t parity) { return warp_wait_on(bar, parity, ms, p.err); };
+  uint32_t T = 0, jobs = 0;
+  Job job;
+  bool ok = true;
+  for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
+    const int32_t n = job.tiles();
+    if (n == 0) continue;
+    ok = jobs == 0 || on(&ms->o_free, jobs - 1);
+    ++jobs;
+    for (int32_t j = 0; j < n && ok; ++j, ++T) {
+      ok = on(&ms->p_full, T);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < kPanels; ++c) {
-          const uint64_t a = key_k + (kPanels * (T & 1) + c) * kPanel;
+          const uint64_t a = key_mn + (kPanels * (T & 1) + c) * kPanel;
           const uint32_t d = tmem + kColO + kRows * c;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 32 keys each: 4 KB of a panel, 2 KB of a term of P
@@ -408,7 +516,6 @@ __device__ __forceinline__ void run_mma(const SharedParams& p, Misc* ms, uint8_t
       }
       __syncwarp();
     }
-    ++jobs;
   }
   if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
   __syncwarp();
@@ -450,107 +557,141 @@ __device__ __forceinline__ bool any_of_group(bool v, int g) {
                : "=r"(r) : "r"(static_cast<uint32_t>(v)), "r"(kBarSoftmax + g) : "memory");
   return r != 0;
 }
-// 16 probabilities (0 .. 2^8) as two e4m3 terms, hi = e4m3(p), lo = e4m3(p - hi), each
-// packed four to a word.  By way of half precision, whose 11 bits both terms fit in.
-__device__ __forceinline__ void split_p(const float (&x)[16], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+  const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, float by) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(by));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two e4m3 terms without the conversion instructions, whose rate is a fraction of the
+// others'.  A half precision value below 2 in magnitude has a fifth exponent bit of zero, so
+// its bits 13 .. 7 are the e4m3 code of the value times 2^8, cut to its four leading bits:
+// denormals included, since both formats' exponents end 2^8 apart.  The high term is that
+// cut value, the low term the rest, which half precision holds exactly, rounded.
+constexpr uint32_t kCut = 0xFF80FF80u, kRound = 0x00800080u, kSigns = 0x80008000u;
+// The codes of two pairs, at bits 15 .. 8 of each half, packed.
+__device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+
+// 16 probabilities p 2^-8, 0 <= p <= 2^8, given as pairs: p = hi + lo.  The low term is below a
+// step of the high one, 2^-3 p, so that half of its own step is 2^-8 p at most.
+__device__ __forceinline__ void split_p(const uint32_t (&h)[8], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const __half2 v = __floats2half2_rn(x[2 * k], x[2 * k + 1]);
-    const uint16_t h = cvt_f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&v));
-    const uint32_t back = cvt_e4m3x2_to_f16x2(h);
-    const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2*>(&back));
-    const uint16_t l = cvt_f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
-    if (k & 1) {
-      hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
-      lo[k >> 1] |= static_cast<uint32_t>(l) << 16;
-    } else {
-      hi[k >> 1] = h;
-      lo[k >> 1] = l;
-    }
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = h[2 * k], b = h[2 * k + 1];
+    hi[k] = pack_codes(a << 1, b << 1);
+    lo[k] = pack_codes((half2_sub(a, a & kCut) << 1) + kRound, (half2_sub(b, b & kCut) << 1) + kRound);
   }
 }
-// 16 query values, scaled, as hi = e4m3(x), lo = e4m3(16 (x - hi)).
+// A pair of signed codes at bits 15 .. 8 of each half.
+__device__ __forceinline__ uint32_t signed_codes(uint32_t h, uint32_t round) {
+  return (((h << 1) + round) & ~kSigns) | (h & kSigns);
+}
+// 16 query values, scaled by `up` to at most 448 2^-8, as hi + lo / 8 in units of 2^-8.  They
+// have eight leading bits, so the rest, below 2^5 units, has four and both terms are exact
+// (but for denormals, which are rounded).
 __device__ __forceinline__ void split_q(const uint4& a, const uint4& b, float up, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t x[8], y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float x = __uint_as_float(w[k] << 16) * up, y = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-    const uint16_t h = cvt_e4m3x2(x, y);
-    const uint32_t back = cvt_e4m3x2_to_f16x2(h);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-    const uint16_t l = cvt_e4m3x2((x - f.x) * 16.0f, (y - f.y) * 16.0f);
-    if (k & 1) {
-      hi[k >> 1] |= static_cast<uint32_t>(h) << 16;
-      lo[k >> 1] |= static_cast<uint32_t>(l) << 16;
-    } else {
-      hi[k >> 1] = h;
-      lo[k >> 1] = l;
-    }
+    const uint32_t h = half2_bits(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+    x[k] = signed_codes(h, 0);
+    y[k] = signed_codes(half2_mul(half2_sub(h, h & kCut), 8.0f), kRound);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    hi[k] = pack_codes(x[2 * k], x[2 * k + 1]);
+    lo[k] = pack_codes(y[2 * k], y[2 * k + 1]);
   }
 }
-// Byte address of 16-dim piece `ch` of operand row `row` of the query.
-__device__ __forceinline__ uint32_t q_piece(uint32_t sbase, int row, int ch) {
-  if (ch < 32) return sbase + kOffQ + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-  return sbase + kOffQRope + row * 64 + (((ch - 32) ^ ((row >> 1) & 3)) << 4);
-}
-
 // The query operand's rows of warpgroup g's two tokens, each scaled by a power of two so
 // that its largest magnitude lies in (224, 448].  scale[i]: what turns token i's products
 // into powers of two (NaN for a query that is not finite, whose outputs become NaN).
+// A warp has eight of the 32 rows: a lane 16 latent dims of each, and then 16 of the rotated
+// dims of one.
 __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_t sbase, const Job& job, int g,
                                         float kv_scale, float (&scale)[2]) {
-  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31;
-  constexpr int kRounds = 2 * kNumHeads * (kQkDim / 16) / 128;  // pieces a thread
-  static_assert(kRounds * 128 == 2 * kNumHeads * (kQkDim / 16), "whole rounds");
-  uint4 raw[kRounds][2];
-  uint32_t amax[2] = {0, 0};
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  constexpr int kWarpRows = 2 * kNumHeads / 4;
+  static_assert(kVDim / 16 == 32 && kWarpRows * ((kQkDim - kVDim) / 16) == 32, "a lane a piece");
+  const int row0 = kWarpRows * warp, mine = warp >> 1;  // the warp's token
+  const int rope_row = row0 + (lane >> 2), rope_ch = kVDim / 16 + (lane & 3);
+  uint4 raw[kWarpRows + 1][2];
+  const bool there = 2 * g + mine < job.nq && MLA_DCHECK(job.q0 >= 0 && job.q0 + 2 * g + mine < p.total_q, p.err);
+  const uint16_t* src = p.q + (static_cast<int64_t>(job.q0 + 2 * g) * kNumHeads) * kQkDim;
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int piece = t + 128 * r, row = piece / (kQkDim / 16), ch = piece % (kQkDim / 16);
-    raw[r][0] = raw[r][1] = make_uint4(0, 0, 0, 0);
-    const int token = 2 * g + (row >> 4);
-    if (token < job.nq && MLA_DCHECK(job.q0 >= 0 && job.q0 + token < p.total_q, p.err)) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (static_cast<int64_t>(job.q0 + 2 * g) * kNumHeads + row) * kQkDim + 16 * ch);
-      raw[r][0] = __ldg(src);
-      raw[r][1] = __ldg(src + 1);
-    }
+  for (int r = 0; r <= kWarpRows; ++r) {
+    const uint4* at = reinterpret_cast<const uint4*>(src + (r < kWarpRows ? (row0 + r) * kQkDim + 16 * lane
+                                                                          : rope_row * kQkDim + 16 * rope_ch));
+    raw[r][0] = there ? __ldg(at) : make_uint4(0, 0, 0, 0);
+    raw[r][1] = there ? __ldg(at + 1) : make_uint4(0, 0, 0, 0);
   }
+  uint32_t top = 0;
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
+  for (int r = 0; r <= kWarpRows; ++r) {
     const uint32_t w[8] = {raw[r][0].x, raw[r][0].y, raw[r][0].z, raw[r][0].w, raw[r][1].x, raw[r][1].y, raw[r][1].z, raw[r][1].w};
-    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-    const int which = (t + 128 * r) / (kQkDim / 16) >> 4;
-    amax[0] = which == 0 ? max(amax[0], top) : amax[0];
-    amax[1] = which == 1 ? max(amax[1], top) : amax[1];
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    amax[i] = __reduce_max_sync(0xffffffffu, amax[i]);
-    if (lane == 0) ms->amax[g][i][warp] = amax[i];
-  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) ms->amax[g][warp] = top;
   named_bar_sync(kBarSoftmax + g, 128);
-  float up[2];
+  float up = 0.0f;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t top = max(max(ms->amax[g][i][0], ms->amax[g][i][1]), max(ms->amax[g][i][2], ms->amax[g][i][3]));
-    // The exponent e of the largest magnitude m 2^e, 1 <= m < 2, of bf16 bits: scaled to
+    top = max(ms->amax[g][2 * i], ms->amax[g][2 * i + 1]);
+    // The exponent e of the largest magnitude m 2^e, 1 <= m < 2, of bf16 bits: scaled by 2^k to
     // 2^8 m where m <= 1.75, else to 2^7 m.  (Zeros and denormals: clamped.)
     const int e = static_cast<int>(top >> 7) - 127;
-    int k2 = (top & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
-    k2 = top == 0 ? 0 : min(max(k2, -126), 126);
-    up[i] = __int_as_float((k2 + 127) << 23);
-    scale[i] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((127 - k2) << 23) * kv_scale * kSmScaleLog2;
+    int k = (top & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
+    k = top == 0 ? 0 : min(k, 126);
+    scale[i] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
+    // 2^(k - 8), which is a denormal for the largest of all
+    if (i == mine) up = __int_as_float(k - 8 + 127 > 0 ? (k - 8 + 127) << 23 : 1 << (22 + (k - 8 + 127)));
   }
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
-    const int piece = t + 128 * r, row = piece / (kQkDim / 16), ch = piece % (kQkDim / 16);
+  for (int r = 0; r <= kWarpRows; ++r) {
     uint32_t hi[4], lo[4];
-    split_q(raw[r][0], raw[r][1], row < kNumHeads ? up[0] : up[1], hi, lo);
-    st_shared_v4(q_piece(sbase, 2 * kNumHeads * g + row, ch), hi);
-    st_shared_v4(q_piece(sbase, kRows + 2 * kNumHeads * g + row, ch), lo);
+    split_q(raw[r][0], raw[r][1], up, hi, lo);
+    const int row = 2 * kNumHeads * g + (r < kWarpRows ? row0 + r : rope_row), ch = r < kWarpRows ? lane : rope_ch;
+    const uint32_t at = r < kWarpRows ? sbase + kOffQ + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4)
+                                      : sbase + kOffQRope + row * 64 + (((ch & 3) ^ ((row >> 1) & 3)) << 4);
+    st_shared_v4(at, hi);
+    st_shared_v4(at + kRows * (r < kWarpRows ? 128 : 64), lo);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -582,48 +723,64 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
   if (live && job.tiles() > 0) write_q(p, ms, sbase, job, g, kv_scale, scale);
   for (uint32_t k = 0; live; ++k) {
     const int32_t n = job.tiles();
-    // off: kTop less the reference; sum: of this thread's keys
-    float off[2][16], sum[2][16];
+    // Of pairs of rows: kTop less the reference, and this thread's keys' sum.
+    uint64_t off[2][8], sum[2][8];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int h = 0; h < 16; ++h) {
-        off[i][h] = INFINITY;
-        sum[i][h] = 0.0f;
+      for (int h = 0; h < 8; ++h) {
+        off[i][h] = pack2(INFINITY, INFINITY);
+        sum[i][h] = 0;
       }
     for (int32_t j = 0; j < n; ++j, ++T) {
       warp_wait_on(&ms->s_full[T & 1], T >> 1, ms, p.err);
       tc_fence_after();
+      const bool partial = (j + 1) * kTileTokens > job.keys;  // (the same for the whole block)
       const bool seen = j * kTileTokens + t < job.keys;
-      float x[2][16], high = -INFINITY;
+      // Scores as powers of two over the reference, kTop up.
+      uint64_t x[2][8];
+      auto exponents = [&] {
+        uint32_t hi[2][16], lo[2][16];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t hi[16], lo[16];
-        tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi);
-        tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo);
-        tmem_wait_ld();
-        const float a = scale[i], b = scale[i] * 0.0625f;
-#pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          x[i][h] = fmaf(__uint_as_float(lo[h]), b, fmaf(__uint_as_float(hi[h]), a, off[i][h]));
-          high = fmaxf(high, x[i][h]);
+        for (int i = 0; i < 2; ++i) {
+          tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi[i]);
+          tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo[i]);
         }
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t a = pack2(scale[i], scale[i]), b = pack2(scale[i] * 0.125f, scale[i] * 0.125f);
+#pragma unroll
+          for (int h = 0; h < 8; ++h)
+            x[i][h] = fma2(pack2(lo[i][2 * h], lo[i][2 * h + 1]), b, fma2(pack2(hi[i][2 * h], hi[i][2 * h + 1]), a, off[i][h]));
+        }
+      };
+      bool look = j == 0;  // (off is infinite)
+      if (!look) {
+        exponents();
+        float high = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            float u, v;
+            unpack2(x[i][h], u, v);
+            high = fmaxf(high, fmaxf(u, v));
+          }
+        look = any_of_group(seen && high > 0.0f, g);
       }
-      // (a job's first tile: off is infinite)
-      bool moved = false;
-      if (any_of_group(seen && high > kTop + kAhead, g)) {
-        moved = j > 0;
+      const bool moved = look && j > 0;
+      if (look) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t hi[16], lo[16];
           tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi);
           tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo);
           tmem_wait_ld();
-          const float a = scale[i], b = scale[i] * 0.0625f;
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
-            x[i][h] = fmaf(__uint_as_float(lo[h]), b, __uint_as_float(hi[h]) * a);
-            const float m = warp_max(seen ? x[i][h] : -INFINITY);
+            const float s = fmaf(__uint_as_float(lo[h]), scale[i] * 0.125f, __uint_as_float(hi[h]) * scale[i]);
+            const float m = warp_max(seen ? s : -INFINITY);
             if (lane == 0) ms->red[g][warp][16 * i + h] = m;
           }
         }
@@ -631,30 +788,47 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-          for (int h = 0; h < 16; ++h) {
-            const float m = fmaxf(fmaxf(ms->red[g][0][16 * i + h], ms->red[g][1][16 * i + h]),
-                                  fmaxf(ms->red[g][2][16 * i + h], ms->red[g][3][16 * i + h]));
-            float factor = 1.0f;
-            if (m + off[i][h] > kTop + kAhead) {
-              const float to = kTop - m;
-              factor = ex2(to - off[i][h]);  // 0 on a job's first tile
-              off[i][h] = to;
-              sum[i][h] *= factor;
+          for (int h = 0; h < 8; ++h) {
+            float o[2], factor[2] = {1.0f, 1.0f};
+            unpack2(off[i][h], o[0], o[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = 16 * i + 2 * h + e;
+              const float m = fmaxf(fmaxf(ms->red[g][0][row], ms->red[g][1][row]), fmaxf(ms->red[g][2][row], ms->red[g][3][row]));
+              if (m + o[e] > 0.0f) {
+                const float to = kTop - m;
+                factor[e] = ex2(to - o[e]);  // 0 on a job's first tile
+                o[e] = to;
+              }
             }
-            if (t == 0) ms->factor[g][16 * i + h] = factor;
-            x[i][h] += off[i][h];
+            off[i][h] = pack2(o[0], o[1]);
+            sum[i][h] = mul2(sum[i][h], pack2(factor[0], factor[1]));
+            if (t == 0) *reinterpret_cast<float2*>(&ms->factor[g][16 * i + 2 * h]) = make_float2(factor[0], factor[1]);
           }
         }
+        exponents();  // (anew, so that a row that stands has the bits it has beside any other rows)
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[T & 1]));
       uint32_t hi[2][4], lo[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        uint32_t halves[8];
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          x[i][h] = seen ? ex2(x[i][h]) : 0.0f;
-          sum[i][h] += x[i][h];
+        for (int h = 0; h < 8; ++h) {
+          float u, v;
+          unpack2(x[i][h], u, v);
+          u = ex2(u);
+          v = ex2(v);
+          if (partial) {
+            u = seen ? u : 0.0f;
+            v = seen ? v : 0.0f;
+          }
+          sum[i][h] = add2(sum[i][h], pack2(u, v));
+          halves[h] = half2_bits(u, v);
         }
-        split_p(x[i], hi[i], lo[i]);
+        split_p(halves, hi[i], lo[i]);
       }
       if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);  // P(T - 1) is read
 #pragma unroll
@@ -677,32 +851,40 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
           tmem_st32(o_addr + kRows * c, o);
         }
         tmem_wait_st();
+        tc_fence_before();
       }
-      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
     }
 
     // ------------------------------------------------ sums over the keys
-    float inv[2][16];  // what divides this job's rows
-    float lse = -INFINITY;
+    float lse = -INFINITY;  // of row t of the warpgroup, in its first warp
     named_bar_sync(bar, 128);  // (red and factor are read)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float s = transposed_sum16(sum[i]);
+      float v[16];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) unpack2(sum[i][h], v[2 * h], v[2 * h + 1]);
+      const float s = transposed_sum16(v);
       if ((lane & 1) == 0) ms->red[g][warp][16 * i + (lane >> 1)] = s;
     }
     named_bar_sync(bar, 128);
+    if (warp == 0) {
+      const float s = (ms->red[g][0][lane] + ms->red[g][1][lane]) + (ms->red[g][2][lane] + ms->red[g][3][lane]);
+      ms->factor[g][lane] = s != 0.0f ? kv_scale * 0x1p-8f / s : 0.0f;  // (P is 2^8 times what was summed)
+      float o = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int h = 0; h < 16; ++h) {
-        const float s = (ms->red[g][0][16 * i + h] + ms->red[g][1][16 * i + h]) +
-                        (ms->red[g][2][16 * i + h] + ms->red[g][3][16 * i + h]);
-        inv[i][h] = s != 0.0f ? kv_scale / s : 0.0f;
-        if (t == 16 * i + h) lse = n > 0 ? kLn2 * (log2f(s) - off[i][h]) : -INFINITY;
-      }
+        for (int h = 0; h < 8; ++h) {
+          float u, v;
+          unpack2(off[i][h], u, v);
+          o = lane == 16 * i + 2 * h ? u : o;
+          o = lane == 16 * i + 2 * h + 1 ? v : o;
+        }
+      if (n > 0) lse = kLn2 * (log2f(s) - o);
     }
+    named_bar_sync(bar, 128);
 
     // ------------------------------------------------ the next job's query, while the last products run
     const bool more = next_job_of_group(p, ms, k + 1, next, g);
@@ -737,7 +919,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
         const int64_t at = (row0 + 16 * i) * kVDim + 128 * c + t;
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
-          const float v = __uint_as_float(o[h]) * inv[i][h];
+          const float v = __uint_as_float(o[h]) * ms->factor[g][16 * i + h];
           if (p.splits > 1) {
             p.part[at + h * kVDim] = v;
           } else {
@@ -761,6 +943,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       if (lane == 0) mbar_arrive(smem_u32(&ms->o_free));
       ++jobs;
     }
+    named_bar_sync(bar, 128);  // (factor is read)
     job = next;
     live = more;
 #pragma unroll
@@ -769,7 +952,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
 }
 
 template <bool kPaged>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<kPaged>(), 1)
     shared_kernel(const __grid_constant__ SharedMaps maps, const SharedParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -777,53 +960,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   Misc* ms = reinterpret_cast<Misc*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5;
-  if (warp == kMmaWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
+  if (warp == kScoreWarp) tmem_alloc(smem_u32(&ms->tmem_base), kTmemCols);
   if (tid == kProducerWarp * 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ms->job_full[i]), 1);
-      mbar_init(smem_u32(&ms->job_empty[i]), kJobReaders);
+      mbar_init(smem_u32(&ms->job_empty[i]), job_readers<kPaged>());
       mbar_init(smem_u32(&ms->s_full[i]), 1);
+      mbar_init(smem_u32(&ms->s_free[i]), kSoftmaxWarps);
     }
     for (int i = 0; i < 2 * kPanels; ++i) {
-      mbar_init(smem_u32(&ms->key_full[i]), 1);
+      mbar_init(smem_u32(&ms->key_full[i]), kPaged ? kCopyWarps : 1);
       mbar_init(smem_u32(&ms->key_empty[i]), 1);
     }
     mbar_init(smem_u32(&ms->claim), 1);
-    mbar_init(smem_u32(&ms->rope_full), 1);
+    mbar_init(smem_u32(&ms->rope_full), kPaged ? kCopyWarps : 1);
     mbar_init(smem_u32(&ms->rope_empty), 1);
     mbar_init(smem_u32(&ms->q_full), kSoftmaxWarps);
     mbar_init(smem_u32(&ms->q_empty), 1);
     mbar_init(smem_u32(&ms->p_full), kSoftmaxWarps);
     mbar_init(smem_u32(&ms->pv_done), 1);
     mbar_init(smem_u32(&ms->o_free), kSoftmaxWarps);
-    mbar_init(smem_u32(&ms->mma_done), 1);
+    mbar_init(smem_u32(&ms->mma_done), 2);
     ms->abort_flag = 0;
     fence_mbar_init();
-    prefetch_tensormap(&maps.latent);
-    prefetch_tensormap(&maps.rope);
+    if (!kPaged) {
+      prefetch_tensormap(&maps.latent);
+      prefetch_tensormap(&maps.rope);
+    }
   }
   pdl_wait_primary();
   pdl_launch_dependents();
+  Batch groups = {};
+  if (warp == kSchedulerWarp) {
+    groups = count_groups(p);
+    find_job(p, groups, blockIdx.x, &ms->job[0]);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
-  if (warp >= kFirstSoftmaxWarp) {
-    setmaxnreg_inc<kSoftmaxRegs>();
+  if (warp >= kFirstSoftmaxWarp && warp < kFirstCopyWarp) {
+    setmaxnreg_inc<softmax_regs<kPaged>()>();
     run_softmax(p, ms, sbase, tmem, (warp - kFirstSoftmaxWarp) >> 2);
   } else {
-    setmaxnreg_dec<kOtherRegs>();
-    if (warp == kProducerWarp)
-      run_producer<kPaged>(p, maps, ms, sbase);
+    setmaxnreg_dec<other_regs<kPaged>()>();
+    if (warp == kScoreWarp)
+      run_scores<kPaged>(p, ms, smem, sbase, tmem);
+    else if (warp == kValueWarp)
+      run_values(p, ms, sbase, tmem);
     else if (warp == kSchedulerWarp)
-      run_scheduler(p, ms);
-    else if (warp == kMmaWarp)
-      run_mma<kPaged>(p, ms, smem, sbase, tmem);
+      run_scheduler(p, groups, ms);
+    else if (kPaged && warp >= kFirstCopyWarp)
+      run_copies(p, ms, sbase);
+    else if (!kPaged && warp == kProducerWarp)
+      run_producer(p, maps, ms, sbase);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     const bool one = (threadIdx.x & 31) == 0;
     if (one) drain(&ms->mma_done, 0);
     __syncwarp();
@@ -853,8 +1048,9 @@ cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStr
   const int64_t jobs = static_cast<int64_t>(p.blocks) * p.splits;
   if (jobs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(jobs < p.num_sms ? jobs : p.num_sms);
-  return p.kv_indices != nullptr ? launch_dependent(shared_kernel<true>, grid, kThreads, kSmemBytes, stream, maps, p)
-                                 : launch_dependent(shared_kernel<false>, grid, kThreads, kSmemBytes, stream, maps, p);
+  return p.kv_indices != nullptr
+             ? launch_dependent(shared_kernel<true>, grid, threads<true>(), kSmemBytes, stream, maps, p)
+             : launch_dependent(shared_kernel<false>, grid, threads<false>(), kSmemBytes, stream, maps, p);
 }
 
 }  // namespace mla
