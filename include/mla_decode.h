@@ -696,11 +696,11 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
  *   lse[t][h] = log sum_j exp(s_j)                       (natural)
  * over all of the group's keys, with K the e4m3 cache's values code * *kv_scale.  A group
  * without keys gives zeros and lse -inf.  The query enters the products as two e4m3 terms
- * (exact down to 2^-13 of its token's largest magnitude), a probability as two e4m3 terms
+ * (exact down to 2^-13 of its head's largest magnitude), a probability as two e4m3 terms
  * (to 2^-8 of itself, or 2^-14 of the row's largest); accumulation and softmax statistics
  * are float32; out is rounded once.
- *   q_bf16     device, bf16 [total_q][16][576], 16-byte aligned.  A token with a value that
- *              is not finite gets NaN, as output and as lse.
+ *   q_bf16     device, bf16 [total_q][16][576], 16-byte aligned.  A token's head with a value
+ *              that is not finite gets NaN, as output and as lse.
  *   kv_fp8     device, e4m3fn codes [kv_rows][576], 16-byte aligned.  Codes of the groups'
  *              keys must be finite; other rows may hold anything.
  *   kv_scale   device, float[1], positive and finite.

@@ -10,7 +10,7 @@
 //                                    once for its low ones
 // K(T) and V(T) are the same e4m3 codes in shared memory (V the first 512 dims), read
 // by key for the first product and by dim for the second, so nothing is converted.  A
-// bf16 query is two e4m3 terms, q 2^k = hi + lo / 8, exact down to 2^-13 of the token's
+// bf16 query is two e4m3 terms, q 2^k = hi + lo / 8, exact down to 2^-13 of the row's
 // largest magnitude; a probability p in [0, 2^8] is hi + lo, to 2^-8 of itself and 2^-10,
 // which is 2^-14 of the row's reference (2^4).  TMEM is full: two S of 128 columns, O in
 // four chunks of 64.
@@ -20,9 +20,9 @@
 //   * warp 3 finds the jobs,
 //   * the keys come as four panels of 128 dims a tile into two buffers, and the 64 rotated
 //     dims into one: by warp 2 through TMA in boxes of 128 rows, or, by a page table, by
-//     warps 12-15 in 16-byte copies (TMA's gathers of four rows take 74 cycles each to
-//     issue from one warp, 160 a tile, and 20 from four; the copies of four warps bring a
-//     panel in 500 cycles),
+//     warps 12-19 in 16-byte copies (TMA's gathers of four rows take 74 cycles each to
+//     issue from one warp, 160 a tile, and 20 from four; alone, the copies of four warps
+//     bring a panel in 500 cycles and of eight in 330),
 //   * warps 0 and 1 issue the products S and O, each as soon as it can,
 //   * warps 4-7 and 8-11 run the softmax of two query tokens each, a thread a key: the
 //     maximum over keys is over lanes, so it is only looked for when a score passes the
@@ -55,17 +55,17 @@ constexpr int kOffMisc = kOffP + 2 * kPBytes;
 
 constexpr int kScoreWarp = 0, kValueWarp = 1, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;
 constexpr int kFirstCopyWarp = 12;
-constexpr uint32_t kSoftmaxWarps = 8, kCopyWarps = 4;
-// Threads of a block, and registers: launched with 168 a thread (128 with a page table),
+constexpr uint32_t kSoftmaxWarps = 8, kCopyWarps = 8;
+// Threads of a block, and registers: launched with 168 a thread (96 with a page table),
 // of which the softmax warpgroups take the others' share.
 template <bool kPaged>
-__host__ __device__ constexpr int threads() { return kPaged ? 512 : 384; }
+__host__ __device__ constexpr int threads() { return kPaged ? 640 : 384; }
 template <bool kPaged>
-__host__ __device__ constexpr int softmax_regs() { return kPaged ? 192 : 200; }
+__host__ __device__ constexpr int softmax_regs() { return kPaged ? 168 : 200; }
 template <bool kPaged>
-__host__ __device__ constexpr int other_regs() { return kPaged ? 64 : 104; }
+__host__ __device__ constexpr int other_regs() { return kPaged ? 48 : 104; }
 static_assert(2 * 128 * softmax_regs<false>() + 128 * other_regs<false>() <= threads<false>() * 168 &&
-                  2 * 128 * softmax_regs<true>() + 256 * other_regs<true>() <= threads<true>() * 128,
+                  2 * 128 * softmax_regs<true>() + 384 * other_regs<true>() <= threads<true>() * 96,
               "register split exceeds the launch allocation");
 // What reads a job: two issuers, the softmax, and the producer or the copying warps.
 template <bool kPaged>
@@ -113,11 +113,13 @@ struct Misc {
   uint32_t tmem_base;
   volatile int32_t abort_flag;
   Job job[2];
+  // Of a warpgroup's 32 rows:
   alignas(16) float red[2][4][32];  // [warpgroup][warp][row]: maxima, sums
-  alignas(16) float factor[2][32];  // of O's rows: rescaling, at the end the division
-  uint32_t amax[2][4];              // [warpgroup][warp]: of |q|
+  alignas(16) float scale[2][32];   // products to powers of two
+  alignas(16) float off[2][32];     // kTop less the reference
+  alignas(16) float factor[2][32];  // of O: rescaling, at the end the division
 };
-constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
+constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc));
 static_assert(kSmemBytes <= 232448, "shared memory of one block");
 
 // Bounded waits on an mbarrier phase by a whole warp, which polls and gives up
@@ -638,61 +640,70 @@ __device__ __forceinline__ void split_q(const uint4& a, const uint4& b, float up
     lo[k] = pack_codes(y[2 * k], y[2 * k + 1]);
   }
 }
-// The query operand's rows of warpgroup g's two tokens, each scaled by a power of two so
-// that its largest magnitude lies in (224, 448].  scale[i]: what turns token i's products
-// into powers of two (NaN for a query that is not finite, whose outputs become NaN).
-// A warp has eight of the 32 rows: a lane 16 latent dims of each, and then 16 of the rotated
-// dims of one.
-__device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_t sbase, const Job& job, int g,
-                                        float kv_scale, float (&scale)[2]) {
+// The query operand's rows of warpgroup g's two tokens, each row scaled by a power of two so
+// that its largest magnitude lies in (224, 448], and what turns its products into powers of
+// two (NaN for a row that is not finite, whose output becomes NaN).  A warp has eight of
+// the 32 rows: a lane 16 latent dims of each and 16 of the rotated dims of one.  Rows are
+// written as they arrive.
+__device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_t sbase, const Job& job, int g, float kv_scale) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   constexpr int kWarpRows = 2 * kNumHeads / 4;
   static_assert(kVDim / 16 == 32 && kWarpRows * ((kQkDim - kVDim) / 16) == 32, "a lane a piece");
-  const int row0 = kWarpRows * warp, mine = warp >> 1;  // the warp's token
+  const int row0 = kWarpRows * warp, token = 2 * g + (warp >> 1);
   const int rope_row = row0 + (lane >> 2), rope_ch = kVDim / 16 + (lane & 3);
-  uint4 raw[kWarpRows + 1][2];
-  const bool there = 2 * g + mine < job.nq && MLA_DCHECK(job.q0 >= 0 && job.q0 + 2 * g + mine < p.total_q, p.err);
+  const bool there = token < job.nq && MLA_DCHECK(job.q0 >= 0 && job.q0 + token < p.total_q, p.err);
   const uint16_t* src = p.q + (static_cast<int64_t>(job.q0 + 2 * g) * kNumHeads) * kQkDim;
+  uint4 raw[kWarpRows + 1][2];  // the rotated dims last
 #pragma unroll
-  for (int r = 0; r <= kWarpRows; ++r) {
+  for (int i = 0; i <= kWarpRows; ++i) {
+    const int r = (i + kWarpRows) % (kWarpRows + 1);  // they come first
     const uint4* at = reinterpret_cast<const uint4*>(src + (r < kWarpRows ? (row0 + r) * kQkDim + 16 * lane
                                                                           : rope_row * kQkDim + 16 * rope_ch));
     raw[r][0] = there ? __ldg(at) : make_uint4(0, 0, 0, 0);
     raw[r][1] = there ? __ldg(at + 1) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t top = 0;
+  auto largest = [&](const uint4 (&v)[2]) {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t lo = 0, hi = 0;
 #pragma unroll
-  for (int r = 0; r <= kWarpRows; ++r) {
-    const uint32_t w[8] = {raw[r][0].x, raw[r][0].y, raw[r][0].z, raw[r][0].w, raw[r][1].x, raw[r][1].y, raw[r][1].z, raw[r][1].w};
+    for (int i = 0; i < 8; ++i) {
+      lo = max(lo, w[i] & 0x7FFFu);
+      hi = max(hi, w[i] & 0x7FFF0000u);
+    }
+    return max(lo, hi >> 16);
+  };
+  auto store = [&](const uint4 (&v)[2], float up, uint32_t at, uint32_t low_at) {
+    uint32_t hi[4], lo[4];
+    split_q(v[0], v[1], up, hi, lo);
+    st_shared_v4(at, hi);
+    st_shared_v4(low_at, lo);
+  };
+  uint32_t rope_top = largest(raw[kWarpRows]);
+  rope_top = max(rope_top, __shfl_xor_sync(0xffffffffu, rope_top, 1));
+  rope_top = max(rope_top, __shfl_xor_sync(0xffffffffu, rope_top, 2));
+  float rope_up = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) ms->amax[g][warp] = top;
-  named_bar_sync(kBarSoftmax + g, 128);
-  float up = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    top = max(ms->amax[g][2 * i], ms->amax[g][2 * i + 1]);
+  for (int r = 0; r < kWarpRows; ++r) {
+    uint32_t top = largest(raw[r]);
+    top = max(__reduce_max_sync(0xffffffffu, top), __shfl_sync(0xffffffffu, rope_top, 4 * r));
     // The exponent e of the largest magnitude m 2^e, 1 <= m < 2, of bf16 bits: scaled by 2^k to
     // 2^8 m where m <= 1.75, else to 2^7 m.  (Zeros and denormals: clamped.)
     const int e = static_cast<int>(top >> 7) - 127;
     int k = (top & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
     k = top == 0 ? 0 : min(k, 126);
-    scale[i] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
     // 2^(k - 8), which is a denormal for the largest of all
-    if (i == mine) up = __int_as_float(k - 8 + 127 > 0 ? (k - 8 + 127) << 23 : 1 << (22 + (k - 8 + 127)));
+    const float up = __int_as_float(k - 8 + 127 > 0 ? (k - 8 + 127) << 23 : 1 << (22 + (k - 8 + 127)));
+    if (lane >> 2 == r) rope_up = up;
+    const int row = 2 * kNumHeads * g + row0 + r;
+    if (lane == r)
+      ms->scale[g][row0 + r] = top >= 0x7F80u ? __int_as_float(0x7FC00000)
+                                              : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
+    const uint32_t at = sbase + kOffQ + (lane >> 3) * kPanelBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+    store(raw[r], up, at, at + kRows * 128);
   }
-#pragma unroll
-  for (int r = 0; r <= kWarpRows; ++r) {
-    uint32_t hi[4], lo[4];
-    split_q(raw[r][0], raw[r][1], up, hi, lo);
-    const int row = 2 * kNumHeads * g + (r < kWarpRows ? row0 + r : rope_row), ch = r < kWarpRows ? lane : rope_ch;
-    const uint32_t at = r < kWarpRows ? sbase + kOffQ + (ch >> 3) * kPanelBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4)
-                                      : sbase + kOffQRope + row * 64 + (((ch & 3) ^ ((row >> 1) & 3)) << 4);
-    st_shared_v4(at, hi);
-    st_shared_v4(at + kRows * (r < kWarpRows ? 128 : 64), lo);
-  }
+  const int row = 2 * kNumHeads * g + rope_row;
+  const uint32_t at = sbase + kOffQRope + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4);
+  store(raw[kWarpRows], rope_up, at, at + kRows * 64);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
@@ -717,93 +728,90 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
   const uint32_t p_row = sbase + kOffP + t * kRows;
   const uint32_t swizzle = (t >> 1) & 3;
   uint32_t T = 0, jobs = 0;
-  float scale[2], next_scale[2];
   Job job, next;
   bool live = next_job_of_group(p, ms, 0, job, g);
-  if (live && job.tiles() > 0) write_q(p, ms, sbase, job, g, kv_scale, scale);
+  if (live && job.tiles() > 0) write_q(p, ms, sbase, job, g, kv_scale);
+  const ulonglong2* scales = reinterpret_cast<const ulonglong2*>(ms->scale[g]);  // four rows each
+  const ulonglong2* offs = reinterpret_cast<const ulonglong2*>(ms->off[g]);
+  const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(ms->factor[g]);
   for (uint32_t k = 0; live; ++k) {
     const int32_t n = job.tiles();
-    // Of pairs of rows: kTop less the reference, and this thread's keys' sum.
-    uint64_t off[2][8], sum[2][8];
+    float off = 0.0f;     // of row `lane` of the warpgroup, alike in its four warps
+    uint64_t sum[16];     // of pairs of rows: this thread's keys'
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        off[i][h] = pack2(INFINITY, INFINITY);
-        sum[i][h] = 0;
-      }
+    for (int h = 0; h < 16; ++h) sum[h] = 0;
     for (int32_t j = 0; j < n; ++j, ++T) {
       warp_wait_on(&ms->s_full[T & 1], T >> 1, ms, p.err);
       tc_fence_after();
       const bool partial = (j + 1) * kTileTokens > job.keys;  // (the same for the whole block)
       const bool seen = j * kTileTokens + t < job.keys;
+      const uint32_t s_at = 128 * (T & 1);
+      const uint64_t eighth = pack2(0.125f, 0.125f);
       // Scores as powers of two over the reference, kTop up.
-      uint64_t x[2][8];
+      uint64_t x[16];
       auto exponents = [&] {
         uint32_t hi[2][16], lo[2][16];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi[i]);
-          tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo[i]);
+          tmem_ld16(s_hi + s_at + 16 * i, hi[i]);
+          tmem_ld16(s_lo + s_at + 16 * i, lo[i]);
         }
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint64_t a = pack2(scale[i], scale[i]), b = pack2(scale[i] * 0.125f, scale[i] * 0.125f);
-#pragma unroll
-          for (int h = 0; h < 8; ++h)
-            x[i][h] = fma2(pack2(lo[i][2 * h], lo[i][2 * h + 1]), b, fma2(pack2(hi[i][2 * h], hi[i][2 * h + 1]), a, off[i][h]));
+        for (int h = 0; h < 8; ++h) {
+          const ulonglong2 a = scales[h], o = offs[h];
+          const int i = h >> 2, r = 4 * (h & 3);
+          x[2 * h] = fma2(fma2(pack2(lo[i][r], lo[i][r + 1]), eighth, pack2(hi[i][r], hi[i][r + 1])), a.x, o.x);
+          x[2 * h + 1] = fma2(fma2(pack2(lo[i][r + 2], lo[i][r + 3]), eighth, pack2(hi[i][r + 2], hi[i][r + 3])), a.y, o.y);
         }
       };
-      bool look = j == 0;  // (off is infinite)
+      bool look = j == 0;
       if (!look) {
         exponents();
         float high = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            float u, v;
-            unpack2(x[i][h], u, v);
-            high = fmaxf(high, fmaxf(u, v));
-          }
+        for (int h = 0; h < 16; ++h) {
+          float u, v;
+          unpack2(x[h], u, v);
+          high = fmaxf(high, fmaxf(u, v));
+        }
         look = any_of_group(seen && high > 0.0f, g);
       }
       const bool moved = look && j > 0;
       if (look) {
+        float mine = 0.0f;  // the maximum of row `lane`
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t hi[16], lo[16];
-          tmem_ld16(s_hi + 128 * (T & 1) + 16 * i, hi);
-          tmem_ld16(s_lo + 128 * (T & 1) + 16 * i, lo);
+          tmem_ld16(s_hi + s_at + 16 * i, hi);
+          tmem_ld16(s_lo + s_at + 16 * i, lo);
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
-            const float s = fmaf(__uint_as_float(lo[h]), scale[i] * 0.125f, __uint_as_float(hi[h]) * scale[i]);
+            const float s = fmaf(__uint_as_float(lo[h]), 0.125f, __uint_as_float(hi[h])) * ms->scale[g][16 * i + h];
             const float m = warp_max(seen ? s : -INFINITY);
-            if (lane == 0) ms->red[g][warp][16 * i + h] = m;
+            mine = lane == 16 * i + h ? m : mine;
           }
         }
+        ms->red[g][warp][lane] = mine;
         named_bar_sync(bar, 128);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        mine = fmaxf(fmaxf(ms->red[g][0][lane], ms->red[g][1][lane]), fmaxf(ms->red[g][2][lane], ms->red[g][3][lane]));
+        float factor = 1.0f;
+        if (j == 0 || mine + off > 0.0f) {
+          const float to = kTop - mine;
+          factor = ex2(to - off);  // (of a job's first tile nothing is scaled)
+          off = to;
+        }
+        // (the four warps write the same)
+        ms->off[g][lane] = off;
+        ms->factor[g][lane] = factor;
+        __syncwarp();
+        if (moved) {
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
-            float o[2], factor[2] = {1.0f, 1.0f};
-            unpack2(off[i][h], o[0], o[1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int row = 16 * i + 2 * h + e;
-              const float m = fmaxf(fmaxf(ms->red[g][0][row], ms->red[g][1][row]), fmaxf(ms->red[g][2][row], ms->red[g][3][row]));
-              if (m + o[e] > 0.0f) {
-                const float to = kTop - m;
-                factor[e] = ex2(to - o[e]);  // 0 on a job's first tile
-                o[e] = to;
-              }
-            }
-            off[i][h] = pack2(o[0], o[1]);
-            sum[i][h] = mul2(sum[i][h], pack2(factor[0], factor[1]));
-            if (t == 0) *reinterpret_cast<float2*>(&ms->factor[g][16 * i + 2 * h]) = make_float2(factor[0], factor[1]);
+            const ulonglong2 f = factors[h];
+            sum[2 * h] = mul2(sum[2 * h], f.x);
+            sum[2 * h + 1] = mul2(sum[2 * h + 1], f.y);
           }
         }
         exponents();  // (anew, so that a row that stands has the bits it has beside any other rows)
@@ -818,19 +826,21 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
 #pragma unroll
         for (int h = 0; h < 8; ++h) {
           float u, v;
-          unpack2(x[i][h], u, v);
+          unpack2(x[8 * i + h], u, v);
           u = ex2(u);
           v = ex2(v);
           if (partial) {
             u = seen ? u : 0.0f;
             v = seen ? v : 0.0f;
           }
-          sum[i][h] = add2(sum[i][h], pack2(u, v));
+          sum[8 * i + h] = add2(sum[8 * i + h], pack2(u, v));
           halves[h] = half2_bits(u, v);
         }
         split_p(halves, hi[i], lo[i]);
       }
       if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);  // P(T - 1) is read
+      // (and the other warpgroup's rows of the job before have left through P's memory)
+      if (j == 0 && jobs > 0) warp_wait_on(&ms->o_free, jobs - 1, ms, p.err);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t at = p_row + (((2 * g + i) ^ swizzle) << 4);
@@ -839,7 +849,6 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       }
       fence_proxy_async_smem();
       if (moved) {
-        named_bar_sync(bar, 128);  // thread 0's factors are written
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < kPanels; ++c) {
@@ -858,13 +867,13 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     }
 
     // ------------------------------------------------ sums over the keys
-    float lse = -INFINITY;  // of row t of the warpgroup, in its first warp
+    float lse = -INFINITY;  // of row `lane`, in the warpgroup's first warp
     named_bar_sync(bar, 128);  // (red and factor are read)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float v[16];
 #pragma unroll
-      for (int h = 0; h < 8; ++h) unpack2(sum[i][h], v[2 * h], v[2 * h + 1]);
+      for (int h = 0; h < 8; ++h) unpack2(sum[8 * i + h], v[2 * h], v[2 * h + 1]);
       const float s = transposed_sum16(v);
       if ((lane & 1) == 0) ms->red[g][warp][16 * i + (lane >> 1)] = s;
     }
@@ -872,17 +881,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     if (warp == 0) {
       const float s = (ms->red[g][0][lane] + ms->red[g][1][lane]) + (ms->red[g][2][lane] + ms->red[g][3][lane]);
       ms->factor[g][lane] = s != 0.0f ? kv_scale * 0x1p-8f / s : 0.0f;  // (P is 2^8 times what was summed)
-      float o = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          float u, v;
-          unpack2(off[i][h], u, v);
-          o = lane == 16 * i + 2 * h ? u : o;
-          o = lane == 16 * i + 2 * h + 1 ? v : o;
-        }
-      if (n > 0) lse = kLn2 * (log2f(s) - o);
+      if (n > 0) lse = kLn2 * (log2f(s) - off);
     }
     named_bar_sync(bar, 128);
 
@@ -890,7 +889,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     const bool more = next_job_of_group(p, ms, k + 1, next, g);
     if (more && next.tiles() > 0) {
       if (jobs > 0 || n > 0) warp_wait_on(&ms->q_empty, jobs + (n > 0) - 1, ms, p.err);
-      write_q(p, ms, sbase, next, g, kv_scale, next_scale);
+      write_q(p, ms, sbase, next, g, kv_scale);
     }
     if (n > 0) {
       warp_wait_on(&ms->pv_done, T - 1, ms, p.err);
@@ -898,37 +897,68 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     }
 
     // ------------------------------------------------ output
-    // A thread has one dim of a chunk; a warp's lanes write 32 neighbouring ones.
+    // A thread has one dim of a chunk, so rows go through shared memory (P's, which is free: a
+    // term for a warpgroup) to leave in 16-byte pieces: 2-byte stores of a warp's 32 dims took
+    // 3.5 us a job.
     const int tokens = min(2, job.nq - 2 * g);  // of this warpgroup
     const int64_t row0 = (static_cast<int64_t>(p.splits > 1 ? job.split : 0) * p.total_q + job.q0 + 2 * g) * kNumHeads;
     const bool fits = !ms->abort_flag && MLA_DCHECK(tokens <= 0 || (job.q0 >= 0 && job.q0 + 2 * g + tokens <= p.total_q && job.split >= 0 &&
                                  job.split < p.splits && (p.splits == 1 || row0 + tokens * kNumHeads <= p.part_rows)), p.err);
+    uint8_t* stage = reinterpret_cast<uint8_t*>(ms) - kOffMisc + kOffP + g * kPBytes;
+    const bool parts = p.splits > 1;
 #pragma unroll 1
-    for (int c = 0; c < kPanels; ++c) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (i >= tokens || !fits) break;
-        uint32_t o[16];
-        if (n > 0) {
-          tmem_ld16(o_addr + kRows * c + 16 * i, o);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int h = 0; h < 16; ++h) o[h] = 0;
+    for (int step = 0; step < 2 * kPanels; ++step) {  // a token's 16 rows of a chunk
+      const int c = step >> 1, i = step & 1;
+      if (i >= tokens) continue;  // (the same for the warpgroup)
+      const int64_t first = (row0 + 16 * i) * kVDim + 128 * c;
+      if (n == 0) {  // no keys: zeros (P's memory may be at work)
+        if (fits && parts) {
+          for (int row = warp; row < 16; row += 4)
+            *reinterpret_cast<float4*>(p.part + first + row * kVDim + 4 * lane) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        } else if (fits) {
+          for (int row = t >> 4; row < 16; row += 8)
+            *reinterpret_cast<uint4*>(p.out + first + row * kVDim + 8 * (t & 15)) = make_uint4(0, 0, 0, 0);
         }
-        const int64_t at = (row0 + 16 * i) * kVDim + 128 * c + t;
+        continue;
+      }
+      uint32_t o[16];
+      tmem_ld16(o_addr + kRows * c + 16 * i, o);
+      tmem_wait_ld();
+      const float4* by = reinterpret_cast<const float4*>(&ms->factor[g][16 * i]);
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          const float v = __uint_as_float(o[h]) * ms->factor[g][16 * i + h];
-          if (p.splits > 1) {
-            p.part[at + h * kVDim] = v;
+      for (int q = 0; q < 4; ++q) {
+        const float4 f = by[q];
+        const float v[4] = {__uint_as_float(o[4 * q]) * f.x, __uint_as_float(o[4 * q + 1]) * f.y,
+                            __uint_as_float(o[4 * q + 2]) * f.z, __uint_as_float(o[4 * q + 3]) * f.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 4 * q + e;
+          if (parts) {
+            reinterpret_cast<float*>(stage)[row * 128 + t] = v[e];
           } else {
             uint16_t b;
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v));
-            p.out[at + h * kVDim] = b;
+            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v[e]));
+            reinterpret_cast<uint16_t*>(stage)[row * 128 + t] = b;
           }
         }
       }
+      named_bar_sync(bar, 128);
+      if (fits && parts) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = 4 * q + warp;  // 512 bytes a warp
+          *reinterpret_cast<float4*>(p.part + first + row * kVDim + 4 * lane) =
+              reinterpret_cast<const float4*>(stage)[row * 32 + lane];
+        }
+      } else if (fits) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = 8 * q + (t >> 4), piece = t & 15;  // 256 bytes a row
+          *reinterpret_cast<uint4*>(p.out + first + row * kVDim + 8 * piece) =
+              reinterpret_cast<const uint4*>(stage)[row * 16 + piece];
+        }
+      }
+      named_bar_sync(bar, 128);
     }
     if (t < 16 * tokens && fits) {
       if (p.splits > 1)
@@ -946,17 +976,14 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     named_bar_sync(bar, 128);  // (factor is read)
     job = next;
     live = more;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) scale[i] = next_scale[i];
   }
 }
 
 template <bool kPaged>
 __global__ void __launch_bounds__(threads<kPaged>(), 1)
     shared_kernel(const __grid_constant__ SharedMaps maps, const SharedParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  // (aligned as the panels' swizzle needs it: there is no room to align it here)
+  extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = reinterpret_cast<Misc*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5;

@@ -1,7 +1,7 @@
 """mla_shared_fwd against the float64 definition.
 
 Tolerances, from the operator's arithmetic.  Scores: float32 sums of 2 x 576 products, within
-2^-14 of ``spread`` = sum |q||k| / 24, and the query's two terms, off by 2^-20 of its token's
+2^-14 of ``spread`` = sum |q||k| / 24, and the query's two terms, off by 2^-20 of its head's
 largest magnitude at most (half a step of the low term, 2^-10 / 8, where the largest is 224
 or more): e = max_j (2^-14 spread + 2^-20 max|q| sum |k| / 24) + 2^-20 for exp2, relative in a
 probability and absolute in the lse.  A probability's two terms: 2^-8 of it (twice half a
@@ -90,7 +90,7 @@ class Case:
             if a == b:
                 continue
             spread = np.abs(q[a:b]) @ np.abs(k).T / 24
-            low = np.abs(q[a:b]).max(axis=(1, 2))[:, None] * np.abs(k).sum(axis=1).max() / 24
+            low = np.abs(q[a:b]).max(axis=2) * np.abs(k).sum(axis=1).max() / 24
             e = 2.0**-14 * spread.max(axis=2) + 2.0**-20 * low + 2.0**-20
             s = q[a:b] @ k.T / 24
             p = np.exp(s - s.max(axis=2, keepdims=True))
@@ -159,8 +159,8 @@ def test_a_query_that_is_not_finite_stays_alone():
     c = Case([9], [500], seed=9, sms=5)
     c.q[2, 4, 100], c.q[7, 0, 575] = float("nan"), float("inf")
     assert c.run() == 0
-    bad = torch.zeros(9, dtype=torch.bool, device="cuda")
-    bad[[2, 7]] = True
+    bad = torch.zeros(9, 16, dtype=torch.bool, device="cuda")
+    bad[2, 4] = bad[7, 0] = True
     assert c.out[bad].isnan().all() and c.lse[bad].isnan().all()
     good = Case([9], [500], seed=9, sms=5)
     good.run()
