@@ -712,27 +712,31 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
  *   out_bf16   device, bf16 [total_q][16][512], 16-byte aligned; lse device float
  *              [total_q][16], or NULL.  Tokens of no group are left alone.
  *   plan, workspace  from mla_shared_plan; workspace 256-byte aligned, zeroed once (it holds
- *              the error word, counters that each call leaves zero, and the parts of split
- *              keys).  Calls sharing a workspace must not overlap on the GPU.
+ *              the error word and the parts of shared keys).  Calls sharing a workspace must
+ *              not overlap on the GPU.
  * No output may overlap an input.  Groups outside total_q or the keys (kv_indices_len, or
  * kv_rows), or with more than MLA_SHARED_MAX_KEYS keys, set MLA_DERR_QO_INDPTR /
- * MLA_DERR_KV_INDPTR and are not written; where offsets of queries decrease, other groups
- * may be left unwritten too, and so may any group of a call that reports MLA_DERR_TIMEOUT.
+ * MLA_DERR_KV_INDPTR and are not written; where offsets of queries decrease nothing is
+ * written, and any group may be left unwritten by a call that reports MLA_DERR_TIMEOUT.
  * Deterministic for given groups and a given plan.
  */
 #define MLA_SHARED_MAX_GROUPS 65536
+#define MLA_SHARED_MAX_WORKERS 4096
 #define MLA_SHARED_MAX_KEYS (1 << 25) /* half a second of one block's work: the waits are bounded */
 typedef struct {
   int32_t batch;       /* groups                                                      */
   int32_t total_q;     /* query tokens that q and out have room for (0 allowed)        */
   int32_t max_kv_len;  /* upper bound on a group's keys (sizes the split only)         */
   int32_t num_sms;     /* SMs the split is sized for                                   */
-  int32_t splits;      /* parts a group's keys are cut into when the queries alone leave
-                        * SMs idle; the parts are joined by a second kernel            */
+  int32_t workers;     /* blocks of the kernel, 1 .. MLA_SHARED_MAX_WORKERS             */
+  int32_t split;       /* 1: a group's keys may be shared by workers, whose parts a second
+                        * kernel joins (batch up to 1024); 0: they are not             */
+  int32_t start;       /* key tiles that the start of a block of four queries counts for
+                        * where all keys are cut into equal shares (0 .. 64)           */
   int32_t abi_version; /* MLA_ABI_VERSION                                              */
   uint64_t ws_bytes;   /* workspace bytes mla_shared_fwd needs                         */
-  uint64_t ws_lse_offset;     /* float[splits][total_q][16] when splits > 1            */
-  uint64_t ws_partial_offset; /* float[splits][total_q][16][512] when splits > 1       */
+  uint64_t ws_lse_offset;     /* float[2 * workers][64] when split                     */
+  uint64_t ws_partial_offset; /* float[2 * workers][64][512] when split                */
 } mla_shared_plan_t;
 
 /* Pure host.  batch 1 .. MLA_SHARED_MAX_GROUPS, total_q and max_kv_len >= 0; num_sms <= 0 asks the device. */

@@ -53,7 +53,8 @@ class mla_prefill_plan_t(ctypes.Structure):
 class mla_shared_plan_t(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32),
                 ("max_kv_len", ctypes.c_int32), ("num_sms", ctypes.c_int32),
-                ("splits", ctypes.c_int32), ("abi_version", ctypes.c_int32),
+                ("workers", ctypes.c_int32), ("split", ctypes.c_int32),
+                ("start", ctypes.c_int32), ("abi_version", ctypes.c_int32),
                 ("ws_bytes", ctypes.c_uint64), ("ws_lse_offset", ctypes.c_uint64),
                 ("ws_partial_offset", ctypes.c_uint64)]
 

@@ -9,7 +9,7 @@
 namespace {
 
 constexpr uint64_t kAlign = 256;
-constexpr uint64_t kSchedOffset = 64;  // in a workspace's first 256 bytes, behind the error word
+constexpr uint64_t kMissingOffset = 64;  // in a workspace's first 256 bytes, behind the error word
 uint64_t round_up(uint64_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 constexpr int64_t kMaxStride = INT64_C(1) << 36;
@@ -27,24 +27,38 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
   return groups == 0 ? 0 : (total_q - groups) / mla::kSharedTokens + groups;
 }
 
-// Parts that a group's keys are cut into where the blocks of queries leave SMs idle.
-int32_t key_splits(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms) {
-  // (The second kernel looks for its tokens' groups, so thousands of empty ones are not cut.)
-  if (blocks == 0 || batch > 1024) return 1;
-  int64_t best = 1, least = INT64_MAX;
-  for (int64_t s = 1; s <= key_tiles && s <= 64 && s * blocks <= 8 * sms; ++s) {
-    const int64_t rounds = (blocks * s + sms - 1) / sms;
-    const int64_t time = rounds * (60 + 15 * ((key_tiles + s - 1) / s)) + (s == 1 ? 0 : 30 + s * blocks / 4);
+// Workers, whether blocks are shared between them, and the units that a block's start counts
+// for.  Either a block's keys are cut into k equal parts, or all blocks' keys, one behind the
+// other, among all SMs, where a worker whose range has the end of one block and the start of
+// another does two jobs; by the time that it should take, in twentieths of a microsecond: 35 a
+// key tile, 100 a job, and for the second kernel 80 and 4 a part of a block.
+struct Cut {
+  int32_t workers, split, start;
+};
+constexpr int32_t kStartUnits = 3;
+Cut cut_of(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms) {
+  Cut best = {static_cast<int32_t>(blocks < sms ? (blocks > 0 ? blocks : 1) : sms), 0, 0};
+  // (The second kernel looks for its tokens' groups, so thousands of them are not cut.)
+  if (blocks == 0 || batch > 1024) return best;
+  const int64_t rounds = (blocks + sms - 1) / sms;
+  int64_t least = rounds * (100 + 35 * key_tiles);
+  for (int64_t k = 2; k <= key_tiles && k * blocks <= sms; ++k) {
+    const int64_t time = 100 + 35 * ((key_tiles + k - 1) / k) + 80 + 4 * k;
     if (time < least) {
       least = time;
-      best = s;
+      best = Cut{static_cast<int32_t>(k * blocks), 1, 0};
     }
   }
-  return static_cast<int32_t>(best);
+  const int64_t tiles = blocks * key_tiles;
+  if (tiles >= sms) {
+    const int64_t time = 200 + 100 * blocks / sms + 35 * ((tiles + sms - 1) / sms) + 80 + 4 * (sms / blocks + 1);
+    if (time < least) best = Cut{static_cast<int32_t>(sms), 1, kStartUnits};
+  }
+  return best;
 }
 
-// The plan's fields for a number of parts; false if it cannot be run.
-bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_sms, int32_t splits,
+// The plan's fields for a number of workers; false if it cannot be run.
+bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num_sms, Cut cut,
                  mla_shared_plan_t* out) {
   mla_shared_plan_t p;
   std::memset(&p, 0, sizeof(p));
@@ -52,13 +66,17 @@ bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num
   p.total_q = total_q;
   p.max_kv_len = max_kv_len;
   p.num_sms = num_sms;
-  p.splits = splits;
+  p.workers = cut.workers;
+  p.split = cut.split;
+  p.start = cut.start;
   p.abi_version = MLA_ABI_VERSION;
-  if (splits < 1 || most_blocks(total_q, batch) > INT32_MAX / splits) return false;
+  if (cut.workers < 1 || cut.workers > MLA_SHARED_MAX_WORKERS || (cut.split != 0 && cut.split != 1) ||
+      cut.start < 0 || cut.start > 64 || (cut.split == 1 && batch > 1024))
+    return false;
   uint64_t off = kAlign;  // error word
   p.ws_lse_offset = p.ws_partial_offset = off;
-  if (splits > 1) {
-    const uint64_t rows = static_cast<uint64_t>(splits) * total_q * mla::kNumHeads;
+  if (cut.split == 1) {
+    const uint64_t rows = 2ull * cut.workers * mla::kSharedTokens * mla::kNumHeads;
     off += round_up(rows * sizeof(float));
     p.ws_partial_offset = off;
     off += round_up(rows * mla::kVDim * sizeof(float));
@@ -75,7 +93,8 @@ mla_status_t run_shared(const void* q, const void* kv, const float* kv_scale, co
   mla_shared_plan_t want;
   if (plan == nullptr || plan->abi_version != MLA_ABI_VERSION || plan->batch < 1 ||
       plan->batch > MLA_SHARED_MAX_GROUPS || plan->total_q < 0 || plan->max_kv_len < 0 || plan->num_sms < 1 ||
-      !plan_fields(plan->batch, plan->total_q, plan->max_kv_len, plan->num_sms, plan->splits, &want) ||
+      !plan_fields(plan->batch, plan->total_q, plan->max_kv_len, plan->num_sms, Cut{plan->workers, plan->split, plan->start},
+                   &want) ||
       std::memcmp(&want, plan, sizeof(want)) != 0)
     return MLA_ERR_INVALID_ARG;
   if (workspace == nullptr || !aligned(workspace, kAlign)) return MLA_ERR_INVALID_ARG;
@@ -106,37 +125,17 @@ mla_status_t run_shared(const void* q, const void* kv, const float* kv_scale, co
   p.part = reinterpret_cast<float*>(ws + plan->ws_partial_offset);
   p.part_lse = reinterpret_cast<float*>(ws + plan->ws_lse_offset);
   p.err = reinterpret_cast<int32_t*>(ws);
-  p.sched = reinterpret_cast<uint32_t*>(ws + kSchedOffset);
+  p.missing = reinterpret_cast<uint32_t*>(ws + kMissingOffset);
   p.kv_rows = kv_rows;
   p.kv_limit = kv_indices != nullptr ? kv_indices_len : kv_rows;
-  p.part_rows = static_cast<int64_t>((workspace_bytes - plan->ws_partial_offset) / (mla::kVDim * sizeof(float)));
   p.batch = plan->batch;
   p.total_q = plan->total_q;
-  p.blocks = static_cast<int32_t>(most_blocks(plan->total_q, plan->batch));
-  p.splits = plan->splits;
-  p.num_sms = plan->num_sms;
+  p.workers = plan->workers;
+  p.split = plan->split;
+  p.start = plan->start;
   p.stall_stream = stall_stream ? 1 : 0;
   st = launched(mla::launch_shared(p, m, stream));
-  if (st != MLA_OK || plan->splits == 1) return st;
-  mla::MergeParams g;
-  g.parts = p.part;
-  g.lses = p.part_lse;
-  g.out = p.out;
-  g.lse_out = lse;
-  g.rows = static_cast<int64_t>(plan->total_q) * mla::kNumHeads;
-  g.pieces = plan->splits;
-  g.dim = mla::kVDim;
-  g.missing = p.sched + 2;
-  g.qo_indptr = qo_indptr;
-  g.kv_indptr = kv_indptr;
-  g.total_kv = p.kv_limit;
-  g.batch = plan->batch;
-  g.heads = mla::kNumHeads;
-  g.total_q = plan->total_q;
-  g.num_sms = plan->num_sms;
-  g.part_rows = p.part_rows;
-  g.err = p.err;
-  return launched(mla::launch_attn_merge(g, true, stream));
+  return st != MLA_OK || plan->split == 0 ? st : launched(mla::launch_shared_join(p, stream));
 }
 
 mla_status_t run_means(const void* cache, const float* kv_scale, bool e4m3, int64_t kv_rows,
@@ -183,8 +182,10 @@ mla_status_t mla_shared_plan(int32_t batch, int32_t total_q, int32_t max_kv_len,
         cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
       return MLA_ERR_CUDA;
   }
-  const int32_t splits = key_splits(most_blocks(total_q, batch), batch, mla::tiles_of_length(max_kv_len), num_sms);
-  return plan_fields(batch, total_q, max_kv_len, num_sms, splits, plan) ? MLA_OK : MLA_ERR_INVALID_ARG;
+  // (no more workers than the workspace is laid out for: a GPU has fewer SMs)
+  const int32_t sms = num_sms < MLA_SHARED_MAX_WORKERS ? num_sms : MLA_SHARED_MAX_WORKERS;
+  const Cut cut = cut_of(most_blocks(total_q, batch), batch, mla::tiles_of_length(max_kv_len), sms);
+  return plan_fields(batch, total_q, max_kv_len, num_sms, cut, plan) ? MLA_OK : MLA_ERR_INVALID_ARG;
 }
 
 mla_status_t mla_shared_fwd(const void* q_bf16, const void* kv_fp8, const float* kv_scale,

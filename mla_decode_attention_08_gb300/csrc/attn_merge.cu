@@ -52,8 +52,8 @@ struct Piece {
   }
 };
 
-// Whether `token` is one that the attention before has computed: it belongs to a row
-// (mla_shared_fwd: a group), and the row's tokens and keys lie in their tensors.  (A batch whose keys are
+// Whether `token` is one that mla_prefill_fwd has computed: it belongs to a row,
+// and the row's tokens and keys lie in their tensors.  (A batch whose keys are
 // split has at most 1024 rows; the plan does not cut more.)
 __device__ __forceinline__ bool in_a_row(const MergeParams& p, int64_t token) {
   for (int32_t b = 0; b < p.batch; ++b) {
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeParams 
   uint32_t missing = 0;
   if constexpr (kF32) {
     missing = __ldcg(p.missing);
-    if (!MLA_DCHECK(dim0 + kVec <= p.dim && p.rows == static_cast<int64_t>(p.total_q) * p.heads &&
+    if (!MLA_DCHECK(dim0 + kVec <= p.dim && p.dim == 128 && p.rows == static_cast<int64_t>(p.total_q) * p.heads &&
                         p.pieces * p.rows <= p.part_rows, p.err))
       return;
   }
@@ -162,7 +162,8 @@ cudaError_t launch_vec(const MergeParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream) {
-  if (f32_parts) return merges_at_once(p.rows, p.num_sms, p.dim) ? launch_vec<true, 4, 16>(p, stream) : launch_vec<true, 8, 4>(p, stream);
+  // (The parts are rows of 128.)
+  if (f32_parts) return merges_at_once(p.rows, p.num_sms) ? launch_vec<true, 4, 16>(p, stream) : launch_vec<true, 8, 4>(p, stream);
   return p.dim % 16 == 0 ? launch_vec<false, 16, 4>(p, stream) : launch_vec<false, 8, 4>(p, stream);
 }
 

@@ -76,9 +76,9 @@ cudaError_t launch_kv_append(const KvAppendParams& p, bool e4m3, bool interleave
                              cudaStream_t stream);
 
 // Joins `pieces` outputs [pieces][rows][dim] by their log-sum-exps
-// [pieces][rows].  bf16 pieces (the public operator) or float ones (the splits
-// of mla_prefill_fwd and mla_shared_fwd, a row for each token and head; tokens that
-// they have not computed are left alone).
+// [pieces][rows].  bf16 pieces (the public operator) or float ones (the split
+// of mla_prefill_fwd, a row for each token and head; tokens that it has not
+// computed are left alone).
 struct MergeParams {
   const void* parts;
   const float* lses;
@@ -95,11 +95,9 @@ struct MergeParams {
   int64_t part_rows;
   int32_t* err;
 };
-// Whether float parts of `rows` rows of `dim` are joined by threads that are all on the
+// Whether float parts of `rows` rows of 128 are joined by threads that are all on the
 // GPU at once: four values each, two blocks of 256 an SM.
-inline bool merges_at_once(int64_t rows, int32_t sms, int32_t dim = 128) {
-  return rows * (dim / 4) <= static_cast<int64_t>(sms) * 2 * 256;
-}
+inline bool merges_at_once(int64_t rows, int32_t sms) { return rows * (128 / 4) <= static_cast<int64_t>(sms) * 2 * 256; }
 cudaError_t launch_attn_merge(const MergeParams& p, bool f32_parts, cudaStream_t stream);
 
 // mla_prefill_fwd: a persistent block an SM; a job is up to 256 queries of a row
@@ -135,8 +133,8 @@ size_t prefill_smem_bytes();
 cudaError_t prefill_prepare();
 cudaError_t launch_prefill(const PrefillParams& p, const PrefillMaps& maps, cudaStream_t stream);
 
-// mla_shared_fwd: a persistent block an SM; a job is up to four query tokens of a group
-// over one split of its keys.
+// mla_shared_fwd: a persistent block an SM, a worker; a job is up to four query tokens of a
+// group over its keys, or the part of them that falls to the worker.
 struct SharedParams {
   const uint16_t* q;         // bf16 [total_q][16][576]
   const uint8_t* kv;         // e4m3 codes [kv_rows][576]
@@ -146,14 +144,15 @@ struct SharedParams {
   const int32_t* kv_indices; // or null: keys are rows of the cache
   uint16_t* out;             // bf16 [total_q][16][512]
   float* lse;                // [total_q][16] or null
-  float* part;               // splits > 1: [splits][total_q][16][512]
-  float* part_lse;           // splits > 1: [splits][total_q][16]
+  float* part;               // if split: [2 * workers][64][512], see shared.cu
+  float* part_lse;           // if split: [2 * workers][64]
   int32_t* err;
-  uint32_t* sched;           // as PrefillParams::sched
+  uint32_t* missing;         // nonzero if not all parts of this call were computed
   int64_t kv_rows;
   int64_t kv_limit;          // keys that kv_indptr may count: kv_indices' entries, or kv_rows
-  int64_t part_rows;         // rows of parts that the workspace has room for (for the debug build's checks)
-  int32_t batch, total_q, blocks, splits, num_sms;
+  int32_t batch, total_q, workers;
+  int32_t split;             // whether a block's keys may be shared by workers
+  int32_t start;             // units of work that a block's start counts for
   int32_t stall_stream;      // test hook: no copies are issued, so the waits run out
 };
 struct SharedMaps {
@@ -163,6 +162,7 @@ constexpr int kSharedTokens = 4;  // query tokens of a job
 size_t shared_smem_bytes();
 cudaError_t shared_prepare();
 cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream);
+cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
 
 struct BlockMeansParams {
   const uint8_t* cache;      // e4m3 codes or bf16 rows

@@ -15,8 +15,10 @@
 // which is 2^-14 of the row's reference (2^4).  TMEM is full: two S of 128 columns, O in
 // four chunks of 64.
 //
-// Persistent blocks, one an SM, take jobs (four query tokens of a group over a part of its
-// keys) from a counter:
+// Persistent blocks, one an SM, are workers.  Every four query tokens of a group, with their
+// keys, are a block of units, a unit a key tile and some for its start; all blocks' units
+// one behind the other are cut into equal ranges, a worker each.  A job is what a range has
+// of one block:
 //   * warp 3 finds the jobs,
 //   * the keys come as four panels of 128 dims a tile into two buffers, and the 64 rotated
 //     dims into one: by warp 2 through TMA in boxes of 128 rows, or, by a page table, by
@@ -27,7 +29,7 @@
 //   * warps 4-7 and 8-11 run the softmax of two query tokens each, a thread a key: the
 //     maximum over keys is over lanes, so it is only looked for when a score passes the
 //     running reference by four powers of two, which few tiles' do.
-// Parts of keys leave float32 results, which attn_merge.cu joins.
+// A job without all of its block's keys leaves a float32 part, and a second kernel joins them.
 #include <cstddef>
 
 #include <cuda_fp16.h>
@@ -88,8 +90,9 @@ constexpr float kTop = -4.0f;
 struct Job {
   int32_t q0, nq;    // first query token, number of them (up to four)
   int32_t k0, keys;  // first key of the part (of all groups' keys), and keys
-  int32_t split;
+  int32_t slot;      // of the part in the workspace; -1: these are all of the block's keys
   int32_t live;      // 0: no more jobs
+  int64_t end;       // unit behind the block's last
   __device__ __forceinline__ int32_t tiles() const { return (keys + kTileTokens - 1) / kTileTokens; }
 };
 
@@ -99,7 +102,6 @@ struct Job {
 // other roles, that its waiters have passed the one before (said at each).
 struct Misc {
   uint64_t job_full[2], job_empty[2];
-  uint64_t claim;        // the copies of a job's last tile are due: take the next job
   uint64_t key_full[2 * kPanels], key_empty[2 * kPanels];  // panel c of tile T: kPanels (T & 1) + c
   uint64_t rope_full, rope_empty;
   uint64_t q_full;       // a job's query operand written ...
@@ -149,7 +151,7 @@ __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
   }
 }
 
-// ------------------------------------------------------------ scheduler (one warp)
+// ------------------------------------------------------------ who does what
 struct Group {
   int32_t qs, n, ks, len;
 };
@@ -164,16 +166,34 @@ __device__ __forceinline__ Group load_group(const SharedParams& p, int32_t g, bo
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
   return bad_q || bad_k ? Group{0, 0, 0, 0} : Group{qs, qe - qs, ks, ke - ks};
 }
-__device__ __forceinline__ int32_t blocks_of(int32_t n) { return (n + kTokens - 1) / kTokens; }
+__device__ __forceinline__ int64_t blocks_of(const Group& g) { return (g.n + kTokens - 1) / kTokens; }
 
-// The groups as the warp holds them: a run of consecutive groups a lane.
-struct Batch {
-  int32_t g0, first, count, total;  // the lane's first group, blocks before and in its run; all blocks
+// A block's units: of a split plan its key tiles (one if it has none) behind `start` ones,
+// else one.
+__device__ __forceinline__ int64_t units_of(const SharedParams& p, const Group& g) {
+  return p.split ? p.start + max(1, tiles_of_length(g.len)) : 1;
+}
+// Worker c of `workers` has the units [unit(c), unit(c + 1)) of `all`, none of them empty;
+// unit u is worker owner(u)'s.
+struct Ranges {
+  int64_t all, workers;
+  __device__ __forceinline__ int64_t unit(int64_t c) const { return c * all / workers; }
+  __device__ __forceinline__ int64_t owner(int64_t u) const { return ((u + 1) * workers - 1) / all; }
 };
-// Groups that overlap, which decreasing offsets make (and which are reported), could have
-// any number of blocks.  No more are worked on than groups in order can have, so some may
-// be left out, and the joining kernel is told so.
-constexpr int32_t kManyBlocks = 1 << 25;
+// A bound on units that keeps every product above within 64 bits.
+constexpr int64_t kManyUnits = INT64_C(1) << 48;
+
+// The groups as a warp holds them: a run of consecutive groups a lane.
+struct Batch {
+  int32_t g0;
+  int64_t first, count;  // units before the lane's run, and in it
+  Ranges ranges;
+};
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
 __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
   const int lane = threadIdx.x & 31;
   const int32_t run = (p.batch + 31) / 32;
@@ -182,69 +202,83 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
   const int32_t g1 = min(p.batch, r.g0 + run);
   bool back = false;
   r.count = 0;
-  for (int32_t g = r.g0; g < g1; ++g)
-    r.count = min(r.count + blocks_of(load_group(p, g, blockIdx.x == 0, back).n), kManyBlocks);
-  if (blockIdx.x == 0) {
-    back = __any_sync(0xffffffffu, back);
-    if (lane == 0) p.sched[2] = back;  // (of every call anew)
+  for (int32_t i = r.g0; i < g1; ++i) {
+    const Group g = load_group(p, i, blockIdx.x == 0, back);
+    r.count = min(r.count + blocks_of(g) * units_of(p, g), kManyUnits / 32);
   }
-  int32_t incl = r.count;
+  back = __any_sync(0xffffffffu, back);
+  if (blockIdx.x == 0 && lane == 0) *p.missing = back;  // (of every call anew)
+  int64_t incl = r.count;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
   r.first = incl - r.count;
-  r.total = min(__shfl_sync(0xffffffffu, incl, 31), p.blocks);
+  // Groups overlap where offsets of queries decrease (which is reported) and could come to
+  // any amount of work, so nothing is done then, and nothing joined.
+  r.ranges.all = back ? 0 : __shfl_sync(0xffffffffu, incl, 31);
+  r.ranges.workers = min(static_cast<int64_t>(p.workers), r.ranges.all);
   return r;
 }
 
-// Job `index` into `job`: blocks run fastest, so that the SMs at work read the same keys.
-__device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, uint32_t index, Job* job) {
-  const uint32_t total = static_cast<uint32_t>(r.total);
-  if (total == 0 || index >= total * static_cast<uint32_t>(p.splits)) {
+// The job at unit `u` of this worker's range into `job` (a warp); none behind the range's end.
+__device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, int64_t u, Job* job) {
+  const int64_t c = blockIdx.x;
+  int64_t stop = 0;
+  if (c < r.ranges.workers) stop = r.ranges.unit(c + 1);
+  if (u >= stop) {
     if ((threadIdx.x & 31) == 0) job->live = job->nq = job->keys = 0;
     __syncwarp();
     return;
   }
-  const int32_t split = static_cast<int32_t>(index / total);
-  int32_t block = static_cast<int32_t>(index % total) - r.first;
-  if (block >= 0 && block < r.count) {
+  if (u >= r.first && u < r.first + r.count) {
     bool back = false;
-    Group g = load_group(p, r.g0, false, back);
-    for (int32_t at = r.g0; block >= blocks_of(g.n);) {  // (ends within the lane's run)
-      block -= blocks_of(g.n);
-      g = load_group(p, ++at, false, back);
+    int64_t at = u - r.first;
+    int32_t i = r.g0;
+    Group g = load_group(p, i, false, back);
+    while (at >= blocks_of(g) * units_of(p, g)) {  // (ends within the lane's run)
+      at -= blocks_of(g) * units_of(p, g);
+      g = load_group(p, ++i, false, back);
     }
-    const int32_t tiles = tiles_of_length(g.len), share = (tiles + p.splits - 1) / p.splits;
-    const int32_t a = min(g.len, split * share * kTileTokens), b = min(g.len, (split + 1) * share * kTileTokens);
-    job->q0 = g.qs + block * kTokens;
-    job->nq = min(kTokens, g.n - block * kTokens);
-    job->k0 = g.ks + a;
-    job->keys = b - a;
-    job->split = split;
+    const int64_t size = units_of(p, g), block = at / size, begin = u - (at - block * size);
+    const int32_t tiles = tiles_of_length(g.len);
+    int32_t j0 = 0, j1 = tiles;
+    if (p.split) {  // the range's tiles of the block
+      const int64_t tile0 = begin + p.start;
+      j0 = static_cast<int32_t>(max(u - tile0, static_cast<int64_t>(0)));
+      j1 = static_cast<int32_t>(max(min(stop - tile0, static_cast<int64_t>(tiles)), static_cast<int64_t>(0)));
+    }
+    const bool whole = j0 == 0 && j1 == tiles;
+    job->q0 = g.qs + static_cast<int32_t>(block) * kTokens;
+    // (a range that ends among a block's start units has none of it)
+    job->nq = whole || j1 > j0 ? min(kTokens, g.n - static_cast<int32_t>(block) * kTokens) : 0;
+    job->k0 = g.ks + j0 * kTileTokens;
+    job->keys = j1 > j0 ? min(g.len, j1 * kTileTokens) - j0 * kTileTokens : 0;
+    // a worker's first part continues a block, its last begins one
+    job->slot = whole ? -1 : 2 * static_cast<int32_t>(c) + (j0 == 0);
     job->live = 1;
+    job->end = begin + size;
   }
   __syncwarp();
 }
 
-// The first job is the block's own and found before the roles start; the others come from
-// a counter.
+// ------------------------------------------------------------ scheduler (one warp)
+// The first job is found before the roles start.
 __device__ __forceinline__ void run_scheduler(const SharedParams& p, const Batch& groups, Misc* ms) {
   const int lane = threadIdx.x & 31;
+  int64_t u = 0;
   for (uint32_t k = 0;; ++k) {
     Job* job = &ms->job[k & 1];
     if (k > 0) {
-      uint32_t index = 0;
-      if (lane == 0) index = gridDim.x + atomicAdd(p.sched, 1u);
-      index = __shfl_sync(0xffffffffu, index, 0);
       if (k > 1 && !warp_wait_on(&ms->job_empty[k & 1], (k >> 1) - 1, ms, p.err)) return;
-      find_job(p, groups, index, job);
+      find_job(p, groups, u, job);
     }
     const int32_t live = job->live;
+    u = job->end;
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
-    if (live == 0 || !warp_wait_on(&ms->claim, k, ms, p.err)) return;
+    if (live == 0) return;
   }
 }
 
@@ -267,10 +301,8 @@ __device__ __forceinline__ void run_producer(const SharedParams& p, const Shared
   bool ok = true;
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t n = p.stall_stream ? 0 : job.tiles();
-    if (n == 0 && lane == 0) mbar_arrive(smem_u32(&ms->claim));
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
       const int32_t key = job.k0 + j * kTileTokens;
-      if (j == n - 1 && lane == 0) mbar_arrive(smem_u32(&ms->claim));
       if (!MLA_DCHECK(key >= 0 && key < p.kv_rows, p.err)) {
         ms->abort_flag = 1;
         ok = false;
@@ -381,10 +413,8 @@ __device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint
   };
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t n = p.stall_stream ? 0 : job.tiles();
-    if (n == 0 && t == 0) mbar_arrive(smem_u32(&ms->claim));
     if (n > 0) next.load(p, job, 0);
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
-      if (j == n - 1 && t == 0) mbar_arrive(smem_u32(&ms->claim));
       rows = next;
       rows.check(p);
       if (j + 1 < n) next.load(p, job, j + 1);
@@ -901,11 +931,12 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     // term for a warpgroup) to leave in 16-byte pieces: 2-byte stores of a warp's 32 dims took
     // 3.5 us a job.
     const int tokens = min(2, job.nq - 2 * g);  // of this warpgroup
-    const int64_t row0 = (static_cast<int64_t>(p.splits > 1 ? job.split : 0) * p.total_q + job.q0 + 2 * g) * kNumHeads;
-    const bool fits = !ms->abort_flag && MLA_DCHECK(tokens <= 0 || (job.q0 >= 0 && job.q0 + 2 * g + tokens <= p.total_q && job.split >= 0 &&
-                                 job.split < p.splits && (p.splits == 1 || row0 + tokens * kNumHeads <= p.part_rows)), p.err);
+    const bool parts = job.slot >= 0;
+    const int64_t row0 = parts ? static_cast<int64_t>(job.slot) * kRows + 2 * g * kNumHeads
+                               : (static_cast<int64_t>(job.q0) + 2 * g) * kNumHeads;
+    const bool fits = !ms->abort_flag && MLA_DCHECK(tokens <= 0 || (parts ? job.slot < 2 * p.workers && p.split
+                                                                          : job.q0 >= 0 && job.q0 + 2 * g + tokens <= p.total_q), p.err);
     uint8_t* stage = reinterpret_cast<uint8_t*>(ms) - kOffMisc + kOffP + g * kPBytes;
-    const bool parts = p.splits > 1;
 #pragma unroll 1
     for (int step = 0; step < 2 * kPanels; ++step) {  // a token's 16 rows of a chunk
       const int c = step >> 1, i = step & 1;
@@ -961,7 +992,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       named_bar_sync(bar, 128);
     }
     if (t < 16 * tokens && fits) {
-      if (p.splits > 1)
+      if (parts)
         p.part_lse[row0 + t] = lse;
       else if (p.lse != nullptr)
         p.lse[row0 + t] = lse;
@@ -999,7 +1030,6 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
       mbar_init(smem_u32(&ms->key_full[i]), kPaged ? kCopyWarps : 1);
       mbar_init(smem_u32(&ms->key_empty[i]), 1);
     }
-    mbar_init(smem_u32(&ms->claim), 1);
     mbar_init(smem_u32(&ms->rope_full), kPaged ? kCopyWarps : 1);
     mbar_init(smem_u32(&ms->rope_empty), 1);
     mbar_init(smem_u32(&ms->q_full), kSoftmaxWarps);
@@ -1020,7 +1050,7 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
   Batch groups = {};
   if (warp == kSchedulerWarp) {
     groups = count_groups(p);
-    find_job(p, groups, blockIdx.x, &ms->job[0]);
+    find_job(p, groups, blockIdx.x < groups.ranges.workers ? groups.ranges.unit(blockIdx.x) : 0, &ms->job[0]);
   }
   tc_fence_before();
   __syncthreads();
@@ -1052,13 +1082,95 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
     // (Abandoned: the parts are not whole.  Block 0 has written the word long before a wait runs out.)
-    if (one && ms->abort_flag) p.sched[2] = 1;
-    // The last block leaves the counters zero for the workspace's next call.
-    if (one && atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
-      p.sched[0] = 0;
-      p.sched[1] = 0;
+    if (one && ms->abort_flag) *p.missing = 1;
+  }
+}
+
+// ------------------------------------------------------------ joining
+// A block a row (token and head): out = sum_w 2^(..) part_w over the workers that share the
+// token's block of queries, a thread four of the 512 values, eight parts in flight.  Rows
+// whose keys one worker had are written already.  The groups are an input of the attention
+// before as well, which waited for whoever wrote them, so the row's workers are found before
+// the wait for it.
+constexpr int kJoinThreads = 128, kJoinAhead = 8;
+__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p) {
+  __shared__ int64_t sums[2][kJoinThreads / 32];
+  __shared__ int32_t mine;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t token = static_cast<int32_t>(blockIdx.x) / kNumHeads, head = static_cast<int32_t>(blockIdx.x) % kNumHeads;
+  if (tid == 0) mine = -1;
+  __syncthreads();
+  bool back = false;
+  int64_t all = 0, before = 0;
+  for (int32_t g = tid; g < p.batch; g += kJoinThreads) {
+    const Group x = load_group(p, g, false, back);
+    const int64_t n = blocks_of(x) * units_of(p, x);
+    all = min(all + n, kManyUnits / 32);
+    if (x.qs + x.n <= token) before = min(before + n, kManyUnits / 32);
+    if (token >= x.qs && token < x.qs + x.n) mine = g;  // (of groups that overlap any: nothing is joined then)
+  }
+  all = warp_sum(all);
+  before = warp_sum(before);
+  if (lane == 0) {
+    sums[0][warp] = all;
+    sums[1][warp] = before;
+  }
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    all += sums[0][w];
+    before += sums[1][w];
+  }
+  const int32_t own = mine;
+  int32_t w0 = 0, w1 = 0, row = 0;
+  if (own >= 0) {
+    const Group x = load_group(p, own, false, back);
+    const int32_t n = tiles_of_length(x.len), block = (token - x.qs) / kTokens;
+    const Ranges ranges = {all, min(static_cast<int64_t>(p.workers), all)};
+    const int64_t tile0 = before + block * units_of(p, x) + p.start;
+    w0 = static_cast<int32_t>(ranges.owner(tile0));
+    w1 = n > 0 ? static_cast<int32_t>(ranges.owner(tile0 + n - 1)) : w0;
+    row = (token - x.qs - block * kTokens) * kNumHeads + head;
+  }
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (w0 == w1 || *p.missing != 0) return;
+  if (!MLA_DCHECK(w0 >= 0 && w1 < p.workers && row < kRows, p.err)) return;
+  // The first worker's part is its last job's, the others' their first.
+  auto slot = [&](int32_t w) { return 2 * static_cast<int64_t>(w) + (w == w0); };
+  float top = -INFINITY;
+  for (int32_t w = w0; w <= w1; ++w) top = fmaxf(top, __ldcg(p.part_lse + slot(w) * kRows + row));
+  if (top == -INFINITY) top = 0.0f;
+  float acc[4] = {}, sum = 0.0f;
+  for (int32_t at = w0; at <= w1; at += kJoinAhead) {
+    float4 v[kJoinAhead];
+    float l[kJoinAhead];
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      if (at + i > w1) break;
+      const int64_t r = slot(at + i) * kRows + row;
+      v[i] = __ldcs(reinterpret_cast<const float4*>(p.part + r * kVDim) + tid);
+      l[i] = __ldcg(p.part_lse + r);
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      if (at + i > w1) break;
+      const float f = expf(l[i] - top);  // (a NaN reaches the result)
+      sum += f;
+      acc[0] = fmaf(f, v[i].x, acc[0]);
+      acc[1] = fmaf(f, v[i].y, acc[1]);
+      acc[2] = fmaf(f, v[i].z, acc[2]);
+      acc[3] = fmaf(f, v[i].w, acc[3]);
     }
   }
+  const float inv = 1.0f / sum;
+  uint2 packed;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed.x) : "f"(acc[1] * inv), "f"(acc[0] * inv));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed.y) : "f"(acc[3] * inv), "f"(acc[2] * inv));
+  const int64_t out = static_cast<int64_t>(token) * kNumHeads + head;
+  reinterpret_cast<uint2*>(p.out + out * kVDim)[tid] = packed;
+  if (tid == 0 && p.lse != nullptr) p.lse[out] = top + logf(sum);
 }
 
 }  // namespace
@@ -1072,12 +1184,16 @@ cudaError_t shared_prepare() {
 }
 
 cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream) {
-  const int64_t jobs = static_cast<int64_t>(p.blocks) * p.splits;
-  if (jobs > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(jobs < p.num_sms ? jobs : p.num_sms);
+  const unsigned grid = static_cast<unsigned>(p.workers);
   return p.kv_indices != nullptr
              ? launch_dependent(shared_kernel<true>, grid, threads<true>(), kSmemBytes, stream, maps, p)
              : launch_dependent(shared_kernel<false>, grid, threads<false>(), kSmemBytes, stream, maps, p);
+}
+
+cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.total_q) * kNumHeads;
+  if (rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  return launch_dependent(shared_join_kernel, static_cast<unsigned>(rows), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace mla

@@ -41,14 +41,15 @@ def shared_args(made, **change):
     (dict(ws_bytes=0), WS_SMALL)])
 def test_shared_refusals(lib, change, status):
     plan = binding.mla_shared_plan(1, 64, 8192, 152)
-    assert plan.splits > 1
+    assert plan.split == 1
     assert lib.mla_shared_fwd(*shared_args(plan, **change)) == status
     assert lib.mla_shared_fwd_stall_stream(*shared_args(plan, **change)) == status
 
 
 def test_shared_refuses_a_changed_plan(lib):
-    for field, value in [("splits", 0), ("splits", 1), ("abi_version", 4), ("ws_lse_offset", 0), ("batch", 0),
-                         ("batch", 65537), ("total_q", -1), ("max_kv_len", -1), ("num_sms", 0)]:
+    for field, value in [("workers", 0), ("workers", 3), ("workers", 4097), ("split", 0), ("split", 2),
+                         ("abi_version", 4), ("start", -1), ("start", 65), ("ws_lse_offset", 0), ("batch", 0), ("batch", 65537),
+                         ("batch", 1025), ("total_q", -1), ("max_kv_len", -1), ("num_sms", 0)]:
         plan = binding.mla_shared_plan(1, 64, 8192, 152)
         setattr(plan, field, value)
         assert lib.mla_shared_fwd(*shared_args(plan)) == INVALID, (field, value)
@@ -64,9 +65,9 @@ def test_shared_of_no_queries_launches_nothing(lib):
                                                 (1, 70000, 100, 152), (1, 1, 2**31 - 1, 152)])
 def test_shared_plan(lib, batch, total, kv, sms):
     plan = binding.mla_shared_plan(batch, total, kv, sms)
-    assert 1 <= plan.splits <= max(1, min(64, -(-kv // 128)))
-    assert batch <= 1024 or plan.splits == 1
-    rows = 16 * plan.splits * total if plan.splits > 1 else 0
+    assert 1 <= plan.workers <= sms and plan.split in (0, 1) and plan.start >= 0
+    assert batch <= 1024 or plan.split == 0
+    rows = 2 * plan.workers * 64 if plan.split else 0
     assert plan.ws_lse_offset == 256 and plan.ws_partial_offset % 256 == 0
     assert plan.ws_partial_offset >= 256 + 4 * rows and plan.ws_bytes >= plan.ws_partial_offset + 4 * 512 * rows
 
