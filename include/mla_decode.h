@@ -698,7 +698,7 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
  * without keys gives zeros and lse -inf.  The query enters the products as two e4m3 terms
  * (exact down to 2^-13 of its head's largest magnitude), a probability as two e4m3 terms
  * (to 2^-8 of itself, or 2^-14 of the row's largest); accumulation and softmax statistics
- * are float32; out is rounded once.
+ * are float32; out is rounded to bf16, parts of shared keys to half precision before.
  *   q_bf16     device, bf16 [total_q][16][576], 16-byte aligned.  A token's head with a value
  *              that is not finite gets NaN, as output and as lse.
  *   kv_fp8     device, e4m3fn codes [kv_rows][576], 16-byte aligned.  Codes of the groups'
@@ -736,7 +736,7 @@ typedef struct {
   int32_t abi_version; /* MLA_ABI_VERSION                                              */
   uint64_t ws_bytes;   /* workspace bytes mla_shared_fwd needs                         */
   uint64_t ws_lse_offset;     /* float[2 * workers][64] when split                     */
-  uint64_t ws_partial_offset; /* float[2 * workers][64][512] when split                */
+  uint64_t ws_partial_offset; /* half[2 * workers][4][4][128][16] when split           */
 } mla_shared_plan_t;
 
 /* Pure host.  batch 1 .. MLA_SHARED_MAX_GROUPS, total_q and max_kv_len >= 0; num_sms <= 0 asks the device. */

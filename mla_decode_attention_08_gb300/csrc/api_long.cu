@@ -79,7 +79,7 @@ bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num
     const uint64_t rows = 2ull * cut.workers * mla::kSharedTokens * mla::kNumHeads;
     off += round_up(rows * sizeof(float));
     p.ws_partial_offset = off;
-    off += round_up(rows * mla::kVDim * sizeof(float));
+    off += round_up(rows * mla::kVDim * sizeof(uint16_t));
   }
   p.ws_bytes = off;
   *out = p;
@@ -122,7 +122,7 @@ mla_status_t run_shared(const void* q, const void* kv, const float* kv_scale, co
   p.kv_indices = kv_indices;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.part = reinterpret_cast<float*>(ws + plan->ws_partial_offset);
+  p.part = reinterpret_cast<uint16_t*>(ws + plan->ws_partial_offset);
   p.part_lse = reinterpret_cast<float*>(ws + plan->ws_lse_offset);
   p.err = reinterpret_cast<int32_t*>(ws);
   p.missing = reinterpret_cast<uint32_t*>(ws + kMissingOffset);

@@ -144,7 +144,7 @@ struct SharedParams {
   const int32_t* kv_indices; // or null: keys are rows of the cache
   uint16_t* out;             // bf16 [total_q][16][512]
   float* lse;                // [total_q][16] or null
-  float* part;               // if split: [2 * workers][64][512], see shared.cu
+  uint16_t* part;            // if split: half [2 * workers][4 chunks][4 tokens][128 dims][16]
   float* part_lse;           // if split: [2 * workers][64]
   int32_t* err;
   uint32_t* missing;         // nonzero if not all parts of this call were computed

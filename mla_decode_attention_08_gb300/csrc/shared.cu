@@ -29,7 +29,9 @@
 //   * warps 4-7 and 8-11 run the softmax of two query tokens each, a thread a key: the
 //     maximum over keys is over lanes, so it is only looked for when a score passes the
 //     running reference by four powers of two, which few tiles' do.
-// A job without all of its block's keys leaves a float32 part, and a second kernel joins them.
+// A job without all of its block's keys leaves a part of half precision, in units of the
+// cache's codes (at most 448; 11 bits, 2^-4 of the output's rounding: blocks store at 30 bytes
+// a cycle, and float32 parts took 4300 cycles a job), and a second kernel joins them.
 #include <cstddef>
 
 #include <cuda_fp16.h>
@@ -474,16 +476,18 @@ __device__ __forceinline__ void run_scores(const SharedParams& p, Misc* ms, uint
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t n = job.tiles();
     if (n == 0) continue;
-    ok = on(&ms->q_full, jobs++);
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
       const uint32_t d = tmem + kColS + 128 * (T & 1), first = kPanels * (T & 1);
       const int32_t keys = job.keys - j * kTileTokens;
-      if (!kPaged && keys < kTileTokens) {
+      const bool clean = !kPaged && keys < kTileTokens;
+      // A job's first keys land before its query, and a look at a barrier costs 100 cycles.
+      const bool landed = j == 0 || clean;
+      if (landed) {
         for (int c = 0; c < kPanels && ok; ++c) ok = on(&ms->key_full[first + c], T >> 1);
         if (!ok) break;
-        clean_keys(smem + kOffKeys + first * kPanelBytes, keys);
+        if (clean) clean_keys(smem + kOffKeys + first * kPanelBytes, keys);
       }
-      ok = (T < 2 || on(&ms->s_free[T & 1], (T >> 1) - 1)) && on(&ms->rope_full, T);
+      ok = (T < 2 || on(&ms->s_free[T & 1], (T >> 1) - 1)) && on(&ms->rope_full, T) && (j > 0 || on(&ms->q_full, jobs));
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
@@ -494,7 +498,7 @@ __device__ __forceinline__ void run_scores(const SharedParams& p, Misc* ms, uint
       __syncwarp();
 #pragma unroll
       for (int c = 0; c < kPanels; ++c) {
-        ok = ok && on(&ms->key_full[first + c], T >> 1);
+        ok = ok && (landed || on(&ms->key_full[first + c], T >> 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -509,6 +513,7 @@ __device__ __forceinline__ void run_scores(const SharedParams& p, Misc* ms, uint
         __syncwarp();
       }
     }
+    ++jobs;
   }
   if (elect_one()) umma_commit(smem_u32(&ms->mma_done));
   __syncwarp();
@@ -629,6 +634,11 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, float by) {
   const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(by));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// 32 bytes, aligned so.
+__device__ __forceinline__ void store_sector(uint16_t* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
 // Two e4m3 terms without the conversion instructions, whose rate is a fraction of the
 // others'.  A half precision value below 2 in magnitude has a fifth exponent bit of zero, so
 // its bits 13 .. 7 are the e4m3 code of the value times 2^8, cut to its four leading bits:
@@ -711,23 +721,26 @@ __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_
   uint32_t rope_top = largest(raw[kWarpRows]);
   rope_top = max(rope_top, __shfl_xor_sync(0xffffffffu, rope_top, 1));
   rope_top = max(rope_top, __shfl_xor_sync(0xffffffffu, rope_top, 2));
+  // (all rows' maxima first: the rows' conversions then overlap)
+  uint32_t top[kWarpRows];
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) top[r] = __reduce_max_sync(0xffffffffu, largest(raw[r]));
   float rope_up = 0.0f;
 #pragma unroll
   for (int r = 0; r < kWarpRows; ++r) {
-    uint32_t top = largest(raw[r]);
-    top = max(__reduce_max_sync(0xffffffffu, top), __shfl_sync(0xffffffffu, rope_top, 4 * r));
+    top[r] = max(top[r], __shfl_sync(0xffffffffu, rope_top, 4 * r));
     // The exponent e of the largest magnitude m 2^e, 1 <= m < 2, of bf16 bits: scaled by 2^k to
     // 2^8 m where m <= 1.75, else to 2^7 m.  (Zeros and denormals: clamped.)
-    const int e = static_cast<int>(top >> 7) - 127;
-    int k = (top & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
-    k = top == 0 ? 0 : min(k, 126);
+    const int e = static_cast<int>(top[r] >> 7) - 127;
+    int k = (top[r] & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
+    k = top[r] == 0 ? 0 : min(k, 126);
     // 2^(k - 8), which is a denormal for the largest of all
     const float up = __int_as_float(k - 8 + 127 > 0 ? (k - 8 + 127) << 23 : 1 << (22 + (k - 8 + 127)));
     if (lane >> 2 == r) rope_up = up;
     const int row = 2 * kNumHeads * g + row0 + r;
     if (lane == r)
-      ms->scale[g][row0 + r] = top >= 0x7F80u ? __int_as_float(0x7FC00000)
-                                              : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
+      ms->scale[g][row0 + r] = top[r] >= 0x7F80u ? __int_as_float(0x7FC00000)
+                                                 : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
     const uint32_t at = sbase + kOffQ + (lane >> 3) * kPanelBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
     store(raw[r], up, at, at + kRows * 128);
   }
@@ -910,7 +923,8 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     named_bar_sync(bar, 128);
     if (warp == 0) {
       const float s = (ms->red[g][0][lane] + ms->red[g][1][lane]) + (ms->red[g][2][lane] + ms->red[g][3][lane]);
-      ms->factor[g][lane] = s != 0.0f ? kv_scale * 0x1p-8f / s : 0.0f;  // (P is 2^8 times what was summed)
+      // (P is 2^8 times what was summed; a part is left in units of codes)
+      ms->factor[g][lane] = s != 0.0f ? (job.slot >= 0 ? 1.0f : kv_scale) * 0x1p-8f / s : 0.0f;
       if (n > 0) lse = kLn2 * (log2f(s) - off);
     }
     named_bar_sync(bar, 128);
@@ -927,13 +941,11 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     }
 
     // ------------------------------------------------ output
-    // A thread has one dim of a chunk, so rows go through shared memory (P's, which is free: a
-    // term for a warpgroup) to leave in 16-byte pieces: 2-byte stores of a warp's 32 dims took
-    // 3.5 us a job.
+    // A thread has one dim of a chunk.  Parts keep that order, [chunk][token][dim][head]: 16
+    // heads are a sector.  Rows of the output go through shared memory (P's, which is
+    // free: a term for a warpgroup) to leave in 16-byte pieces.
     const int tokens = min(2, job.nq - 2 * g);  // of this warpgroup
     const bool parts = job.slot >= 0;
-    const int64_t row0 = parts ? static_cast<int64_t>(job.slot) * kRows + 2 * g * kNumHeads
-                               : (static_cast<int64_t>(job.q0) + 2 * g) * kNumHeads;
     const bool fits = !ms->abort_flag && MLA_DCHECK(tokens <= 0 || (parts ? job.slot < 2 * p.workers && p.split
                                                                           : job.q0 >= 0 && job.q0 + 2 * g + tokens <= p.total_q), p.err);
     uint8_t* stage = reinterpret_cast<uint8_t*>(ms) - kOffMisc + kOffP + g * kPBytes;
@@ -941,15 +953,11 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     for (int step = 0; step < 2 * kPanels; ++step) {  // a token's 16 rows of a chunk
       const int c = step >> 1, i = step & 1;
       if (i >= tokens) continue;  // (the same for the warpgroup)
-      const int64_t first = (row0 + 16 * i) * kVDim + 128 * c;
-      if (n == 0) {  // no keys: zeros (P's memory may be at work)
-        if (fits && parts) {
-          for (int row = warp; row < 16; row += 4)
-            *reinterpret_cast<float4*>(p.part + first + row * kVDim + 4 * lane) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        } else if (fits) {
+      uint16_t* dst = p.out + (static_cast<int64_t>(job.q0 + 2 * g + i) * kNumHeads) * kVDim + 128 * c;
+      if (n == 0) {  // no keys: zeros (P's memory may be at work; of a part the log-sum-exp says so)
+        if (fits && !parts)
           for (int row = t >> 4; row < 16; row += 8)
-            *reinterpret_cast<uint4*>(p.out + first + row * kVDim + 8 * (t & 15)) = make_uint4(0, 0, 0, 0);
-        }
+            *reinterpret_cast<uint4*>(dst + row * kVDim + 8 * (t & 15)) = make_uint4(0, 0, 0, 0);
         continue;
       }
       uint32_t o[16];
@@ -959,43 +967,40 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float4 f = by[q];
-        const float v[4] = {__uint_as_float(o[4 * q]) * f.x, __uint_as_float(o[4 * q + 1]) * f.y,
-                            __uint_as_float(o[4 * q + 2]) * f.z, __uint_as_float(o[4 * q + 3]) * f.w};
+        o[4 * q] = __float_as_uint(__uint_as_float(o[4 * q]) * f.x);
+        o[4 * q + 1] = __float_as_uint(__uint_as_float(o[4 * q + 1]) * f.y);
+        o[4 * q + 2] = __float_as_uint(__uint_as_float(o[4 * q + 2]) * f.z);
+        o[4 * q + 3] = __float_as_uint(__uint_as_float(o[4 * q + 3]) * f.w);
+      }
+      if (parts) {
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 4 * q + e;
-          if (parts) {
-            reinterpret_cast<float*>(stage)[row * 128 + t] = v[e];
-          } else {
-            uint16_t b;
-            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(v[e]));
-            reinterpret_cast<uint16_t*>(stage)[row * 128 + t] = b;
-          }
-        }
+        for (int h = 0; h < 8; ++h) w[h] = half2_bits(__uint_as_float(o[2 * h]), __uint_as_float(o[2 * h + 1]));
+        if (fits)
+          store_sector(p.part + ((static_cast<int64_t>(job.slot) * kPanels + c) * kTokens + 2 * g + i) * (128 * kNumHeads) + t * kNumHeads, w);
+        continue;
+      }
+#pragma unroll
+      for (int row = 0; row < 16; ++row) {
+        uint16_t b;
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(__uint_as_float(o[row])));
+        reinterpret_cast<uint16_t*>(stage)[row * 128 + t] = b;
       }
       named_bar_sync(bar, 128);
-      if (fits && parts) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = 4 * q + warp;  // 512 bytes a warp
-          *reinterpret_cast<float4*>(p.part + first + row * kVDim + 4 * lane) =
-              reinterpret_cast<const float4*>(stage)[row * 32 + lane];
-        }
-      } else if (fits) {
+      if (fits) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int row = 8 * q + (t >> 4), piece = t & 15;  // 256 bytes a row
-          *reinterpret_cast<uint4*>(p.out + first + row * kVDim + 8 * piece) =
-              reinterpret_cast<const uint4*>(stage)[row * 16 + piece];
+          *reinterpret_cast<uint4*>(dst + row * kVDim + 8 * piece) = reinterpret_cast<const uint4*>(stage)[row * 16 + piece];
         }
       }
       named_bar_sync(bar, 128);
     }
     if (t < 16 * tokens && fits) {
       if (parts)
-        p.part_lse[row0 + t] = lse;
+        p.part_lse[static_cast<int64_t>(job.slot) * kRows + 2 * g * kNumHeads + t] = lse;
       else if (p.lse != nullptr)
-        p.lse[row0 + t] = lse;
+        p.lse[(static_cast<int64_t>(job.q0) + 2 * g) * kNumHeads + t] = lse;
     }
     __syncwarp();
     if (n > 0) {
@@ -1087,17 +1092,22 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
 }
 
 // ------------------------------------------------------------ joining
-// A block a row (token and head): out = sum_w 2^(..) part_w over the workers that share the
-// token's block of queries, a thread four of the 512 values, eight parts in flight.  Rows
-// whose keys one worker had are written already.  The groups are an input of the attention
-// before as well, which waited for whoever wrote them, so the row's workers are found before
-// the wait for it.
-constexpr int kJoinThreads = 128, kJoinAhead = 8;
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p) {
+// A block a token, chunk of 128 dims and half of the heads: out = sum_w 2^(..) part_w over the
+// workers that share the token's block of queries.  A thread has eight heads of a dim, eight
+// parts in flight, the first ones' values beside the log-sum-exps; the weights are formed once
+// a block (by every thread they took longer than the bytes), and the rows are turned through
+// shared memory.  Rows whose keys one worker had are written already.
+constexpr int kJoinThreads = 128, kJoinAhead = 8, kJoinHeads = 8;
+constexpr int kJoinStep = kJoinThreads / kJoinHeads;  // parts whose weights are formed together
+__global__ void __launch_bounds__(kJoinThreads, 8) shared_join_kernel(const SharedParams p) {
+  __shared__ __align__(16) uint16_t rows[kJoinHeads][kJoinThreads];
+  __shared__ __align__(16) float weight[kJoinStep][kJoinHeads];
+  __shared__ float red[2][kJoinThreads / 32][kJoinHeads];
   __shared__ int64_t sums[2][kJoinThreads / 32];
   __shared__ int32_t mine;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int32_t token = static_cast<int32_t>(blockIdx.x) / kNumHeads, head = static_cast<int32_t>(blockIdx.x) % kNumHeads;
+  const int32_t token = static_cast<int32_t>(blockIdx.x) / (2 * kPanels), c = static_cast<int32_t>(blockIdx.x) % (2 * kPanels) >> 1;
+  const int32_t head0 = kJoinHeads * (static_cast<int32_t>(blockIdx.x) & 1);
   if (tid == 0) mine = -1;
   __syncthreads();
   bool back = false;
@@ -1123,7 +1133,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
     before += sums[1][w];
   }
   const int32_t own = mine;
-  int32_t w0 = 0, w1 = 0, row = 0;
+  int32_t w0 = 0, w1 = 0, place = 0;
   if (own >= 0) {
     const Group x = load_group(p, own, false, back);
     const int32_t n = tiles_of_length(x.len), block = (token - x.qs) / kTokens;
@@ -1131,46 +1141,81 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
     const int64_t tile0 = before + block * units_of(p, x) + p.start;
     w0 = static_cast<int32_t>(ranges.owner(tile0));
     w1 = n > 0 ? static_cast<int32_t>(ranges.owner(tile0 + n - 1)) : w0;
-    row = (token - x.qs - block * kTokens) * kNumHeads + head;
+    place = token - x.qs - block * kTokens;
   }
   pdl_wait_primary();
   pdl_launch_dependents();
   if (w0 == w1 || *p.missing != 0) return;
-  if (!MLA_DCHECK(w0 >= 0 && w1 < p.workers && row < kRows, p.err)) return;
+  if (!MLA_DCHECK(w0 >= 0 && w1 < p.workers && place >= 0 && place < kTokens, p.err)) return;
   // The first worker's part is its last job's, the others' their first.
   auto slot = [&](int32_t w) { return 2 * static_cast<int64_t>(w) + (w == w0); };
-  float top = -INFINITY;
-  for (int32_t w = w0; w <= w1; ++w) top = fmaxf(top, __ldcg(p.part_lse + slot(w) * kRows + row));
-  if (top == -INFINITY) top = 0.0f;
-  float acc[4] = {}, sum = 0.0f;
-  for (int32_t at = w0; at <= w1; at += kJoinAhead) {
-    float4 v[kJoinAhead];
-    float l[kJoinAhead];
+  const uint16_t* part = p.part + (static_cast<int64_t>(c) * kTokens + place) * (128 * kNumHeads) + tid * kNumHeads + head0;
+  constexpr int64_t kSlot = static_cast<int64_t>(kRows) * kVDim;
+  uint4 v[kJoinAhead];
+  auto load = [&](int32_t at) {
 #pragma unroll
-    for (int i = 0; i < kJoinAhead; ++i) {
-      if (at + i > w1) break;
-      const int64_t r = slot(at + i) * kRows + row;
-      v[i] = __ldcs(reinterpret_cast<const float4*>(p.part + r * kVDim) + tid);
-      l[i] = __ldcg(p.part_lse + r);
-    }
+    for (int i = 0; i < kJoinAhead; ++i)
+      if (at + i <= w1) v[i] = __ldcs(reinterpret_cast<const uint4*>(part + slot(at + i) * kSlot));
+  };
+  load(w0);
+  // Thread (i, h): head h of the parts i, i + 16, ...
+  const int h = tid % kJoinHeads, first = w0 + tid / kJoinHeads;
+  const float* lses = p.part_lse + place * kNumHeads + head0 + h;
+  const float lse0 = first <= w1 ? __ldcg(lses + slot(first) * kRows) : -INFINITY;
+  float top = lse0;
+  for (int32_t w = first + kJoinStep; w <= w1; w += kJoinStep) top = fmaxf(top, __ldcg(lses + slot(w) * kRows));
+  auto over_parts = [&](float x, int which, auto join) {  // over the threads of a head
+    x = join(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    x = join(x, __shfl_xor_sync(0xffffffffu, x, 16));
+    if (lane < kJoinHeads) red[which][warp][lane] = x;
+    __syncthreads();
+    return join(join(red[which][0][h], red[which][1][h]), join(red[which][2][h], red[which][3][h]));
+  };
+  top = over_parts(top, 0, [](float a, float b) { return fmaxf(a, b); });
+  float sum = 0.0f, acc[kJoinHeads] = {};
+  for (int32_t at = w0; at <= w1; at += kJoinStep) {
+    const int32_t w = at + tid / kJoinHeads;
+    float f = 0.0f;
+    // (every part has keys; a NaN reaches the result)
+    if (w <= w1) f = expf((at == w0 ? lse0 : __ldcg(lses + slot(w) * kRows)) - top);
+    sum += f;
+    if (at > w0) __syncthreads();  // (the weights before are read)
+    weight[tid / kJoinHeads][h] = f;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kJoinAhead; ++i) {
-      if (at + i > w1) break;
-      const float f = expf(l[i] - top);  // (a NaN reaches the result)
-      sum += f;
-      acc[0] = fmaf(f, v[i].x, acc[0]);
-      acc[1] = fmaf(f, v[i].y, acc[1]);
-      acc[2] = fmaf(f, v[i].z, acc[2]);
-      acc[3] = fmaf(f, v[i].w, acc[3]);
+    for (int half = 0; half < kJoinStep; half += kJoinAhead) {
+      if (at + half > w1) break;
+      if (at + half > w0) load(at + half);
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) {
+        if (at + half + i > w1) break;
+        const uint32_t halves[kJoinHeads / 2] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const float4 f0 = *reinterpret_cast<const float4*>(&weight[half + i][0]), f1 = *reinterpret_cast<const float4*>(&weight[half + i][4]);
+        const float fs[kJoinHeads] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+        for (int e = 0; e < kJoinHeads / 2; ++e) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&halves[e]));
+          acc[2 * e] = fmaf(fs[2 * e], x.x, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(fs[2 * e + 1], x.y, acc[2 * e + 1]);
+        }
+      }
     }
   }
-  const float inv = 1.0f / sum;
-  uint2 packed;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed.x) : "f"(acc[1] * inv), "f"(acc[0] * inv));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed.y) : "f"(acc[3] * inv), "f"(acc[2] * inv));
-  const int64_t out = static_cast<int64_t>(token) * kNumHeads + head;
-  reinterpret_cast<uint2*>(p.out + out * kVDim)[tid] = packed;
-  if (tid == 0 && p.lse != nullptr) p.lse[out] = top + logf(sum);
+  sum = over_parts(sum, 1, [](float a, float b) { return a + b; });
+  if (tid < kJoinHeads) {
+    weight[0][tid] = __ldg(p.kv_scale) / sum;
+    if (c == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(token) * kNumHeads + head0 + tid] = top + logf(sum);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kJoinHeads; ++e) {
+    uint16_t b;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(acc[e] * weight[0][e]));
+    rows[e][tid] = b;
+  }
+  __syncthreads();
+  uint16_t* out = p.out + (static_cast<int64_t>(token) * kNumHeads + head0) * kVDim + 128 * c;
+  *reinterpret_cast<uint4*>(out + (tid >> 4) * kVDim + 8 * (tid & 15)) = *reinterpret_cast<const uint4*>(&rows[tid >> 4][8 * (tid & 15)]);
 }
 
 }  // namespace
@@ -1191,9 +1236,9 @@ cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStr
 }
 
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.total_q) * kNumHeads;
-  if (rows > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  return launch_dependent(shared_join_kernel, static_cast<unsigned>(rows), kJoinThreads, 0, stream, p);
+  const int64_t blocks = static_cast<int64_t>(p.total_q) * 2 * kPanels;
+  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+  return launch_dependent(shared_join_kernel, static_cast<unsigned>(blocks), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace mla

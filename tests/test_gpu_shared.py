@@ -7,9 +7,10 @@ or more): e = max_j (2^-14 spread + 2^-20 max|q| sum |k| / 24) + 2^-20 for exp2,
 probability and absolute in the lse.  A probability's two terms: 2^-8 of it (twice half a
 step of e4m3, 2^-4), 2^-11 by way of half precision, and half the smallest step, 2^-10, where
 the row's reference, which is not above its maximum, stands at 2^4: 2^-14 of the maximum's
-probability.  The output is rounded to bf16, 2^-8.  So with reach = sum_j p_j |v_j| / z and
+probability.  Parts of split keys are half precision in units of codes: 2^-11, and 2^-25 codes.
+The output is rounded to bf16, 2^-8.  So with reach = sum_j p_j |v_j| / z and
 z the sum of probabilities relative to the largest,
-|out - exact| <= 2^-8 |exact| + (2^-8 + 2^-11 + 2 e) reach + 2^-14 sum_j |v_j| / z.
+|out - exact| <= 2^-8 |exact| + (2^-8 + 2^-10 + 2 e) reach + 2^-14 sum_j |v_j| / z + 2^-25 kv_scale.
 Those are worst cases; rounding errors have independent signs, so in the 2-norm the two
 roundings of 2^-8 stay below 2^-8 of the result each: 2^-7 bounds the relative error."""
 import numpy as np
@@ -96,8 +97,8 @@ class Case:
             p = np.exp(s - s.max(axis=2, keepdims=True))
             z = p.sum(axis=2, keepdims=True)
             reach = p @ np.abs(k[:, :512]) / z
-            bound = (2.0**-8 * np.abs(out) + (2.0**-8 + 2.0**-11 + 2 * e[..., None]) * reach
-                     + 2.0**-14 * np.abs(k[:, :512]).sum(axis=0) / z)
+            bound = (2.0**-8 * np.abs(out) + (2.0**-8 + 2.0**-10 + 2 * e[..., None]) * reach
+                     + 2.0**-14 * np.abs(k[:, :512]).sum(axis=0) / z + 2.0**-25 * float(self.scale))
             assert (np.abs(got[a:b] - out) <= bound).all(), (g, np.abs(got[a:b] - out).max())
             assert np.linalg.norm(got[a:b] - out) <= 2.0**-7 * np.linalg.norm(out), g
             assert (np.abs(lse[a:b] - ref_lse) <= e + 2.0**-22 * np.abs(ref_lse)).all(), (g, np.abs(lse[a:b] - ref_lse).max())

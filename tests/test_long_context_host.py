@@ -69,7 +69,7 @@ def test_shared_plan(lib, batch, total, kv, sms):
     assert batch <= 1024 or plan.split == 0
     rows = 2 * plan.workers * 64 if plan.split else 0
     assert plan.ws_lse_offset == 256 and plan.ws_partial_offset % 256 == 0
-    assert plan.ws_partial_offset >= 256 + 4 * rows and plan.ws_bytes >= plan.ws_partial_offset + 4 * 512 * rows
+    assert plan.ws_partial_offset >= 256 + 4 * rows and plan.ws_bytes >= plan.ws_partial_offset + 2 * 512 * rows
 
 
 def test_shared_plan_refusals(lib):
