@@ -341,26 +341,7 @@ __device__ __forceinline__ void run_producer(const SharedParams& p, const Shared
   __syncwarp();
 }
 
-// ------------------------------------------------------------ keys by a page table (four warps)
-// Panel f of a block: five a tile, the rotated dims, then the latent ones.  A thread's copies
-// complete in order, so it can hand over a panel once at most the later ones are in flight;
-// before it waits for a buffer it hands over everything, since the buffer may wait for that.
-struct Copies {
-  uint32_t done = 0;    // panels handed over
-  uint32_t issued = 0;
-  __device__ __forceinline__ void hand_over(Misc* ms) {
-    const uint32_t T = done / (kPanels + 1), c = done % (kPanels + 1);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-      mbar_arrive(smem_u32(c == 0 ? &ms->rope_full : &ms->key_full[kPanels * (T & 1) + c - 1]));
-    ++done;
-  }
-  __device__ __forceinline__ void finish(Misc* ms) {
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    while (done < issued) hand_over(ms);
-  }
-};
+// ------------------------------------------------------------ keys by a page table (eight warps)
 constexpr int kCopyThreads = 32 * kCopyWarps;
 
 // A thread's rows of a tile: it copies piece t & 7 of latent row 16 i + t / 8 and piece t & 3 of
@@ -402,17 +383,10 @@ __device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint
   // (of the rows that a thread copies all have the same place in a swizzle's pattern)
   const uint32_t latent_at = sbase + kOffKeys + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
   const uint32_t rope_at = sbase + kOffRope + rope_row0 * 64 + ((rope_piece ^ ((rope_row0 >> 1) & 3)) << 4);
-  Copies copies;
   CopyRows rows, next;
   uint32_t T = 0;
   Job job;
   bool ok = true;
-  // A buffer is free, or everything before is handed over and it is waited for.
-  auto buffer = [&](const uint64_t* empty, uint32_t phase) {
-    if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(empty), phase & 1))) return true;
-    copies.finish(ms);
-    return warp_wait_on(empty, phase, ms, p.err);
-  };
   for (uint32_t k = 0; ok && next_job(p, ms, k, job); ++k) {
     const int32_t n = p.stall_stream ? 0 : job.tiles();
     if (n > 0) next.load(p, job, 0);
@@ -420,30 +394,26 @@ __device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint
       rows = next;
       rows.check(p);
       if (j + 1 < n) next.load(p, job, j + 1);
-      if (T > 0) ok = buffer(&ms->rope_empty, T - 1);
+      if (T > 0) ok = warp_wait_on(&ms->rope_empty, T - 1, ms, p.err);
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < kRopeRows; ++i)
         cp_async_16(rope_at + i * (kCopyThreads / 4) * 64, rope + static_cast<int64_t>(rows.rope[i]) * kQkDim);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      ++copies.issued;
+      cp_async_arrive(smem_u32(&ms->rope_full));
 #pragma unroll 1
       for (int c = 0; c < kPanels; ++c) {
         const uint32_t at = kPanels * (T & 1) + c;
-        if (T > 1) ok = buffer(&ms->key_empty[at], (T >> 1) - 1);
+        if (T > 1) ok = warp_wait_on(&ms->key_empty[at], (T >> 1) - 1, ms, p.err);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < kLatentRows; ++i)
           cp_async_16(latent_at + at * kPanelBytes + i * (kCopyThreads / 8) * 128,
                       latent + static_cast<int64_t>(rows.latent[i]) * kQkDim + 128 * c);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        ++copies.issued;
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        while (copies.done + 2 < copies.issued) copies.hand_over(ms);
+        cp_async_arrive(smem_u32(&ms->key_full[at]));
       }
     }
-    copies.finish(ms);  // (the next job may be far off)
   }
+  cp_async_wait_all();  // (nothing lands behind the block's end)
 }
 
 // ------------------------------------------------------------ MMA issuers (a warp each, an elected lane issues)
@@ -489,6 +459,7 @@ __device__ __forceinline__ void run_scores(const SharedParams& p, Misc* ms, uint
       }
       ok = (T < 2 || on(&ms->s_free[T & 1], (T >> 1) - 1)) && on(&ms->rope_full, T) && (j > 0 || on(&ms->q_full, jobs));
       if (!ok) break;
+      if (kPaged) fence_proxy_async_smem();  // the copies' writes, observed above, before the products' reads
       tc_fence_after();
       if (elect_one()) {
         umma_f8(d, rope_k, q_rope, kIdescQK, 0);
@@ -500,6 +471,7 @@ __device__ __forceinline__ void run_scores(const SharedParams& p, Misc* ms, uint
       for (int c = 0; c < kPanels; ++c) {
         ok = ok && (landed || on(&ms->key_full[first + c], T >> 1));
         if (!ok) break;
+        if (kPaged && !landed) fence_proxy_async_smem();
         tc_fence_after();
         if (elect_one()) {
           const uint64_t a = key_k + (first + c) * kPanel, b = q_k + c * kPanel;
@@ -1032,10 +1004,10 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
       mbar_init(smem_u32(&ms->s_free[i]), kSoftmaxWarps);
     }
     for (int i = 0; i < 2 * kPanels; ++i) {
-      mbar_init(smem_u32(&ms->key_full[i]), kPaged ? kCopyWarps : 1);
+      mbar_init(smem_u32(&ms->key_full[i]), kPaged ? kCopyThreads : 1);
       mbar_init(smem_u32(&ms->key_empty[i]), 1);
     }
-    mbar_init(smem_u32(&ms->rope_full), kPaged ? kCopyWarps : 1);
+    mbar_init(smem_u32(&ms->rope_full), kPaged ? kCopyThreads : 1);
     mbar_init(smem_u32(&ms->rope_empty), 1);
     mbar_init(smem_u32(&ms->q_full), kSoftmaxWarps);
     mbar_init(smem_u32(&ms->q_empty), 1);
