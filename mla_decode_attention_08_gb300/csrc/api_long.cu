@@ -234,9 +234,10 @@ mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* m
     return MLA_ERR_INVALID_ARG;
   mla_status_t st = check_step_workspace(workspace, workspace_bytes);
   if (st != MLA_OK) return st;
-  int device = 0;
+  int device = 0, sms = 0;
   st = mla::device_ready(&device);
   if (st != MLA_OK) return st;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return MLA_ERR_CUDA;
   mla::BlockScoresParams p;
   p.q = static_cast<const uint16_t*>(q_bf16);
   p.means = static_cast<const uint16_t*>(means);
@@ -252,7 +253,7 @@ mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* m
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.page_size = page_size;
-  return launched(mla::launch_block_scores(p, stream));
+  return launched(mla::launch_block_scores(p, sms, stream));
 }
 
 mla_status_t mla_block_select(const float* scores, int64_t scores_stride, const int32_t* block_table,

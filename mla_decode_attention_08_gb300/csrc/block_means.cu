@@ -3,8 +3,10 @@
 // Of the new tokens' slots, in order, one ends its page when the next slot is not the
 // row behind it or lies on another page; the page then holds the rows from its first
 // one up to that slot.  A block walks every gridDim-th token, finds the ends among them
-// and averages their pages: a thread 16 bytes of every eighth (bf16: fourth) row, in
-// float32, then the eight sums of a dim through shared memory.
+// and averages their pages in float32, one with all of its threads (16 bytes of every
+// eighth row each, bf16 every fourth; then the sums of a dim through shared memory), or
+// two or four side by side where it has more.  Bound by the trips to memory, slots and
+// then rows, and by the blocks that have the most pages.
 #include <cuda_fp16.h>
 
 #include "kernels.h"
@@ -16,7 +18,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 288;
-constexpr int kInFlight = 8;  // rows loaded together by a thread
+constexpr int kBatch = 8;  // rows of a thread loaded together
 
 // 16 bytes of a cache row, added to `sum`.
 template <bool kE4m3>
@@ -66,38 +68,46 @@ __global__ void __launch_bounds__(kThreads) block_means_kernel(const BlockMeansP
     }
     __syncthreads();
     const int32_t n = num_ends;
-    for (int32_t e = 0; e < n; ++e) {
-      const int32_t slot = ends[e], page = slot / p.page_size;
-      const int32_t rows = slot - page * p.page_size + 1;
-      const uint8_t* src = p.cache + static_cast<int64_t>(page) * p.page_size * kRowBytes + piece * 16;
+    // Teams of threads, a page each.
+    const int teams = n >= 3 ? 4 : n < 1 ? 1 : n, apart = kGroups / teams;  // (rows of a thread lie `apart`)
+    const int team = group / apart;
+    for (int32_t e0 = 0; e0 < n; e0 += teams) {
       float sum[kDims] = {};
-      for (int32_t r0 = group; r0 < rows; r0 += kGroups * kInFlight) {
-        uint4 v[kInFlight];
+      if (e0 + team < n) {
+        const int32_t slot = ends[e0 + team], page = slot / p.page_size;
+        const int32_t rows = slot - page * p.page_size + 1;
+        const int64_t first = static_cast<int64_t>(page) * p.page_size;
+        const uint8_t* src = p.cache + first * kRowBytes + piece * 16;
+        for (int32_t r0 = group % apart; r0 < rows; r0 += kBatch * apart) {
+          uint4 v[kBatch];
 #pragma unroll
-        for (int i = 0; i < kInFlight; ++i) {
-          const int32_t r = r0 + i * kGroups;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows && MLA_DCHECK(static_cast<int64_t>(page) * p.page_size + r < p.kv_rows, p.err))
-            v[i] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(r) * kRowBytes);
+          for (int i = 0; i < kBatch; ++i) {
+            const int32_t r = r0 + i * apart;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows && MLA_DCHECK(first + r < p.kv_rows, p.err))
+              v[i] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(r) * kRowBytes));
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) add_piece<kE4m3>(v[i], sum);
         }
-#pragma unroll
-        for (int i = 0; i < kInFlight; ++i) add_piece<kE4m3>(v[i], sum);
       }
 #pragma unroll
       for (int i = 0; i < kDims; i += 4)
         *reinterpret_cast<float4*>(&part[group][piece * kDims + i]) = make_float4(sum[i], sum[i + 1], sum[i + 2], sum[i + 3]);
       __syncthreads();
-      float x = 0.0f, y = 0.0f;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float2 v = *reinterpret_cast<const float2*>(&part[g][2 * tid]);
-        x += v.x;
-        y += v.y;
+      for (int u = 0; u < teams && e0 + u < n; ++u) {
+        float x = 0.0f, y = 0.0f;
+        for (int i = u * apart; i < (u + 1) * apart; ++i) {
+          const float2 w = *reinterpret_cast<const float2*>(&part[i][2 * tid]);
+          x += w.x;
+          y += w.y;
+        }
+        const int32_t slot = ends[e0 + u], page = slot / p.page_size;
+        const float count = static_cast<float>(slot - page * p.page_size + 1);
+        uint32_t packed;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed) : "f"(y / count * scale), "f"(x / count * scale));
+        reinterpret_cast<uint32_t*>(p.means + static_cast<int64_t>(page) * kQkDim)[tid] = packed;
       }
-      const float count = static_cast<float>(rows);
-      uint32_t packed;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed) : "f"(y / count * scale), "f"(x / count * scale));
-      reinterpret_cast<uint32_t*>(p.means + static_cast<int64_t>(page) * kQkDim)[tid] = packed;
       __syncthreads();  // (part is written again)
     }
   }

@@ -8,7 +8,8 @@
 // registers: a lane's 16 bytes of a page are 8 neighbouring dims, which stand for the
 // dims that two products expect there; the queries, in shared memory, are read in the
 // same order, so the sums are over the same pairs.  At 16 rows a product this is no work
-// for tcgen05, whose tiles have 128.
+// for tcgen05, whose tiles have 128.  Six products' operands are under way at a time, across
+// the groups of 16 pages that a warp works through.
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -20,7 +21,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpPages = 16;                       // two columns' worth of 8
-constexpr int kBlockPages = kWarps * kWarpPages;
+constexpr int kMaxGroups = 4;                        // of 16 pages, of a warp
 constexpr int kChunks = kQkDim / 32;                 // of 32 dims: two products
 constexpr int kAhead = 6;                            // chunks loaded together
 static_assert(kChunks % kAhead == 0, "whole groups of chunks");
@@ -43,11 +44,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // kTokens: query tokens that are scored together; rows of more take the means again.
 template <int kTokens>
-__global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScoresParams p) {
+__global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScoresParams p, int32_t groups) {
   extern __shared__ __align__(16) uint8_t sq[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, col = lane >> 2;
   const int32_t b = blockIdx.y;
-  const int32_t first = static_cast<int32_t>(blockIdx.x) * kBlockPages + warp * kWarpPages;
+  const int32_t block0 = static_cast<int32_t>(blockIdx.x) * kWarps * kWarpPages * groups;  // the block's first page
+  const int32_t first = block0 + warp * kWarpPages * groups;                               // and the warp's
   pdl_wait_primary();
   pdl_launch_dependents();
   const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
@@ -60,30 +62,32 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScore
   const int32_t n = bad_q || bad_k ? 0 : static_cast<int32_t>(pages);
   const int32_t tokens = bad_q ? 0 : qe - qs;
   float* out = p.scores + static_cast<int64_t>(b) * p.scores_stride;
-  if (static_cast<int32_t>(blockIdx.x) * kBlockPages >= n || tokens == 0) {  // (the same for the whole block)
-    const int32_t j = first + lane;
-    if (lane < kWarpPages && j < p.max_pages) out[j] = -INFINITY;
+  if (block0 >= n || tokens == 0) {  // (the same for the whole block)
+    for (int32_t j = block0 + tid; j < min(p.max_pages, block0 + kWarps * kWarpPages * groups); j += kThreads) out[j] = -INFINITY;
     return;
   }
 
-  // The pages of this lane's column in either half, and their rows' pieces.
-  const uint8_t* src[2];
-  bool here[2];
+  // The pages of this lane's column, in either half of each group; -1 where there is none.
+  int32_t page[kMaxGroups][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int32_t j = first + 8 * i + col;
-    int32_t id = j < n ? __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + j) : 0;
-    here[i] = j < n;
-    if (id < 0 || id >= p.num_pages) {
-      atomicOr(p.err, MLA_DERR_KV_INDEX);
-      here[i] = false;
-      id = 0;
+  for (int u = 0; u < kMaxGroups; ++u)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int32_t j = first + kWarpPages * u + 8 * i + col;
+      const bool here = u < groups && j < n;
+      page[u][i] = here ? __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + j) : -1;
+      if (here && (page[u][i] < 0 || page[u][i] >= p.num_pages)) {
+        atomicOr(p.err, MLA_DERR_KV_INDEX);
+        page[u][i] = -1;
+      }
     }
-    src[i] = reinterpret_cast<const uint8_t*>(p.means) + static_cast<int64_t>(id) * (2 * kQkDim) + 16 * quad;
-  }
-  float best[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) best[i][0] = best[i][1] = -INFINITY;
+  const uint8_t* means = reinterpret_cast<const uint8_t*>(p.means) + 16 * quad;
+  auto load = [&](int32_t id, int c) {
+    return id >= 0 ? __ldg(reinterpret_cast<const uint4*>(means + static_cast<int64_t>(id) * (2 * kQkDim) + 64 * c))
+                   : make_uint4(0, 0, 0, 0);
+  };
+  // (a warp behind the row's pages only brings its share of the queries)
+  const int32_t live = min(groups, max(0, (n - first + kWarpPages - 1) / kWarpPages));
 
   for (int32_t t0 = 0; t0 < tokens; t0 += kTokens) {
     const int32_t here_tokens = min(kTokens, tokens - t0);
@@ -94,74 +98,88 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScore
       const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(qs + t0) * kNumHeads + row) * kQkDim);
       cp_async_16(smem_u32(sq + row * kQStride + 16 * at), q + at);
     }
-    float acc[kTokens][2][4] = {};
     uint4 v[2][kAhead];
 #pragma unroll
     for (int c = 0; c < kAhead; ++c)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[i][c] = here[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + 64 * c)) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 2; ++i) v[i][c] = load(page[0][i], c);
     cp_async_wait_all();
     __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMaxGroups; ++u) {
+      if (u >= live) break;
+      float acc[kTokens][2][4] = {};
 #pragma unroll 1
-    for (int c0 = 0; c0 < kChunks; c0 += kAhead) {
+      for (int c0 = 0; c0 < kChunks; c0 += kAhead) {
+        // the chunks that follow: this group's, or the next one's first
+        const bool last = c0 + kAhead == kChunks;
+        const int32_t after = last ? 0 : c0 + kAhead;
+        int32_t from[2];
 #pragma unroll
-      for (int c = 0; c < kAhead; ++c) {
-        const uint4 v0 = v[0][c], v1 = v[1][c];
-        if (c0 + kAhead < kChunks) {
+        for (int i = 0; i < 2; ++i) from[i] = !last ? page[u][i] : u + 1 < kMaxGroups && u + 1 < live ? page[u + 1 < kMaxGroups ? u + 1 : u][i] : -1;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            v[i][c] = here[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + 64 * (c0 + kAhead + c))) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < kAhead; ++c) {
+          const uint4 v0 = v[0][c], v1 = v[1][c];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) v[i][c] = load(from[i], after + c);
+#pragma unroll
+          for (int t = 0; t < kTokens; ++t) {
+            if (t >= here_tokens) break;
+            const uint8_t* q = sq + t * kQTokenBytes + col * kQStride + 64 * (c0 + c) + 16 * quad;
+            const uint4 lo = *reinterpret_cast<const uint4*>(q), hi = *reinterpret_cast<const uint4*>(q + 8 * kQStride);
+            mma_16816(acc[t][0], lo.x, hi.x, lo.y, hi.y, v0.x, v0.y);
+            mma_16816(acc[t][1], lo.x, hi.x, lo.y, hi.y, v1.x, v1.y);
+            mma_16816(acc[t][0], lo.z, hi.z, lo.w, hi.w, v0.z, v0.w);
+            mma_16816(acc[t][1], lo.z, hi.z, lo.w, hi.w, v1.z, v1.w);
+          }
         }
+      }
+      // Over the tokens, the lane's two heads of each page, and the heads: lanes with the same
+      // quad hold the same two pages.
+      float best[2][2];
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
-          if (t >= here_tokens) break;
-          const uint8_t* q = sq + t * kQTokenBytes + col * kQStride + 64 * (c0 + c) + 16 * quad;
-          const uint4 lo = *reinterpret_cast<const uint4*>(q), hi = *reinterpret_cast<const uint4*>(q + 8 * kQStride);
-          mma_16816(acc[t][0], lo.x, hi.x, lo.y, hi.y, v0.x, v0.y);
-          mma_16816(acc[t][1], lo.x, hi.x, lo.y, hi.y, v1.x, v1.y);
-          mma_16816(acc[t][0], lo.z, hi.z, lo.w, hi.w, v0.z, v0.w);
-          mma_16816(acc[t][1], lo.z, hi.z, lo.w, hi.w, v1.z, v1.w);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < kTokens; ++t)
+            if (t < here_tokens) x = max_nan(x, max_nan(acc[t][i][e], acc[t][i][2 + e]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, d));
+          best[i][e] = x;
+        }
+      // Column 2 quad + e is the page of the lanes whose col is that; they know whether it counts.
+      uint32_t valid[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) valid[i] = __ballot_sync(0xffffffffu, page[u][i] >= 0);
+      if (col < 2) {  // lanes 0-3 the first half, 4-7 the second
+        const int i = col;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = 2 * quad + e;
+          const int32_t j = first + kWarpPages * u + 8 * i + c;
+          const bool counts = ((i ? valid[1] : valid[0]) >> (4 * c)) & 1;
+          float x = counts ? (i ? best[1][e] : best[0][e]) * (1.0f / 24.0f) : -INFINITY;
+          if (j < p.max_pages) out[j] = t0 > 0 ? max_nan(x, out[j]) : x;  // (the lane's own, of the tokens before)
         }
       }
     }
-#pragma unroll
-    for (int t = 0; t < kTokens; ++t) {
-      if (t >= here_tokens) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        best[i][0] = max_nan(best[i][0], max_nan(acc[t][i][0], acc[t][i][2]));
-        best[i][1] = max_nan(best[i][1], max_nan(acc[t][i][1], acc[t][i][3]));
-      }
-    }
   }
-  // Over the heads: lanes with the same quad hold the same two pages.
-#pragma unroll
-  for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) best[i][e] = max_nan(best[i][e], __shfl_xor_sync(0xffffffffu, best[i][e], d));
-  // Column 2 quad + e is the page of the lanes whose col is that; their `here` says whether it counts.
-  uint32_t valid[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) valid[i] = __ballot_sync(0xffffffffu, here[i]);
-  if (col < 2) {  // lanes 0-3 the first half, 4-7 the second
-    const int i = col;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = 2 * quad + e;
-      const int32_t j = first + 8 * i + c;
-      const bool counts = ((i ? valid[1] : valid[0]) >> (4 * c)) & 1;
-      const float best_e = i ? best[1][e] : best[0][e];
-      if (j < p.max_pages) out[j] = counts ? best_e * (1.0f / 24.0f) : -INFINITY;
-    }
-  }
+  // behind the row's pages
+  for (int32_t j = first + kWarpPages * live + lane; j < min(p.max_pages, first + kWarpPages * groups); j += 32) out[j] = -INFINITY;
 }
 
+// A warp's groups of 16 pages: one where the warps then fit the GPU at once (16 an SM), up to
+// four where they would follow one another, since a warp's start is two trips to memory.
 template <int kTokens>
-cudaError_t launch_tokens(const BlockScoresParams& p, cudaStream_t stream) {
+cudaError_t launch_tokens(const BlockScoresParams& p, int32_t num_sms, cudaStream_t stream) {
+  const int64_t warps = static_cast<int64_t>(p.batch) * ((p.max_pages + kWarpPages - 1) / kWarpPages);
+  int64_t groups = warps / (16 * static_cast<int64_t>(num_sms));
+  groups = groups < 1 ? 1 : groups > kMaxGroups ? kMaxGroups : groups;
+  const int64_t pages = kWarps * kWarpPages * groups;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.max_pages + kBlockPages - 1) / kBlockPages), static_cast<unsigned>(p.batch));
+  cfg.gridDim = dim3(static_cast<unsigned>((p.max_pages + pages - 1) / pages), static_cast<unsigned>(p.batch));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kTokens * kQTokenBytes;
   cfg.stream = stream;
@@ -170,7 +188,7 @@ cudaError_t launch_tokens(const BlockScoresParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_scores_kernel<kTokens>, p);
+  return cudaLaunchKernelEx(&cfg, block_scores_kernel<kTokens>, p, static_cast<int32_t>(groups));
 }
 
 }  // namespace
@@ -183,10 +201,10 @@ cudaError_t block_scores_prepare() {
 
 // The rows' tokens are on the GPU; a row has total_q / batch of them as a rule, and any
 // number is computed.
-cudaError_t launch_block_scores(const BlockScoresParams& p, cudaStream_t stream) {
-  if (p.total_q <= p.batch) return launch_tokens<1>(p, stream);
-  if (p.total_q <= 2 * static_cast<int64_t>(p.batch)) return launch_tokens<2>(p, stream);
-  return launch_tokens<4>(p, stream);
+cudaError_t launch_block_scores(const BlockScoresParams& p, int32_t num_sms, cudaStream_t stream) {
+  if (p.total_q <= p.batch) return launch_tokens<1>(p, num_sms, stream);
+  if (p.total_q <= 2 * static_cast<int64_t>(p.batch)) return launch_tokens<2>(p, num_sms, stream);
+  return launch_tokens<4>(p, num_sms, stream);
 }
 
 }  // namespace mla

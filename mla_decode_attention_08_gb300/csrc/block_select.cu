@@ -4,9 +4,12 @@
 // rest those with the highest scores, the lower page where two are alike.  The last page
 // is always among them, so the number of chosen tokens follows from the lengths alone:
 // every block forms the prefix sums over all rows for itself, and one launch does the
-// step.  A block then finds its row's threshold, the score of the last page that is
-// taken, by radix selection (four digits of 8 bits of the scores as ordered integers,
-// counted in shared memory), walks the pages in order and writes them out.
+// step.  A block holds its row's scores in registers, consecutive pages a thread, and finds
+// the ones that are taken by their place in 256 equal steps between the lowest and the highest:
+// the steps above the one in which the last page falls are taken whole, and in that one the
+// pages are ranked against each other.  Where that leaves many (scores far apart, or alike),
+// and in rows of more pages than registers, the last taken score is found bit by bit, each a
+// count over the block.  Bound by the steps' latency.
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -16,6 +19,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kSteps = 256;   // of equal width between the lowest and the highest score
+constexpr int kListed = 256;  // pages that are ranked against each other
 
 // Scores as integers in the same order; both zeros are alike, and a NaN counts as the
 // highest, so that it is not passed over.
@@ -23,6 +28,11 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   if (x != x) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(x + 0.0f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+constexpr uint32_t kMinusInf = 0x007FFFFFu, kPlusInf = 0xFF800000u;  // ordered(-inf), ordered(+inf)
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
 struct RowCount {
@@ -42,43 +52,67 @@ __device__ __forceinline__ RowCount count_row(const BlockSelectParams& p, int32_
   return r;
 }
 
+// The sum over the block's threads before this one, and over all (in *all).  (`sums`: read by
+// the calls before, which a barrier has ended.)
+__device__ __forceinline__ int32_t sum_before(int32_t v, int32_t* sums, int32_t* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t incl = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += u;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int32_t before = incl - v;
+  *all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sums[w];
+    *all += sums[w];
+  }
+  return before;
+}
+
+// kHeld: scores that a thread holds; with 0 they are read anew whenever they are needed.
+template <int kHeld>
 __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelectParams p) {
   extern __shared__ int32_t rows[];  // [blocks]: first cache row of each chosen page, or -1
-  __shared__ uint32_t counts[256];
   __shared__ int64_t sums[kWarps], totals[kWarps];
-  __shared__ int32_t warp_ties[kWarps], warp_taken[kWarps];
-  __shared__ uint32_t digit, above;
+  __shared__ int32_t scan[2][kWarps];
+  __shared__ int32_t counts[kSteps], listed;
+  __shared__ uint2 list[kListed];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t b = blockIdx.x;
   pdl_wait_primary();
   pdl_launch_dependents();
 
   // Tokens of the rows before this one, and of all rows.
-  int64_t before = 0, all = 0;
+  int64_t before = 0, total = 0;
   bool bad = false;
   for (int32_t r = tid; r < p.batch; r += kThreads) {
     const RowCount c = count_row(p, r);
-    all += c.tokens;
+    total += c.tokens;
     if (r < b) before += c.tokens;
     bad = bad || c.bad;
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, d);
-    all += __shfl_xor_sync(0xffffffffu, all, d);
+    total += __shfl_xor_sync(0xffffffffu, total, d);
   }
   if (lane == 0) {
     sums[warp] = before;
-    totals[warp] = all;
+    totals[warp] = total;
   }
   bad = __syncthreads_or(bad);
-  before = all = 0;
+  before = total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     before += sums[w];
-    all += totals[w];
+    total += totals[w];
   }
-  const bool full = all > p.indices_len;
+  const bool full = total > p.indices_len;
   const RowCount row = count_row(p, b);
   int32_t* chosen = p.chosen == nullptr ? nullptr : p.chosen + static_cast<int64_t>(b) * p.blocks;
   if (bad || full) {  // the whole step is emptied
@@ -90,114 +124,202 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
     return;
   }
   if (tid == 0) p.sel_indptr[b] = static_cast<int32_t>(before);
-  if (tid == 0 && b == p.batch - 1) p.sel_indptr[p.batch] = static_cast<int32_t>(all);
+  if (tid == 0 && b == p.batch - 1) p.sel_indptr[p.batch] = static_cast<int32_t>(total);
   const float* scores = p.scores + static_cast<int64_t>(b) * p.scores_stride;
   const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.table_stride;
 
-  // The threshold: of the middle pages those above it are taken, and `ties` of those at it.
+  // This thread's pages, and those that are chosen by score.
+  const int32_t each = kHeld > 0 ? kHeld : (row.pages + kThreads - 1) / kThreads, first = min(row.pages, tid * each);
+  const int32_t last = min(row.pages, first + each);
   const int32_t lo = p.sink, hi = row.pages - p.recent;
-  uint32_t threshold = 0;
-  int32_t ties = 0;
   const bool choose = row.pages > p.blocks;
-  if (choose) {
-    uint32_t want = static_cast<uint32_t>(p.blocks - p.sink - p.recent);  // still to be found
-    if (want == 0) threshold = 0xFFFFFFFFu;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kThreads) counts[i] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int32_t j = lo + tid; j < hi; j += kThreads) {
-        const uint32_t key = ordered(scores[j]);
-        if ((key & mask) == threshold) atomicAdd(&counts[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      // The highest digit d for which the pages with a digit of d or more are enough.
-      if (warp == 0) {
-        uint32_t mine = 0;
+  uint32_t held[kHeld > 0 ? kHeld : 1];
+  if constexpr (kHeld > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mine += counts[8 * lane + i];
-        uint32_t higher = mine;  // of lanes above, inclusive
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t v = __shfl_down_sync(0xffffffffu, higher, d);
-          if (lane + d < 32) higher += v;
-        }
-        uint32_t past = higher - mine;
-        if (past < want && higher >= want) {
-          for (int i = 7; i >= 0; --i) {
-            const uint32_t c = counts[8 * lane + i];
-            if (past + c >= want) {
-              digit = 8 * lane + i;
-              above = past;
-              break;
-            }
-            past += c;
-          }
-        }
-      }
-      __syncthreads();
-      threshold |= digit << shift;
-      want -= above;
+    for (int i = 0; i < kHeld; ++i) {
+      const int32_t j = first + i;
+      held[i] = choose && j >= lo && j < hi ? ordered(scores[j]) : 0u;  // (0: no score's)
     }
-    ties = static_cast<int32_t>(want);
   }
+  // Calls `f(place, key)` for this thread's middle pages.
+  auto each_key = [&](auto f) {
+    if constexpr (kHeld > 0) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (held[i] != 0) f(first + i, held[i]);
+    } else {
+      for (int32_t j = max(first, lo); j < min(last, hi); ++j) f(j, ordered(scores[j]));
+    }
+  };
+  // Pages with a key above `threshold` are taken, and `ties` of those at it; or, where the
+  // steps decide, the ones marked in `mine`.
+  uint32_t threshold = 0, marks = 0;
+  int32_t ties = 0;
+  bool by_steps = false;
+  const int32_t want = p.blocks - p.sink - p.recent;
+  if (kHeld > 0 && choose && want > 0) {
+    // Between the lowest and the highest finite score; what is not finite falls on the ends.
+    uint32_t low = 0xFFFFFFFFu, high = 0;
+    each_key([&](int32_t, uint32_t key) {
+      if (key > kMinusInf && key < kPlusInf) {
+        low = min(low, key);
+        high = max(high, key);
+      }
+    });
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) {
+      scan[0][warp] = static_cast<int32_t>(low);
+      scan[1][warp] = static_cast<int32_t>(high);
+    }
+    if (tid < kSteps) counts[tid] = 0;
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    low = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(scan[0][lane % kWarps]));
+    high = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(scan[1][lane % kWarps]));
+    const float least = score_of(low), width = score_of(high) - least;
+    const float by = width > 0.0f ? (kSteps - 1) / width : 0.0f;
+    // (never falls as the score rises; a width that overflows puts all in one step)
+    auto step_of = [&](uint32_t key) {
+      const float at = key <= kMinusInf ? 0.0f : key >= kPlusInf ? kSteps - 1.0f : (score_of(key) - least) * by;
+      return static_cast<int>(fminf(at, kSteps - 1.0f));
+    };
+    each_key([&](int32_t, uint32_t key) { atomicAdd(&counts[step_of(key)], 1); });
+    __syncthreads();
+    // The highest step with which there are enough (every warp for itself): lane l has the
+    // steps 8 l .. 8 l + 7.
+    int32_t c[8], own = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) own += c[i] = counts[8 * lane + i];
+    int32_t from = own;  // in this lane's steps and above
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t v = __shfl_down_sync(0xffffffffu, from, d);
+      if (lane + d < 32) from += v;
+    }
+    int32_t above = from - own, step = -1, inside = 0;
+    if (above < want && from >= want) {
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        if (step >= 0) continue;
+        if (above + c[i] >= want) {
+          step = 8 * lane + i;
+          inside = c[i];
+        } else {
+          above += c[i];
+        }
+      }
+    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, step >= 0)) - 1;
+    step = __shfl_sync(0xffffffffu, step, who);
+    above = __shfl_sync(0xffffffffu, above, who);
+    inside = __shfl_sync(0xffffffffu, inside, who);
+    by_steps = inside <= kListed;
+    if (by_steps) {
+      each_key([&](int32_t j, uint32_t key) {
+        const int at = step_of(key);
+        if (at > step) marks |= 1u << (j - first);
+        if (at == step) list[atomicAdd(&listed, 1)] = make_uint2(key, static_cast<uint32_t>(j));
+      });
+      __syncthreads();
+      each_key([&](int32_t j, uint32_t key) {
+        if (step_of(key) != step) return;
+        int32_t rank = above;
+        for (int i = 0; i < inside; ++i) {
+          const uint2 other = list[i];
+          rank += other.x > key || (other.x == key && other.y < static_cast<uint32_t>(j));
+        }
+        if (rank < want) marks |= 1u << (j - first);
+      });
+    }
+  }
+  if (choose && !by_steps) {
+    int32_t above = 0;  // pages above threshold | what is still open
+    bool exact = want == 0;
+    if (exact) threshold = 0xFFFFFFFFu;
+    __syncthreads();  // (scan is read)
+    for (uint32_t bit = 0x80000000u; bit != 0 && !exact; bit >>= 1) {
+      int32_t mine = 0;
+      each_key([&](int32_t, uint32_t key) { mine += key >= (threshold | bit); });
+      const int32_t sum = __reduce_add_sync(0xffffffffu, mine);
+      int32_t* part = scan[bit & 0x55555555u ? 0 : 1];  // (alternating: the others may still be read)
+      if (lane == 0) part[warp] = sum;
+      __syncthreads();
+      int32_t enough = lane < kWarps ? part[lane] : 0;
+      enough = __reduce_add_sync(0xffffffffu, enough);
+      if (enough >= want) threshold |= bit;
+      else above = enough;
+      if (enough == want) {  // these are the ones
+        exact = true;
+        threshold -= 1;  // (a key above it is one of them)
+      }
+    }
+    if (!exact) ties = want - above;
+  }
+  __syncthreads();  // (scan is read)
 
   // The pages in order: a page's place among the chosen is the number before it.
-  int32_t done_ties = 0, done = 0;
-  for (int32_t j0 = 0; j0 < row.pages; j0 += kThreads) {
-    const int32_t j = j0 + tid;
-    const bool in = j < row.pages;
-    bool take = in, tie = false;
-    if (choose && in && j >= lo && j < hi) {
-      const uint32_t key = ordered(scores[j]);
-      tie = ties > 0 && key == threshold;
-      take = key > threshold;
-    }
-    const uint32_t tie_mask = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) warp_ties[warp] = __popc(tie_mask);
-    __syncthreads();
-    int32_t rank = done_ties + __popc(tie_mask & ((1u << lane) - 1u));
+  auto is_middle = [&](int32_t j) { return choose && j >= lo && j < hi; };
+  int32_t mine = 0, all = 0;
+  if (ties > 0) each_key([&](int32_t, uint32_t key) { mine += key == threshold; });
+  const int32_t rank = ties > 0 ? sum_before(mine, scan[0], &all) : 0;
+  // (a tie is taken while its rank among them is below `ties`)
+  int32_t taken = 0, tie = rank;
+  auto walk = [&](auto f) {
+    auto one = [&](int32_t j, uint32_t key) {
+      bool take = !is_middle(j);
+      if (!take) take = by_steps ? marks >> (j - first) & 1 : key > threshold || (ties > 0 && key == threshold && tie++ < ties);
+      if (take) f(j);
+    };
+    if constexpr (kHeld > 0) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) rank += warp_ties[w];
-      done_ties += warp_ties[w];
+      for (int i = 0; i < kHeld; ++i)
+        if (first + i < last) one(first + i, held[i]);
+    } else {
+      for (int32_t j = first; j < last; ++j) one(j, is_middle(j) ? ordered(scores[j]) : 0u);
     }
-    if (tie && rank < ties) take = true;
-    const uint32_t mask = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) warp_taken[warp] = __popc(mask);
-    __syncthreads();
-    int32_t place = done + __popc(mask & ((1u << lane) - 1u));
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) place += warp_taken[w];
-      done += warp_taken[w];
-    }
-    if (take && place < p.blocks) {
+  };
+  walk([&](int32_t) { ++taken; });
+  int32_t place = sum_before(taken, scan[1], &all);
+  tie = rank;
+  walk([&](int32_t j) {
+    if (place < p.blocks) {
       const int32_t id = table[j];
       const bool ok = id >= 0 && id < p.num_pages;
       if (!ok) atomicOr(p.err, MLA_DERR_KV_INDEX);
       rows[place] = ok ? id * p.page_size : -1;
       if (chosen != nullptr) chosen[place] = j;
     }
-  }
+    ++place;
+  });
   if (chosen != nullptr)
     for (int32_t i = row.taken + tid; i < p.blocks; i += kThreads) chosen[i] = -1;
   __syncthreads();
   int32_t* out = p.sel_indices + before;
+  const bool shifts = (p.page_size & (p.page_size - 1)) == 0;
+  const int shift = __ffs(p.page_size) - 1;
   for (int32_t t = tid; t < row.tokens; t += kThreads) {
-    const int32_t at = t / p.page_size, first = rows[at];
-    out[t] = first < 0 ? -1 : first + (t - at * p.page_size);
+    const int32_t at = shifts ? t >> shift : t / p.page_size, start = rows[at];
+    out[t] = start < 0 ? -1 : start + (t - at * p.page_size);
   }
 }
 
 }  // namespace
 
 cudaError_t block_select_prepare() {
-  return cudaFuncSetAttribute(block_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MLA_SELECT_MAX_BLOCKS * 4);
+  for (auto kernel : {block_select_kernel<4>, block_select_kernel<16>, block_select_kernel<0>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MLA_SELECT_MAX_BLOCKS * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream) {
-  return launch_dependent(block_select_kernel, static_cast<unsigned>(p.batch), kThreads, static_cast<size_t>(p.blocks) * 4, stream, p);
+  const unsigned grid = static_cast<unsigned>(p.batch);
+  const size_t smem = static_cast<size_t>(p.blocks) * 4;
+  if (p.max_pages <= 4 * kThreads) return launch_dependent(block_select_kernel<4>, grid, kThreads, smem, stream, p);
+  if (p.max_pages <= 16 * kThreads) return launch_dependent(block_select_kernel<16>, grid, kThreads, smem, stream, p);
+  return launch_dependent(block_select_kernel<0>, grid, kThreads, smem, stream, p);
 }
 
 }  // namespace mla

@@ -189,7 +189,7 @@ struct BlockScoresParams {
   int32_t batch, total_q, max_pages, num_pages, page_size;
 };
 cudaError_t block_scores_prepare();
-cudaError_t launch_block_scores(const BlockScoresParams& p, cudaStream_t stream);
+cudaError_t launch_block_scores(const BlockScoresParams& p, int32_t num_sms, cudaStream_t stream);
 
 struct BlockSelectParams {
   const float* scores;
