@@ -186,7 +186,7 @@ mla_status_t prepare_device(int* device_out) {
     return MLA_ERR_UNSUPPORTED;
   if (mla::stage1_prepare(device) != cudaSuccess || mla::page_map_prepare() != cudaSuccess ||
       mla::prefill_prepare() != cudaSuccess || mla::shared_prepare() != cudaSuccess ||
-      mla::block_scores_prepare() != cudaSuccess || mla::block_select_prepare() != cudaSuccess)
+      mla::block_means_prepare() != cudaSuccess || mla::block_scores_prepare() != cudaSuccess || mla::block_select_prepare() != cudaSuccess)
     return MLA_ERR_CUDA;
   ready[device].store(1, std::memory_order_release);
   return MLA_OK;

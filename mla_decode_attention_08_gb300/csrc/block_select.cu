@@ -9,7 +9,8 @@
 // the steps above the one in which the last page falls are taken whole, and in that one the
 // pages are ranked against each other.  Where that leaves many (scores far apart, or alike),
 // and in rows of more pages than registers, the last taken score is found bit by bit, each a
-// count over the block.  Bound by the steps' latency.
+// count over the block.  Bound by the steps' latency, so scores and table entries are on their
+// way before the row's length is known.
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -20,7 +21,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSteps = 256;   // of equal width between the lowest and the highest score
-constexpr int kListed = 256;  // pages that are ranked against each other
+constexpr int kListed = 256;  // pages that are ranked against each other, at most
 
 // Scores as integers in the same order; both zeros are alike, and a NaN counts as the
 // highest, so that it is not passed over.
@@ -86,6 +87,18 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
   const int32_t b = blockIdx.x;
   pdl_wait_primary();
   pdl_launch_dependents();
+  const float* scores = p.scores + static_cast<int64_t>(b) * p.scores_stride;
+  const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.table_stride;
+  float score[kHeld > 0 ? kHeld : 1];
+  int32_t entry[kHeld > 0 ? kHeld : 1];
+  if constexpr (kHeld > 0) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int32_t j = tid * kHeld + i;
+      score[i] = j < p.max_pages ? scores[j] : 0.0f;
+      entry[i] = j < p.max_pages ? table[j] : -1;
+    }
+  }
 
   // Tokens of the rows before this one, and of all rows.
   int64_t before = 0, total = 0;
@@ -125,9 +138,6 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
   }
   if (tid == 0) p.sel_indptr[b] = static_cast<int32_t>(before);
   if (tid == 0 && b == p.batch - 1) p.sel_indptr[p.batch] = static_cast<int32_t>(total);
-  const float* scores = p.scores + static_cast<int64_t>(b) * p.scores_stride;
-  const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.table_stride;
-
   // This thread's pages, and those that are chosen by score.
   const int32_t each = kHeld > 0 ? kHeld : (row.pages + kThreads - 1) / kThreads, first = min(row.pages, tid * each);
   const int32_t last = min(row.pages, first + each);
@@ -138,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
       const int32_t j = first + i;
-      held[i] = choose && j >= lo && j < hi ? ordered(scores[j]) : 0u;  // (0: no score's)
+      held[i] = choose && j >= lo && j < hi ? ordered(score[i]) : 0u;  // (0: no score's)
     }
   }
   // Calls `f(place, key)` for this thread's middle pages.
@@ -265,26 +275,27 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
   const int32_t rank = ties > 0 ? sum_before(mine, scan[0], &all) : 0;
   // (a tie is taken while its rank among them is below `ties`)
   int32_t taken = 0, tie = rank;
+  // Calls `f(page, table entry)` for this thread's pages that are taken.
   auto walk = [&](auto f) {
-    auto one = [&](int32_t j, uint32_t key) {
-      bool take = !is_middle(j);
-      if (!take) take = by_steps ? marks >> (j - first) & 1 : key > threshold || (ties > 0 && key == threshold && tie++ < ties);
-      if (take) f(j);
+    auto takes = [&](int32_t j, uint32_t key) {
+      if (!is_middle(j)) return true;
+      if (by_steps) return (marks >> (j - first) & 1) != 0;
+      return key > threshold || (ties > 0 && key == threshold && tie++ < ties);
     };
     if constexpr (kHeld > 0) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        if (first + i < last) one(first + i, held[i]);
+        if (first + i < last && takes(first + i, held[i])) f(first + i, entry[i]);
     } else {
-      for (int32_t j = first; j < last; ++j) one(j, is_middle(j) ? ordered(scores[j]) : 0u);
+      for (int32_t j = first; j < last; ++j)
+        if (takes(j, is_middle(j) ? ordered(scores[j]) : 0u)) f(j, table[j]);
     }
   };
-  walk([&](int32_t) { ++taken; });
+  walk([&](int32_t, int32_t) { ++taken; });
   int32_t place = sum_before(taken, scan[1], &all);
   tie = rank;
-  walk([&](int32_t j) {
+  walk([&](int32_t j, int32_t id) {
     if (place < p.blocks) {
-      const int32_t id = table[j];
       const bool ok = id >= 0 && id < p.num_pages;
       if (!ok) atomicOr(p.err, MLA_DERR_KV_INDEX);
       rows[place] = ok ? id * p.page_size : -1;
@@ -307,16 +318,18 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
 }  // namespace
 
 cudaError_t block_select_prepare() {
-  for (auto kernel : {block_select_kernel<4>, block_select_kernel<16>, block_select_kernel<0>}) {
+  for (auto kernel : {block_select_kernel<1>, block_select_kernel<4>, block_select_kernel<16>, block_select_kernel<0>}) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MLA_SELECT_MAX_BLOCKS * 4);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
+// Scores in registers where a row's pages fit them, as few a thread as do.
 cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.batch);
   const size_t smem = static_cast<size_t>(p.blocks) * 4;
+  if (p.max_pages <= kThreads) return launch_dependent(block_select_kernel<1>, grid, kThreads, smem, stream, p);
   if (p.max_pages <= 4 * kThreads) return launch_dependent(block_select_kernel<4>, grid, kThreads, smem, stream, p);
   if (p.max_pages <= 16 * kThreads) return launch_dependent(block_select_kernel<16>, grid, kThreads, smem, stream, p);
   return launch_dependent(block_select_kernel<0>, grid, kThreads, smem, stream, p);

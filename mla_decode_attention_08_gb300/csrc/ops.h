@@ -175,6 +175,7 @@ struct BlockMeansParams {
   int64_t num_tokens;
   int32_t page_size;
 };
+cudaError_t block_means_prepare();
 cudaError_t launch_block_means(const BlockMeansParams& p, bool e4m3, int32_t num_sms, cudaStream_t stream);
 
 struct BlockScoresParams {
