@@ -763,7 +763,9 @@ mla_status_t mla_shared_fwd_stall_stream(const void* q_bf16, const void* kv_fp8,
  *   means[page] = bf16(mean of cache rows page P .. s)        (float32 sums, rounded once)
  * The means of other pages are left alone.  That is the mean of what the page holds when a
  * row's new tokens stand one behind the other in `slots` and the row's tokens fill the page
- * from its first row on, as mla_page_map lays them out; negative slots are padding.
+ * from its first row on, as mla_page_map lays them out; negative slots are padding.  (Each page
+ * is to be ended once: of two different slots that end the same page in one call it is open which
+ * one's mean each dim gets.)
  *   kv_fp8     device e4m3fn codes [kv_rows][576] with kv_scale device float[1] (values code *
  *              *kv_scale), or kv_bf16 device bf16 [kv_rows][576]; 16-byte aligned.
  *   slots      device int32 [num_tokens] (num_tokens 0 launches nothing).
@@ -789,10 +791,12 @@ mla_status_t mla_block_means_bf16kv(const void* kv_bf16, int64_t kv_rows, const 
  *   block_table device int32, row b at block_table + b * table_stride, max_pages entries.
  *   qo_indptr, kv_indptr  device int32 [batch + 1]; batch 1 .. MLA_MAX_MAP_ROWS.
  *   scores      device float, row b at scores + b * scores_stride, max_pages entries.
- * Strides are in elements and at least max_pages.  A page id outside [0, num_pages) sets
- * MLA_DERR_KV_INDEX and scores -inf; a row outside total_q, or with a negative length or more
- * than max_pages pages, sets MLA_DERR_QO_INDPTR / MLA_DERR_KV_INDPTR and scores -inf throughout.
+ * max_pages is 1 .. MLA_MAX_ROW_PAGES; strides are in elements and at least max_pages.  A page
+ * id outside [0, num_pages) sets MLA_DERR_KV_INDEX and scores -inf; a row outside total_q, or
+ * with a negative length or more than max_pages pages, sets MLA_DERR_QO_INDPTR /
+ * MLA_DERR_KV_INDPTR and scores -inf throughout.
  */
+#define MLA_MAX_ROW_PAGES (1 << 30)
 mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* means, int32_t num_pages,
                               const int32_t* block_table, int64_t table_stride, int32_t max_pages,
                               const int32_t* qo_indptr, const int32_t* kv_indptr, int32_t batch,
@@ -801,7 +805,7 @@ mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* m
 
 /*
  * mla_block_select - the pages that each row attends, as the page table of mla_decode_fwd.
- * Row b (lengths and pages as in mla_block_scores) takes all of its n_b pages if n_b <= blocks;
+ * Row b (lengths, pages and limits as in mla_block_scores) takes all of its n_b pages if n_b <= blocks;
  * else `blocks` of them: the first `sink`, the last `recent`, and of the others those with the
  * highest scores, the lower page where scores are alike (both zeros are; a NaN is above all).
  *   chosen[b][i]  = the i-th page taken, in rising order, -1 behind the last (or chosen is NULL)

@@ -31,10 +31,12 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
 // for.  A block is one worker's, or the keys of one group's blocks are cut into k equal parts,
 // or all blocks' keys, one behind the other, into equal shares for all SMs, where a worker whose
 // share has the end of one block and the start of another does two jobs.  By the time that it
-// should take, in twentieths of a microsecond: a key tile 35, a job 100 (130 where it writes
-// the output), the second kernel 80 and 1 a part, and 1 more a part of a block; groups' keys on
-// average at 0.7 of the longest.  (Of 34 batches run with 6 to 20 cuts each, the one taken is up
-// to 14 % slower than the best, 1 % on average.)
+// should take, in twentieths of a microsecond: a key tile 35, a block's start and end 100, the
+// rest of a call 100, or 190 for that and a first part and its join, where each part costs 1 and
+// each part of the same block 2; groups' keys on average at 0.7 of the longest.  (Of 70 batches
+// run with 8 to 20 cuts each, the one taken is 3 % slower than the best on average, 17 % at
+// most: 4 short groups.  Blocks that are one worker's take up to 5 times the best's time where
+// they are few and long, equal shares 1.4 times where they are many and short.)
 struct Cut {
   int32_t workers, split, start;
 };
@@ -43,17 +45,18 @@ Cut cut_of(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms) {
   Cut best = {static_cast<int32_t>(blocks < sms ? (blocks > 0 ? blocks : 1) : sms), 0, 0};
   // (The second kernel looks for its tokens' groups, so thousands of them are not cut.)
   if (blocks == 0 || batch > 1024) return best;
-  int64_t least = (blocks + sms - 1) / sms * (130 + 35 * key_tiles);
-  auto take = [&](int64_t time, int64_t workers, int32_t start) {
+  int64_t least = (blocks + sms - 1) / sms * (100 + 35 * key_tiles) + 100;
+  auto take = [&](int64_t share, int64_t of_block, int64_t parts, int64_t workers, int32_t start) {
+    const int64_t time = 190 + 35 * share + 2 * of_block + parts;
     if (time >= least) return;
     least = time;
     best = Cut{static_cast<int32_t>(workers), 1, start};
   };
   if (batch == 1)
-    for (int64_t k = 2; k <= key_tiles && k * blocks <= sms; ++k)
-      take(180 + 35 * ((key_tiles + k - 1) / k) + k * blocks + k, k * blocks, 0);
-  const int64_t tiles = batch == 1 ? blocks * key_tiles : 7 * blocks * key_tiles / 10;
-  if (tiles >= sms) take(180 + 35 * ((tiles + kStartUnits * blocks + sms - 1) / sms) + sms + blocks, sms, kStartUnits);
+    for (int64_t k = 2; k <= key_tiles && k * blocks <= sms; ++k) take((key_tiles + k - 1) / k, k, k * blocks, k * blocks, 0);
+  const int64_t units = (batch == 1 ? blocks * key_tiles : 7 * blocks * key_tiles / 10) + kStartUnits * blocks;
+  const int64_t share = (units + sms - 1) / sms;
+  if (key_tiles > 0) take(share, key_tiles / share, (sms < units ? sms : units) + blocks, sms, kStartUnits);
   return best;
 }
 
@@ -135,7 +138,7 @@ mla_status_t run_shared(const void* q, const void* kv, const float* kv_scale, co
   p.start = plan->start;
   p.stall_stream = stall_stream ? 1 : 0;
   st = launched(mla::launch_shared(p, m, stream));
-  return st != MLA_OK || plan->split == 0 ? st : launched(mla::launch_shared_join(p, stream));
+  return st != MLA_OK || plan->split == 0 ? st : launched(mla::launch_shared_join(p, plan->num_sms, stream));
 }
 
 mla_status_t run_means(const void* cache, const float* kv_scale, bool e4m3, int64_t kv_rows,
@@ -224,7 +227,7 @@ mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* m
                               const int32_t* qo_indptr, const int32_t* kv_indptr, int32_t batch,
                               int32_t page_size, float* scores, int64_t scores_stride, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
-  if (batch < 1 || batch > MLA_MAX_MAP_ROWS || total_q < 0 || max_pages < 1 || num_pages < 1 || page_size < 1 ||
+  if (batch < 1 || batch > MLA_MAX_MAP_ROWS || total_q < 0 || max_pages < 1 || max_pages > MLA_MAX_ROW_PAGES || num_pages < 1 || page_size < 1 ||
       table_stride < max_pages || table_stride >= kMaxStride || scores_stride < max_pages ||
       scores_stride >= kMaxStride)
     return MLA_ERR_INVALID_ARG;
@@ -261,7 +264,7 @@ mla_status_t mla_block_select(const float* scores, int64_t scores_stride, const 
                               int32_t page_size, int32_t num_pages, int32_t blocks, int32_t sink, int32_t recent,
                               int32_t* sel_indptr, int32_t* sel_indices, int64_t sel_indices_len,
                               int32_t* chosen, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  if (batch < 1 || batch > MLA_MAX_MAP_ROWS || max_pages < 1 || page_size < 1 || num_pages < 1 ||
+  if (batch < 1 || batch > MLA_MAX_MAP_ROWS || max_pages < 1 || max_pages > MLA_MAX_ROW_PAGES || page_size < 1 || num_pages < 1 ||
       static_cast<int64_t>(page_size) * num_pages > INT32_MAX || table_stride < max_pages ||
       table_stride >= kMaxStride || scores_stride < max_pages || scores_stride >= kMaxStride || blocks < 1 ||
       blocks > MLA_SELECT_MAX_BLOCKS || sink < 0 || recent < 1 || sink > blocks - recent || sel_indices_len < 0 ||

@@ -162,7 +162,7 @@ constexpr int kSharedTokens = 4;  // query tokens of a job
 size_t shared_smem_bytes();
 cudaError_t shared_prepare();
 cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream);
-cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
+cudaError_t launch_shared_join(const SharedParams& p, int32_t num_sms, cudaStream_t stream);
 
 struct BlockMeansParams {
   const uint8_t* cache;      // e4m3 codes or bf16 rows

@@ -119,4 +119,36 @@ MLA_HD int32_t partial_slot(int32_t c, int32_t worker_t0, int32_t prefix_b) {
   return worker_t0 >= prefix_b ? 2 * c : 2 * c + 1;
 }
 
+// Equal shares of `all` units of work for `workers` workers (at most `all` of them, so that
+// none is empty): worker c has the units [begin(c), begin(c + 1)), and unit u is owner(u)'s.
+// (all below 2^50 and workers below 2^13, so the products fit 64 bits.)
+struct Shares {
+  int64_t all, workers;
+  MLA_HD int64_t begin(int64_t c) const { return c * all / workers; }
+  MLA_HD int64_t owner(int64_t u) const { return ((u + 1) * workers - 1) / all; }
+};
+
+// What a worker whose units end at `stop` has of a block of `tiles` key tiles (one unit each,
+// behind `start` units for the block's start, which begin at unit `begin`), from unit u of it on:
+// the key tiles [j0, j1).  A block without key tiles has one unit behind its start
+// and is whole where that unit is.
+struct SharedPiece {
+  int32_t j0, j1;
+  bool whole;
+};
+MLA_HD SharedPiece shared_piece(int64_t begin, int32_t tiles, int32_t start, int64_t u, int64_t stop) {
+  const int64_t tile0 = begin + start;
+  int64_t j0 = u - tile0, j1 = stop - tile0;
+  j0 = j0 < 0 ? 0 : j0;
+  j1 = j1 < 0 ? 0 : j1 > tiles ? tiles : j1;
+  SharedPiece p;
+  p.j0 = static_cast<int32_t>(j0 < tiles ? j0 : tiles);
+  p.j1 = static_cast<int32_t>(j1);
+  p.whole = p.j0 == 0 && p.j1 == tiles && stop > tile0;
+  return p;
+}
+// Where the worker leaves that piece, if it is not whole: its first piece may continue a block
+// (slot 2 c), its last may begin one (slot 2 c + 1).
+MLA_HD int64_t shared_slot(int64_t c, bool begins) { return 2 * c + (begins ? 1 : 0); }
+
 }  // namespace mla

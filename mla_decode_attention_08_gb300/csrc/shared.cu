@@ -175,21 +175,14 @@ __device__ __forceinline__ int64_t blocks_of(const Group& g) { return (g.n + kTo
 __device__ __forceinline__ int64_t units_of(const SharedParams& p, const Group& g) {
   return p.split ? p.start + max(1, tiles_of_length(g.len)) : 1;
 }
-// Worker c of `workers` has the units [unit(c), unit(c + 1)) of `all`, none of them empty;
-// unit u is worker owner(u)'s.
-struct Ranges {
-  int64_t all, workers;
-  __device__ __forceinline__ int64_t unit(int64_t c) const { return c * all / workers; }
-  __device__ __forceinline__ int64_t owner(int64_t u) const { return ((u + 1) * workers - 1) / all; }
-};
-// A bound on units that keeps every product above within 64 bits.
+// A bound on units that keeps the shares' products within 64 bits.
 constexpr int64_t kManyUnits = INT64_C(1) << 48;
 
 // The groups as a warp holds them: a run of consecutive groups a lane.
 struct Batch {
   int32_t g0;
   int64_t first, count;  // units before the lane's run, and in it
-  Ranges ranges;
+  Shares shares;
 };
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -219,8 +212,8 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
   r.first = incl - r.count;
   // Groups overlap where offsets of queries decrease (which is reported) and could come to
   // any amount of work, so nothing is done then, and nothing joined.
-  r.ranges.all = back ? 0 : __shfl_sync(0xffffffffu, incl, 31);
-  r.ranges.workers = min(static_cast<int64_t>(p.workers), r.ranges.all);
+  r.shares.all = back ? 0 : __shfl_sync(0xffffffffu, incl, 31);
+  r.shares.workers = min(static_cast<int64_t>(p.workers), r.shares.all);
   return r;
 }
 
@@ -228,7 +221,7 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
 __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, int64_t u, Job* job) {
   const int64_t c = blockIdx.x;
   int64_t stop = 0;
-  if (c < r.ranges.workers) stop = r.ranges.unit(c + 1);
+  if (c < r.shares.workers) stop = r.shares.begin(c + 1);
   if (u >= stop) {
     if ((threadIdx.x & 31) == 0) job->live = job->nq = job->keys = 0;
     __syncwarp();
@@ -245,20 +238,14 @@ __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, 
     }
     const int64_t size = units_of(p, g), block = at / size, begin = u - (at - block * size);
     const int32_t tiles = tiles_of_length(g.len);
-    int32_t j0 = 0, j1 = tiles;
-    if (p.split) {  // the range's tiles of the block
-      const int64_t tile0 = begin + p.start;
-      j0 = static_cast<int32_t>(max(u - tile0, static_cast<int64_t>(0)));
-      j1 = static_cast<int32_t>(max(min(stop - tile0, static_cast<int64_t>(tiles)), static_cast<int64_t>(0)));
-    }
-    const bool whole = j0 == 0 && j1 == tiles;
+    SharedPiece piece = {0, tiles, true};
+    if (p.split) piece = shared_piece(begin, tiles, p.start, u, stop);
     job->q0 = g.qs + static_cast<int32_t>(block) * kTokens;
-    // (a range that ends among a block's start units has none of it)
-    job->nq = whole || j1 > j0 ? min(kTokens, g.n - static_cast<int32_t>(block) * kTokens) : 0;
-    job->k0 = g.ks + j0 * kTileTokens;
-    job->keys = j1 > j0 ? min(g.len, j1 * kTileTokens) - j0 * kTileTokens : 0;
-    // a worker's first part continues a block, its last begins one
-    job->slot = whole ? -1 : 2 * static_cast<int32_t>(c) + (j0 == 0);
+    // (a share that ends among a block's start units has none of it)
+    job->nq = piece.whole || piece.j1 > piece.j0 ? min(kTokens, g.n - static_cast<int32_t>(block) * kTokens) : 0;
+    job->k0 = g.ks + piece.j0 * kTileTokens;
+    job->keys = piece.j1 > piece.j0 ? min(g.len, piece.j1 * kTileTokens) - piece.j0 * kTileTokens : 0;
+    job->slot = piece.whole ? -1 : static_cast<int32_t>(shared_slot(c, piece.j0 == 0));
     job->live = 1;
     job->end = begin + size;
   }
@@ -1027,7 +1014,7 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
   Batch groups = {};
   if (warp == kSchedulerWarp) {
     groups = count_groups(p);
-    find_job(p, groups, blockIdx.x < groups.ranges.workers ? groups.ranges.unit(blockIdx.x) : 0, &ms->job[0]);
+    find_job(p, groups, blockIdx.x < groups.shares.workers ? groups.shares.begin(blockIdx.x) : 0, &ms->job[0]);
   }
   tc_fence_before();
   __syncthreads();
@@ -1071,7 +1058,9 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
 // shared memory.  Rows whose keys one worker had are written already.
 constexpr int kJoinThreads = 128, kJoinAhead = 8, kJoinHeads = 8;
 constexpr int kJoinStep = kJoinThreads / kJoinHeads;  // parts whose weights are formed together
-__global__ void __launch_bounds__(kJoinThreads, 8) shared_join_kernel(const SharedParams p) {
+constexpr int kJoinPerSm = 8;                         // blocks, at most
+constexpr int kJoinOwnBytes = 3 << 10;                  // of shared memory (its arrays)
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) shared_join_kernel(const SharedParams p) {
   __shared__ __align__(16) uint16_t rows[kJoinHeads][kJoinThreads];
   __shared__ __align__(16) float weight[kJoinStep][kJoinHeads];
   __shared__ float red[2][kJoinThreads / 32][kJoinHeads];
@@ -1109,10 +1098,10 @@ __global__ void __launch_bounds__(kJoinThreads, 8) shared_join_kernel(const Shar
   if (own >= 0) {
     const Group x = load_group(p, own, false, back);
     const int32_t n = tiles_of_length(x.len), block = (token - x.qs) / kTokens;
-    const Ranges ranges = {all, min(static_cast<int64_t>(p.workers), all)};
+    const Shares shares = {all, min(static_cast<int64_t>(p.workers), all)};
     const int64_t tile0 = before + block * units_of(p, x) + p.start;
-    w0 = static_cast<int32_t>(ranges.owner(tile0));
-    w1 = n > 0 ? static_cast<int32_t>(ranges.owner(tile0 + n - 1)) : w0;
+    w0 = static_cast<int32_t>(shares.owner(tile0));
+    w1 = n > 0 ? static_cast<int32_t>(shares.owner(tile0 + n - 1)) : w0;
     place = token - x.qs - block * kTokens;
   }
   pdl_wait_primary();
@@ -1120,7 +1109,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) shared_join_kernel(const Shar
   if (w0 == w1 || *p.missing != 0) return;
   if (!MLA_DCHECK(w0 >= 0 && w1 < p.workers && place >= 0 && place < kTokens, p.err)) return;
   // The first worker's part is its last job's, the others' their first.
-  auto slot = [&](int32_t w) { return 2 * static_cast<int64_t>(w) + (w == w0); };
+  auto slot = [&](int32_t w) { return shared_slot(w, w == w0); };
   const uint16_t* part = p.part + (static_cast<int64_t>(c) * kTokens + place) * (128 * kNumHeads) + tid * kNumHeads + head0;
   constexpr int64_t kSlot = static_cast<int64_t>(kRows) * kVDim;
   uint4 v[kJoinAhead];
@@ -1192,10 +1181,16 @@ __global__ void __launch_bounds__(kJoinThreads, 8) shared_join_kernel(const Shar
 
 }  // namespace
 
+// Shared memory that a block of the second kernel asks for beside its own, so that no more than
+// `blocks` of them share an SM (of its 228 KB each also costs 1 KB).
+static int32_t join_room(int32_t blocks) { return 228 * 1024 / blocks - 1024 - kJoinOwnBytes; }
+
 size_t shared_smem_bytes() { return kSmemBytes; }
 
 cudaError_t shared_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(shared_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(shared_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(shared_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, join_room(1));
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(shared_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
 }
@@ -1207,10 +1202,15 @@ cudaError_t launch_shared(const SharedParams& p, const SharedMaps& maps, cudaStr
              : launch_dependent(shared_kernel<false>, grid, threads<false>(), kSmemBytes, stream, maps, p);
 }
 
-cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
+cudaError_t launch_shared_join(const SharedParams& p, int32_t num_sms, cudaStream_t stream) {
   const int64_t blocks = static_cast<int64_t>(p.total_q) * 2 * kPanels;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  return launch_dependent(shared_join_kernel, static_cast<unsigned>(blocks), kJoinThreads, 0, stream, p);
+  // Few blocks are spread over the SMs: left alone, the first SMs that are done take eight each, and
+  // what an SM can load bounds the call (13 queries over 9000 keys 36 us, spread 24; 64 over 8192
+  // 34.4, spread 31.7).
+  const int64_t each = blocks / num_sms + 1;
+  const size_t room = each < kJoinPerSm ? join_room(static_cast<int32_t>(each)) : 0;
+  return launch_dependent(shared_join_kernel, static_cast<unsigned>(blocks), kJoinThreads, room, stream, p);
 }
 
 }  // namespace mla
