@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScore
     for (int i = tid; i < here_tokens * kNumHeads * kRowPieces; i += kThreads) {
       const int row = i / kRowPieces, at = i % kRowPieces;
       const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(qs + t0) * kNumHeads + row) * kQkDim);
-      cp_async_16(smem_u32(sq + row * kQStride + 16 * at), q + at);
+      if (MLA_DCHECK(qs >= 0 && qs + t0 + row / kNumHeads < p.total_q && row < kTokens * kNumHeads, p.err))
+        cp_async_16(smem_u32(sq + row * kQStride + 16 * at), q + at);
     }
     uint4 v[2][kAhead];
 #pragma unroll

@@ -229,7 +229,9 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
       each_key([&](int32_t j, uint32_t key) {
         const int at = step_of(key);
         if (at > step) marks |= 1u << (j - first);
-        if (at == step) list[atomicAdd(&listed, 1)] = make_uint2(key, static_cast<uint32_t>(j));
+        if (at != step) return;
+        const int to = atomicAdd(&listed, 1);
+        if (MLA_DCHECK(to < inside && to < kListed, p.err)) list[to] = make_uint2(key, static_cast<uint32_t>(j));
       });
       __syncthreads();
       each_key([&](int32_t j, uint32_t key) {
@@ -309,9 +311,12 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
   int32_t* out = p.sel_indices + before;
   const bool shifts = (p.page_size & (p.page_size - 1)) == 0;
   const int shift = __ffs(p.page_size) - 1;
-  for (int32_t t = tid; t < row.tokens; t += kThreads) {
-    const int32_t at = shifts ? t >> shift : t / p.page_size, start = rows[at];
-    out[t] = start < 0 ? -1 : start + (t - at * p.page_size);
+  // (unsigned: a row may have close to 2^31 tokens)
+  for (uint32_t t = tid; t < static_cast<uint32_t>(row.tokens); t += kThreads) {
+    const uint32_t at = shifts ? t >> shift : t / static_cast<uint32_t>(p.page_size);
+    if (!MLA_DCHECK(at < static_cast<uint32_t>(row.taken) && before + t < p.indices_len, p.err)) return;
+    const int32_t start = rows[at];
+    out[t] = start < 0 ? -1 : start + static_cast<int32_t>(t - at * p.page_size);
   }
 }
 

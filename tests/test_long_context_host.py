@@ -130,7 +130,8 @@ SCORES = dict(q=ptr(), total=4, means=ptr(), pages=64, table=ptr(), row=16, widt
     (dict(row=15), INVALID), (dict(row=1 << 36), INVALID), (dict(width=0), INVALID), (dict(qo=None), INVALID),
     (dict(kv=None), INVALID), (dict(qo=ptr(1)), INVALID), (dict(kv=ptr(1)), INVALID), (dict(batch=0), INVALID),
     (dict(batch=16385), INVALID), (dict(page=0), INVALID), (dict(scores=None), INVALID), (dict(scores=ptr(2)), INVALID),
-    (dict(out_row=15), INVALID), (dict(out_row=1 << 36), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=8), WS_SMALL)])
+    (dict(out_row=15), INVALID), (dict(out_row=1 << 36), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=8), WS_SMALL),
+    (dict(width=(1 << 30) + 1, row=1 << 31, out_row=1 << 31), INVALID)])
 def test_scores_refusals(lib, change, status):
     assert lib.mla_block_scores(*{**SCORES, **change}.values(), None) == status
 
@@ -148,7 +149,7 @@ SELECT = dict(scores=ptr(), in_row=16, table=ptr(), row=16, width=16, kv=ptr(), 
     (dict(sink=7), INVALID), (dict(sink=2**31 - 1), INVALID), (dict(recent=9), INVALID), (dict(recent=2**31 - 1), INVALID),
     (dict(ptr=None), INVALID), (dict(ptr=ptr(2)), INVALID), (dict(indices=None), INVALID), (dict(indices=ptr(2)), INVALID),
     (dict(room=-1), INVALID), (dict(room=2**31), INVALID), (dict(chosen=ptr(2)), INVALID), (dict(ws=None), INVALID),
-    (dict(ws_bytes=0), WS_SMALL)])
+    (dict(ws_bytes=0), WS_SMALL), (dict(width=(1 << 30) + 1, row=1 << 31, in_row=1 << 31), INVALID)])
 def test_select_refusals(lib, change, status):
     assert lib.mla_block_select(*{**SELECT, **change}.values(), None) == status
 
