@@ -22,11 +22,11 @@
 //   * warp 3 finds the jobs,
 //   * the keys come as four panels of 128 dims a tile into two buffers, and the 64 rotated
 //     dims into one: by warp 2 through TMA in boxes of 128 rows, or, by a page table, by
-//     warps 12-19 in 16-byte copies (TMA's gathers of four rows take 74 cycles each to
+//     warps 20-27 in 16-byte copies (TMA's gathers of four rows take 74 cycles each to
 //     issue from one warp, 160 a tile, and 20 from four; alone, the copies of four warps
 //     bring a panel in 500 cycles and of eight in 330),
 //   * warps 0 and 1 issue the products S and O, each as soon as it can,
-//   * warps 4-7 and 8-11 run the softmax of two query tokens each, a thread a key: the
+//   * four warpgroups, warps 4-19, run the softmax of a query token each, a thread a key: the
 //     maximum over keys is over lanes, so it is only looked for when a score passes the
 //     running reference by four powers of two, which few tiles' do.
 // A job without all of its block's keys leaves a part of half precision, in units of the
@@ -58,18 +58,18 @@ constexpr int kOffP = kOffQRope + kRopeBytes;      // high terms, low terms
 constexpr int kOffMisc = kOffP + 2 * kPBytes;
 
 constexpr int kScoreWarp = 0, kValueWarp = 1, kProducerWarp = 2, kSchedulerWarp = 3, kFirstSoftmaxWarp = 4;
-constexpr int kFirstCopyWarp = 12;
-constexpr uint32_t kSoftmaxWarps = 8, kCopyWarps = 8;
-// Threads of a block, and registers: launched with 168 a thread (96 with a page table),
+constexpr uint32_t kSoftmaxWarps = 4 * kTokens, kCopyWarps = 8;
+constexpr int kFirstCopyWarp = kFirstSoftmaxWarp + static_cast<int>(kSoftmaxWarps);
+// Threads of a block, and registers: launched with 96 a thread (72 with a page table),
 // of which the softmax warpgroups take the others' share.
 template <bool kPaged>
-__host__ __device__ constexpr int threads() { return kPaged ? 640 : 384; }
+__host__ __device__ constexpr int threads() { return 32 * (kFirstCopyWarp + (kPaged ? static_cast<int>(kCopyWarps) : 0)); }
 template <bool kPaged>
-__host__ __device__ constexpr int softmax_regs() { return kPaged ? 168 : 200; }
+__host__ __device__ constexpr int softmax_regs() { return kPaged ? 88 : 104; }
 template <bool kPaged>
-__host__ __device__ constexpr int other_regs() { return kPaged ? 48 : 104; }
-static_assert(2 * 128 * softmax_regs<false>() + 128 * other_regs<false>() <= threads<false>() * 168 &&
-                  2 * 128 * softmax_regs<true>() + 384 * other_regs<true>() <= threads<true>() * 96,
+__host__ __device__ constexpr int other_regs() { return kPaged ? 48 : 64; }
+static_assert(kTokens * 128 * softmax_regs<false>() + (threads<false>() - kTokens * 128) * other_regs<false>() <= threads<false>() * 96 &&
+                  kTokens * 128 * softmax_regs<true>() + (threads<true>() - kTokens * 128) * other_regs<true>() <= threads<true>() * 72,
               "register split exceeds the launch allocation");
 // What reads a job: two issuers, the softmax, and the producer or the copying warps.
 template <bool kPaged>
@@ -117,11 +117,11 @@ struct Misc {
   uint32_t tmem_base;
   volatile int32_t abort_flag;
   Job job[2];
-  // Of a warpgroup's 32 rows:
-  alignas(16) float red[2][4][32];  // [warpgroup][warp][row]: maxima, sums
-  alignas(16) float scale[2][32];   // products to powers of two
-  alignas(16) float off[2][32];     // kTop less the reference
-  alignas(16) float factor[2][32];  // of O: rescaling, at the end the division
+  // Of a warpgroup's rows, its token's heads:
+  alignas(16) float red[kTokens][4][kNumHeads];  // [warpgroup][warp][row]: maxima, sums
+  alignas(16) float scale[kTokens][kNumHeads];   // products to powers of two
+  alignas(16) float off[kTokens][kNumHeads];     // kTop less the reference
+  alignas(16) float factor[kTokens][kNumHeads];  // of O: rescaling, at the end the division
 };
 constexpr int kSmemBytes = kOffMisc + static_cast<int>(sizeof(Misc));
 static_assert(kSmemBytes <= 232448, "shared memory of one block");
@@ -517,7 +517,7 @@ __device__ __forceinline__ void run_values(const SharedParams& p, Misc* ms, uint
   __syncwarp();
 }
 
-// ------------------------------------------------------------ softmax (two warpgroups)
+// ------------------------------------------------------------ softmax (a warpgroup a token)
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -639,27 +639,31 @@ __device__ __forceinline__ void split_q(const uint4& a, const uint4& b, float up
     lo[k] = pack_codes(y[2 * k], y[2 * k + 1]);
   }
 }
-// The query operand's rows of warpgroup g's two tokens, each row scaled by a power of two so
+// The query operand's rows of warpgroup g's token, each row scaled by a power of two so
 // that its largest magnitude lies in (224, 448], and what turns its products into powers of
-// two (NaN for a row that is not finite, whose output becomes NaN).  A warp has eight of
-// the 32 rows: a lane 16 latent dims of each and 16 of the rotated dims of one.  Rows are
-// written as they arrive.
+// two (NaN for a row that is not finite, whose output becomes NaN).  A warp has four of
+// the 16 rows: a lane 16 latent dims of each and 16 of the rotated dims of one (half of the
+// lanes write what the others do).  Rows are written as they arrive.  Of a token that is not
+// there nothing is written, nor read: its columns of both products mean nothing.
 __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_t sbase, const Job& job, int g, float kv_scale) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
-  constexpr int kWarpRows = 2 * kNumHeads / 4;
-  static_assert(kVDim / 16 == 32 && kWarpRows * ((kQkDim - kVDim) / 16) == 32, "a lane a piece");
-  const int row0 = kWarpRows * warp, token = 2 * g + (warp >> 1);
-  const int rope_row = row0 + (lane >> 2), rope_ch = kVDim / 16 + (lane & 3);
-  const bool there = token < job.nq && MLA_DCHECK(job.q0 >= 0 && job.q0 + token < p.total_q, p.err);
-  const uint16_t* src = p.q + (static_cast<int64_t>(job.q0 + 2 * g) * kNumHeads) * kQkDim;
+  constexpr int kWarpRows = kNumHeads / 4;
+  static_assert(kVDim / 16 == 32 && 2 * kWarpRows * ((kQkDim - kVDim) / 16) == 32, "a lane a piece");
+  if (g >= job.nq || !MLA_DCHECK(job.q0 >= 0 && job.q0 + g < p.total_q, p.err)) {
+    if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
+    return;
+  }
+  const int row0 = kWarpRows * warp;
+  const int rope_row = row0 + (lane >> 2) % kWarpRows, rope_ch = kVDim / 16 + (lane & 3);
+  const uint16_t* src = p.q + (static_cast<int64_t>(job.q0 + g) * kNumHeads) * kQkDim;
   uint4 raw[kWarpRows + 1][2];  // the rotated dims last
 #pragma unroll
   for (int i = 0; i <= kWarpRows; ++i) {
     const int r = (i + kWarpRows) % (kWarpRows + 1);  // they come first
     const uint4* at = reinterpret_cast<const uint4*>(src + (r < kWarpRows ? (row0 + r) * kQkDim + 16 * lane
                                                                           : rope_row * kQkDim + 16 * rope_ch));
-    raw[r][0] = there ? __ldg(at) : make_uint4(0, 0, 0, 0);
-    raw[r][1] = there ? __ldg(at + 1) : make_uint4(0, 0, 0, 0);
+    raw[r][0] = __ldg(at);
+    raw[r][1] = __ldg(at + 1);
   }
   auto largest = [&](const uint4 (&v)[2]) {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
@@ -695,15 +699,15 @@ __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_
     k = top[r] == 0 ? 0 : min(k, 126);
     // 2^(k - 8), which is a denormal for the largest of all
     const float up = __int_as_float(k - 8 + 127 > 0 ? (k - 8 + 127) << 23 : 1 << (22 + (k - 8 + 127)));
-    if (lane >> 2 == r) rope_up = up;
-    const int row = 2 * kNumHeads * g + row0 + r;
+    if ((lane >> 2) % kWarpRows == r) rope_up = up;
+    const int row = kNumHeads * g + row0 + r;
     if (lane == r)
       ms->scale[g][row0 + r] = top[r] >= 0x7F80u ? __int_as_float(0x7FC00000)
                                                  : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
     const uint32_t at = sbase + kOffQ + (lane >> 3) * kPanelBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
     store(raw[r], up, at, at + kRows * 128);
   }
-  const int row = 2 * kNumHeads * g + rope_row;
+  const int row = kNumHeads * g + rope_row;
   const uint32_t at = sbase + kOffQRope + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4);
   store(raw[kWarpRows], rope_up, at, at + kRows * 64);
   fence_proxy_async_smem();
@@ -720,15 +724,14 @@ __device__ __forceinline__ bool next_job_of_group(const SharedParams& p, Misc* m
 }
 
 __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int g) {
-  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31;
+  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31, row = lane & 15;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t bar = kBarSoftmax + g;
   const float kv_scale = __ldg(p.kv_scale);
-  const uint32_t s_hi = tmem + lanes + kColS + 32 * g, s_lo = s_hi + kRows;
-  const uint32_t o_addr = tmem + lanes + kColO + 32 * g;
-  // this thread's key of a tile: its row of either term of P, two 16-byte pieces a warpgroup
-  const uint32_t p_row = sbase + kOffP + t * kRows;
-  const uint32_t swizzle = (t >> 1) & 3;
+  const uint32_t s_hi = tmem + lanes + kColS + kNumHeads * g, s_lo = s_hi + kRows;
+  const uint32_t o_addr = tmem + lanes + kColO + kNumHeads * g;
+  // this thread's key of a tile: its row of either term of P, 16 bytes a warpgroup
+  const uint32_t p_at = sbase + kOffP + t * kRows + ((g ^ ((t >> 1) & 3)) << 4);
   uint32_t T = 0, jobs = 0;
   Job job, next;
   bool live = next_job_of_group(p, ms, 0, job, g);
@@ -738,33 +741,37 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
   const ulonglong2* factors = reinterpret_cast<const ulonglong2*>(ms->factor[g]);
   for (uint32_t k = 0; live; ++k) {
     const int32_t n = job.tiles();
-    float off = 0.0f;     // of row `lane` of the warpgroup, alike in its four warps
-    uint64_t sum[16];     // of pairs of rows: this thread's keys'
+    const bool here = g < job.nq;
+    float off = 0.0f;     // of row `lane % 16` of the warpgroup, alike in its four warps
+    uint64_t sum[8];      // of pairs of rows: this thread's keys'
 #pragma unroll
-    for (int h = 0; h < 16; ++h) sum[h] = 0;
+    for (int h = 0; h < 8; ++h) sum[h] = 0;
     for (int32_t j = 0; j < n; ++j, ++T) {
       warp_wait_on(&ms->s_full[T & 1], T >> 1, ms, p.err);
       tc_fence_after();
+      if (!here) {  // nothing to read; P of a token that is not there means nothing
+        if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[T & 1]));
+        if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);
+        if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
+        continue;
+      }
       const bool partial = (j + 1) * kTileTokens > job.keys;  // (the same for the whole block)
       const bool seen = j * kTileTokens + t < job.keys;
       const uint32_t s_at = 128 * (T & 1);
       const uint64_t eighth = pack2(0.125f, 0.125f);
       // Scores as powers of two over the reference, kTop up.
-      uint64_t x[16];
+      uint64_t x[8];
       auto exponents = [&] {
-        uint32_t hi[2][16], lo[2][16];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          tmem_ld16(s_hi + s_at + 16 * i, hi[i]);
-          tmem_ld16(s_lo + s_at + 16 * i, lo[i]);
-        }
+        uint32_t hi[16], lo[16];
+        tmem_ld16(s_hi + s_at, hi);
+        tmem_ld16(s_lo + s_at, lo);
         tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
+        for (int h = 0; h < 4; ++h) {
           const ulonglong2 a = scales[h], o = offs[h];
-          const int i = h >> 2, r = 4 * (h & 3);
-          x[2 * h] = fma2(fma2(pack2(lo[i][r], lo[i][r + 1]), eighth, pack2(hi[i][r], hi[i][r + 1])), a.x, o.x);
-          x[2 * h + 1] = fma2(fma2(pack2(lo[i][r + 2], lo[i][r + 3]), eighth, pack2(hi[i][r + 2], hi[i][r + 3])), a.y, o.y);
+          const int r = 4 * h;
+          x[2 * h] = fma2(fma2(pack2(lo[r], lo[r + 1]), eighth, pack2(hi[r], hi[r + 1])), a.x, o.x);
+          x[2 * h + 1] = fma2(fma2(pack2(lo[r + 2], lo[r + 3]), eighth, pack2(hi[r + 2], hi[r + 3])), a.y, o.y);
         }
       };
       bool look = j == 0;
@@ -772,7 +779,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
         exponents();
         float high = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
+        for (int h = 0; h < 8; ++h) {
           float u, v;
           unpack2(x[h], u, v);
           high = fmaxf(high, fmaxf(u, v));
@@ -781,23 +788,22 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       }
       const bool moved = look && j > 0;
       if (look) {
-        float mine = 0.0f;  // the maximum of row `lane`
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        float mine = 0.0f;  // the maximum of row `lane % 16`
+        {
           uint32_t hi[16], lo[16];
-          tmem_ld16(s_hi + s_at + 16 * i, hi);
-          tmem_ld16(s_lo + s_at + 16 * i, lo);
+          tmem_ld16(s_hi + s_at, hi);
+          tmem_ld16(s_lo + s_at, lo);
           tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
-            const float s = fmaf(__uint_as_float(lo[h]), 0.125f, __uint_as_float(hi[h])) * ms->scale[g][16 * i + h];
+            const float s = fmaf(__uint_as_float(lo[h]), 0.125f, __uint_as_float(hi[h])) * ms->scale[g][h];
             const float m = warp_max(seen ? s : -INFINITY);
-            mine = lane == 16 * i + h ? m : mine;
+            mine = row == h ? m : mine;
           }
         }
-        ms->red[g][warp][lane] = mine;
+        ms->red[g][warp][row] = mine;
         named_bar_sync(bar, 128);
-        mine = fmaxf(fmaxf(ms->red[g][0][lane], ms->red[g][1][lane]), fmaxf(ms->red[g][2][lane], ms->red[g][3][lane]));
+        mine = fmaxf(fmaxf(ms->red[g][0][row], ms->red[g][1][row]), fmaxf(ms->red[g][2][row], ms->red[g][3][row]));
         float factor = 1.0f;
         if (j == 0 || mine + off > 0.0f) {
           const float to = kTop - mine;
@@ -805,12 +811,12 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
           off = to;
         }
         // (the four warps write the same)
-        ms->off[g][lane] = off;
-        ms->factor[g][lane] = factor;
+        ms->off[g][row] = off;
+        ms->factor[g][row] = factor;
         __syncwarp();
         if (moved) {
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
+          for (int h = 0; h < 4; ++h) {
             const ulonglong2 f = factors[h];
             sum[2 * h] = mul2(sum[2 * h], f.x);
             sum[2 * h + 1] = mul2(sum[2 * h + 1], f.y);
@@ -821,45 +827,37 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[T & 1]));
-      uint32_t hi[2][4], lo[2][4];
+      uint32_t hi[4], lo[4], halves[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t halves[8];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          float u, v;
-          unpack2(x[8 * i + h], u, v);
-          u = ex2(u);
-          v = ex2(v);
-          if (partial) {
-            u = seen ? u : 0.0f;
-            v = seen ? v : 0.0f;
-          }
-          sum[8 * i + h] = add2(sum[8 * i + h], pack2(u, v));
-          halves[h] = half2_bits(u, v);
+      for (int h = 0; h < 8; ++h) {
+        float u, v;
+        unpack2(x[h], u, v);
+        u = ex2(u);
+        v = ex2(v);
+        if (partial) {
+          u = seen ? u : 0.0f;
+          v = seen ? v : 0.0f;
         }
-        split_p(halves, hi[i], lo[i]);
+        sum[h] = add2(sum[h], pack2(u, v));
+        halves[h] = half2_bits(u, v);
       }
+      split_p(halves, hi, lo);
       if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);  // P(T - 1) is read
-      // (and the other warpgroup's rows of the job before have left through P's memory)
+      // (and the other warpgroups' rows of the job before have left through P's memory)
       if (j == 0 && jobs > 0) warp_wait_on(&ms->o_free, jobs - 1, ms, p.err);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t at = p_row + (((2 * g + i) ^ swizzle) << 4);
-        st_shared_v4(at, hi[i]);
-        st_shared_v4(at + kPBytes, lo[i]);
-      }
+      st_shared_v4(p_at, hi);
+      st_shared_v4(p_at + kPBytes, lo);
       fence_proxy_async_smem();
       if (moved) {
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < kPanels; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + kRows * c, o);
+          uint32_t o[16];
+          tmem_ld16(o_addr + kRows * c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ms->factor[g][i]);
-          tmem_st32(o_addr + kRows * c, o);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ms->factor[g][i]);
+          tmem_st16(o_addr + kRows * c, o);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -869,24 +867,23 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     }
 
     // ------------------------------------------------ sums over the keys
-    float lse = -INFINITY;  // of row `lane`, in the warpgroup's first warp
-    named_bar_sync(bar, 128);  // (red and factor are read)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    float lse = -INFINITY;  // of row `lane % 16`, in the warpgroup's first warp
+    if (here) {
+      named_bar_sync(bar, 128);  // (red and factor are read)
       float v[16];
 #pragma unroll
-      for (int h = 0; h < 8; ++h) unpack2(sum[8 * i + h], v[2 * h], v[2 * h + 1]);
-      const float s = transposed_sum16(v);
-      if ((lane & 1) == 0) ms->red[g][warp][16 * i + (lane >> 1)] = s;
+      for (int h = 0; h < 8; ++h) unpack2(sum[h], v[2 * h], v[2 * h + 1]);
+      const float s16 = transposed_sum16(v);
+      if ((lane & 1) == 0) ms->red[g][warp][lane >> 1] = s16;
+      named_bar_sync(bar, 128);
+      if (warp == 0) {
+        const float s = (ms->red[g][0][row] + ms->red[g][1][row]) + (ms->red[g][2][row] + ms->red[g][3][row]);
+        // (P is 2^8 times what was summed; a part is left in units of codes)
+        ms->factor[g][row] = s != 0.0f ? (job.slot >= 0 ? 1.0f : kv_scale) * 0x1p-8f / s : 0.0f;
+        if (n > 0) lse = kLn2 * (log2f(s) - off);
+      }
+      named_bar_sync(bar, 128);
     }
-    named_bar_sync(bar, 128);
-    if (warp == 0) {
-      const float s = (ms->red[g][0][lane] + ms->red[g][1][lane]) + (ms->red[g][2][lane] + ms->red[g][3][lane]);
-      // (P is 2^8 times what was summed; a part is left in units of codes)
-      ms->factor[g][lane] = s != 0.0f ? (job.slot >= 0 ? 1.0f : kv_scale) * 0x1p-8f / s : 0.0f;
-      if (n > 0) lse = kLn2 * (log2f(s) - off);
-    }
-    named_bar_sync(bar, 128);
 
     // ------------------------------------------------ the next job's query, while the last products run
     const bool more = next_job_of_group(p, ms, k + 1, next, g);
@@ -902,27 +899,24 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
     // ------------------------------------------------ output
     // A thread has one dim of a chunk.  Parts keep that order, [chunk][token][dim][head]: 16
     // heads are a sector.  Rows of the output go through shared memory (P's, which is
-    // free: a term for a warpgroup) to leave in 16-byte pieces.
-    const int tokens = min(2, job.nq - 2 * g);  // of this warpgroup
+    // free: a quarter for a warpgroup) to leave in 16-byte pieces.
     const bool parts = job.slot >= 0;
-    const bool fits = !ms->abort_flag && MLA_DCHECK(tokens <= 0 || (parts ? job.slot < 2 * p.workers && p.split
-                                                                          : job.q0 >= 0 && job.q0 + 2 * g + tokens <= p.total_q), p.err);
-    uint8_t* stage = reinterpret_cast<uint8_t*>(ms) - kOffMisc + kOffP + g * kPBytes;
+    const bool fits = !ms->abort_flag && MLA_DCHECK(!here || (parts ? job.slot < 2 * p.workers && p.split
+                                                                    : job.q0 >= 0 && job.q0 + g < p.total_q), p.err);
+    uint8_t* stage = reinterpret_cast<uint8_t*>(ms) - kOffMisc + kOffP + g * (2 * kPBytes / kTokens);
 #pragma unroll 1
-    for (int step = 0; step < 2 * kPanels; ++step) {  // a token's 16 rows of a chunk
-      const int c = step >> 1, i = step & 1;
-      if (i >= tokens) continue;  // (the same for the warpgroup)
-      uint16_t* dst = p.out + (static_cast<int64_t>(job.q0 + 2 * g + i) * kNumHeads) * kVDim + 128 * c;
+    for (int c = 0; c < (here ? kPanels : 0); ++c) {  // the token's 16 rows of a chunk
+      uint16_t* dst = p.out + (static_cast<int64_t>(job.q0 + g) * kNumHeads) * kVDim + 128 * c;
       if (n == 0) {  // no keys: zeros (P's memory may be at work; of a part the log-sum-exp says so)
         if (fits && !parts)
-          for (int row = t >> 4; row < 16; row += 8)
-            *reinterpret_cast<uint4*>(dst + row * kVDim + 8 * (t & 15)) = make_uint4(0, 0, 0, 0);
+          for (int i = t >> 4; i < 16; i += 8)
+            *reinterpret_cast<uint4*>(dst + i * kVDim + 8 * (t & 15)) = make_uint4(0, 0, 0, 0);
         continue;
       }
       uint32_t o[16];
-      tmem_ld16(o_addr + kRows * c + 16 * i, o);
+      tmem_ld16(o_addr + kRows * c, o);
       tmem_wait_ld();
-      const float4* by = reinterpret_cast<const float4*>(&ms->factor[g][16 * i]);
+      const float4* by = reinterpret_cast<const float4*>(ms->factor[g]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float4 f = by[q];
@@ -936,30 +930,30 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
 #pragma unroll
         for (int h = 0; h < 8; ++h) w[h] = half2_bits(__uint_as_float(o[2 * h]), __uint_as_float(o[2 * h + 1]));
         if (fits)
-          store_sector(p.part + ((static_cast<int64_t>(job.slot) * kPanels + c) * kTokens + 2 * g + i) * (128 * kNumHeads) + t * kNumHeads, w);
+          store_sector(p.part + ((static_cast<int64_t>(job.slot) * kPanels + c) * kTokens + g) * (128 * kNumHeads) + t * kNumHeads, w);
         continue;
       }
 #pragma unroll
-      for (int row = 0; row < 16; ++row) {
+      for (int i = 0; i < 16; ++i) {
         uint16_t b;
-        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(__uint_as_float(o[row])));
-        reinterpret_cast<uint16_t*>(stage)[row * 128 + t] = b;
+        asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(b) : "f"(__uint_as_float(o[i])));
+        reinterpret_cast<uint16_t*>(stage)[i * 128 + t] = b;
       }
       named_bar_sync(bar, 128);
       if (fits) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const int row = 8 * q + (t >> 4), piece = t & 15;  // 256 bytes a row
-          *reinterpret_cast<uint4*>(dst + row * kVDim + 8 * piece) = reinterpret_cast<const uint4*>(stage)[row * 16 + piece];
+          const int i = 8 * q + (t >> 4), piece = t & 15;  // 256 bytes a row
+          *reinterpret_cast<uint4*>(dst + i * kVDim + 8 * piece) = reinterpret_cast<const uint4*>(stage)[i * 16 + piece];
         }
       }
       named_bar_sync(bar, 128);
     }
-    if (t < 16 * tokens && fits) {
+    if (t < 16 && here && fits) {
       if (parts)
-        p.part_lse[static_cast<int64_t>(job.slot) * kRows + 2 * g * kNumHeads + t] = lse;
+        p.part_lse[static_cast<int64_t>(job.slot) * kRows + g * kNumHeads + t] = lse;
       else if (p.lse != nullptr)
-        p.lse[(static_cast<int64_t>(job.q0) + 2 * g) * kNumHeads + t] = lse;
+        p.lse[(static_cast<int64_t>(job.q0) + g) * kNumHeads + t] = lse;
     }
     __syncwarp();
     if (n > 0) {
