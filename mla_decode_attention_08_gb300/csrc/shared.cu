@@ -110,8 +110,11 @@ struct Misc {
   uint64_t q_empty;      // ... and read by its last scores
   uint64_t s_full[2];    // S(T) complete, T & 1 ...
   uint64_t s_free[2];    // ... and read; S(T + 2) is issued behind that
-  uint64_t p_full;       // P(T) written, O rescaled; P(T + 1) is written behind pv_done(T)
-  uint64_t pv_done;      // O(T) complete
+  uint64_t p_full[4];    // 32 keys' P(T) written (those of warp w of the warpgroups), O rescaled ...
+  // ... and read by the last chunk, T & 1; P(T + 1) is written behind that.  With the last 32 keys
+  // O(T) is complete: who waits for that has not waited for O(T - 1) and O(T - 2), of which the
+  // latter is, since warp 3 waits for each before it writes the next P.
+  uint64_t p_free[2][4];
   uint64_t o_free;       // a job's O read out
   uint64_t mma_done;     // both issuers' last products
   uint32_t tmem_base;
@@ -493,22 +496,33 @@ __device__ __forceinline__ void run_values(const SharedParams& p, Misc* ms, uint
     ok = jobs == 0 || on(&ms->o_free, jobs - 1);
     ++jobs;
     for (int32_t j = 0; j < n && ok; ++j, ++T) {
-      ok = on(&ms->p_full, T);
+      const uint64_t a = key_mn + kPanels * (T & 1) * kPanel;
+      // 32 keys of a chunk: 4 KB of a panel, 2 KB of a term of P
+      auto products = [&](int c, int kk) {
+        const uint32_t d = tmem + kColO + kRows * c;
+        umma_f8(d, a + c * kPanel + 256 * kk, p_mn + 128 * kk, kIdescPV, j != 0 || kk != 0);
+        umma_f8(d, a + c * kPanel + 256 * kk, p_mn + (kPBytes >> 4) + 128 * kk, kIdescPV, 1);
+      };
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {  // the first chunk, as the keys' P are written
+        ok = ok && on(&ms->p_full[kk], T);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) products(0, kk);
+        __syncwarp();
+      }
       if (!ok) break;
-      tc_fence_after();
       if (elect_one()) {
+        umma_commit(smem_u32(&ms->key_empty[kPanels * (T & 1)]));
 #pragma unroll
-        for (int c = 0; c < kPanels; ++c) {
-          const uint64_t a = key_mn + (kPanels * (T & 1) + c) * kPanel;
-          const uint32_t d = tmem + kColO + kRows * c;
+        for (int c = 1; c < kPanels; ++c) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 32 keys each: 4 KB of a panel, 2 KB of a term of P
-            umma_f8(d, a + 256 * kk, p_mn + 128 * kk, kIdescPV, j != 0 || kk != 0);
-            umma_f8(d, a + 256 * kk, p_mn + (kPBytes >> 4) + 128 * kk, kIdescPV, 1);
+          for (int kk = 0; kk < 4; ++kk) {
+            products(c, kk);
+            if (c == kPanels - 1) umma_commit(smem_u32(&ms->p_free[T & 1][kk]));
           }
           umma_commit(smem_u32(&ms->key_empty[kPanels * (T & 1) + c]));
         }
-        umma_commit(smem_u32(&ms->pv_done));
       }
       __syncwarp();
     }
@@ -751,8 +765,8 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       tc_fence_after();
       if (!here) {  // nothing to read; P of a token that is not there means nothing
         if (lane == 0) mbar_arrive(smem_u32(&ms->s_free[T & 1]));
-        if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);
-        if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
+        if (T > 0) warp_wait_on(&ms->p_free[(T - 1) & 1][warp], (T - 1) >> 1, ms, p.err);
+        if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[warp]));
         continue;
       }
       const bool partial = (j + 1) * kTileTokens > job.keys;  // (the same for the whole block)
@@ -842,13 +856,14 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
         halves[h] = half2_bits(u, v);
       }
       split_p(halves, hi, lo);
-      if (T > 0) warp_wait_on(&ms->pv_done, T - 1, ms, p.err);  // P(T - 1) is read
+      if (T > 0) warp_wait_on(&ms->p_free[(T - 1) & 1][warp], (T - 1) >> 1, ms, p.err);  // this warp's keys' P(T - 1) are read
       // (and the other warpgroups' rows of the job before have left through P's memory)
       if (j == 0 && jobs > 0) warp_wait_on(&ms->o_free, jobs - 1, ms, p.err);
       st_shared_v4(p_at, hi);
       st_shared_v4(p_at + kPBytes, lo);
       fence_proxy_async_smem();
       if (moved) {
+        warp_wait_on(&ms->p_free[(T - 1) & 1][3], (T - 1) >> 1, ms, p.err);
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < kPanels; ++c) {
@@ -861,9 +876,10 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
         }
         tmem_wait_st();
         tc_fence_before();
+        named_bar_sync(bar, 128);  // (each key's products add to all four warps' dims)
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full));
+      if (lane == 0) mbar_arrive(smem_u32(&ms->p_full[warp]));
     }
 
     // ------------------------------------------------ sums over the keys
@@ -892,7 +908,7 @@ __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uin
       write_q(p, ms, sbase, next, g, kv_scale);
     }
     if (n > 0) {
-      warp_wait_on(&ms->pv_done, T - 1, ms, p.err);
+      warp_wait_on(&ms->p_free[(T - 1) & 1][3], (T - 1) >> 1, ms, p.err);
       tc_fence_after();
     }
 
@@ -992,8 +1008,11 @@ __global__ void __launch_bounds__(threads<kPaged>(), 1)
     mbar_init(smem_u32(&ms->rope_empty), 1);
     mbar_init(smem_u32(&ms->q_full), kSoftmaxWarps);
     mbar_init(smem_u32(&ms->q_empty), 1);
-    mbar_init(smem_u32(&ms->p_full), kSoftmaxWarps);
-    mbar_init(smem_u32(&ms->pv_done), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&ms->p_full[i]), kTokens);
+      mbar_init(smem_u32(&ms->p_free[0][i]), 1);
+      mbar_init(smem_u32(&ms->p_free[1][i]), 1);
+    }
     mbar_init(smem_u32(&ms->o_free), kSoftmaxWarps);
     mbar_init(smem_u32(&ms->mma_done), 2);
     ms->abort_flag = 0;
