@@ -261,3 +261,37 @@ def test_captured_and_on_two_streams():
         graph.replay()
         torch.cuda.synchronize()
         a.check()
+
+
+@pytest.mark.parametrize("page", [2, 16, 24, 64, 1000])
+@pytest.mark.parametrize("skew", [0, 5])
+def test_rows_that_follow_one_another_in_the_cache(page, skew):
+    """Pages of rows: sixteen of a tile's that are one behind the other are copied as one, others piece by piece
+    (a prefix that begins inside a page, pages that end inside a tile, the cache's last rows); the same bits
+    as from the same keys in any other rows."""
+    q_lens, kv_lens = [9, 6], [700, 333]
+    a, b = (Case(q_lens, kv_lens, paged=True, seed=17 + page, tail=2) for _ in range(2))
+    tk = sum(kv_lens)
+    pages = -(-(tk + skew) // page)
+    order = torch.randperm(pages, generator=torch.Generator(device="cuda").manual_seed(page), device="cuda")
+    order[(order == pages - 1).nonzero()[0, 0]], order[pages // 2] = order[pages // 2].clone(), pages - 1
+    t = torch.arange(skew, skew + tk, device="cuda")
+    rows = order[t // page] * page + t % page
+    codes = torch.full((pages * page, 576), 0x7F, dtype=torch.uint8, device="cuda")
+    codes[rows] = a.codes[a.indices[:tk].long()]
+    last = int(rows.max()) + 1
+    b.codes, b.indices = codes[:last].clone(), rows.to(torch.int32)
+    assert a.run() == 0 and b.run() == 0
+    b.check()
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
+
+
+def test_a_bad_page_entry_in_a_run_is_reported():
+    c = Case([4], [256], paged=True, seed=18)
+    c.indices = torch.arange(100, 356, dtype=torch.int32, device="cuda")
+    c.codes = c.codes[torch.randint(256, (300,), device="cuda") % c.codes.shape[0]].clone()
+    c.codes[c.codes == 0x7F] = 0
+    assert c.run() == KV_INDEX  # rows 300 .. 355 are outside
+    c.indices -= 100
+    assert c.run() == 0
+    c.check()
