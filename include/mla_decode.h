@@ -815,8 +815,9 @@ mla_status_t mla_block_scores(const void* q_bf16, int32_t total_q, const void* m
  * row's query tokens ((recent - 1) * page_size + 1 >= tokens), the decode step masks as it does
  * over the whole row.
  *   blocks        1 .. MLA_SELECT_MAX_BLOCKS;  sink >= 0, recent >= 1, sink + recent <= blocks.
- *   scores        device float, row b at scores + b * scores_stride; those of the first `sink` and
- *                 last `recent` pages and of rows of up to `blocks` pages are not read.
+ *   scores        device float, row b at scores + b * scores_stride, max_pages entries; those of the
+ *                 first `sink` and last `recent` pages, of rows of up to `blocks` pages and behind a
+ *                 row's pages may be anything.
  *   sel_indptr    device int32 [batch + 1];  sel_indices device int32 [sel_indices_len];
  *   chosen        device int32 [batch][blocks], or NULL.
  * sel_indices past the last token keeps its values.  No output may overlap another array.  A

@@ -240,8 +240,8 @@ def _fwd(fn: str, args: tuple, q, lse, at: int) -> None:
     it that reports them, whose argument it is in place ``at``."""
     if lse is not None:
         p_lse = _dev_ptr(lse, "lse", torch.float32)
-        if lse.shape != q.shape[:2]:
-            raise ValueError(f"lse must be {list(q.shape[:2])}, got {list(lse.shape)}")
+        if lse.shape != q.shape[:2] or lse.device != q.device:
+            raise ValueError(f"lse must be {list(q.shape[:2])} on {q.device}, got {list(lse.shape)} on {lse.device}")
         fn, args = fn + "_lse", (*args[:at], p_lse, *args[at:])
     _check(fn, getattr(load_library(), fn)(*args))
 
@@ -717,10 +717,10 @@ def mla_shared_fwd_stall_stream(q, kv_fp8, kv_scale, qo_indptr, kv_indptr, out, 
 
 
 def _pages_of(means, dev: int):
-    p = _ptr(means, "means", _BF16, dev)
-    if means.dim() != 2 or means.shape[1] != QK_HEAD_DIM:
-        raise ValueError(f"means must be [pages, {QK_HEAD_DIM}], got {list(means.shape)}")
-    return p, means.shape[0]
+    p, shape = _ptr(means, "means", _BF16, dev), means.shape
+    if len(shape) != 2 or shape[1] != QK_HEAD_DIM:
+        raise ValueError(f"means must be [pages, {QK_HEAD_DIM}], got {list(shape)}")
+    return p, shape[0]
 
 
 def _means(fn, cache, rows, scale, slots, means, stream, page_size, workspace, dev):
@@ -750,13 +750,18 @@ def mla_block_means_bf16kv(kv_bf16, slots, means, stream=None, *, page_size: int
 
 def _rows_of(name: str, t, dtype, dev: int, batch: int):
     """Address, row stride and width of a [batch, width] operand with dense rows."""
-    p = _view_ptr(t, name, dtype, dev)
-    if t.dim() != 2 or t.shape[0] != batch:
-        raise ValueError(f"{name} must be [{batch}, max_pages], got {list(t.shape)}")
-    row = _stride1(name, t)
-    if row < t.shape[1]:
+    p, shape = _view_ptr(t, name, dtype, dev), t.shape
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError(f"{name} must be [{batch}, max_pages], got {list(shape)}")
+    width = shape[1]
+    row, col = t.stride()
+    if col != 1 and width > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if batch == 1:  # (a dimension of size one has no stride of its own)
+        row = width
+    if row < width:
         raise ValueError(f"{name}'s rows must not overlap")
-    return p, row, t.shape[1]
+    return p, row, width
 
 
 def mla_block_scores(q, means, block_table, qo_indptr, kv_indptr, scores, stream=None, *, page_size: int,
@@ -768,9 +773,9 @@ def mla_block_scores(q, means, block_table, qo_indptr, kv_indptr, scores, stream
     ``scores`` float32 [B, max_pages] (rows may be strided), ``qo_indptr``/``kv_indptr`` int32
     [B + 1]; scores behind a row's pages are -inf."""
     dev = _device_of(q, "q")
-    p_q, (p_means, pages) = _ptr(q, "q", _BF16, dev), _pages_of(means, dev)
-    if q.dim() != 3 or q.shape[1] != NUM_HEADS or q.shape[2] != QK_HEAD_DIM:
-        raise ValueError(f"q must be [tokens, {NUM_HEADS}, {QK_HEAD_DIM}], got {list(q.shape)}")
+    p_q, (p_means, pages), shape = _ptr(q, "q", _BF16, dev), _pages_of(means, dev), q.shape
+    if len(shape) != 3 or shape[1] != NUM_HEADS or shape[2] != QK_HEAD_DIM:
+        raise ValueError(f"q must be [tokens, {NUM_HEADS}, {QK_HEAD_DIM}], got {list(shape)}")
     p_qo, p_kv = _ptr(qo_indptr, "qo_indptr", _I32T, dev), _ptr(kv_indptr, "kv_indptr", _I32T, dev)
     b = kv_indptr.numel() - 1
     if qo_indptr.numel() != b + 1:
@@ -780,7 +785,7 @@ def mla_block_scores(q, means, block_table, qo_indptr, kv_indptr, scores, stream
     if scores_width != width:
         raise ValueError("block_table and scores must have one width")
     p_ws = _workspace(workspace, dev)
-    _call("mla_block_scores", dev, p_q, q.shape[0], p_means, pages, p_table, table_row, width, p_qo, p_kv, b,
+    _call("mla_block_scores", dev, p_q, shape[0], p_means, pages, p_table, table_row, width, p_qo, p_kv, b,
           page_size, p_scores, scores_row, p_ws, workspace.nbytes, _on("mla_block_scores", stream, dev))
     return scores
 
