@@ -122,10 +122,14 @@ MLA_HD int32_t partial_slot(int32_t c, int32_t worker_t0, int32_t prefix_b) {
 // Equal shares of `all` units of work for `workers` workers (at most `all` of them, so that
 // none is empty): worker c has the units [begin(c), begin(c + 1)), and unit u is owner(u)'s.
 // (all below 2^50 and workers below 2^13, so the products fit 64 bits.)
+// (Division in 32 bits where both fit: in 64 bits it takes the GPU some hundred cycles.)
+MLA_HD int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
 struct Shares {
   int64_t all, workers;
-  MLA_HD int64_t begin(int64_t c) const { return c * all / workers; }
-  MLA_HD int64_t owner(int64_t u) const { return ((u + 1) * workers - 1) / all; }
+  MLA_HD int64_t begin(int64_t c) const { return quotient(c * all, workers); }
+  MLA_HD int64_t owner(int64_t u) const { return quotient((u + 1) * workers - 1, all); }
 };
 
 // What a worker whose units end at `stop` has of a block of `tiles` key tiles (one unit each,

@@ -245,7 +245,7 @@ __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, 
       at -= blocks_of(g) * units_of(p, g);
       g = load_group(p, ++i, false, back);
     }
-    const int64_t size = units_of(p, g), block = at / size, begin = u - (at - block * size);
+    const int64_t size = units_of(p, g), block = quotient(at, size), begin = u - (at - block * size);
     const int32_t tiles = tiles_of_length(g.len);
     SharedPiece piece = {0, tiles, true};
     if (p.split) piece = shared_piece(begin, tiles, p.start, u, stop);
@@ -262,7 +262,7 @@ __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, 
 }
 
 // ------------------------------------------------------------ scheduler (one warp)
-// The first job is found before the roles start.
+// The first job is found before the roles start, and known to them when they do.
 __device__ __forceinline__ void run_scheduler(const SharedParams& p, const Batch& groups, Misc* ms) {
   const int lane = threadIdx.x & 31;
   int64_t u = 0;
@@ -275,14 +275,14 @@ __device__ __forceinline__ void run_scheduler(const SharedParams& p, const Batch
     const int32_t live = job->live;
     u = job->end;
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
+    if (lane == 0 && k > 0) mbar_arrive(smem_u32(&ms->job_full[k & 1]));
     if (live == 0) return;
   }
 }
 
 // Job number `k` of this block, for one of its readers (a whole warp).
 __device__ __forceinline__ bool next_job(const SharedParams& p, Misc* ms, uint32_t k, Job& job) {
-  if (!warp_wait_on(&ms->job_full[k & 1], k >> 1, ms, p.err)) return false;
+  if (k > 0 && !warp_wait_on(&ms->job_full[k & 1], (k - 1) >> 1, ms, p.err)) return false;
   job = ms->job[k & 1];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&ms->job_empty[k & 1]));
@@ -609,10 +609,6 @@ __device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
   const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t half2_mul(uint32_t a, float by) {
-  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), __float2half2_rn(by));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // 32 bytes, aligned so.
 __device__ __forceinline__ void store_sector(uint16_t* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -637,21 +633,37 @@ __device__ __forceinline__ void split_p(const uint32_t (&h)[8], uint32_t (&hi)[4
     lo[k] = pack_codes((half2_sub(a, a & kCut) << 1) + kRound, (half2_sub(b, b & kCut) << 1) + kRound);
   }
 }
-// A pair of signed codes at bits 15 .. 8 of each half.
-__device__ __forceinline__ uint32_t signed_codes(uint32_t h, uint32_t round) {
-  return (((h << 1) + round) & ~kSigns) | (h & kSigns);
+// bf16 arithmetic on pairs (exact or rounded to nearest; denormals are kept).
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-// 16 query values, scaled by `up` to at most 448 2^-8, as hi + lo / 8 in units of 2^-8.  They
-// have eight leading bits, so the rest, below 2^5 units, has four and both terms are exact
-// (but for denormals, which are rounded).
-__device__ __forceinline__ void split_q(const uint4& a, const uint4& b, float up, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The bf16 bits of 2^e, twice.
+__device__ __forceinline__ uint32_t bf16x2_power(int e) { return static_cast<uint32_t>(e + 127) * 0x00800080u; }
+// The same for a query's bf16 values, scaled so that the largest is below 2^-111: their exponent's
+// upper four bits are zero then, and bits 10 .. 4 are the e4m3 code of the value times 2^120.
+constexpr int kQueryPower = -120;
+constexpr uint32_t kQueryCut = 0xFFF0FFF0u;
+__device__ __forceinline__ uint32_t signed_codes(uint32_t v, uint32_t round) {
+  return ((v * 16 + round) & ~kSigns) | (v & kSigns);
+}
+// 16 query values, scaled by `up` to at most 448 2^-120, as hi + lo / 8 in units of 2^-120.
+// They have eight leading bits, so the rest has four and both terms are exact (but for
+// denormals, which are rounded).
+__device__ __forceinline__ void split_q(const uint4& a, const uint4& b, uint32_t up, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t x[8], y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t h = half2_bits(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
-    x[k] = signed_codes(h, 0);
-    y[k] = signed_codes(half2_mul(half2_sub(h, h & kCut), 8.0f), kRound);
+    const uint32_t v = bf16x2_mul(w[k], up);
+    x[k] = signed_codes(v, 0);
+    y[k] = signed_codes(bf16x2_mul(bf16x2_sub(v, v & kQueryCut), bf16x2_power(3)), kRound);
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -687,17 +699,22 @@ __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_
   }
   auto largest = [&](const uint4 (&v)[2]) {
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-    uint32_t lo = 0, hi = 0;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = max(lo, w[i] & 0x7FFFu);
-      hi = max(hi, w[i] & 0x7FFF0000u);
-    }
-    return max(lo, hi >> 16);
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    return max(m & 0xFFFFu, m >> 16);
   };
-  auto store = [&](const uint4 (&v)[2], float up, uint32_t at, uint32_t low_at) {
+  // Scaled by 2^by, in two steps where that is no bf16 (rows of 2^15 and more).
+  auto store = [&](uint4 (&v)[2], int by, uint32_t at, uint32_t low_at) {
     uint32_t hi[4], lo[4];
-    split_q(v[0], v[1], up, hi, lo);
+    if (__any_sync(0xffffffffu, by < -126)) {
+      const uint32_t first = bf16x2_power(by < -126 ? -120 : 0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = make_uint4(bf16x2_mul(v[i].x, first), bf16x2_mul(v[i].y, first), bf16x2_mul(v[i].z, first), bf16x2_mul(v[i].w, first));
+      by = by < -126 ? by + 120 : by;
+    }
+    split_q(v[0], v[1], bf16x2_power(by), hi, lo);
     st_shared_v4(at, hi);
     st_shared_v4(low_at, lo);
   };
@@ -708,7 +725,7 @@ __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_
   uint32_t top[kWarpRows];
 #pragma unroll
   for (int r = 0; r < kWarpRows; ++r) top[r] = __reduce_max_sync(0xffffffffu, largest(raw[r]));
-  float rope_up = 0.0f;
+  int rope_by = 0;
 #pragma unroll
   for (int r = 0; r < kWarpRows; ++r) {
     top[r] = max(top[r], __shfl_sync(0xffffffffu, rope_top, 4 * r));
@@ -717,19 +734,17 @@ __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_
     const int e = static_cast<int>(top[r] >> 7) - 127;
     int k = (top[r] & 0x7Fu) <= 0x60u ? 8 - e : 7 - e;
     k = top[r] == 0 ? 0 : min(k, 126);
-    // 2^(k - 8), which is a denormal for the largest of all
-    const float up = __int_as_float(k - 8 + 127 > 0 ? (k - 8 + 127) << 23 : 1 << (22 + (k - 8 + 127)));
-    if ((lane >> 2) % kWarpRows == r) rope_up = up;
+    if ((lane >> 2) % kWarpRows == r) rope_by = k + kQueryPower;
     const int row = kNumHeads * g + row0 + r;
     if (lane == r)
       ms->scale[g][row0 + r] = top[r] >= 0x7F80u ? __int_as_float(0x7FC00000)
                                                  : __int_as_float((127 - k) << 23) * kv_scale * kSmScaleLog2;
     const uint32_t at = sbase + kOffQ + (lane >> 3) * kPanelBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-    store(raw[r], up, at, at + kRows * 128);
+    store(raw[r], k + kQueryPower, at, at + kRows * 128);
   }
   const int row = kNumHeads * g + rope_row;
   const uint32_t at = sbase + kOffQRope + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4);
-  store(raw[kWarpRows], rope_up, at, at + kRows * 64);
+  store(raw[kWarpRows], rope_by, at, at + kRows * 64);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(smem_u32(&ms->q_full));
@@ -740,7 +755,7 @@ __device__ __forceinline__ void write_q(const SharedParams& p, Misc* ms, uint32_
 // written), and a job is taken by all four warps or by none.
 __device__ __forceinline__ bool next_job_of_group(const SharedParams& p, Misc* ms, uint32_t k, Job& job, int g) {
   const bool live = next_job(p, ms, k, job);
-  return !any_of_group(!live, g);
+  return k == 0 ? live : !any_of_group(!live, g);
 }
 
 __device__ __forceinline__ void run_softmax(const SharedParams& p, Misc* ms, uint32_t sbase, uint32_t tmem, int g) {
