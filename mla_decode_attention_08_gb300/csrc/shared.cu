@@ -187,11 +187,12 @@ __device__ __forceinline__ int64_t units_of(const SharedParams& p, const Group& 
 // A bound on units that keeps the shares' products within 64 bits.
 constexpr int64_t kManyUnits = INT64_C(1) << 48;
 
-// The groups as a warp holds them: a run of consecutive groups a lane.
+// The groups as a warp holds them: a run of consecutive groups a lane, or every lane the only one.
 struct Batch {
   int32_t g0;
   int64_t first, count;  // units before the lane's run, and in it
   Shares shares;
+  Group only;
 };
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -202,41 +203,65 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
   const int lane = threadIdx.x & 31;
   const int32_t run = (p.batch + 31) / 32;
   Batch r;
-  r.g0 = min(p.batch, lane * run);
-  const int32_t g1 = min(p.batch, r.g0 + run);
+  r.only = Group{};
   bool back = false;
-  r.count = 0;
-  for (int32_t i = r.g0; i < g1; ++i) {
-    const Group g = load_group(p, i, blockIdx.x == 0, back);
-    r.count = min(r.count + blocks_of(g) * units_of(p, g), kManyUnits / 32);
+  if (p.batch == 1) {
+    r.g0 = 0;
+    r.only = load_group(p, 0, blockIdx.x == 0 && lane == 0, back);
+    r.first = 0;
+    r.shares.all = r.count = min(blocks_of(r.only) * units_of(p, r.only), kManyUnits / 32);
+  } else {
+    r.g0 = min(p.batch, lane * run);
+    const int32_t g1 = min(p.batch, r.g0 + run);
+    r.count = 0;
+    for (int32_t i = r.g0; i < g1; ++i) {
+      const Group g = load_group(p, i, blockIdx.x == 0, back);
+      r.count = min(r.count + blocks_of(g) * units_of(p, g), kManyUnits / 32);
+    }
+    int64_t incl = r.count;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    r.first = incl - r.count;
+    r.shares.all = __shfl_sync(0xffffffffu, incl, 31);
   }
   back = __any_sync(0xffffffffu, back);
   if (blockIdx.x == 0 && lane == 0) *p.missing = back;  // (of every call anew)
-  int64_t incl = r.count;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  r.first = incl - r.count;
   // Groups overlap where offsets of queries decrease (which is reported) and could come to
   // any amount of work, so nothing is done then, and nothing joined.
-  r.shares.all = back ? 0 : __shfl_sync(0xffffffffu, incl, 31);
+  if (back) r.shares.all = 0;
   r.shares.workers = min(static_cast<int64_t>(p.workers), r.shares.all);
   return r;
 }
 
-// The job at unit `u` of this worker's range into `job` (a warp); none behind the range's end.
+// The job at unit `u` of this worker's share, which ends at `stop`: at unit `at` of group g.
+__device__ __forceinline__ void make_job(const SharedParams& p, const Group& g, int64_t u, int64_t at, int64_t stop, Job* job) {
+  const int64_t size = units_of(p, g), block = quotient(at, size), begin = u - (at - block * size);
+  const int32_t tiles = tiles_of_length(g.len);
+  SharedPiece piece = {0, tiles, true};
+  if (p.split) piece = shared_piece(begin, tiles, p.start, u, stop);
+  job->q0 = g.qs + static_cast<int32_t>(block) * kTokens;
+  // (a share that ends among a block's start units has none of it)
+  job->nq = piece.whole || piece.j1 > piece.j0 ? min(kTokens, g.n - static_cast<int32_t>(block) * kTokens) : 0;
+  job->k0 = g.ks + piece.j0 * kTileTokens;
+  job->keys = piece.j1 > piece.j0 ? min(g.len, piece.j1 * kTileTokens) - piece.j0 * kTileTokens : 0;
+  job->slot = piece.whole ? -1 : static_cast<int32_t>(shared_slot(blockIdx.x, piece.j0 == 0));
+  job->live = 1;
+  job->end = begin + size;
+}
+
+// The job at unit `u` of this worker's share into `job` (a warp); none behind the share's end.
 __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, int64_t u, Job* job) {
   const int64_t c = blockIdx.x;
   int64_t stop = 0;
   if (c < r.shares.workers) stop = r.shares.begin(c + 1);
   if (u >= stop) {
     if ((threadIdx.x & 31) == 0) job->live = job->nq = job->keys = 0;
-    __syncwarp();
-    return;
-  }
-  if (u >= r.first && u < r.first + r.count) {
+  } else if (p.batch == 1) {
+    if ((threadIdx.x & 31) == 0) make_job(p, r.only, u, u, stop, job);
+  } else if (u >= r.first && u < r.first + r.count) {
     bool back = false;
     int64_t at = u - r.first;
     int32_t i = r.g0;
@@ -245,18 +270,7 @@ __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, 
       at -= blocks_of(g) * units_of(p, g);
       g = load_group(p, ++i, false, back);
     }
-    const int64_t size = units_of(p, g), block = quotient(at, size), begin = u - (at - block * size);
-    const int32_t tiles = tiles_of_length(g.len);
-    SharedPiece piece = {0, tiles, true};
-    if (p.split) piece = shared_piece(begin, tiles, p.start, u, stop);
-    job->q0 = g.qs + static_cast<int32_t>(block) * kTokens;
-    // (a share that ends among a block's start units has none of it)
-    job->nq = piece.whole || piece.j1 > piece.j0 ? min(kTokens, g.n - static_cast<int32_t>(block) * kTokens) : 0;
-    job->k0 = g.ks + piece.j0 * kTileTokens;
-    job->keys = piece.j1 > piece.j0 ? min(g.len, piece.j1 * kTileTokens) - piece.j0 * kTileTokens : 0;
-    job->slot = piece.whole ? -1 : static_cast<int32_t>(shared_slot(c, piece.j0 == 0));
-    job->live = 1;
-    job->end = begin + size;
+    make_job(p, g, u, at, stop, job);
   }
   __syncwarp();
 }
