@@ -1154,7 +1154,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) shared_join_kernel(c
   }
   pdl_wait_primary();
   pdl_launch_dependents();
-  if (w0 == w1 || *p.missing != 0) return;
+  if (w0 == w1) return;
+  const uint32_t missing = __ldcg(p.missing);  // (looked at behind the parts, which are read all the same)
   if (!MLA_DCHECK(w0 >= 0 && w1 < p.workers && place >= 0 && place < kTokens, p.err)) return;
   // The first worker's part is its last job's, the others' their first.
   auto slot = [&](int32_t w) { return shared_slot(w, w == w0); };
@@ -1211,6 +1212,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) shared_join_kernel(c
     }
   }
   sum = over_parts(sum, 1, [](float a, float b) { return a + b; });
+  if (missing != 0) return;  // (the same for the whole block)
   if (tid < kJoinHeads) {
     weight[0][tid] = __ldg(p.kv_scale) / sum;
     if (c == 0 && p.lse != nullptr) p.lse[static_cast<int64_t>(token) * kNumHeads + head0 + tid] = top + logf(sum);
