@@ -204,3 +204,53 @@ def test_operands_of_the_wrong_kind_are_refused():
     for more in (dict(blocks=0), dict(blocks=2, sink=2), dict(recent=0), dict(num_pages=0)):
         with pytest.raises((ValueError, RuntimeError)):
             select(**more)()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_two_queries_over_three_hundred_thousand_keys(paged):
+    """Float64 sums over the keys on the GPU; the tolerances are those of the shorter rows (the probabilities' least
+    step weighs more the more keys there are: 2^-14 of the largest for each, and the others' 2^-8)."""
+    n, g = 300_001, gen(8)
+    rows = n + (99 if paged else 0)
+    codes = (torch.randn(rows, 576, generator=g, device="cuda") * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+    index = torch.randperm(rows, generator=g, device="cuda")[:n].to(torch.int32) if paged else None
+    q = (1.5 * torch.randn(2, 16, 576, generator=g, device="cuda")).bfloat16()
+    out, lse = torch.empty(2, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 16, device="cuda")
+    plan = binding.mla_shared_plan(1, 2, n)
+    ws = binding.new_workspace(plan)
+    assert plan.split == 1
+    binding.mla_shared_fwd(q, codes.view(torch.uint8), torch.full((1,), 1 / 60, device="cuda"), i32([0, 2]), i32([0, n]), out,
+                           plan=plan, workspace=ws, kv_indices=index, lse=lse)
+    assert binding.mla_decode_read_error(ws) == 0
+    keys = (codes[index.long()] if paged else codes).double() / 60
+    s = q.double().flatten(0, 1) @ keys.T / 24
+    p = (s - s.max(dim=1, keepdim=True).values).exp()
+    z = p.sum(dim=1, keepdim=True)
+    ref, reach = p @ keys[:, :512] / z, p @ keys[:, :512].abs() / z
+    e = 2.0**-14 * (q.double().flatten(0, 1).abs() @ keys.abs().T / 24).max(dim=1).values[:, None] + 2.0**-12
+    bound = (2.0**-8 * ref.abs() + (2.0**-8 + 2.0**-10 + 2 * e) * reach + 2.0**-14 * keys[:, :512].abs().sum(dim=0) / z
+             + 2.0**-25 / 60)
+    assert bool(((out.double().flatten(0, 1) - ref).abs() <= bound).all())
+    want = s.logsumexp(dim=1)
+    assert bool(((lse.double().flatten() - want).abs() <= e[:, 0] + 2.0**-22 * want.abs()).all())
+
+
+def test_scores_of_a_long_row():
+    """70,001 pages of two tokens, a second row of one page beside them."""
+    page, g, lens = 2, gen(9), [140_001, 2]
+    pages = 70_002
+    host = np.full((2, pages), -1, dtype=np.int64)
+    ids = np.random.default_rng(9).permutation(pages)
+    host[0, :70_001], host[1, 0] = ids[:70_001], ids[70_001]
+    q = torch.randn(3, 16, 576, generator=g, device="cuda").bfloat16()
+    means = (0.3 * torch.randn(pages, 576, generator=g, device="cuda")).bfloat16()
+    scores, ws = torch.full((2, pages), 7.0, device="cuda"), workspace()
+    binding.mla_block_scores(q, means, i32(host), i32([0, 2, 3]), i32(indptr(lens)), scores, page_size=page, workspace=ws)
+    assert binding.mla_decode_read_error(ws) == 0
+    ref = torch.full((2, pages), -torch.inf, dtype=torch.float64, device="cuda")
+    for b, (lo, hi, n) in enumerate(((0, 2, 70_001), (2, 3, 1))):
+        m = means[torch.from_numpy(host[b, :n]).cuda()].double()
+        ref[b, :n] = (q[lo:hi].double().flatten(0, 1) @ m.T).max(dim=0).values / 24
+    spread = float((q.double().flatten(0, 1).abs() @ means.double().abs().T).max()) / 24
+    on = ref > -torch.inf
+    assert bool(((scores > -torch.inf) == on).all()) and bool(((scores.double() - ref)[on].abs() <= 2.0**-14 * spread).all())
