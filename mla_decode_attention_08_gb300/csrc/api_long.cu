@@ -31,10 +31,10 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
 // for.  A block is one worker's, or the keys of one group's blocks are cut into k equal parts,
 // or all blocks' keys, one behind the other, into equal shares for all SMs, where a worker whose
 // share has the end of one block and the start of another does two jobs.  By the time that it
-// should take, in twentieths of a microsecond: a key tile 35, a block's start and end 100, the
-// rest of a call 100, or 190 for that and a first part and its join, where each part costs 1 and
-// each part of the same block 2; groups' keys on average at 0.7 of the longest.  (Of 70 batches
-// run with 8 to 20 cuts each, the one taken is 3 % slower than the best on average, 17 % at
+// should take, in eightieths of a microsecond: a key tile 140, a block's start and end 400, the
+// rest of a call 400, or 680 for that and a first part and its join, where each part costs 1 and
+// each part of the same block 12; groups' keys on average at 0.7 of the longest.  (Of 90 batches
+// run with 8 to 20 cuts each, the one taken is 2 % slower than the best on average, 14 % at
 // most: 4 short groups.  Blocks that are one worker's take up to 5 times the best's time where
 // they are few and long, equal shares 1.4 times where they are many and short.)
 struct Cut {
@@ -45,9 +45,9 @@ Cut cut_of(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms) {
   Cut best = {static_cast<int32_t>(blocks < sms ? (blocks > 0 ? blocks : 1) : sms), 0, 0};
   // (The second kernel looks for its tokens' groups, so thousands of them are not cut.)
   if (blocks == 0 || batch > 1024) return best;
-  int64_t least = (blocks + sms - 1) / sms * (100 + 35 * key_tiles) + 100;
+  int64_t least = (blocks + sms - 1) / sms * (400 + 140 * key_tiles) + 400;
   auto take = [&](int64_t share, int64_t of_block, int64_t parts, int64_t workers, int32_t start) {
-    const int64_t time = 190 + 35 * share + 2 * of_block + parts;
+    const int64_t time = 680 + 140 * share + 12 * of_block + parts;
     if (time >= least) return;
     least = time;
     best = Cut{static_cast<int32_t>(workers), 1, start};
