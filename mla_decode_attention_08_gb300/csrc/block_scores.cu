@@ -8,7 +8,7 @@
 // registers: a lane's 16 bytes of a page are 8 neighbouring dims, which stand for the
 // dims that two products expect there; the queries, in shared memory, are read in the
 // same order, so the sums are over the same pairs.  At 16 rows a product this is no work
-// for tcgen05, whose tiles have 128.  Six products' operands are under way at a time, across
+// for tcgen05, whose tiles have 128.  Several products' operands are under way at a time, across
 // the groups of 16 pages that a warp works through.  64 rows of up to 131072 tokens in pages of
 // 64 take 22.3 us, 115 MB at 5.2 TB/s (one group a warp at all sizes 26.8; 32 bytes a lane 29.8); 4 rows of up to
 // 8192 4.9 us, launch and three trips to memory.
@@ -20,13 +20,18 @@
 namespace mla {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpPages = 16;                       // two columns' worth of 8
 constexpr int kMaxGroups = 4;                        // of 16 pages, of a warp
 constexpr int kChunks = kQkDim / 32;                 // of 32 dims: two products
-constexpr int kAhead = 6;                            // chunks loaded together
-static_assert(kChunks % kAhead == 0, "whole groups of chunks");
+// Warps of a block, which share the queries in shared memory, and chunks of the means that a warp
+// has under way.  Four tokens' queries and sums leave room for two blocks of four warps an SM, so
+// where there is work for more warps, blocks are wide (four tokens, 64 rows of up to 131072: 41
+// us, wide 32; of up to 32768: 17.8, 13.5); with less, the queries come faster to more blocks (4
+// rows of up to 8192: 6.9, wide 8.4).
+template <bool kWide>
+constexpr int kWarpsOf = kWide ? 8 : 4;
+template <bool kWide>
+constexpr int kAheadOf = kWide ? 3 : 6;
 constexpr int kQStride = kQkDim * 2 + 64;            // bytes of a query row in shared memory: no bank twice
 constexpr int kQTokenBytes = kNumHeads * kQStride;
 
@@ -52,8 +57,10 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* src) {
 }
 
 // kTokens: query tokens that are scored together; rows of more take the means again.
-template <int kTokens>
-__global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScoresParams p, int32_t groups) {
+template <int kTokens, bool kWide>
+__global__ void __launch_bounds__(32 * kWarpsOf<kWide>, kWide ? 2 : 0) block_scores_kernel(const BlockScoresParams p, int32_t groups) {
+  constexpr int kWarps = kWarpsOf<kWide>, kThreads = 32 * kWarps, kAhead = kAheadOf<kWide>;
+  static_assert(kChunks % kAhead == 0, "whole groups of chunks");
   extern __shared__ __align__(16) uint8_t sq[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 3, col = lane >> 2;
   const int32_t b = blockIdx.y;
@@ -182,15 +189,18 @@ __global__ void __launch_bounds__(kThreads) block_scores_kernel(const BlockScore
 
 // A warp's groups of 16 pages: one where the warps then fit the GPU at once (16 an SM), up to
 // four where they would follow one another, since a warp's start is two trips to memory.
-template <int kTokens>
-cudaError_t launch_tokens(const BlockScoresParams& p, int32_t num_sms, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(p.batch) * ((p.max_pages + kWarpPages - 1) / kWarpPages);
-  int64_t groups = warps / (16 * static_cast<int64_t>(num_sms));
-  groups = groups < 1 ? 1 : groups > kMaxGroups ? kMaxGroups : groups;
-  const int64_t pages = kWarps * kWarpPages * groups;
+int64_t warps_of(const BlockScoresParams& p) { return static_cast<int64_t>(p.batch) * ((p.max_pages + kWarpPages - 1) / kWarpPages); }
+int32_t warp_groups(const BlockScoresParams& p, int32_t num_sms) {
+  const int64_t groups = warps_of(p) / (16 * static_cast<int64_t>(num_sms));
+  return static_cast<int32_t>(groups < 1 ? 1 : groups > kMaxGroups ? kMaxGroups : groups);
+}
+
+template <int kTokens, bool kWide>
+cudaError_t launch_tokens(const BlockScoresParams& p, int32_t groups, cudaStream_t stream) {
+  const int64_t pages = static_cast<int64_t>(kWarpsOf<kWide>) * kWarpPages * groups;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.max_pages + pages - 1) / pages), static_cast<unsigned>(p.batch));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * kWarpsOf<kWide>);
   cfg.dynamicSmemBytes = kTokens * kQTokenBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -198,23 +208,28 @@ cudaError_t launch_tokens(const BlockScoresParams& p, int32_t num_sms, cudaStrea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_scores_kernel<kTokens>, p, static_cast<int32_t>(groups));
+  return cudaLaunchKernelEx(&cfg, block_scores_kernel<kTokens, kWide>, p, groups);
 }
 
 }  // namespace
 
 cudaError_t block_scores_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(block_scores_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kQTokenBytes);
+  const cudaError_t e = cudaFuncSetAttribute(block_scores_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kQTokenBytes);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(block_scores_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kQTokenBytes);
+  for (auto kernel : {block_scores_kernel<4, false>, block_scores_kernel<4, true>}) {
+    const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kQTokenBytes);
+    if (f != cudaSuccess) return f;
+  }
+  return cudaSuccess;
 }
 
 // The rows' tokens are on the GPU; a row has total_q / batch of them as a rule, and any
 // number is computed.
 cudaError_t launch_block_scores(const BlockScoresParams& p, int32_t num_sms, cudaStream_t stream) {
-  if (p.total_q <= p.batch) return launch_tokens<1>(p, num_sms, stream);
-  if (p.total_q <= 2 * static_cast<int64_t>(p.batch)) return launch_tokens<2>(p, num_sms, stream);
-  return launch_tokens<4>(p, num_sms, stream);
+  const int32_t groups = warp_groups(p, num_sms);
+  if (p.total_q <= p.batch) return launch_tokens<1, false>(p, groups, stream);
+  if (p.total_q <= 2 * static_cast<int64_t>(p.batch)) return launch_tokens<2, false>(p, groups, stream);
+  return warps_of(p) <= 8 * static_cast<int64_t>(num_sms) ? launch_tokens<4, false>(p, groups, stream) : launch_tokens<4, true>(p, groups, stream);
 }
 
 }  // namespace mla

@@ -313,3 +313,19 @@ def test_captured_on_another_stream():
         assert (np.abs(f64(scores)[on] - ref[on]) <= 2.0**-14 * 40).all() and ((f64(scores) > -np.inf) == on).all()
         assert np.array_equal(sel.cpu().numpy(), want["indptr"])
         assert np.array_equal(idx.cpu().numpy()[:len(want["indices"])], want["indices"])
+
+
+@pytest.mark.parametrize("tokens", [3, 4, 5, 9])
+def test_scores_of_several_tokens_over_many_pages(tokens):
+    """More pages than narrow blocks hold at once (wide ones for four tokens), rows of several rounds of tokens."""
+    g, page, lens = gen(tokens), 2, [2 * 9001, 2 * 8000 + 1, 0, 2 * 4001]
+    table, pages = pages_of(lens, page, tokens)
+    q = torch.randn(4 * tokens, 16, 576, generator=g, device="cuda").bfloat16()
+    means = (0.3 * torch.randn(pages, 576, generator=g, device="cuda")).bfloat16()
+    scores, ws = torch.empty(table.shape, device="cuda"), workspace()
+    binding.mla_block_scores(q, means, i32(table), i32(tokens * np.arange(5)), i32(indptr(lens)), scores, page_size=page, workspace=ws)
+    assert binding.mla_decode_read_error(ws) == 0
+    ref, got = block_scores_ref(f64(q), f64(means), table, tokens * np.arange(5), indptr(lens), page), f64(scores)
+    spread = (np.abs(f64(q)).reshape(-1, 576) @ np.abs(f64(means)).T).max() / 24
+    on = ref > -np.inf
+    assert ((got > -np.inf) == on).all() and (np.abs(got[on] - ref[on]) <= 2.0**-14 * spread).all()
