@@ -4,14 +4,15 @@
 // rest those with the highest scores, the lower page where two are alike.  The last page
 // is always among them, so the number of chosen tokens follows from the lengths alone:
 // every block forms the prefix sums over all rows for itself, and one launch does the
-// step.  A block holds its row's scores in registers, consecutive pages a thread, and finds
-// the ones that are taken by their place in 256 equal steps between the lowest and the highest:
-// the steps above the one in which the last page falls are taken whole, and in that one the
-// pages are ranked against each other.  Where that leaves many (scores far apart, or alike),
-// and in rows of more pages than registers, the last taken score is found bit by bit, each a
-// count over the block.  Bound by the steps' latency, so scores and table entries are on their
-// way before the row's length is known (4 rows of 128 pages 4.2 us, 6.8 when they were loaded
-// behind it; 64 rows of 2048 pages 6.8, bit by bit alone 10.8).
+// step.  A block holds its row's scores in registers, consecutive pages a thread, or of more
+// than 8192 pages reads them anew from L2 whenever they are needed.  It finds the ones that are
+// taken by their place in 256 equal steps between the lowest and the highest: the steps above the
+// one in which the last page falls are taken whole, and in that one the pages are ranked
+// against each other, or, where it holds too many for that (scores far apart, or alike), divided
+// into steps again, of the scores' bits now, until few are left or all are the same.  Bound by the
+// steps' latency, so scores and table entries are on their way before the row's length is known
+// (4 rows of 128 pages 4.2 us, 6.8 when they were loaded behind it; 64 rows of 2048 pages 6.2, with
+// the last score found bit by bit 10.8; 64 of 8192 13.9; 8 of 16384 22.6, bit by bit 198).
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -78,7 +79,7 @@ __device__ __forceinline__ int32_t sum_before(int32_t v, int32_t* sums, int32_t*
 
 // kHeld: scores that a thread holds; with 0 they are read anew whenever they are needed.
 template <int kHeld>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelectParams p) {
+__global__ void __launch_bounds__(kThreads, kHeld > 4 ? 1 : 2) block_select_kernel(const BlockSelectParams p) {
   extern __shared__ int32_t rows[];  // [blocks]: first cache row of each chosen page, or -1
   __shared__ int64_t sums[kWarps], totals[kWarps];
   __shared__ int32_t scan[2][kWarps];
@@ -139,11 +140,10 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
   }
   if (tid == 0) p.sel_indptr[b] = static_cast<int32_t>(before);
   if (tid == 0 && b == p.batch - 1) p.sel_indptr[p.batch] = static_cast<int32_t>(total);
-  // This thread's pages, and those that are chosen by score.
-  const int32_t each = kHeld > 0 ? kHeld : (row.pages + kThreads - 1) / kThreads, first = min(row.pages, tid * each);
-  const int32_t last = min(row.pages, first + each);
-  const int32_t lo = p.sink, hi = row.pages - p.recent;
+  // Of the middle pages, [lo, hi), as many are taken as `want` says.
+  const int32_t lo = p.sink, hi = row.pages - p.recent, want = p.blocks - p.sink - p.recent;
   const bool choose = row.pages > p.blocks;
+  const int32_t first = tid * kHeld;  // of the pages in registers
   uint32_t held[kHeld > 0 ? kHeld : 1];
   if constexpr (kHeld > 0) {
 #pragma unroll
@@ -152,23 +152,28 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
       held[i] = choose && j >= lo && j < hi ? ordered(score[i]) : 0u;  // (0: no score's)
     }
   }
-  // Calls `f(place, key)` for this thread's middle pages.
+  // Calls `f(page, key)` for this thread's middle pages, in no order.
   auto each_key = [&](auto f) {
     if constexpr (kHeld > 0) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
         if (held[i] != 0) f(first + i, held[i]);
     } else {
-      for (int32_t j = max(first, lo); j < min(last, hi); ++j) f(j, ordered(scores[j]));
+      constexpr int kAtOnce = 16;
+      for (int32_t j0 = lo + tid; j0 < hi; j0 += kAtOnce * kThreads) {
+        float x[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) x[i] = j0 + i * kThreads < hi ? scores[j0 + i * kThreads] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+          if (j0 + i * kThreads < hi) f(j0 + i * kThreads, ordered(x[i]));
+      }
     }
   };
-  // Pages with a key above `threshold` are taken, and `ties` of those at it; or, where the
-  // steps decide, the ones marked in `mine`.
-  uint32_t threshold = 0, marks = 0;
+  // Middle pages with a key above `threshold` are taken, and the first `ties` of those at it.
+  uint32_t threshold = 0xFFFFFFFFu;
   int32_t ties = 0;
-  bool by_steps = false;
-  const int32_t want = p.blocks - p.sink - p.recent;
-  if (kHeld > 0 && choose && want > 0) {
+  if (choose && want > 0) {
     // Between the lowest and the highest finite score; what is not finite falls on the ends.
     uint32_t low = 0xFFFFFFFFu, high = 0;
     each_key([&](int32_t, uint32_t key) {
@@ -199,113 +204,165 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
     __syncthreads();
     // The highest step with which there are enough (every warp for itself): lane l has the
     // steps 8 l .. 8 l + 7.
-    int32_t c[8], own = 0;
+    int32_t above = 0, inside = 0;  // pages above the step, and in it
+    auto find_step = [&] {
+      const int32_t need = want - above;
+      int32_t c[8], own = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) own += c[i] = counts[8 * lane + i];
-    int32_t from = own;  // in this lane's steps and above
+      for (int i = 0; i < 8; ++i) own += c[i] = counts[8 * lane + i];
+      int32_t from = own;  // in this lane's steps and above
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t v = __shfl_down_sync(0xffffffffu, from, d);
-      if (lane + d < 32) from += v;
-    }
-    int32_t above = from - own, step = -1, inside = 0;
-    if (above < want && from >= want) {
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t v = __shfl_down_sync(0xffffffffu, from, d);
+        if (lane + d < 32) from += v;
+      }
+      int32_t over = from - own, step = -1, in = 0;
+      if (over < need && from >= need) {
 #pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        if (step >= 0) continue;
-        if (above + c[i] >= want) {
-          step = 8 * lane + i;
-          inside = c[i];
-        } else {
-          above += c[i];
+        for (int i = 7; i >= 0; --i) {
+          if (step >= 0) continue;
+          if (over + c[i] >= need) {
+            step = 8 * lane + i;
+            in = c[i];
+          } else {
+            over += c[i];
+          }
         }
       }
+      const int who = __ffs(__ballot_sync(0xffffffffu, step >= 0)) - 1;
+      above += __shfl_sync(0xffffffffu, over, who);
+      inside = __shfl_sync(0xffffffffu, in, who);
+      return __shfl_sync(0xffffffffu, step, who);
+    };
+    const int step = find_step();
+    bool by_value = true;  // the open pages are the step's, else those with a key in [low, high]
+    if (inside > kListed) {
+      by_value = false;
+      low = 0xFFFFFFFFu, high = 0;
+      each_key([&](int32_t, uint32_t key) {
+        if (step_of(key) != step) return;
+        low = min(low, key);
+        high = max(high, key);
+      });
+      low = __reduce_min_sync(0xffffffffu, low);
+      high = __reduce_max_sync(0xffffffffu, high);
+      if (lane == 0) {
+        scan[0][warp] = static_cast<int32_t>(low);
+        scan[1][warp] = static_cast<int32_t>(high);
+      }
+      __syncthreads();  // (counts are read, too)
+      low = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(scan[0][lane % kWarps]));
+      high = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(scan[1][lane % kWarps]));
+      while (inside > kListed && low < high) {  // (each time a range 2^7 times smaller, or more)
+        if (tid < kSteps) counts[tid] = 0;
+        __syncthreads();
+        const int shift = max(0, 24 - __clz(high - low));
+        each_key([&](int32_t, uint32_t key) {
+          if (key >= low && key <= high) atomicAdd(&counts[(key - low) >> shift], 1);
+        });
+        __syncthreads();
+        low += static_cast<uint32_t>(find_step()) << shift;
+        high = low + min(high - low, (1u << shift) - 1);
+        __syncthreads();  // (counts are read)
+      }
     }
-    const int who = __ffs(__ballot_sync(0xffffffffu, step >= 0)) - 1;
-    step = __shfl_sync(0xffffffffu, step, who);
-    above = __shfl_sync(0xffffffffu, above, who);
-    inside = __shfl_sync(0xffffffffu, inside, who);
-    by_steps = inside <= kListed;
-    if (by_steps) {
+    if (inside > kListed) {  // all alike
+      threshold = low;
+      ties = want - above;
+    } else {
       each_key([&](int32_t j, uint32_t key) {
-        const int at = step_of(key);
-        if (at > step) marks |= 1u << (j - first);
-        if (at != step) return;
+        if (by_value ? step_of(key) != step : key < low || key > high) return;
         const int to = atomicAdd(&listed, 1);
         if (MLA_DCHECK(to < inside && to < kListed, p.err)) list[to] = make_uint2(key, static_cast<uint32_t>(j));
       });
       __syncthreads();
-      each_key([&](int32_t j, uint32_t key) {
-        if (step_of(key) != step) return;
-        int32_t rank = above;
+      // The last page that is taken gives the threshold.
+      if (tid < inside) {
+        const uint2 mine = list[tid];
+        int32_t over = above, alike = 0, before_it = 0;
         for (int i = 0; i < inside; ++i) {
           const uint2 other = list[i];
-          rank += other.x > key || (other.x == key && other.y < static_cast<uint32_t>(j));
+          over += other.x > mine.x;
+          alike += other.x == mine.x;
+          before_it += other.x == mine.x && other.y < mine.y;
         }
-        if (rank < want) marks |= 1u << (j - first);
-      });
-    }
-  }
-  if (choose && !by_steps) {
-    int32_t above = 0;  // pages above threshold | what is still open
-    bool exact = want == 0;
-    if (exact) threshold = 0xFFFFFFFFu;
-    __syncthreads();  // (scan is read)
-    for (uint32_t bit = 0x80000000u; bit != 0 && !exact; bit >>= 1) {
-      int32_t mine = 0;
-      each_key([&](int32_t, uint32_t key) { mine += key >= (threshold | bit); });
-      const int32_t sum = __reduce_add_sync(0xffffffffu, mine);
-      int32_t* part = scan[bit & 0x55555555u ? 0 : 1];  // (alternating: the others may still be read)
-      if (lane == 0) part[warp] = sum;
-      __syncthreads();
-      int32_t enough = lane < kWarps ? part[lane] : 0;
-      enough = __reduce_add_sync(0xffffffffu, enough);
-      if (enough >= want) threshold |= bit;
-      else above = enough;
-      if (enough == want) {  // these are the ones
-        exact = true;
-        threshold -= 1;  // (a key above it is one of them)
+        if (over + before_it == want - 1) {  // (with all that are like it: the ones above the next lower key)
+          const bool whole = before_it + 1 == alike;
+          scan[0][0] = static_cast<int32_t>(mine.x - whole);
+          scan[1][0] = whole ? 0 : before_it + 1;
+        }
       }
+      __syncthreads();
+      threshold = static_cast<uint32_t>(scan[0][0]);
+      ties = scan[1][0];
     }
-    if (!exact) ties = want - above;
   }
   __syncthreads();  // (scan is read)
 
   // The pages in order: a page's place among the chosen is the number before it.
   auto is_middle = [&](int32_t j) { return choose && j >= lo && j < hi; };
-  int32_t mine = 0, all = 0;
-  if (ties > 0) each_key([&](int32_t, uint32_t key) { mine += key == threshold; });
-  const int32_t rank = ties > 0 ? sum_before(mine, scan[0], &all) : 0;
-  // (a tie is taken while its rank among them is below `ties`)
-  int32_t taken = 0, tie = rank;
-  // Calls `f(page, table entry)` for this thread's pages that are taken.
-  auto walk = [&](auto f) {
+  auto put = [&](int32_t place, int32_t j, int32_t id) {
+    if (place >= p.blocks) return;
+    const bool ok = id >= 0 && id < p.num_pages;
+    if (!ok) atomicOr(p.err, MLA_DERR_KV_INDEX);
+    rows[place] = ok ? id * p.page_size : -1;
+    if (chosen != nullptr) chosen[place] = j;
+  };
+  int32_t all = 0;
+  if constexpr (kHeld > 0) {
+    int32_t alike = 0;
+    if (ties > 0) each_key([&](int32_t, uint32_t key) { alike += key == threshold; });
+    const int32_t rank = ties > 0 ? sum_before(alike, scan[0], &all) : 0;
+    // (a tie is taken while its rank among them is below `ties`)
+    int32_t taken = 0, tie = rank;
     auto takes = [&](int32_t j, uint32_t key) {
       if (!is_middle(j)) return true;
-      if (by_steps) return (marks >> (j - first) & 1) != 0;
-      return key > threshold || (ties > 0 && key == threshold && tie++ < ties);
+      return key > threshold || (key == threshold && tie++ < ties);
     };
-    if constexpr (kHeld > 0) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        if (first + i < last && takes(first + i, held[i])) f(first + i, entry[i]);
-    } else {
-      for (int32_t j = first; j < last; ++j)
-        if (takes(j, is_middle(j) ? ordered(scores[j]) : 0u)) f(j, table[j]);
+    for (int i = 0; i < kHeld; ++i)
+      if (first + i < row.pages && takes(first + i, held[i])) ++taken;
+    int32_t place = sum_before(taken, scan[1], &all);
+    tie = rank;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (first + i < row.pages && takes(first + i, held[i])) put(place++, first + i, entry[i]);
+  } else {
+    // Some consecutive pages a thread at a time; the table is read where one is taken.
+    constexpr int kEach = 16;
+    int32_t done = 0, tied = 0;  // pages and ties taken before
+    for (int32_t base = 0; base < row.pages; base += kEach * kThreads) {
+      const int32_t j0 = base + kEach * tid;
+      uint32_t take = 0, equal = 0;
+      float x[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) x[i] = j0 + i < row.pages ? scores[j0 + i] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int32_t j = j0 + i;
+        if (j >= row.pages) continue;
+        const uint32_t key = ordered(x[i]);
+        if (!is_middle(j) || key > threshold) take |= 1u << i;
+        else if (key == threshold) equal |= 1u << i;
+      }
+      if (ties > 0) {  // (the same for the whole block)
+        const int32_t rank = tied + sum_before(__popc(equal), scan[0], &all);
+        tied += all;
+        // as many of this thread's, the first of them, as there is room for
+        for (int32_t room = ties - rank; room > 0 && equal != 0; --room) {
+          take |= equal & -equal;
+          equal &= equal - 1;
+        }
+      }
+      int32_t place = done + sum_before(__popc(take), scan[1], &all);
+      done += all;
+      for (; take != 0; take &= take - 1) {
+        const int32_t j = j0 + __ffs(take) - 1;
+        put(place++, j, table[j]);
+      }
+      if (ties == 0) __syncthreads();  // (scan[1] is read)
     }
-  };
-  walk([&](int32_t, int32_t) { ++taken; });
-  int32_t place = sum_before(taken, scan[1], &all);
-  tie = rank;
-  walk([&](int32_t j, int32_t id) {
-    if (place < p.blocks) {
-      const bool ok = id >= 0 && id < p.num_pages;
-      if (!ok) atomicOr(p.err, MLA_DERR_KV_INDEX);
-      rows[place] = ok ? id * p.page_size : -1;
-      if (chosen != nullptr) chosen[place] = j;
-    }
-    ++place;
-  });
+  }
   if (chosen != nullptr)
     for (int32_t i = row.taken + tid; i < p.blocks; i += kThreads) chosen[i] = -1;
   __syncthreads();
@@ -324,19 +381,21 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const BlockSelec
 }  // namespace
 
 cudaError_t block_select_prepare() {
-  for (auto kernel : {block_select_kernel<1>, block_select_kernel<4>, block_select_kernel<16>, block_select_kernel<0>}) {
+  for (auto kernel : {block_select_kernel<1>, block_select_kernel<4>, block_select_kernel<8>, block_select_kernel<16>, block_select_kernel<0>}) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MLA_SELECT_MAX_BLOCKS * 4);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-// Scores in registers where a row's pages fit them, as few a thread as do.
+// Scores in registers where a row's pages fit them, as few a thread as do (64 rows of 4096 pages: 7.9
+// us with eight, 12.2 with sixteen; of 16384 from L2 23.4).
 cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.batch);
   const size_t smem = static_cast<size_t>(p.blocks) * 4;
   if (p.max_pages <= kThreads) return launch_dependent(block_select_kernel<1>, grid, kThreads, smem, stream, p);
   if (p.max_pages <= 4 * kThreads) return launch_dependent(block_select_kernel<4>, grid, kThreads, smem, stream, p);
+  if (p.max_pages <= 8 * kThreads) return launch_dependent(block_select_kernel<8>, grid, kThreads, smem, stream, p);
   if (p.max_pages <= 16 * kThreads) return launch_dependent(block_select_kernel<16>, grid, kThreads, smem, stream, p);
   return launch_dependent(block_select_kernel<0>, grid, kThreads, smem, stream, p);
 }

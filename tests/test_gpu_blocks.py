@@ -329,3 +329,37 @@ def test_scores_of_several_tokens_over_many_pages(tokens):
     spread = (np.abs(f64(q)).reshape(-1, 576) @ np.abs(f64(means)).T).max() / 24
     on = ref > -np.inf
     assert ((got > -np.inf) == on).all() and (np.abs(got[on] - ref[on]) <= 2.0**-14 * spread).all()
+
+
+@pytest.mark.parametrize("kind", ["same", "two", "close", "far", "huge", "mixed", "steps"])
+@pytest.mark.parametrize("pages", [900, 2048, 4096, 8192, 8193, 20_000])
+def test_choice_where_the_steps_hold_many(pages, kind):
+    """Scores alike, close together beside a few far away, over the whole range of float32, not finite: the steps
+    are divided again until few pages are left."""
+    g, lens, page = gen(pages), [3 * pages, 3 * (pages // 2) + 1], 3
+    table, num = pages_of(lens, page, pages)
+    x = torch.randn(table.shape, generator=g, device="cuda")
+    if kind == "same":
+        x[:] = -2.5
+    elif kind == "two":
+        x = torch.where(x > 0.5, 1.0, -0.0)
+    elif kind == "close":
+        x = 1.0 + x * 2.0**-20
+        x[:, 77] = 1e20
+        x[:, 78] = -1e20
+    elif kind == "far":
+        x = x.sign() * (x * 30).exp()
+    elif kind == "huge":
+        x = x.sign() * 3.3e38 * torch.rand(x.shape, generator=g, device="cuda")
+    elif kind == "mixed":
+        x[x > 1.0] = float("inf")
+        x[x < -0.5] = -float("inf")
+        x[:, 5::17] = float("nan")
+    else:
+        x = (x * 4).round() * 2.0**-30
+    for blocks in (4, pages // 3, pages - 5):
+        if blocks > 8192:
+            blocks = 8192
+        ref, (ptr, idx, chosen), err = select(x, table, lens, page, num, blocks, 1, 2)
+        assert err == 0 and np.array_equal(ptr, ref["indptr"]) and np.array_equal(chosen, ref["chosen"]), blocks
+        assert np.array_equal(idx[:-4], ref["indices"]) and (idx[-4:] == -7).all()
