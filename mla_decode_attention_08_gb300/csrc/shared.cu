@@ -166,16 +166,20 @@ __device__ __forceinline__ void drain(const uint64_t* bar, uint32_t parity) {
 struct Group {
   int32_t qs, n, ks, len;
 };
-// (`back`: set when the group ends before it begins; a bad group has no tokens.)
-__device__ __forceinline__ Group load_group(const SharedParams& p, int32_t g, bool report, bool& back) {
-  const int32_t qs = __ldg(p.qo_indptr + g), qe = __ldg(p.qo_indptr + g + 1);
-  const int32_t ks = __ldg(p.kv_indptr + g), ke = __ldg(p.kv_indptr + g + 1);
+// A group from its offsets.  (`back`: set when the group ends before it begins; a bad group has no
+// tokens.)
+__device__ __forceinline__ Group group_of(const SharedParams& p, int32_t qs, int32_t qe, int32_t ks, int32_t ke, bool report,
+                                          bool& back) {
   const bool bad_q = qs < 0 || qe < qs || qe > p.total_q;
   const bool bad_k = ks < 0 || ke < ks || ke > p.kv_limit || ke - ks > MLA_SHARED_MAX_KEYS;
   back = back || qe < qs;
   if (report && (bad_q || bad_k))
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
   return bad_q || bad_k ? Group{0, 0, 0, 0} : Group{qs, qe - qs, ks, ke - ks};
+}
+__device__ __forceinline__ Group load_group(const SharedParams& p, int32_t g, bool report, bool& back) {
+  return group_of(p, __ldg(p.qo_indptr + g), __ldg(p.qo_indptr + g + 1), __ldg(p.kv_indptr + g), __ldg(p.kv_indptr + g + 1), report,
+                  back);
 }
 __device__ __forceinline__ int64_t blocks_of(const Group& g) { return (g.n + kTokens - 1) / kTokens; }
 
@@ -189,8 +193,9 @@ constexpr int64_t kManyUnits = INT64_C(1) << 48;
 
 // The groups as a warp holds them: a run of consecutive groups a lane, or every lane the only one.
 struct Batch {
-  int32_t g0;
   int64_t first, count;  // units before the lane's run, and in it
+  int32_t at;            // the group of the run that the last job was found in (or before it) ...
+  int64_t at_unit;       // ... and units before it
   Shares shares;
   Group only;
 };
@@ -206,17 +211,28 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
   r.only = Group{};
   bool back = false;
   if (p.batch == 1) {
-    r.g0 = 0;
+    r.at = 0;
     r.only = load_group(p, 0, blockIdx.x == 0 && lane == 0, back);
     r.first = 0;
     r.shares.all = r.count = min(blocks_of(r.only) * units_of(p, r.only), kManyUnits / 32);
   } else {
-    r.g0 = min(p.batch, lane * run);
-    const int32_t g1 = min(p.batch, r.g0 + run);
+    r.at = min(p.batch, lane * run);
+    const int32_t g1 = min(p.batch, r.at + run);
     r.count = 0;
-    for (int32_t i = r.g0; i < g1; ++i) {
-      const Group g = load_group(p, i, blockIdx.x == 0, back);
-      r.count = min(r.count + blocks_of(g) * units_of(p, g), kManyUnits / 32);
+    constexpr int kAtOnce = 4;  // offsets loaded together: one by one, each is a trip to L2
+    for (int32_t i0 = r.at; i0 < g1; i0 += kAtOnce) {
+      int32_t q[kAtOnce + 1], k[kAtOnce + 1];
+#pragma unroll
+      for (int i = 0; i <= kAtOnce; ++i) {
+        q[i] = __ldg(p.qo_indptr + min(i0 + i, g1));
+        k[i] = __ldg(p.kv_indptr + min(i0 + i, g1));
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i0 + i >= g1) break;
+        const Group g = group_of(p, q[i], q[i + 1], k[i], k[i + 1], blockIdx.x == 0, back);
+        r.count = min(r.count + blocks_of(g) * units_of(p, g), kManyUnits / 32);
+      }
     }
     int64_t incl = r.count;
 #pragma unroll
@@ -224,7 +240,7 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += v;
     }
-    r.first = incl - r.count;
+    r.first = r.at_unit = incl - r.count;
     r.shares.all = __shfl_sync(0xffffffffu, incl, 31);
   }
   back = __any_sync(0xffffffffu, back);
@@ -253,7 +269,8 @@ __device__ __forceinline__ void make_job(const SharedParams& p, const Group& g, 
 }
 
 // The job at unit `u` of this worker's share into `job` (a warp); none behind the share's end.
-__device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, int64_t u, Job* job) {
+// Units only rise, so a lane looks on from the group where it found the last one.
+__device__ __forceinline__ void find_job(const SharedParams& p, Batch& r, int64_t u, Job* job) {
   const int64_t c = blockIdx.x;
   int64_t stop = 0;
   if (c < r.shares.workers) stop = r.shares.begin(c + 1);
@@ -263,21 +280,19 @@ __device__ __forceinline__ void find_job(const SharedParams& p, const Batch& r, 
     if ((threadIdx.x & 31) == 0) make_job(p, r.only, u, u, stop, job);
   } else if (u >= r.first && u < r.first + r.count) {
     bool back = false;
-    int64_t at = u - r.first;
-    int32_t i = r.g0;
-    Group g = load_group(p, i, false, back);
-    while (at >= blocks_of(g) * units_of(p, g)) {  // (ends within the lane's run)
-      at -= blocks_of(g) * units_of(p, g);
-      g = load_group(p, ++i, false, back);
+    Group g = load_group(p, r.at, false, back);
+    while (u - r.at_unit >= blocks_of(g) * units_of(p, g)) {  // (ends within the lane's run)
+      r.at_unit += blocks_of(g) * units_of(p, g);
+      g = load_group(p, ++r.at, false, back);
     }
-    make_job(p, g, u, at, stop, job);
+    make_job(p, g, u, u - r.at_unit, stop, job);
   }
   __syncwarp();
 }
 
 // ------------------------------------------------------------ scheduler (one warp)
 // The first job is found before the roles start, and known to them when they do.
-__device__ __forceinline__ void run_scheduler(const SharedParams& p, const Batch& groups, Misc* ms) {
+__device__ __forceinline__ void run_scheduler(const SharedParams& p, Batch& groups, Misc* ms) {
   const int lane = threadIdx.x & 31;
   int64_t u = 0;
   for (uint32_t k = 0;; ++k) {

@@ -254,3 +254,27 @@ def test_scores_of_a_long_row():
     spread = float((q.double().flatten(0, 1).abs() @ means.double().abs().T).max()) / 24
     on = ref > -torch.inf
     assert bool(((scores > -torch.inf) == on).all()) and bool(((scores.double() - ref)[on].abs() <= 2.0**-14 * spread).all())
+
+
+def test_twenty_thousand_groups():
+    """Runs of hundreds of groups a lane of the warp that finds the jobs, some without queries or keys."""
+    rng = np.random.default_rng(11)
+    q, kv = rng.integers(0, 3, 20_000), rng.integers(0, 4, 20_000)
+    q[[0, 5000, 19_999]] = [9, 0, 6]
+    c = Case([int(x) for x in q], [int(x) for x in kv], True, seed=11, lead=1, tail=1)
+    assert c.run() == 0
+    got, lse, group = f64(c.out), f64(c.lse), np.repeat(np.arange(20_000), q)
+    assert (got[0] == 7).all() and (got[-1] == 7).all()
+    empty = kv[group] == 0
+    assert (got[1:-1][empty] == 0).all() and (lse[1:-1][empty] == -np.inf).all()
+    one = kv[group] == 1  # a single key's values, twice rounded
+    keys = f64(c.codes.view(torch.float8_e4m3fn)[c.indices.long()].float()) / 60
+    first = keys[c.kv[:-1][group[one]]]
+    assert (np.abs(got[1:-1][one] - first[:, None, :512]) <= (2.0**-8 + 2.0**-8) * np.abs(first[:, None, :512]) + 2.0**-14).all()
+    for g in rng.integers(0, 20_000, 300):
+        a, b = int(c.qo[g]), int(c.qo[g + 1])
+        if a == b or kv[g] == 0:
+            continue
+        ref, ref_lse = attend_ref(f64(c.q[a:b]), keys[int(c.kv[g]):int(c.kv[g + 1])])
+        assert np.linalg.norm(got[a:b] - ref) <= 2.0**-7 * np.linalg.norm(ref)
+        assert np.abs(lse[a:b] - ref_lse).max() <= 2.0**-8  # 2^-14 of spreads below 40, and the query's terms
