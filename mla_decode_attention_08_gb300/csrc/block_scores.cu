@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<kWide>, kWide ? 2 : 0) block_sco
   const int32_t qs = __ldg(p.qo_indptr + b), qe = __ldg(p.qo_indptr + b + 1);
   const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
   const int64_t len = static_cast<int64_t>(ke) - ks;
-  const int64_t pages = (len + p.page_size - 1) / p.page_size;
-  const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || len < 0 || pages > p.max_pages;
+  const uint32_t pages = pages_of(len, p.page_size);
+  const bool bad_q = qs < 0 || qe < qs || qe > p.total_q, bad_k = ks < 0 || len < 0 || pages > static_cast<uint32_t>(p.max_pages);
   if ((bad_q || bad_k) && tid == 0 && blockIdx.x == 0)
     atomicOr(p.err, (bad_q ? MLA_DERR_QO_INDPTR : 0) | (bad_k ? MLA_DERR_KV_INDPTR : 0));
   const int32_t n = bad_q || bad_k ? 0 : static_cast<int32_t>(pages);

@@ -11,11 +11,12 @@
 // against each other, or, where it holds too many for that (scores far apart, or alike), divided
 // into steps again, of the scores' bits now, until few are left or all are the same.  Bound by the
 // steps' latency, so scores and table entries are on their way before the row's length is known
-// (4 rows of 128 pages 4.2 us, 6.8 when they were loaded behind it; 64 rows of 2048 pages 6.2, with
+// (4 rows of 128 pages 4.0 us, 6.8 when they were loaded behind it; 64 rows of 2048 pages 5.7, with
 // the last score found bit by bit 10.8; 64 of 8192 13.9; 8 of 16384 22.6, bit by bit 198).
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
+#include "schedule.h"
 
 namespace mla {
 namespace {
@@ -46,8 +47,8 @@ __device__ __forceinline__ RowCount count_row(const BlockSelectParams& p, int32_
   const int32_t ks = __ldg(p.kv_indptr + b), ke = __ldg(p.kv_indptr + b + 1);
   const int64_t len = static_cast<int64_t>(ke) - ks;
   RowCount r;
-  const int64_t pages = (len + p.page_size - 1) / p.page_size;
-  r.bad = ks < 0 || len < 0 || pages > p.max_pages;
+  const uint32_t pages = pages_of(len, p.page_size);
+  r.bad = ks < 0 || len < 0 || pages > static_cast<uint32_t>(p.max_pages);
   r.pages = r.bad ? 0 : static_cast<int32_t>(pages);
   r.taken = min(r.pages, p.blocks);
   // all pages but the last are full

@@ -155,4 +155,10 @@ MLA_HD SharedPiece shared_piece(int64_t begin, int32_t tiles, int32_t start, int
 // (slot 2 c), its last may begin one (slot 2 c + 1).
 MLA_HD int64_t shared_slot(int64_t c, bool begins) { return 2 * c + (begins ? 1 : 0); }
 
+// Pages of a row of `len` tokens, 0 .. 2^31 - 1 (anything for other lengths): divided in 32 bits, since in 64
+// bits it takes the GPU some hundred cycles.
+MLA_HD uint32_t pages_of(int64_t len, int32_t page_size) {
+  return (static_cast<uint32_t>(len) + static_cast<uint32_t>(page_size) - 1u) / static_cast<uint32_t>(page_size);
+}
+
 }  // namespace mla
