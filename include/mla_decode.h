@@ -732,7 +732,8 @@ typedef struct {
   int32_t split;       /* 1: a group's keys may be shared by workers, whose parts a second
                         * kernel joins (batch up to 1024); 0: they are not             */
   int32_t start;       /* key tiles that the start of a block of four queries counts for
-                        * where all keys are cut into equal shares (0 .. 64)           */
+                        * where all keys are cut into equal shares, or whole blocks are
+                        * dealt out by such shares (0 .. 64)                           */
   int32_t abi_version; /* MLA_ABI_VERSION                                              */
   uint64_t ws_bytes;   /* workspace bytes mla_shared_fwd needs                         */
   uint64_t ws_lse_offset;     /* float[2 * workers][64] when split                     */

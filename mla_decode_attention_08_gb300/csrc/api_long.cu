@@ -37,14 +37,25 @@ int64_t most_blocks(int64_t total_q, int64_t batch) {
 // run with 8 to 20 cuts each, the one taken is 2 % slower than the best on average, 14 % at
 // most: 4 short groups.  Blocks that are one worker's take up to 5 times the best's time where
 // they are few and long, equal shares 1.4 times where they are many and short.)
+// More groups than the second kernel looks through are not cut, whatever their blocks' time, so
+// their whole blocks are dealt out by those shares, each to the worker that its start falls to: 256
+// queries over 32768 keys among 1100 groups of one over up to 200 take 571 us, by count 3147; 2000
+// groups of up to eight over up to 3000 651, by count 743.  By count where blocks can differ by
+// no tile (16384 groups of one over 30 keys: 1080, by shares 1097), and of fewer groups, where
+// whole blocks are only taken if as many of the longest are fast enough (300 of one over up to 1000:
+// 42, by shares 45).
 struct Cut {
   int32_t workers, split, start;
 };
 constexpr int32_t kStartUnits = 4;
+constexpr int64_t kMostCutGroups = 1024;
 Cut cut_of(int64_t blocks, int64_t batch, int64_t key_tiles, int64_t sms) {
   Cut best = {static_cast<int32_t>(blocks < sms ? (blocks > 0 ? blocks : 1) : sms), 0, 0};
-  // (The second kernel looks for its tokens' groups, so thousands of them are not cut.)
-  if (blocks == 0 || batch > 1024) return best;
+  if (blocks == 0) return best;
+  if (batch > kMostCutGroups) {  // (the second kernel looks for its tokens' groups)
+    if (blocks > sms && key_tiles > 1) best.start = kStartUnits;
+    return best;
+  }
   int64_t least = (blocks + sms - 1) / sms * (400 + 140 * key_tiles) + 400;
   auto take = [&](int64_t share, int64_t of_block, int64_t parts, int64_t workers, int32_t start) {
     const int64_t time = 680 + 140 * share + 12 * of_block + parts;
@@ -74,7 +85,7 @@ bool plan_fields(int32_t batch, int32_t total_q, int32_t max_kv_len, int32_t num
   p.start = cut.start;
   p.abi_version = MLA_ABI_VERSION;
   if (cut.workers < 1 || cut.workers > MLA_SHARED_MAX_WORKERS || (cut.split != 0 && cut.split != 1) ||
-      cut.start < 0 || cut.start > 64 || (cut.split == 1 && batch > 1024))
+      cut.start < 0 || cut.start > 64 || (cut.split == 1 && batch > kMostCutGroups))
     return false;
   uint64_t off = kAlign;  // error word
   p.ws_lse_offset = p.ws_partial_offset = off;

@@ -151,6 +151,11 @@ MLA_HD SharedPiece shared_piece(int64_t begin, int32_t tiles, int32_t start, int
   p.whole = p.j0 == 0 && p.j1 == tiles && stop > tile0;
   return p;
 }
+// The same of blocks that are not cut: a block is whole and the worker's that has its first unit, and
+// nothing at its other units, where a worker's share may begin.
+MLA_HD SharedPiece uncut_piece(int64_t begin, int32_t tiles, int64_t u) {
+  return u == begin ? SharedPiece{0, tiles, true} : SharedPiece{0, 0, false};
+}
 // Where the worker leaves that piece, if it is not whole: its first piece may continue a block
 // (slot 2 c), its last may begin one (slot 2 c + 1).
 MLA_HD int64_t shared_slot(int64_t c, bool begins) { return 2 * c + (begins ? 1 : 0); }

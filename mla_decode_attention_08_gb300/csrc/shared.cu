@@ -18,7 +18,7 @@
 // Persistent blocks, one an SM, are workers.  Every four query tokens of a group, with their
 // keys, are a block of units, a unit a key tile and some for its start; all blocks' units
 // one behind the other are cut into equal ranges, a worker each.  A job is what a range has
-// of one block:
+// of one block, or, of blocks that are not cut, the whole of each that begins in the range:
 //   * warp 3 finds the jobs,
 //   * the keys come as four panels of 128 dims a tile into two buffers, and the 64 rotated
 //     dims into one: by warp 2 through TMA in boxes of 128 rows, or, by a page table, by
@@ -183,10 +183,10 @@ __device__ __forceinline__ Group load_group(const SharedParams& p, int32_t g, bo
 }
 __device__ __forceinline__ int64_t blocks_of(const Group& g) { return (g.n + kTokens - 1) / kTokens; }
 
-// A block's units: of a split plan its key tiles (one if it has none) behind `start` ones,
-// else one.
+// A block's units: its key tiles (one if it has none) behind `start` ones, or one where blocks are
+// dealt out by their number.
 __device__ __forceinline__ int64_t units_of(const SharedParams& p, const Group& g) {
-  return p.split ? p.start + max(1, tiles_of_length(g.len)) : 1;
+  return p.split || p.start > 0 ? p.start + max(1, tiles_of_length(g.len)) : 1;
 }
 // A bound on units that keeps the shares' products within 64 bits.
 constexpr int64_t kManyUnits = INT64_C(1) << 48;
@@ -256,10 +256,10 @@ __device__ __forceinline__ Batch count_groups(const SharedParams& p) {
 __device__ __forceinline__ void make_job(const SharedParams& p, const Group& g, int64_t u, int64_t at, int64_t stop, Job* job) {
   const int64_t size = units_of(p, g), block = quotient(at, size), begin = u - (at - block * size);
   const int32_t tiles = tiles_of_length(g.len);
-  SharedPiece piece = {0, tiles, true};
-  if (p.split) piece = shared_piece(begin, tiles, p.start, u, stop);
+  const SharedPiece piece = p.split ? shared_piece(begin, tiles, p.start, u, stop) : uncut_piece(begin, tiles, u);
   job->q0 = g.qs + static_cast<int32_t>(block) * kTokens;
-  // (a share that ends among a block's start units has none of it)
+  // (a share that ends among a block's start units, or begins inside a block that is not cut, has none
+  // of it: a job without query tokens, which all roles pass over)
   job->nq = piece.whole || piece.j1 > piece.j0 ? min(kTokens, g.n - static_cast<int32_t>(block) * kTokens) : 0;
   job->k0 = g.ks + piece.j0 * kTileTokens;
   job->keys = piece.j1 > piece.j0 ? min(g.len, piece.j1 * kTileTokens) - piece.j0 * kTileTokens : 0;
