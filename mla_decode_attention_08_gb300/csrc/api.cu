@@ -348,9 +348,8 @@ mla_status_t run_decode(const void* q, const void* kv, const float* kv_scale,
 
 mla_status_t mla::device_ready(int* device) { return prepare_device(device); }
 
-bool mla::cache_maps(const void* kv_fp8, int64_t rows, bool gather, int device, CUtensorMap* latent,
-                     CUtensorMap* rope) {
-  return kv_maps(kv_fp8, rows, gather, false, device, latent, rope);
+bool mla::cache_maps(const void* kv_fp8, int64_t rows, int device, CUtensorMap* latent, CUtensorMap* rope) {
+  return kv_maps(kv_fp8, rows, false, false, device, latent, rope);
 }
 
 extern "C" {

@@ -124,8 +124,8 @@ mla_status_t run_shared(const void* q, const void* kv, const float* kv_scale, co
   int device = 0;
   mla_status_t st = mla::device_ready(&device);
   if (st != MLA_OK) return st;
-  mla::SharedMaps m;
-  if (!mla::cache_maps(kv, kv_rows, kv_indices != nullptr, device, &m.latent, &m.rope)) return MLA_ERR_CUDA;
+  mla::SharedMaps m = {};
+  if (kv_indices == nullptr && !mla::cache_maps(kv, kv_rows, device, &m.latent, &m.rope)) return MLA_ERR_CUDA;
   auto* ws = static_cast<uint8_t*>(workspace);
   mla::SharedParams p;
   p.q = static_cast<const uint16_t*>(q);

@@ -11,9 +11,8 @@ namespace mla {
 
 // api.cu: MLA_OK when the current device is an sm_103 part whose kernels are set up.
 mla_status_t device_ready(int* device);
-// api.cu: the descriptors of an e4m3 cache's latent and rope boxes (tiles of 128 rows, or
-// single rows for gathers of four).
-bool cache_maps(const void* kv_fp8, int64_t rows, bool gather, int device, CUtensorMap* latent, CUtensorMap* rope);
+// api.cu: the descriptors of an e4m3 cache's latent and rope boxes (tiles of 128 rows).
+bool cache_maps(const void* kv_fp8, int64_t rows, int device, CUtensorMap* latent, CUtensorMap* rope);
 
 // A launch as a programmatic dependent of the previous kernel of the stream:
 // the kernel may be scheduled while that one finishes and waits for it
@@ -156,7 +155,7 @@ struct SharedParams {
   int32_t stall_stream;      // test hook: no copies are issued, so the waits run out
 };
 struct SharedMaps {
-  CUtensorMap latent, rope;
+  CUtensorMap latent, rope;  // (zeros with kv_indices: those keys are copied without descriptors)
 };
 constexpr int kSharedTokens = 4;  // query tokens of a job
 size_t shared_smem_bytes();
