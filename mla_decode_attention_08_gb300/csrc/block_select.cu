@@ -13,6 +13,8 @@
 // steps' latency, so scores and table entries are on their way before the row's length is known
 // (4 rows of 128 pages 4.0 us, 6.8 when they were loaded behind it; 64 rows of 2048 pages 5.7, with
 // the last score found bit by bit 10.8; 64 of 8192 13.9; 8 of 16384 22.6, bit by bit 198).
+#include <cfloat>
+
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"
@@ -195,11 +197,15 @@ __global__ void __launch_bounds__(kThreads, kHeld > 4 ? 1 : 2) block_select_kern
     low = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(scan[0][lane % kWarps]));
     high = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(scan[1][lane % kWarps]));
     const float least = score_of(low), width = score_of(high) - least;
-    const float by = width > 0.0f ? (kSteps - 1) / width : 0.0f;
-    // (never falls as the score rises; a width that overflows puts all in one step)
+    // Where the width or the steps a unit pass float32's range (or there is no width), 0: all finite
+    // scores share the lowest step.
+    const float steps = (kSteps - 1) / width;
+    const float by = width > 0.0f && width <= FLT_MAX && steps <= FLT_MAX ? steps : 0.0f;
+    // (Never falls as the score rises.  With a finite width no difference overflows.)
     auto step_of = [&](uint32_t key) {
-      const float at = key <= kMinusInf ? 0.0f : key >= kPlusInf ? kSteps - 1.0f : (score_of(key) - least) * by;
-      return static_cast<int>(fminf(at, kSteps - 1.0f));
+      if (key >= kPlusInf) return kSteps - 1;
+      if (key <= kMinusInf || by == 0.0f) return 0;
+      return static_cast<int>(fminf((score_of(key) - least) * by, kSteps - 1.0f));
     };
     each_key([&](int32_t, uint32_t key) { atomicAdd(&counts[step_of(key)], 1); });
     __syncthreads();
