@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(kThreads) block_means_kernel(const BlockMeansP
       if (slot >= p.limit) {
         atomicOr(p.err, MLA_DERR_KV_INDEX);
       } else if (slot >= 0 && (after != slot + 1 || (slot + 1) % p.page_size == 0)) {
-        ends[atomicAdd(&num_ends, 1)] = slot;
+        const int32_t at = atomicAdd(&num_ends, 1);
+        if (MLA_DCHECK(at < kThreads, p.err)) ends[at] = slot;
       }
     }
     __syncthreads();
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(kThreads) block_means_kernel(const BlockMeansP
         const float count = static_cast<float>(now.rows);
         uint32_t packed;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed) : "f"(y / count * scale), "f"(x / count * scale));
-        reinterpret_cast<uint32_t*>(p.means + static_cast<int64_t>(now.page) * kQkDim)[tid] = packed;
+        if (MLA_DCHECK(now.page >= 0 && static_cast<int64_t>(now.page) * p.page_size < p.limit, p.err))
+          reinterpret_cast<uint32_t*>(p.means + static_cast<int64_t>(now.page) * kQkDim)[tid] = packed;
         x = y = 0.0f;
       }
     }

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<kWide>, kWide ? 2 : 0) block_sco
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int32_t j = first + kWarpPages * u + 8 * i + col;
-      const bool here = u < groups && j < n;
+      const bool here = u < groups && j < n && MLA_DCHECK(j < p.max_pages, p.err);
       page[u][i] = here ? __ldg(p.block_table + static_cast<int64_t>(b) * p.table_stride + j) : -1;
       if (here && (page[u][i] < 0 || page[u][i] >= p.num_pages)) {
         atomicOr(p.err, MLA_DERR_KV_INDEX);
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<kWide>, kWide ? 2 : 0) block_sco
     }
   const uint8_t* means = reinterpret_cast<const uint8_t*>(p.means) + 16 * quad;
   auto load = [&](int32_t id, int c) {
-    return id >= 0 ? load_once(means + static_cast<int64_t>(id) * (2 * kQkDim) + 64 * c)
+    return id >= 0 && MLA_DCHECK(id < p.num_pages, p.err) ? load_once(means + static_cast<int64_t>(id) * (2 * kQkDim) + 64 * c)
                    : make_uint4(0, 0, 0, 0);
   };
   // (a warp behind the row's pages only brings its share of the queries)
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<kWide>, kWide ? 2 : 0) block_sco
           const int32_t j = first + kWarpPages * u + 8 * i + c;
           const bool counts = ((i ? valid[1] : valid[0]) >> (4 * c)) & 1;
           float x = counts ? (i ? best[1][e] : best[0][e]) * (1.0f / 24.0f) : -INFINITY;
-          if (j < p.max_pages) out[j] = t0 > 0 ? max_nan(x, out[j]) : x;  // (the lane's own, of the tokens before)
+          if (j < p.max_pages && MLA_DCHECK(j >= 0 && j < p.max_pages, p.err)) out[j] = t0 > 0 ? max_nan(x, out[j]) : x;  // (the lane's own, of the tokens before)
         }
       }
     }

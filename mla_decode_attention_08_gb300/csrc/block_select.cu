@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, kHeld > 4 ? 1 : 2) block_select_kern
   // Of the middle pages, [lo, hi), as many are taken as `want` says.
   const int32_t lo = p.sink, hi = row.pages - p.recent, want = p.blocks - p.sink - p.recent;
   const bool choose = row.pages > p.blocks;
+  if (!MLA_DCHECK(row.pages <= p.max_pages && hi <= row.pages, p.err)) return;
   const int32_t first = tid * kHeld;  // of the pages in registers
   uint32_t held[kHeld > 0 ? kHeld : 1];
   if constexpr (kHeld > 0) {
@@ -207,7 +208,10 @@ __global__ void __launch_bounds__(kThreads, kHeld > 4 ? 1 : 2) block_select_kern
       if (key <= kMinusInf || by == 0.0f) return 0;
       return static_cast<int>(fminf((score_of(key) - least) * by, kSteps - 1.0f));
     };
-    each_key([&](int32_t, uint32_t key) { atomicAdd(&counts[step_of(key)], 1); });
+    each_key([&](int32_t, uint32_t key) {
+      const int step = step_of(key);
+      if (MLA_DCHECK(step >= 0 && step < kSteps, p.err)) atomicAdd(&counts[step], 1);
+    });
     __syncthreads();
     // The highest step with which there are enough (every warp for itself): lane l has the
     // steps 8 l .. 8 l + 7.
@@ -265,7 +269,8 @@ __global__ void __launch_bounds__(kThreads, kHeld > 4 ? 1 : 2) block_select_kern
         __syncthreads();
         const int shift = max(0, 24 - __clz(high - low));
         each_key([&](int32_t, uint32_t key) {
-          if (key >= low && key <= high) atomicAdd(&counts[(key - low) >> shift], 1);
+          const uint32_t step = (key - low) >> shift;
+          if (key >= low && key <= high && MLA_DCHECK(step < kSteps, p.err)) atomicAdd(&counts[step], 1);
         });
         __syncthreads();
         low += static_cast<uint32_t>(find_step()) << shift;
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, kHeld > 4 ? 1 : 2) block_select_kern
   // The pages in order: a page's place among the chosen is the number before it.
   auto is_middle = [&](int32_t j) { return choose && j >= lo && j < hi; };
   auto put = [&](int32_t place, int32_t j, int32_t id) {
-    if (place >= p.blocks) return;
+    if (place >= p.blocks || !MLA_DCHECK(place >= 0 && j >= 0 && j < row.pages, p.err)) return;
     const bool ok = id >= 0 && id < p.num_pages;
     if (!ok) atomicOr(p.err, MLA_DERR_KV_INDEX);
     rows[place] = ok ? id * p.page_size : -1;

@@ -282,6 +282,7 @@ __device__ __forceinline__ void find_job(const SharedParams& p, Batch& r, int64_
     bool back = false;
     Group g = load_group(p, r.at, false, back);
     while (u - r.at_unit >= blocks_of(g) * units_of(p, g)) {  // (ends within the lane's run)
+      if (!MLA_DCHECK(r.at + 1 < p.batch, p.err)) break;
       r.at_unit += blocks_of(g) * units_of(p, g);
       g = load_group(p, ++r.at, false, back);
     }
@@ -380,6 +381,13 @@ struct CopyRows {
     const int t = threadIdx.x - 32 * kFirstCopyWarp;
     const int32_t* at = p.kv_indices + job.k0;
     const int32_t last = job.keys - 1, key = j * kTileTokens;
+    if (!MLA_DCHECK(job.k0 >= 0 && job.keys > 0 && static_cast<int64_t>(job.k0) + job.keys <= p.kv_limit, p.err)) {
+#pragma unroll
+      for (int i = 0; i < kLatentRows; ++i) latent[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kRopeRows; ++i) rope[i] = 0;
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kLatentRows; ++i) latent[i] = __ldg(at + min(last, key + (t >> 3) + i * (kCopyThreads / 8)));
 #pragma unroll
@@ -405,6 +413,9 @@ __device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint
   const int piece = t & 7, row0 = t >> 3, rope_piece = t & 3, rope_row0 = t >> 2;
   const uint8_t* latent = p.kv + 16 * piece;
   const uint8_t* rope = p.kv + kVDim + 16 * rope_piece;
+  auto at_row = [&](const uint8_t* first, int32_t row) {
+    return first + static_cast<int64_t>(MLA_DCHECK(row >= 0 && row < p.kv_rows, p.err) ? row : 0) * kQkDim;
+  };
   // (of the rows that a thread copies all have the same place in a swizzle's pattern)
   const uint32_t latent_at = sbase + kOffKeys + row0 * 128 + ((piece ^ (row0 & 7)) << 4);
   const uint32_t rope_at = sbase + kOffRope + rope_row0 * 64 + ((rope_piece ^ ((rope_row0 >> 1) & 3)) << 4);
@@ -423,7 +434,7 @@ __device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint
       if (!ok) break;
 #pragma unroll
       for (int i = 0; i < kRopeRows; ++i)
-        cp_async_16(rope_at + i * (kCopyThreads / 4) * 64, rope + static_cast<int64_t>(rows.rope[i]) * kQkDim);
+        cp_async_16(rope_at + i * (kCopyThreads / 4) * 64, at_row(rope, rows.rope[i]));
       cp_async_arrive(smem_u32(&ms->rope_full));
 #pragma unroll 1
       for (int c = 0; c < kPanels; ++c) {
@@ -433,7 +444,7 @@ __device__ __forceinline__ void run_copies(const SharedParams& p, Misc* ms, uint
 #pragma unroll
         for (int i = 0; i < kLatentRows; ++i)
           cp_async_16(latent_at + at * kPanelBytes + i * (kCopyThreads / 8) * 128,
-                      latent + static_cast<int64_t>(rows.latent[i]) * kQkDim + 128 * c);
+                      at_row(latent, rows.latent[i]) + 128 * c);
         cp_async_arrive(smem_u32(&ms->key_full[at]));
       }
     }
@@ -1171,7 +1182,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) shared_join_kernel(c
   pdl_launch_dependents();
   if (w0 == w1) return;
   const uint32_t missing = __ldcg(p.missing);  // (looked at behind the parts, which are read all the same)
-  if (!MLA_DCHECK(w0 >= 0 && w1 < p.workers && place >= 0 && place < kTokens, p.err)) return;
+  if (!MLA_DCHECK(token < p.total_q && w0 >= 0 && w1 < p.workers && place >= 0 && place < kTokens, p.err)) return;
   // The first worker's part is its last job's, the others' their first.
   auto slot = [&](int32_t w) { return shared_slot(w, w == w0); };
   const uint16_t* part = p.part + (static_cast<int64_t>(c) * kTokens + place) * (128 * kNumHeads) + tid * kNumHeads + head0;
