@@ -772,6 +772,9 @@ mla_status_t mla_shared_fwd_stall_stream(const void* q_bf16, const void* kv_fp8,
  *   slots      device int32 [num_tokens] (num_tokens 0 launches nothing).
  *   means      device bf16 [num_pages][576], 16-byte aligned.
  * A slot outside the cache or on a page without a mean sets MLA_DERR_KV_INDEX and is skipped.
+ * Of the decode calls mla_decode_fwd alone takes kv_indices, so a step over the pages that
+ * mla_block_select chooses is the e4m3 cache's; what is chosen by a bf16 cache's means is for a
+ * reader of the caller's own.
  */
 mla_status_t mla_block_means(const void* kv_fp8, const float* kv_scale, int64_t kv_rows, const int32_t* slots,
                              int64_t num_tokens, void* means, int32_t num_pages, int32_t page_size,

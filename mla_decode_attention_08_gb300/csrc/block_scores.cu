@@ -10,8 +10,10 @@
 // same order, so the sums are over the same pairs.  At 16 rows a product this is no work
 // for tcgen05, whose tiles have 128.  Several products' operands are under way at a time, across
 // the groups of 16 pages that a warp works through.  64 rows of up to 131072 tokens in pages of
-// 64 take 22.3 us, 115 MB at 5.2 TB/s (one group a warp at all sizes 26.8; 32 bytes a lane 29.8); 4 rows of up to
-// 8192 4.9 us, launch and three trips to memory.
+// 64 take 21.7 us, 115 MB at 5.3 TB/s (one group a warp at all sizes 26.8; 32 bytes a lane 29.8); 4 rows of up to
+// 8192 4.8 us, launch and three trips to memory.  Two query tokens take 23.7; three and four, 30.7 and
+// 31.9, have half as many bytes under way, since their sums need the registers, and read 4 KB of
+// queries from shared memory for each KB of means.
 #include "kernels.h"
 #include "ops.h"
 #include "ptx.cuh"

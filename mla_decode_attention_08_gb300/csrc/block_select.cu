@@ -11,8 +11,10 @@
 // against each other, or, where it holds too many for that (scores far apart, or alike), divided
 // into steps again, of the scores' bits now, until few are left or all are the same.  Bound by the
 // steps' latency, so scores and table entries are on their way before the row's length is known
-// (4 rows of 128 pages 4.0 us, 6.8 when they were loaded behind it; 64 rows of 2048 pages 5.7, with
-// the last score found bit by bit 10.8; 64 of 8192 13.9; 8 of 16384 22.6, bit by bit 198).
+// (4 rows of up to 128 pages 4.0 us, 6.8 when they were loaded behind it; 64 rows of up to 2048 pages
+// 6.3, with the last score found bit by bit 10.8; 64 of 8192 14.1; 8 of 16384 22.3, bit by bit 198).
+// Longer rows are one block's all the same, an SM that reads its row four times or more: 8 of 100000
+// take 121.
 #include <cfloat>
 
 #include "kernels.h"
@@ -400,8 +402,8 @@ cudaError_t block_select_prepare() {
   return cudaSuccess;
 }
 
-// Scores in registers where a row's pages fit them, as few a thread as do (64 rows of 4096 pages: 7.9
-// us with eight, 12.2 with sixteen; of 16384 from L2 23.4).
+// Scores in registers where a row's pages fit them, as few a thread as do (64 rows of 4096 pages: 8.3
+// us with eight, 12.2 with sixteen; of 16384 from L2 22.6).
 cudaError_t launch_block_select(const BlockSelectParams& p, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p.batch);
   const size_t smem = static_cast<size_t>(p.blocks) * 4;

@@ -12,9 +12,9 @@ namespace mla {
 // kernels, the query loads, the cache tile coordinates and the converters'
 // shared-memory addresses are checked against their buffers first; a failed
 // check sets MLA_DERR_DEBUG_BOUNDS in the workspace error word and skips the
-// access (a stand-in for a memory checker).  The operators around the decode step and over long contexts
-// check the accesses whose place comes from device data.  Release builds compile the
-// checks away.
+// access (a stand-in for a memory checker).  The operators around the decode step and
+// over long contexts check the accesses whose place comes from device data.  Release
+// builds compile the checks away.
 #ifdef MLA_DEBUG
 #define MLA_DCHECK(cond, err) ((cond) ? true : (atomicOr((err), MLA_DERR_DEBUG_BOUNDS), false))
 #else

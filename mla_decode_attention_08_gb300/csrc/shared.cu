@@ -35,8 +35,8 @@
 //
 // A tile's products are 18 of 64 cycles and 32 of 48, 2690 in all; it takes 2950.  The second
 // product reads 6 KB of operands for 32 cycles' work and waits for shared memory.  256
-// queries over 32768 keys take 200 us (1.46 PFLOP/s), by a page table 235, where a buffer's way
-// back is longer than TMA's; 64 over 8192 26.7 and 28.7, 8 over 1000 12.5 and 13.5, of which a
+// queries over 32768 keys take 204 us (1.43 PFLOP/s), by a page table 235, where a buffer's way
+// back is longer than TMA's; 64 over 8192 26.8 and 28.9, 8 over 1000 12.3 and 13.4, of which a
 // job's start (finding it, the query's two terms) is 4.5 and the second kernel 3.
 #include <cstddef>
 
