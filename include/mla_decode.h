@@ -698,7 +698,9 @@ mla_status_t mla_attn_merge(const void* parts_bf16, const float* lses, int32_t n
  * without keys gives zeros and lse -inf.  The query enters the products as two e4m3 terms
  * (exact down to 2^-13 of its head's largest magnitude), a probability as two e4m3 terms
  * (to 2^-8 of itself, or 2^-14 of the row's largest); accumulation and softmax statistics
- * are float32; out is rounded to bf16, parts of shared keys to half precision before.
+ * are float32; out is rounded to bf16, parts of shared keys to half precision before.  (So scores
+ * are to stay below 2^24 in magnitude, where float32 ends to hold their fractions: a head
+ * with larger ones gets values that mean nothing.)
  *   q_bf16     device, bf16 [total_q][16][576], 16-byte aligned.  A token's head with a value
  *              that is not finite gets NaN, as output and as lse.
  *   kv_fp8     device, e4m3fn codes [kv_rows][576], 16-byte aligned.  Codes of the groups'
